@@ -41,7 +41,9 @@ EXPORTS = ("w4_status_str", "w4_abi_version", "w4_last_cuda_error", "w4a16_gemv"
            "w4_dev_pool_stage", "w4_dev_pool_stats", "w4a16_gemv_chain",
            "w4a16_gemv_chain_workspace_bytes", "w4a16_gemv_chain_plan",
            "w4a16_gemv_chain_task_plan", "w4a16_gemv_id_plan", "w4a16_gemv_prefetch_l2",
-           "w4a16_gemv_plan_flags")
+           "w4a16_gemv_plan_flags", "w4_kv8_append", "w4_kv8_attn", "w4_kv8_attn_workspace_bytes",
+           "w4_kv8_select", "w4_kv8_select_workspace_bytes", "w4_kv8_weigh", "w4_kv8_evict",
+           "w4_kv8_evict_workspace_bytes")
 W4_TASK_SILU_MUL = 1
 W4_MAX_L2_RANGES = 4
 CHAIN_MAX_TASKS = 320
@@ -84,6 +86,22 @@ class ChainPlanInfo(ctypes.Structure):
 class ChainTaskInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("rows_per_window", "rows_per_lane", "team",
                                             "chunk_steps", "chunks", "windows_per_item", "dot")]
+
+
+class KV8CacheStruct(ctypes.Structure):
+    """struct w4_kv8_cache of include/w4a16.h."""
+    _fields_ = [("kc", ctypes.c_void_p), ("vc", ctypes.c_void_p), ("ks", ctypes.c_void_p),
+                ("vs", ctypes.c_void_p), ("ranges", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("page_tokens", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_stride", ctypes.c_size_t), ("head_stride", ctypes.c_size_t)]
+
+
+class KV8BatchStruct(ctypes.Structure):
+    """struct w4_kv8_batch of include/w4a16.h."""
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("batch", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("rows", ctypes.c_int), ("max_new", ctypes.c_int), ("max_len", ctypes.c_int)]
 
 
 _lib = None
@@ -162,6 +180,24 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4a16_gemv_chain_task_plan.restype = i32
     lib.w4a16_gemv_chain_task_plan.argtypes = [ctypes.POINTER(GemvTask), i32, i32,
                                                ctypes.POINTER(ChainTaskInfo)]
+    cp, bp, f32 = ctypes.POINTER(KV8CacheStruct), ctypes.POINTER(KV8BatchStruct), ctypes.c_float
+    lib.w4_kv8_append.restype = i32
+    lib.w4_kv8_append.argtypes = [cp, bp, vp, vp, sz, vp, u32, vp]
+    lib.w4_kv8_attn.restype = i32
+    lib.w4_kv8_attn.argtypes = [vp, vp, vp, sz, i32, cp, bp, f32, i32, vp, vp, i32, vp, sz, vp,
+                                u32, vp]
+    lib.w4_kv8_attn_workspace_bytes.restype = sz
+    lib.w4_kv8_attn_workspace_bytes.argtypes = [cp, bp, i32, i32]
+    lib.w4_kv8_select.restype = i32
+    lib.w4_kv8_select.argtypes = [vp, vp, i32, i32, i32, vp, sz, i32, cp, bp, vp, sz, vp, u32, vp]
+    lib.w4_kv8_select_workspace_bytes.restype = sz
+    lib.w4_kv8_select_workspace_bytes.argtypes = [cp, bp]
+    lib.w4_kv8_weigh.restype = i32
+    lib.w4_kv8_weigh.argtypes = [vp, sz, i32, vp, cp, bp, f32, i32, vp, u32, vp]
+    lib.w4_kv8_evict.restype = i32
+    lib.w4_kv8_evict.argtypes = [vp, vp, vp, i32, i32, i32, cp, bp, vp, sz, vp, u32, vp]
+    lib.w4_kv8_evict_workspace_bytes.restype = sz
+    lib.w4_kv8_evict_workspace_bytes.argtypes = [cp, bp, i32]
     _lib = lib
     return lib
 
@@ -640,3 +676,269 @@ def gemv_chain(tasks, workspace: torch.Tensor, status: torch.Tensor = None, pdl:
                stream=None):
     """Run the tasks (dicts from gemv_task / gemv_id_task) as one launch."""
     bind_gemv_chain(tasks, workspace, status)(pdl=pdl, stream=stream)
+
+
+# ------------------------------------------------------------------ 8-bit key/value cache
+class KV8Cache:
+    """The pages of an 8-bit key/value cache (struct w4_kv8_cache).
+
+    kc, vc: uint8 [pages, kv_heads, page_tokens, head_dim], the last two dimensions dense, both
+    with the same strides (views of one larger tensor, of a layer say, are fine); ks, vs: fp32
+    [pages, kv_heads]; ranges: uint8 [pages, kv_heads, 2, head_dim] or None (kv8_select needs
+    it); weight: fp32 [pages, kv_heads, page_tokens] or None (kv8_weigh and kv8_evict need it).
+    A value is (code - 128) * step."""
+
+    def __init__(self, kc: torch.Tensor, vc: torch.Tensor, ks: torch.Tensor, vs: torch.Tensor,
+                 ranges: torch.Tensor = None, weight: torch.Tensor = None):
+        for t, name in ((kc, "kc"), (vc, "vc")):
+            if not t.is_cuda or t.dtype != torch.uint8 or t.dim() != 4:
+                raise ValueError(f"{name} must be a 4-dimensional uint8 CUDA tensor")
+        if kc.shape != vc.shape or kc.stride() != vc.stride():
+            raise ValueError("kc and vc must have the same shape and strides")
+        n, h, p, d = kc.shape
+        if kc.stride(3) != 1 or kc.stride(2) != d:
+            raise ValueError("tokens and channels of a block must be dense")
+        for t, name, shape, dtype in ((ks, "ks", (n, h), torch.float32),
+                                      (vs, "vs", (n, h), torch.float32),
+                                      (ranges, "ranges", (n, h, 2, d), torch.uint8),
+                                      (weight, "weight", (n, h, p), torch.float32)):
+            if t is None and name in ("ranges", "weight"):
+                continue
+            _need(t, dtype, name)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+        self.tensors = (kc, vc, ks, vs, ranges, weight)
+        self.pages, self.kv_heads, self.page_tokens, self.head_dim = n, h, p, d
+        self.device = kc.device
+        self.struct = KV8CacheStruct(
+            *[None if t is None else t.data_ptr() for t in self.tensors], n, h, p, d,
+            kc.stride(0) if n > 1 else h * p * d, kc.stride(1) if h > 1 else p * d)
+
+
+class KV8Batch:
+    """The sequences of a call (struct w4_kv8_batch): table int32 [batch, max_pages], lens int32
+    [batch] (the new tokens included), offsets int32 [batch + 1] of the packed new rows or None
+    (one row per sequence); rows, max_new and max_len bound them (the tensors may change between
+    calls, within the bounds)."""
+
+    def __init__(self, table: torch.Tensor, lens: torch.Tensor, offsets: torch.Tensor = None,
+                 rows: int = None, max_new: int = 1, max_len: int = None, page_tokens: int = None):
+        _need(table, torch.int32, "table")
+        _need(lens, torch.int32, "lens")
+        if table.dim() != 2 or lens.shape != (table.shape[0],):
+            raise ValueError("table must be [batch, max_pages] and lens [batch]")
+        if offsets is not None:
+            _need(offsets, torch.int32, "offsets")
+            if offsets.shape != (table.shape[0] + 1,):
+                raise ValueError("offsets must be [batch + 1]")
+        self.batch, self.max_pages = table.shape
+        self.rows = rows if rows is not None else (self.batch if offsets is None else None)
+        self.max_new = max_new
+        if max_len is None:
+            if page_tokens is None:
+                raise ValueError("max_len (or page_tokens) is needed")
+            max_len = self.max_pages * page_tokens
+        self.max_len = max_len
+        self.tensors = (table, lens, offsets)
+        self._structs = {}
+
+    def struct(self, rows: int) -> KV8BatchStruct:
+        """The C struct for calls on `rows` packed rows."""
+        if self.rows is not None and rows != self.rows:
+            raise ValueError(f"expected {self.rows} packed rows, got {rows}")
+        if rows not in self._structs:
+            self._structs[rows] = KV8BatchStruct(
+                *[None if t is None else t.data_ptr() for t in self.tensors], self.batch,
+                self.max_pages, rows, self.max_new, self.max_len)
+        return self._structs[rows]
+
+
+def _kv8_rows(t: torch.Tensor, name: str, heads: int, d: int):
+    """Packed rows [T, heads, head_dim] of bf16, heads and channels dense: (row stride, T)."""
+    if not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a CUDA tensor of bfloat16")
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [rows, heads, head_dim]")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"heads and channels of {name} must be dense")
+    return (t.stride(0) if t.shape[0] > 1 else t.shape[1] * d), t.shape[0]
+
+
+def _kv8_bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _kv8_call(fn, name, args, keep):
+    """call(pdl=False, stream=None) that enqueues fn(*args) again."""
+    def call(pdl: bool = False, stream=None):
+        _check(fn(*args, W4_FLAG_PDL if pdl else 0, _stream(stream)), name)
+
+    call.tensors = keep
+    return call
+
+
+def kv8_attn_workspace_bytes(cache: KV8Cache, batch: KV8Batch, q_heads: int, rows: int = None,
+                             max_sel: int = 0) -> int:
+    """Zero-filled scratch of a kv8_attn call (rows: packed rows, if the batch does not say)."""
+    rows = rows if rows is not None else batch.rows if batch.rows is not None else \
+        batch.batch * batch.max_new
+    return int(load().w4_kv8_attn_workspace_bytes(ctypes.byref(cache.struct),
+                                                  ctypes.byref(batch.struct(rows)), q_heads,
+                                                  max_sel))
+
+
+def kv8_select_workspace_bytes(cache: KV8Cache, batch: KV8Batch) -> int:
+    return int(load().w4_kv8_select_workspace_bytes(ctypes.byref(cache.struct),
+                                                    ctypes.byref(batch.struct(batch.batch))))
+
+
+def kv8_evict_workspace_bytes(cache: KV8Cache, batch: KV8Batch, budget: int) -> int:
+    rows = batch.rows if batch.rows is not None else batch.batch
+    return int(load().w4_kv8_evict_workspace_bytes(ctypes.byref(cache.struct),
+                                                   ctypes.byref(batch.struct(rows)), budget))
+
+
+def bind_kv8_append(cache: KV8Cache, batch: KV8Batch, k: torch.Tensor, v: torch.Tensor,
+                    status: torch.Tensor = None):
+    """w4_kv8_append with its arguments marshalled once: returns call(pdl=False, stream=None),
+    which stores whatever rows k and v ([rows, kv_heads, head_dim]) hold at that time."""
+    stride, rows = _kv8_rows(k, "k", cache.kv_heads, cache.head_dim)
+    if _kv8_rows(v, "v", cache.kv_heads, cache.head_dim) != (stride, rows):
+        raise ValueError("k and v must have the same rows and row stride")
+    bs = batch.struct(rows)
+    args = (ctypes.byref(cache.struct), ctypes.byref(bs), _ptr(k), _ptr(v), stride, _ptr(status))
+    return _kv8_call(load().w4_kv8_append, "w4_kv8_append", args, (cache, batch, bs, k, v, status))
+
+
+def kv8_append(cache: KV8Cache, batch: KV8Batch, k: torch.Tensor, v: torch.Tensor,
+               status: torch.Tensor = None, pdl: bool = False, stream=None):
+    """Store the new tokens' keys and values ([rows, kv_heads, head_dim] bf16) in the pages."""
+    bind_kv8_append(cache, batch, k, v, status)(pdl, stream)
+
+
+def bind_kv8_attn(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: float,
+                  out: torch.Tensor, lse: torch.Tensor = None, window: int = 0,
+                  sel: torch.Tensor = None, n_sel: torch.Tensor = None,
+                  workspace: torch.Tensor = None, status: torch.Tensor = None):
+    """w4_kv8_attn with its arguments marshalled once: returns call(pdl=False, stream=None)."""
+    stride, rows = _kv8_rows(q, "q", None, cache.head_dim)
+    q_heads = q.shape[1]
+    _need(out, torch.bfloat16, "out")
+    if tuple(out.shape) != (rows, q_heads, cache.head_dim):
+        raise ValueError("out must be [rows, q_heads, head_dim]")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if tuple(lse.shape) != (rows, q_heads):
+            raise ValueError("lse must be [rows, q_heads]")
+    max_sel = 0
+    if sel is not None or n_sel is not None:
+        if sel is None or n_sel is None:
+            raise ValueError("sel and n_sel go together")
+        _need(sel, torch.int32, "sel")
+        _need(n_sel, torch.int32, "n_sel")
+        max_sel = sel.shape[-1]
+        if tuple(sel.shape) != (batch.batch, cache.kv_heads, max_sel) or \
+                tuple(n_sel.shape) != (batch.batch, cache.kv_heads):
+            raise ValueError("sel must be [batch, kv_heads, max_sel] and n_sel [batch, kv_heads]")
+    bs = batch.struct(rows)
+    args = (_ptr(out), _ptr(lse), _ptr(q), stride, q_heads, ctypes.byref(cache.struct),
+            ctypes.byref(bs), scale, window, _ptr(sel), _ptr(n_sel), max_sel, _ptr(workspace),
+            _kv8_bytes(workspace), _ptr(status))
+    return _kv8_call(load().w4_kv8_attn, "w4_kv8_attn", args,
+                     (cache, batch, bs, q, out, lse, sel, n_sel, workspace, status))
+
+
+def kv8_attn(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: float,
+             out: torch.Tensor = None, lse: torch.Tensor = None, window: int = 0,
+             sel: torch.Tensor = None, n_sel: torch.Tensor = None,
+             workspace: torch.Tensor = None, status: torch.Tensor = None, pdl: bool = False,
+             stream=None) -> torch.Tensor:
+    """Attention of the new rows q [rows, q_heads, head_dim] over their sequences' cached tokens
+    (causal; within `window` tokens if > 0; over the pages of sel / n_sel if given)."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    bind_kv8_attn(cache, batch, q, scale, out, lse, window, sel, n_sel, workspace,
+                  status)(pdl, stream)
+    return out
+
+
+def bind_kv8_select(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, sel: torch.Tensor,
+                    n_sel: torch.Tensor, sink: int = 1, recent: int = 1,
+                    workspace: torch.Tensor = None, status: torch.Tensor = None):
+    """w4_kv8_select with its arguments marshalled once: returns call(pdl=False, stream=None)."""
+    stride, rows = _kv8_rows(q, "q", None, cache.head_dim)
+    _need(sel, torch.int32, "sel")
+    _need(n_sel, torch.int32, "n_sel")
+    if sel.dim() != 3 or tuple(sel.shape[:2]) != (batch.batch, cache.kv_heads) or \
+            tuple(n_sel.shape) != (batch.batch, cache.kv_heads):
+        raise ValueError("sel must be [batch, kv_heads, max_sel] and n_sel [batch, kv_heads]")
+    bs = batch.struct(rows)
+    args = (_ptr(sel), _ptr(n_sel), sel.shape[2], sink, recent, _ptr(q), stride, q.shape[1],
+            ctypes.byref(cache.struct), ctypes.byref(bs), _ptr(workspace), _kv8_bytes(workspace),
+            _ptr(status))
+    return _kv8_call(load().w4_kv8_select, "w4_kv8_select", args,
+                     (cache, batch, bs, q, sel, n_sel, workspace, status))
+
+
+def kv8_select(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, max_sel: int, sink: int = 1,
+               recent: int = 1, workspace: torch.Tensor = None, status: torch.Tensor = None,
+               pdl: bool = False, stream=None):
+    """(sel, n_sel): the logical pages of highest score bound for each sequence's new row."""
+    sel = torch.empty((batch.batch, cache.kv_heads, max_sel), dtype=torch.int32, device=q.device)
+    n_sel = torch.empty((batch.batch, cache.kv_heads), dtype=torch.int32, device=q.device)
+    bind_kv8_select(cache, batch, q, sel, n_sel, sink, recent, workspace, status)(pdl, stream)
+    return sel, n_sel
+
+
+def bind_kv8_weigh(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, lse: torch.Tensor,
+                   scale: float, window: int = 0, status: torch.Tensor = None):
+    """w4_kv8_weigh with its arguments marshalled once: returns call(pdl=False, stream=None)."""
+    stride, rows = _kv8_rows(q, "q", None, cache.head_dim)
+    _need(lse, torch.float32, "lse")
+    if tuple(lse.shape) != (rows, q.shape[1]):
+        raise ValueError("lse must be [rows, q_heads]")
+    bs = batch.struct(rows)
+    args = (_ptr(q), stride, q.shape[1], _ptr(lse), ctypes.byref(cache.struct), ctypes.byref(bs),
+            scale, window, _ptr(status))
+    return _kv8_call(load().w4_kv8_weigh, "w4_kv8_weigh", args,
+                     (cache, batch, bs, q, lse, status))
+
+
+def kv8_weigh(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, lse: torch.Tensor, scale: float,
+              window: int = 0, status: torch.Tensor = None, pdl: bool = False, stream=None):
+    """Add the attention weight that each cached token receives from the new rows to
+    cache.weight (lse as given by kv8_attn for the same rows)."""
+    bind_kv8_weigh(cache, batch, q, lse, scale, window, status)(pdl, stream)
+
+
+def bind_kv8_evict(cache: KV8Cache, batch: KV8Batch, dst_table: torch.Tensor, kept: torch.Tensor,
+                   new_lens: torch.Tensor, sink: int = 0, recent: int = 0,
+                   workspace: torch.Tensor = None, status: torch.Tensor = None):
+    """w4_kv8_evict with its arguments marshalled once: returns call(pdl=False, stream=None)."""
+    for t, name in ((dst_table, "dst_table"), (kept, "kept"), (new_lens, "new_lens")):
+        _need(t, torch.int32, name)
+    if kept.dim() != 3 or tuple(kept.shape[:2]) != (batch.batch, cache.kv_heads):
+        raise ValueError("kept must be [batch, kv_heads, budget]")
+    budget = kept.shape[2]
+    if tuple(dst_table.shape) != (batch.batch, -(-budget // cache.page_tokens)) or \
+            tuple(new_lens.shape) != (batch.batch,):
+        raise ValueError("dst_table must be [batch, ceil(budget / page_tokens)], new_lens [batch]")
+    bs = batch.struct(batch.rows if batch.rows is not None else batch.batch)
+    args = (_ptr(dst_table), _ptr(kept), _ptr(new_lens), budget, sink, recent,
+            ctypes.byref(cache.struct), ctypes.byref(bs), _ptr(workspace), _kv8_bytes(workspace),
+            _ptr(status))
+    return _kv8_call(load().w4_kv8_evict, "w4_kv8_evict", args,
+                     (cache, batch, bs, dst_table, kept, new_lens, workspace, status))
+
+
+def kv8_evict(cache: KV8Cache, batch: KV8Batch, budget: int, dst_table: torch.Tensor,
+              sink: int = 0, recent: int = 0, workspace: torch.Tensor = None,
+              status: torch.Tensor = None, pdl: bool = False, stream=None):
+    """(kept, new_lens): the `budget` tokens of most accumulated weight of each sequence and head,
+    gathered into the pages of dst_table."""
+    kept = torch.empty((batch.batch, cache.kv_heads, budget), dtype=torch.int32,
+                       device=cache.device)
+    new_lens = torch.empty((batch.batch,), dtype=torch.int32, device=cache.device)
+    bind_kv8_evict(cache, batch, dst_table, kept, new_lens, sink, recent, workspace,
+                   status)(pdl, stream)
+    return kept, new_lens

@@ -649,6 +649,206 @@ typedef struct w4_chain_task_info {
 w4_status w4a16_gemv_chain_task_plan(const w4_gemv_task *tasks, int n_tasks, int task,
                                      w4_chain_task_info *info);
 
+/*
+ * kv8 — a key/value cache in 8 bits and the attention that reads it.
+ *
+ * A decoder layer's attention runs between the merged q/k/v product and the
+ * output projection.  Page "Gemma 4 on a 4 GB GPU in Plain PyTorch", sections
+ * "Step 4" and "Step 7", keeps the cache in the engine's own hands, one slot
+ * per position on full layers and a sliding window on the others, with
+ * several query heads on each key head.  Here keys and values are stored in
+ * 8 bits in pages of page_tokens tokens, with one fp32 step for each (page,
+ * head) of keys and one of values:
+ *
+ *   key[t][d] = (kc[page][head][t % page_tokens][d] - 128) * ks[page][head],
+ *   page = table[sequence][t / page_tokens], values likewise from vc and vs.
+ *
+ * The library's writers (w4_kv8_append, w4_kv8_evict) choose steps that are
+ * powers of two, so rescaling a block and reading it back round nowhere but
+ * in the codes; the readers take any finite step.
+ *
+ * Conventions beside those at the top of this file:
+ *   - `offsets` packs the sequences' new (query) rows: rows offsets[b] ..
+ *     offsets[b + 1] - 1 belong to sequence b and are its LAST tokens, at
+ *     positions lens[b] - n .. lens[b] - 1.  NULL: one row per sequence, row
+ *     b.  Lengths count the new tokens.
+ *   - Query row t sees the keys at positions <= its own (and, with a window
+ *     w > 0, > its own - w).  Query head i reads key head i / (q_heads /
+ *     kv_heads).
+ *   - A length or row count that is negative, a length over max_len or the
+ *     table's pages, more new rows than max_new, rows outside the packed
+ *     ones, a page id outside [0, num_pages) that is read: W4_ERR_INDEX in
+ *     *status_dev, and what belongs to that sequence (of a page id: that
+ *     sequence and head) is left unwritten.  Table entries past a sequence's
+ *     pages are not read.  A new row at a negative position (an empty
+ *     sequence of a padded batch) is stored nowhere and sees nothing.
+ *   - Calls are deterministic: no sum's order depends on timing.
+ *   - Codes past a sequence's length may hold anything.
+ */
+typedef struct w4_kv8_cache {
+    void *kc, *vc;       /* uint8 [num_pages][kv_heads][page_tokens][head_dim]: tokens and
+                            channels dense, pages and heads at the strides below; 16-byte
+                            aligned */
+    float *ks, *vs;      /* fp32 [num_pages][kv_heads] steps */
+    void *ranges;        /* uint8 [num_pages][kv_heads][2][head_dim], 16-byte aligned: lowest,
+                            then highest key code of each channel over the page's tokens; kept by
+                            w4_kv8_append and w4_kv8_evict, read by w4_kv8_select.  Or NULL */
+    float *weight;       /* fp32 [num_pages][kv_heads][page_tokens]: accumulated attention weight
+                            of each token; zeroed by w4_kv8_append, added to by w4_kv8_weigh, read
+                            and moved by w4_kv8_evict.  Or NULL */
+    int num_pages;
+    int kv_heads;
+    int page_tokens;     /* 16, 32, 64 or 128 */
+    int head_dim;        /* 64, 128 or 256 */
+    size_t page_stride;  /* bytes between pages of kc and of vc, a multiple of 16 */
+    size_t head_stride;  /* bytes between heads, a multiple of 16, at least page_tokens * head_dim */
+} w4_kv8_cache;
+
+typedef struct w4_kv8_batch {
+    const int32_t *table;    /* device [batch][max_pages]: physical page of each logical one */
+    const int32_t *lens;     /* device [batch]: tokens, the new ones included */
+    const int32_t *offsets;  /* device [batch + 1], or NULL */
+    int batch;               /* sequences, 1 .. W4_KV8_MAX_BATCH */
+    int max_pages;           /* row length of the table */
+    int rows;                /* packed new rows (batch when offsets is NULL) */
+    int max_new;             /* upper bound of a sequence's new rows (1 when offsets is NULL) */
+    int max_len;             /* upper bound of lens, at most max_pages * page_tokens; plans use it,
+                                results do not depend on it beyond the order of sums */
+} w4_kv8_batch;
+
+#define W4_KV8_MAX_BATCH 4096
+#define W4_KV8_MAX_GROUP 128    /* query heads on one key head */
+
+/*
+ * w4_kv8_append — store the new tokens' keys and values.
+ *
+ * For each (page, head) that receives new tokens, with m the largest |value|
+ * among them:
+ *   step' = max(step of the tokens already in the block, the least power of
+ *           two s >= 2^-100 with m <= 127 s)
+ *   code' = 128 + rint((code - 128) * (step / step')) of those tokens
+ *   code  = 128 + rint(value / step') of the new ones
+ * (rint half to even; the quotient step / step' rounded to fp32).  A block
+ * whose first token is new starts over: its old contents count for nothing.
+ * ranges (if given) are brought up to date, weight (if given) is zeroed for
+ * the new tokens.  A second call with the same arguments changes nothing.
+ *
+ * k, v        bf16, row r head h at element r * row_stride + h * head_dim;
+ *             16-byte aligned, row_stride a multiple of 8 (a slice of the
+ *             merged product's rows).
+ * A value that is not finite: its (page, head) block of keys or of values is
+ * left as it was (ranges, for values the weights too) and W4_ERR_VALUE is
+ * recorded.  A page that receives tokens must belong to one sequence only.
+ * flags: W4_FLAG_PDL.
+ */
+w4_status w4_kv8_append(const w4_kv8_cache *cache, const w4_kv8_batch *batch, const void *k,
+                        const void *v, size_t row_stride, int32_t *status_dev, unsigned flags,
+                        w4_stream_t stream);
+
+/*
+ * w4_kv8_attn — attention of the new rows over the cache.
+ *
+ *   out[r][i] = sum_t p_t value[t],  p_t = exp(scale q.key[t]) / sum of them,
+ *   lse[r][i] = log of that sum
+ * over the keys t that row r sees; a row that sees none gives 0 and -inf.
+ * Products are exact and sums fp32; p is rounded to fp16, scaled so that
+ * only weights below 2^-28 of the row's largest lose bits.
+ *
+ * out         bf16 [rows][q_heads][head_dim], 16-byte aligned.
+ * lse         fp32 [rows][q_heads], or NULL.
+ * q           bf16, row r head i at element r * q_row_stride + i * head_dim,
+ *             16-byte aligned, stride a multiple of 8.
+ * q_heads     a multiple of kv_heads, at most W4_KV8_MAX_GROUP times it.
+ * window      > 0: sliding window; 0: none.
+ * sel, n_sel  NULL, or int32 [batch][kv_heads][max_sel] logical pages in
+ *             ascending order and int32 [batch][kv_heads] how many (as written by
+ *             w4_kv8_select): the row sees tokens of those pages only.  One row per
+ *             sequence (W4_ERR_SHAPE otherwise).  An entry outside the
+ *             sequence's pages or a count outside 0 .. max_sel: W4_ERR_INDEX.
+ * workspace   w4_kv8_attn_workspace_bytes(...) bytes, 16-byte aligned,
+ *             zero-filled before its first use and left ready for the next call; not
+ *             shared by calls that may overlap.
+ * flags       W4_FLAG_PDL.
+ */
+w4_status w4_kv8_attn(void *out, float *lse, const void *q, size_t q_row_stride, int q_heads,
+                      const w4_kv8_cache *cache, const w4_kv8_batch *batch, float scale,
+                      int window, const int32_t *sel, const int32_t *n_sel, int max_sel,
+                      void *workspace, size_t workspace_bytes, int32_t *status_dev,
+                      unsigned flags, w4_stream_t stream);
+
+/* max_sel: 0 without a selection.  0 bytes for invalid arguments. */
+size_t w4_kv8_attn_workspace_bytes(const w4_kv8_cache *cache, const w4_kv8_batch *batch,
+                                   int q_heads, int max_sel);
+
+/*
+ * w4_kv8_select — the pages worth reading for each sequence's one new row.
+ *
+ * A page's score bounds from above the sum over the group's query heads of
+ * the largest q.key in the page: with up[d] = sum_i max(q_i[d], 0) and
+ * down[d] = sum_i min(q_i[d], 0) over the heads i of the group (fp32, in
+ * order), rounded to 8 bits with one power-of-two step u for both (the least
+ * with max(up, -down) <= 127 u),
+ *   score = ks[page] * sum_d (rint(up/u) (hi[d] - 128) + rint(down/u) (lo[d] - 128))
+ * a whole number times the block's step: the same on every machine.  The first `sink`
+ * and the last `recent` pages are always taken, the rest by score, equal
+ * scores from the lowest page on, max_sel pages in all (all, if there are
+ * fewer).
+ *
+ * sel         int32 [batch][kv_heads][max_sel], ascending, -1 past the count.
+ * n_sel       int32 [batch][kv_heads].
+ * max_sel     >= max(1, sink + recent).
+ * Needs ranges.  One row per sequence.  workspace, flags: as w4_kv8_attn.
+ */
+w4_status w4_kv8_select(int32_t *sel, int32_t *n_sel, int max_sel, int sink, int recent,
+                        const void *q, size_t q_row_stride, int q_heads,
+                        const w4_kv8_cache *cache, const w4_kv8_batch *batch, void *workspace,
+                        size_t workspace_bytes, int32_t *status_dev, unsigned flags,
+                        w4_stream_t stream);
+
+size_t w4_kv8_select_workspace_bytes(const w4_kv8_cache *cache, const w4_kv8_batch *batch);
+
+/*
+ * w4_kv8_weigh — add up the attention weight that each token received.
+ *
+ *   weight[t] += sum over rows r that see t and heads i of the group of
+ *                exp(scale q_ri.key[t] - lse[r][i])
+ * lse as written by w4_kv8_attn for the same rows (a row with lse = -inf
+ * adds nothing).  flags: W4_FLAG_PDL.
+ */
+w4_status w4_kv8_weigh(const void *q, size_t q_row_stride, int q_heads, const float *lse,
+                       const w4_kv8_cache *cache, const w4_kv8_batch *batch, float scale,
+                       int window, int32_t *status_dev, unsigned flags, w4_stream_t stream);
+
+/*
+ * w4_kv8_evict — keep the `budget` tokens of most weight, in fresh pages.
+ *
+ * For each (sequence, head): the first `sink` and last `recent` tokens and,
+ * of the others, those of most accumulated weight (equal weights from the
+ * lowest position on), min(len, budget) tokens in all, in order.  Their
+ * codes go to the pages of dst_table, slot by slot, each block's step the
+ * largest of its tokens' steps and codes rescaled to it as in
+ * w4_kv8_append; weights move along, ranges (if given) are written.  Heads keep
+ * different tokens, so positions inside the kept cache count order only.
+ * Source pages are not changed.
+ *
+ * dst_table   device int32 [batch][ceil(budget / page_tokens)]: pages in no
+ *             other use (an id outside [0, num_pages): W4_ERR_INDEX, that page
+ *             is left unwritten).  Entries past a sequence's kept pages are not read.
+ * kept        int32 [batch][kv_heads][budget]: positions kept, ascending, -1
+ *             past the count.
+ * new_lens    int32 [batch]: min(len, budget); not the lens array itself.
+ * budget      >= max(1, sink + recent).
+ * A NaN weight counts as the largest.  Needs weight.  offsets and rows are
+ * not used.  workspace, flags: as w4_kv8_attn.
+ */
+w4_status w4_kv8_evict(const int32_t *dst_table, int32_t *kept, int32_t *new_lens, int budget,
+                       int sink, int recent, const w4_kv8_cache *cache,
+                       const w4_kv8_batch *batch, void *workspace, size_t workspace_bytes,
+                       int32_t *status_dev, unsigned flags, w4_stream_t stream);
+
+size_t w4_kv8_evict_workspace_bytes(const w4_kv8_cache *cache, const w4_kv8_batch *batch,
+                                    int budget);
+
 #ifdef __cplusplus
 }
 #endif
