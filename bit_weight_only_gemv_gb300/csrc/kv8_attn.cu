@@ -1,15 +1,75 @@
-// Attention over the 8-bit cache (w4_kv8_attn) and the accumulation of
-// attention weights (w4_kv8_weigh).
-#include "kv8.cuh"
+// Attention over the 8-bit cache for few query rows on a key head: single
+// tokens of a batch, also over chosen pages (w4_kv8_attn), and the entry that
+// picks between this kernel and the prompt-chunk kernel.
+//
+// One pass over the keys and values with a running maximum and sum:
+//   x_t = scale log2(e) q.k_t,  m = max x_t,  l = sum 2^(x_t - m),
+//   o = sum 2^(x_t - m) v_t / l.
+// The bytes of the cache bound it (2 D bytes a token and head against
+// 4 D G flops), so the work is cut into equal runs of 16-token slices over
+// all sequences and heads, one run a CTA, whatever the lengths: a run that
+// begins or ends inside a (sequence, head) leaves a partial result in the
+// workspace, and the last of its CTAs to arrive joins the parts in order.
+// Each warp streams its own slices: a ring of tiled copies (TMA, swizzled so
+// that no read below meets a bank conflict), its own running m, l and o; the
+// CTA's warps join through shared memory once per run and unit.
+//
+// Tensor cores take the products in fp16 (kv8_mma.cuh): codes are exact,
+// query rows are scaled by a power of two, weights 2^(x - m) are scaled by
+// 2^11 times the block's value step over the largest step met so far (so a
+// block's step costs one multiplication per weight).  m moves only when a
+// score passes it by kLag: then, and when a larger step comes, o and l are
+// rescaled; so most slices need no exchange between lanes.  A slice with
+// weights below fp16's normal range takes one more pass over its values for
+// each 29 bits of range: a channel that the heavy tokens leave at zero shows
+// the light ones, and they keep their 11 bits too.
+#include <algorithm>
+#include <mutex>
+
+#include "gemv_host.h"
+#include "kv8_mma.cuh"
+#include "tc_common.cuh"
 
 namespace w4 {
 namespace kv8 {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kMaxD = 256;
+constexpr int kSlice = 16;               // tokens of a slice
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRing = 64;                // slice descriptions kept per warp
+constexpr float kLag = 4.0f;             // log2 of how far a score may pass m
+constexpr float kWeightScale = 2048.0f;  // weights as fp16: at most 2^(4 + 11)
+constexpr float kHalfNormal = 6.103515625e-05f;   // 2^-14, fp16's least normal value
+constexpr float kLevel = 536870912.0f;            // 2^29: from there to 2^15, well in range
+constexpr float kLeast = 7.5e-37f;                // above 2^-120: five ranges reach it
+constexpr long long kWait = 1LL << 31;   // about a second
+constexpr int kMinSlices = 16;           // of a CTA's run: two a warp
+
+template <int D, int NQ>
+struct Shape {
+  static constexpr int kRows = 8 * NQ;                        // query rows of a unit
+  static constexpr int kStageBytes = 2 * kSlice * D;          // keys, then values
+  static constexpr int kPerSm = D == 256 ? 1 : 2;             // resident CTAs
+  static constexpr int kStages = D == 64 ? 6 : 3;
+  static constexpr int kPitch = D + 4;                        // floats of a joined row
+  static constexpr int kStageTotal = kWarps * kStages * kStageBytes;
+  static_assert(kWarps * kRows * kPitch * 4 <= kStageTotal, "the join reuses the stages");
+  static constexpr int kMeta = kStageTotal;                   // [kWarps][kRing] Meta
+  static constexpr int kStats = kMeta + kWarps * kRing * 16;  // [kWarps][kRows] (m, l)
+  static constexpr int kBars = kStats + kWarps * kRows * 8;
+  static constexpr int kMisc = kBars + kWarps * kStages * 8;
+  static constexpr int kSmem = kMisc + 128 + 1024;            // and alignment
+};
+
+struct Meta {
+  int page;   // -1: nothing to read
+  int tok;    // position of the slice's first token
+  float ks, vs;
+};
 
 struct AttnParams {
+  CUtensorMap tm_k, tm_v;   // [page][head][token][channel] bytes, boxes of 16 tokens
   Cache c;
   Batch bt;
   __nv_bfloat16* out;
@@ -22,114 +82,628 @@ struct AttnParams {
   const int32_t* sel;
   const int32_t* n_sel;
   int max_sel;
+  int rts;            // row tiles of a (sequence, head), at most
+  int32_t* arrived;   // [B][H][rts], zero between calls
+  float* parts;       // [2 * CTAs][rows][D]
+  float* part_stats;  // [2 * CTAs][rows][2]: m, l (l = -1: refused)
   int32_t* status;
 };
 
-// The sequence of packed row `row` (-1: none holds it).
-__device__ int sequence_of(const Batch& bt, int row) {
-  if (bt.offsets == nullptr) return row < bt.B ? row : -1;
-  int lo = 0, hi = bt.B;   // the last b with offsets[b] <= row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (__ldg(bt.offsets + mid) <= row) lo = mid;
-    else hi = mid;
+// A row tile of a sequence: its rows' positions and the slices they see.
+struct Tile {
+  int lo, hi;        // first and one past the last visible token of any row
+  int pmin, pmax;    // positions of its first and last row
+  int slices;
+};
+
+__device__ __forceinline__ Tile tile_of(const AttnParams& p, const Seq& s, int rt, int rows, int sel_pages) {
+  Tile t;
+  const int R = s.n * p.G;
+  const int r0 = rt * rows, r1 = min(R, r0 + rows) - 1;
+  t.pmin = s.len - s.n + r0 / p.G;
+  t.pmax = s.len - s.n + r1 / p.G;
+  t.lo = p.window > 0 ? max(0, t.pmin + 1 - p.window) & ~(kSlice - 1) : 0;
+  t.hi = t.pmax + 1;
+  if (sel_pages >= 0) {
+    t.lo = 0;
+    t.slices = sel_pages * (p.c.P / kSlice);
+  } else {
+    t.slices = t.hi > t.lo ? (t.hi - t.lo + kSlice - 1) / kSlice : 0;
   }
-  return lo;
+  t.slices = max(1, t.slices);   // one empty slice: its rows are written too
+  return t;
 }
 
-// One CTA per (row, query head): its warps share out the keys, each with its
-// own running maximum and sum, joined at the end.
-__global__ void __launch_bounds__(32 * kWarps) attn_simple_kernel(const AttnParams p) {
-  __shared__ float part[kWarps][kMaxD + 2];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int row = blockIdx.x, i = blockIdx.y, h = i / p.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int P = p.c.P, D = p.c.D;
-  const int b = sequence_of(p.bt, row);
-  if (b < 0) return;
-  const Seq s = sequence(p.bt, P, b);
-  if (!s.ok) {
-    if (threadIdx.x == 0) report(p.status, W4_ERR_INDEX);
-    return;
+// Pages chosen for a (sequence, head); a count that is none is 0 (refused later).
+__device__ __forceinline__ int chosen(const AttnParams& p, long long bh, bool* bad) {
+  const int n = __ldg(p.n_sel + bh);
+  if (n < 0 || n > p.max_sel) {
+    *bad = true;
+    return 0;
   }
-  if (row < s.row0 || row >= s.row0 + s.n) return;
-  const int pos = s.len - s.n + row - s.row0;
-  const __nv_bfloat16* q = p.q + row * p.q_stride + (long long)i * D;
-  const int per = D / 32;
-  float qv[kMaxD / 32], acc[kMaxD / 32];
-  for (int d = 0; d < per; ++d) {
-    qv[d] = __bfloat162float(q[lane + 32 * d]);
-    acc[d] = 0.0f;
+  return n;
+}
+
+// Slices of an entry: a sequence (all heads), or with chosen pages a
+// (sequence, head).
+__device__ __forceinline__ long long entry_slices(const AttnParams& p, int e, int rows) {
+  const int b = p.sel == nullptr ? e : e / p.c.H;
+  const Seq s = sequence(p.bt, p.c.P, b);
+  if (!s.ok || s.n == 0) return 0;
+  const int rts = (s.n * p.G + rows - 1) / rows;
+  long long sum = 0;
+  if (p.sel == nullptr) {
+    for (int rt = 0; rt < rts; ++rt) sum += tile_of(p, s, rt, rows, -1).slices;
+    return sum * p.c.H;
   }
-  const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
-  const long long bh = (long long)b * p.c.H + h;
-  const int32_t* sel = p.sel == nullptr ? nullptr : p.sel + bh * p.max_sel;
-  const int from = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
-  const int np = (s.len + P - 1) / P;
-  int entries = np;
   bool bad = false;
-  if (sel != nullptr) {
-    entries = __ldg(p.n_sel + bh);
-    if (entries < 0 || entries > p.max_sel) bad = true, entries = 0;
+  const int n = chosen(p, e, &bad);
+  return (long long)tile_of(p, s, 0, rows, n).slices * rts;
+}
+
+__device__ __forceinline__ long long shfl_up64(long long v, int o) {
+  return __shfl_up_sync(0xffffffffu, v, o);
+}
+
+// This CTA's run [g0, g1) of the `total` slices, the entry that holds g0 and
+// the offset in it; *ctas: how many CTAs have one.  false: none.
+struct Run {
+  long long total, g0, g1, off;
+  int ctas, entry;
+};
+
+__device__ bool find_run(const AttnParams& p, int rows, long long* sm, Run* r) {
+  const int E = p.sel == nullptr ? p.bt.B : p.bt.B * p.c.H;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // sums of 32 entries a warp; the first chunk is kept for the search
+  long long first = 0, mine = 0;
+  const bool small = E <= 32;   // every warp by itself
+  if (small) {
+    first = lane < E ? entry_slices(p, lane, rows) : 0;
+    mine = first;
+  } else {
+    for (int e = tid; e < E; e += kThreads) mine += entry_slices(p, e, rows);
   }
-  float m = -INFINITY, l = 0.0f;
-  for (int e = sel == nullptr ? from / P : 0; e < entries; ++e) {
-    const int lp = sel == nullptr ? e : __ldg(sel + e);
-    if (lp < 0 || lp >= np) {
-      bad = true;
-      break;
-    }
-    if (lp * P > pos) break;
-    const int page = __ldg(table + lp);
-    if (page < 0 || page >= p.c.num_pages) {
-      bad = true;
-      break;
-    }
-    const float ks = p.c.ks[p.c.pair(page, h)], vs = p.c.vs[p.c.pair(page, h)];
-    const uint8_t* kc = p.c.kc + p.c.block(page, h);
-    const uint8_t* vc = p.c.vc + p.c.block(page, h);
-    for (int t = warp; t < P; t += kWarps) {
-      const int kp = lp * P + t;
-      if (kp > pos || kp < from) continue;
-      float dot = 0.0f;
-      for (int d = 0; d < per; ++d)
-        dot += qv[d] * (float)((int)kc[(long long)t * D + lane + 32 * d] - 128);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      const float x = dot * ks * p.scale;
-      const float mn = fmaxf(m, x);
-      const float keep = mn == m ? 1.0f : expf(m - mn), w = expf(x - mn);
-      m = mn;
-      l = l * keep + w;
-      for (int d = 0; d < per; ++d)
-        acc[d] = acc[d] * keep + w * vs * (float)((int)vc[(long long)t * D + lane + 32 * d] - 128);
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (!small) {
+    if (lane == 0) sm[warp] = mine;
+    __syncthreads();
+    mine = 0;
+    for (int w = 0; w < kWarps; ++w) mine += sm[w];
+    __syncthreads();
+  }
+  r->total = mine;
+  r->ctas = (int)min((long long)gridDim.x, (mine + kMinSlices - 1) / kMinSlices);
+  if ((int)blockIdx.x >= r->ctas) return false;
+  r->g0 = mine * blockIdx.x / r->ctas;
+  r->g1 = mine * (blockIdx.x + 1) / r->ctas;
+  if (small) {
+    long long inc = first;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = shfl_up64(inc, o);
+      if (lane >= o) inc += t;
+    }
+    const bool here = first > 0 && r->g0 >= inc - first && r->g0 < inc;
+    const int at = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    r->entry = at;
+    r->off = r->g0 - __shfl_sync(0xffffffffu, inc - first, at);
+    return true;
+  }
+  long long base = 0;
+  for (int e0 = 0; e0 < E; e0 += kThreads) {
+    const long long w = e0 + tid < E ? entry_slices(p, e0 + tid, rows) : 0;
+    long long inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = shfl_up64(inc, o);
+      if (lane >= o) inc += t;
+    }
+    if (lane == 31) sm[warp] = inc;
+    __syncthreads();
+    long long all = 0;
+    for (int v = 0; v < kWarps; ++v) {
+      if (v < warp) inc += sm[v];
+      all += sm[v];
+    }
+    const bool here = w > 0 && r->g0 >= base + inc - w && r->g0 < base + inc;
+    if (here) {
+      sm[kWarps] = e0 + tid;
+      sm[kWarps + 1] = r->g0 - (base + inc - w);
+    }
+    const int found = __syncthreads_or(here);
+    if (found) {
+      r->entry = (int)sm[kWarps];
+      r->off = sm[kWarps + 1];
+      __syncthreads();
+      return true;
+    }
+    base += all;
+    __syncthreads();
+  }
+  return false;
+}
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int tok, int h,
+                                       int page, uint32_t bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::"
+      "cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(tok), "r"(h), "r"(page), "r"(bar), "l"(pol)
+      : "memory");
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
+    attn_token_kernel(const __grid_constant__ AttnParams p) {
+  using S = Shape<D, NQ>;
+  constexpr int kRows = S::kRows, kStages = S::kStages, kPitch = S::kPitch;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+  uint8_t* sm = smem_raw + pad;
+  const uint32_t sbase = smem_addr(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i = lane >> 2, j = lane & 3;
+  Meta* meta = reinterpret_cast<Meta*>(sm + S::kMeta) + warp * kRing;
+  float2* stats = reinterpret_cast<float2*>(sm + S::kStats);
+  float* join = reinterpret_cast<float*>(sm);
+  const uint32_t bar0 = sbase + S::kBars + warp * kStages * 8;
+  const uint32_t stage0 = sbase + warp * kStages * S::kStageBytes;
+  volatile int* refused = reinterpret_cast<volatile int*>(sm + S::kMisc);   // [2]: even, odd units
+  volatile int* flag = refused + 2;
+  long long* scan = reinterpret_cast<long long*>(sm + S::kMisc + 16);
+
+  pdl_launch_dependents();
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    mbar_init_fence();
+  }
+  if (tid < 2) refused[tid] = 0;
+  pdl_wait();
+  // sequences whose bounds are broken belong to no run: the first CTA says so
+  if (blockIdx.x == 0)
+    for (int b = tid; b < p.bt.B; b += kThreads)
+      if (!sequence(p.bt, p.c.P, b).ok) report(p.status, W4_ERR_INDEX);
+  Run run;
+  const bool any = find_run(p, kRows, scan, &run);
+  __syncthreads();
+  if (!any) return;
+
+  const uint64_t pol = policy_evict_first();
+  int put = 0, got = 0;              // stages filled and read, modulo kStages
+  uint32_t got_phase = 0;
+  bool dead = false;                 // a wait ran out
+  long long g = run.g0, off = run.off;
+  int entry = run.entry;
+  int odd = 0;                       // units walked, modulo 2
+  while (g < run.g1) {
+    // ---------------------------------------------------------- the unit
+    const int b = p.sel == nullptr ? entry : entry / p.c.H;
+    const Seq s = sequence(p.bt, p.c.P, b);
+    const int rts = (s.n * p.G + kRows - 1) / kRows;
+    int h, rt = 0, sl0, n_pages = -1;
+    bool bad = false;
+    Tile t;
+    long long left;   // slices of the entry from this unit's slice sl0 on
+    if (p.sel != nullptr) {
+      h = entry - b * p.c.H;
+      n_pages = chosen(p, entry, &bad);
+      t = tile_of(p, s, 0, kRows, n_pages);
+      rt = (int)(off / t.slices);
+      sl0 = (int)(off - (long long)rt * t.slices);
+      t = tile_of(p, s, rt, kRows, n_pages);
+      left = (long long)t.slices * rts - off;
+    } else {
+      long long per = 0;
+      for (int k = 0; k < rts; ++k) per += tile_of(p, s, k, kRows, -1).slices;
+      h = (int)(off / per);
+      long long rem = off - per * h;
+      t = tile_of(p, s, 0, kRows, -1);
+      while (rem >= t.slices) {
+        rem -= t.slices;
+        t = tile_of(p, s, ++rt, kRows, -1);
+      }
+      sl0 = (int)rem;
+      left = per * p.c.H - off;
+    }
+    const int sl1 = (int)min((long long)t.slices, sl0 + (run.g1 - g));
+    const long long bh = (long long)b * p.c.H + h;
+    const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
+    const int R = s.n * p.G;
+
+    // --------------------------------------------------- query fragments
+    uint32_t q[NQ][D / 16][2];
+    float f[NQ][2];   // of this lane's two columns: scale log2(e) / the row's power of two
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int r = rt * kRows + 8 * n + i;
+      const __nv_bfloat16* row =
+          r < R ? p.q + (long long)(s.row0 + r / p.G) * p.q_stride + (long long)(h * p.G + r % p.G) * D
+                : nullptr;
+      const float down = load_query<D>(row, j, q[n]);
+      f[n][0] = __shfl_sync(0xffffffffu, down, 8 * j) * (p.scale * kLog2e);
+      f[n][1] = __shfl_sync(0xffffffffu, down, 8 * j + 4) * (p.scale * kLog2e);
+    }
+    float m[NQ][2], l[NQ][2], o[NQ][D / 16][4];
+    float vref = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][c][e] = 0.0f;
+    }
+
+    // ------------------------------------------------- this warp's slices
+    const int count = (sl1 - sl0 - warp + kWarps - 1) / kWarps;   // may be <= 0
+    auto fill = [&](int k0) {   // descriptions k0 .. k0 + 31
+      __syncwarp();
+      const int k = k0 + lane;
+      if (k < count) {
+        const int sl = sl0 + warp + kWarps * k;
+        Meta d = {-1, 0, 0.0f, 0.0f};
+        int lp = 0;
+        bool read = false;
+        if (n_pages >= 0) {
+          const int per = p.c.P / kSlice, e = sl / per;
+          if (e < n_pages) {
+            lp = __ldg(p.sel + bh * p.max_sel + e);
+            if (lp < 0 || (long long)lp * p.c.P >= s.len) {
+              bad = true;
+            } else {
+              d.tok = lp * p.c.P + (sl - e * per) * kSlice;
+              read = d.tok < t.hi && !(p.window > 0 && d.tok + kSlice + p.window <= t.pmin + 1);
+            }
+          }
+        } else {
+          d.tok = t.lo + sl * kSlice;
+          lp = d.tok / p.c.P;
+          read = d.tok < t.hi;
+        }
+        if (read) {
+          const int page = __ldg(table + lp);
+          if (page < 0 || page >= p.c.num_pages) {
+            bad = true;
+          } else {
+            d.page = page;
+            d.ks = __ldg(p.c.ks + p.c.pair(page, h));
+            d.vs = __ldg(p.c.vs + p.c.pair(page, h));
+          }
+        }
+        meta[k & (kRing - 1)] = d;
+      }
+      __syncwarp();
+    };
+    auto issue = [&](int k) {
+      if (k >= count || dead) return;
+      if ((k & 31) == 0) fill(k);
+      if (lane == 0) {
+        const Meta d = meta[k & (kRing - 1)];
+        const uint32_t bar = bar0 + 8 * put, st = stage0 + put * S::kStageBytes;
+        if (d.page < 0) {
+          mbar_arrive(bar);
+        } else {
+          mbar_arrive_expect_tx(bar, S::kStageBytes);
+          const int row = d.tok & (p.c.P - 1);
+#pragma unroll
+          for (int x = 0; x < D; x += 128) {
+            tma_4d(st + x * kSlice, &p.tm_k, x, row, h, d.page, bar, pol);
+            tma_4d(st + kSlice * D + x * kSlice, &p.tm_v, x, row, h, d.page, bar, pol);
+          }
+        }
+      }
+      if (++put == kStages) put = 0;
+    };
+#pragma unroll 1
+    for (int k = 0; k < kStages; ++k) issue(k);
+#pragma unroll 1
+    for (int k = 0; k < count; ++k) {
+      if (!dead && !mbar_wait_bounded(bar0 + 8 * got, got_phase, kWait)) {
+        dead = true;
+        if (lane == 0) report(p.status, W4_ERR_TIMEOUT);
+      }
+      if (dead) break;
+      const Meta d = meta[k & (kRing - 1)];
+      if (d.page >= 0) {
+        const uint32_t st = stage0 + got * S::kStageBytes;
+        float x[NQ][4];
+        key_scores<D, NQ>(st, i, j, q, x);
+        bool over = fabsf(d.vs) > vref;   // a larger step, or a score past m
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[n][e] *= d.ks * f[n][e & 1];
+        if (d.tok + kSlice - 1 > t.pmin || (p.window > 0 && d.tok <= t.pmax - p.window)) {
+          // some row does not see some token
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = min(R - 1, rt * kRows + 8 * n + 2 * j + (e & 1));
+              const int pos = s.len - s.n + r / p.G, tok = d.tok + i + 8 * (e >> 1);
+              if (tok > pos || (p.window > 0 && tok <= pos - p.window)) x[n][e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) over |= x[n][e] > m[n][e & 1] + kLag;
+        if (__any_sync(0xffffffffu, over)) {
+          const float vnew = fmaxf(vref, fabsf(d.vs));
+          const float keep_v = vnew > 0.0f ? __fdividef(vref, vnew) : 0.0f;
+          vref = vnew;
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float mx = fmaxf(x[n][c], x[n][c + 2]);
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              mx = fmaxf(mx, m[n][c]);
+              const float keep = mx == -INFINITY ? 1.0f : exp2_fast(m[n][c] - mx);
+              m[n][c] = mx;
+              l[n][c] *= keep;
+#pragma unroll
+              for (int a = 0; a < D / 16; ++a) {
+                o[n][a][c] *= keep * keep_v;
+                o[n][a][c + 2] *= keep * keep_v;
+              }
+            }
+        }
+        const float r = vref > 0.0f ? __fdividef(d.vs, vref) * kWeightScale : 0.0f;
+        bool small = false;   // a weight below fp16's normal range
+        uint32_t w[NQ][2];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float mm = m[n][c & 1];
+            const float e = exp2_fast(x[n][c] - (mm == -INFINITY ? 0.0f : mm));
+            l[n][c & 1] += e;
+            x[n][c] = e * r;
+            small |= fabsf(x[n][c]) < kHalfNormal && x[n][c] != 0.0f;
+          }
+          w[n][0] = transpose8(pack_half2(x[n][0], x[n][1]));
+          w[n][1] = transpose8(pack_half2(x[n][2], x[n][3]));
+        }
+        if (!__any_sync(0xffffffffu, small)) {
+          value_sums<false, D, NQ>(st + kSlice * D, i, j, w, o);
+        } else {
+          // weights of every size keep fp16's bits: those of one 29-bit
+          // range of exponents at a time, brought into fp16's
+          float up = 1.0f, back = 1.0f;
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (fabsf(x[n][c]) < kLeast) x[n][c] = 0.0f;
+          do {
+            small = false;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+              float y[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float z = x[n][c] * up;
+                y[c] = z;
+                if (fabsf(z) < kHalfNormal) {
+                  y[c] = 0.0f;
+                  small |= x[n][c] != 0.0f;
+                } else {
+                  x[n][c] = 0.0f;
+                }
+              }
+              w[n][0] = transpose8(pack_half2(y[0], y[1]));
+              w[n][1] = transpose8(pack_half2(y[2], y[3]));
+            }
+            value_sums<true, D, NQ>(st + kSlice * D, i, j, w, o, back);
+            up *= kLevel;
+            back *= 1.0f / kLevel;
+          } while (__any_sync(0xffffffffu, small));
+        }
+      }
+      __syncwarp();
+      if (++got == kStages) {
+        got = 0;
+        got_phase ^= 1u;
+      }
+      issue(k + kStages);
+    }
+    if (bad || dead) refused[odd] = 1;
+
+    // ------------------------------------------ join the warps (and CTAs)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], 4);
+        l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], 8);
+        l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], 16);
+        if (i == 0) stats[warp * kRows + 8 * n + 2 * j + c] = make_float2(m[n][c], l[n][c]);
+      }
+    __syncthreads();   // every stage has been read
+    const float back = vref * (1.0f / kWeightScale);
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        float* to = join + (warp * kRows + 8 * n + 2 * j) * kPitch + value_channel<D>(i, c);
+        *reinterpret_cast<float2*>(to) = make_float2(o[n][c][0] * back, o[n][c][2] * back);
+        *reinterpret_cast<float2*>(to + kPitch) = make_float2(o[n][c][1] * back, o[n][c][3] * back);
+      }
+    __syncthreads();
+    const bool no = refused[odd] != 0;
+    if (tid == 0) refused[odd ^ 1] = 0;   // read by all before the last barrier, next set after it
+    const bool whole = sl0 == 0 && sl1 == t.slices;
+    if (no && tid == 0 && !dead) report(p.status, W4_ERR_INDEX);
+    const int slot = 2 * blockIdx.x + (sl0 == 0 ? 1 : 0);
+    for (int x = tid; x < kRows * (D / 4); x += kThreads) {
+      const int r = x / (D / 4), c4 = x % (D / 4);
+      const int row = rt * kRows + r;
+      float M = -INFINITY, L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stats[w * kRows + r].x);
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 st = stats[w * kRows + r];
+        const float k = st.x == -INFINITY ? (st.y == 0.0f ? 0.0f : 1.0f) : exp2_fast(st.x - M);
+        const float4 v = *reinterpret_cast<const float4*>(join + (w * kRows + r) * kPitch + 4 * c4);
+        L += k * st.y;
+        a.x += k * v.x;
+        a.y += k * v.y;
+        a.z += k * v.z;
+        a.w += k * v.w;
+      }
+      if (!whole) {
+        *reinterpret_cast<float4*>(p.parts + ((long long)slot * kRows + r) * D + 4 * c4) = a;
+        if (c4 == 0)
+          *reinterpret_cast<float2*>(p.part_stats + ((long long)slot * kRows + r) * 2) =
+              make_float2(M, no ? -1.0f : L);
+      } else if (row < R && !no) {
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const __nv_bfloat162 u = __floats2bfloat162_rn(a.x * inv, a.y * inv);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+        const long long at = (long long)(s.row0 + row / p.G) * p.Hq + h * p.G + row % p.G;
+        *reinterpret_cast<uint2*>(p.out + at * D + 4 * c4) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+        if (c4 == 0 && p.lse != nullptr)
+          p.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+      }
+    }
+    if (!whole) {
+      // CTAs that hold a part of this unit: those of its first to its last slice
+      const long long u0 = g - sl0, u1 = u0 + t.slices - 1;
+      const int c0 = (int)(((u0 + 1) * run.ctas - 1) / run.total);
+      const int c1 = (int)(((u1 + 1) * run.ctas - 1) / run.total);
+      int32_t* arrived = p.arrived + bh * p.rts + rt;
+      __syncthreads();
+      if (tid == 0) {
+        const int was = atomic_add_acq_rel_gpu(arrived, 1);
+        *flag = was == c1 - c0;
+        if (was == c1 - c0) *arrived = 0;
+      }
+      __syncthreads();
+      if (*flag) {
+        for (int x = tid; x < kRows * (D / 4); x += kThreads) {
+          const int r = x / (D / 4), c4 = x % (D / 4);
+          const int row = rt * kRows + r;
+          if (row >= R) continue;
+          float M = -INFINITY, L = 0.0f;
+          bool none = false;
+          // the first CTA's part began the unit, the others' run began inside it
+          for (int c = c0; c <= c1; ++c) {
+            const int sl = 2 * c + (run.total * c / run.ctas <= u0 ? 1 : 0);
+            const float2 st = __ldcg(reinterpret_cast<const float2*>(p.part_stats) +
+                                     (long long)sl * kRows + r);
+            M = fmaxf(M, st.x);
+            none |= st.y < 0.0f;
+          }
+          if (none) continue;
+          float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+          for (int c = c0; c <= c1; ++c) {
+            const int sl = 2 * c + (run.total * c / run.ctas <= u0 ? 1 : 0);
+            const float2 st = __ldcg(reinterpret_cast<const float2*>(p.part_stats) +
+                                     (long long)sl * kRows + r);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                p.parts + ((long long)sl * kRows + r) * D + 4 * c4));
+            const float k = st.x == -INFINITY ? (st.y == 0.0f ? 0.0f : 1.0f) : exp2_fast(st.x - M);
+            L += k * st.y;
+            a.x += k * v.x;
+            a.y += k * v.y;
+            a.z += k * v.z;
+            a.w += k * v.w;
+          }
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          const __nv_bfloat162 u = __floats2bfloat162_rn(a.x * inv, a.y * inv);
+          const __nv_bfloat162 v = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+          const long long at = (long long)(s.row0 + row / p.G) * p.Hq + h * p.G + row % p.G;
+          *reinterpret_cast<uint2*>(p.out + at * D + 4 * c4) = make_uint2(
+              *reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+          if (c4 == 0 && p.lse != nullptr)
+            p.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+        }
+      }
+    }
+    fence_proxy_async_smem();   // the joined rows, before copies into the same bytes
+    __syncthreads();
+    odd ^= 1;
+    // --------------------------------------------------------- next unit
+    const long long step = sl1 - sl0;
+    g += step;
+    off += step;
+    if (step == left && g < run.g1) {
+      off = 0;
+      do ++entry;
+      while (entry_slices(p, entry, kRows) == 0);
     }
   }
-  if (bad) {   // the same in every warp
-    if (threadIdx.x == 0) report(p.status, W4_ERR_INDEX);
-    return;
+  if (dead) {   // copies still in flight land before the CTA leaves
+    for (int s = 0; s < kStages; ++s) mbar_wait_bounded(bar0 + 8 * s, got_phase, kWait >> 4);
   }
-  for (int d = 0; d < per; ++d) part[warp][lane + 32 * d] = acc[d];
-  if (lane == 0) {
-    part[warp][kMaxD] = m;
-    part[warp][kMaxD + 1] = l;
+}
+
+// ================================================================= host side
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+struct Plan {
+  int nq, rts, ctas;
+  size_t arrived, parts, stats, bytes;
+};
+
+Plan plan_token(const Cache& c, const Batch& b, int G, int sms) {
+  Plan pl;
+  const long long rows = (long long)b.max_new * G;
+  pl.nq = rows <= 8 ? 1 : 2;
+  pl.rts = (int)((rows + 8 * pl.nq - 1) / (8 * pl.nq));
+  pl.ctas = sms * (c.D == 256 ? 1 : 2);
+  pl.arrived = up256((size_t)b.B * c.H * pl.rts * 4);
+  pl.parts = up256((size_t)2 * pl.ctas * 8 * pl.nq * c.D * 4);
+  pl.stats = up256((size_t)2 * pl.ctas * 8 * pl.nq * 8);
+  pl.bytes = pl.arrived + pl.parts + pl.stats;
+  return pl;
+}
+
+bool tensor_map(CUtensorMap* m, uint8_t* codes, const Cache& c, int rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tc::encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.P, (cuuint64_t)c.H,
+                              (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c.D, (cuuint64_t)c.head_stride,
+                                 (cuuint64_t)c.page_stride};
+  const cuuint32_t box[4] = {(cuuint32_t)std::min(c.D, 128), (cuuint32_t)rows, 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, codes, dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             c.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NQ>
+w4_status launch_token(const AttnParams& p, int ctas, bool pdl, w4_stream_t stream, int dev) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  if (dev < 0 || dev >= 64) return W4_ERR_DEVICE;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(attn_token_kernel<D, NQ>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 Shape<D, NQ>::kSmem);
+      if (e != cudaSuccess) {
+        note_cuda_error(e);
+        (void)cudaGetLastError();
+        return W4_ERR_LAUNCH;
+      }
+      done[dev] = true;
+    }
   }
-  __syncthreads();
-  float mm = -INFINITY, ll = 0.0f;
-  for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, part[w][kMaxD]);
-  float f[kWarps];
-  for (int w = 0; w < kWarps; ++w) {
-    f[w] = mm == -INFINITY ? 0.0f : expf(part[w][kMaxD] - mm);
-    ll += f[w] * part[w][kMaxD + 1];
-  }
-  for (int d = threadIdx.x; d < D; d += 32 * kWarps) {
-    float a = 0.0f;
-    for (int w = 0; w < kWarps; ++w) a += f[w] * part[w][d];
-    p.out[((long long)row * p.Hq + i) * D + d] = __float2bfloat16_rn(ll == 0.0f ? 0.0f : a / ll);
-  }
-  if (threadIdx.x == 0 && p.lse != nullptr)
-    p.lse[(long long)row * p.Hq + i] = ll == 0.0f ? -INFINITY : mm + logf(ll);
+  return launch(attn_token_kernel<D, NQ>, dim3((unsigned)ctas), kThreads, Shape<D, NQ>::kSmem, pdl,
+                stream, p);
 }
 
 struct WeighParams {
@@ -145,7 +719,7 @@ struct WeighParams {
 };
 
 // One CTA per (page, head, sequence), one warp per token in turn.
-__global__ void __launch_bounds__(32 * kWarps) weigh_simple_kernel(const WeighParams p) {
+__global__ void __launch_bounds__(128) weigh_simple_kernel(const WeighParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const int lp = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
@@ -164,7 +738,7 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_simple_kernel(const WeighPa
   }
   const float ks = p.c.ks[p.c.pair(page, h)];
   const uint8_t* kc = p.c.kc + p.c.block(page, h);
-  for (int t = warp; t < P && lp * P + t < s.len; t += kWarps) {
+  for (int t = warp; t < P && lp * P + t < s.len; t += 4) {
     const int kp = lp * P + t;
     float sum = 0.0f;
     for (int r = 0; r < s.n; ++r) {
@@ -194,8 +768,14 @@ using namespace w4;
 
 extern "C" size_t w4_kv8_attn_workspace_bytes(const w4_kv8_cache* cache, const w4_kv8_batch* batch,
                                               int q_heads, int max_sel) {
-  (void)cache, (void)batch, (void)q_heads, (void)max_sel;
-  return 0;
+  kv8::Cache c;
+  kv8::Batch b;
+  if (kv8::view(cache, batch, &c, &b) != W4_OK || q_heads < 1 || q_heads % c.H != 0 ||
+      q_heads / c.H > W4_KV8_MAX_GROUP || max_sel < 0)
+    return 0;
+  DeviceInfo di;
+  planning_device(&di);
+  return kv8::plan_token(c, b, q_heads / c.H, di.sms).bytes;
 }
 
 extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_row_stride,
@@ -215,8 +795,13 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
   if (kv8::misaligned(out, 16) || kv8::misaligned(lse, 4) || kv8::misaligned(sel, 4) ||
       kv8::misaligned(n_sel, 4) || kv8::misaligned(workspace, 16))
     return W4_ERR_ALIGN;
-  if (workspace_bytes < w4_kv8_attn_workspace_bytes(cache, batch, q_heads, max_sel))
-    return W4_ERR_WORKSPACE;
+  int dev = -1;
+  DeviceInfo di;
+  const bool have = current_device(&dev, &di);
+  if (!have) planning_device(&di);
+  const kv8::Plan pl = kv8::plan_token(p.c, p.bt, q_heads / p.c.H, di.sms);
+  if (workspace == nullptr || workspace_bytes < pl.bytes) return W4_ERR_WORKSPACE;
+  if (!have) return W4_ERR_DEVICE;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -229,8 +814,25 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
   p.n_sel = n_sel;
   p.max_sel = max_sel;
   p.status = status_dev;
-  return kv8::launch(kv8::attn_simple_kernel, dim3((unsigned)p.bt.rows, (unsigned)q_heads),
-                     32 * kv8::kWarps, 0, (flags & W4_FLAG_PDL) != 0, stream, p);
+  p.rts = pl.rts;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.arrived = reinterpret_cast<int32_t*>(ws);
+  p.parts = reinterpret_cast<float*>(ws + pl.arrived);
+  p.part_stats = reinterpret_cast<float*>(ws + pl.arrived + pl.parts);
+  if (!kv8::tensor_map(&p.tm_k, p.c.kc, p.c, kv8::kSlice) ||
+      !kv8::tensor_map(&p.tm_v, p.c.vc, p.c, kv8::kSlice)) {
+    note_cuda_error(cudaErrorInvalidValue);
+    return W4_ERR_LAUNCH;
+  }
+  const bool pdl = (flags & W4_FLAG_PDL) != 0;
+  switch (p.c.D * 4 + pl.nq) {
+    case 64 * 4 + 1: return kv8::launch_token<64, 1>(p, pl.ctas, pdl, stream, dev);
+    case 64 * 4 + 2: return kv8::launch_token<64, 2>(p, pl.ctas, pdl, stream, dev);
+    case 128 * 4 + 1: return kv8::launch_token<128, 1>(p, pl.ctas, pdl, stream, dev);
+    case 128 * 4 + 2: return kv8::launch_token<128, 2>(p, pl.ctas, pdl, stream, dev);
+    case 256 * 4 + 1: return kv8::launch_token<256, 1>(p, pl.ctas, pdl, stream, dev);
+    default: return kv8::launch_token<256, 2>(p, pl.ctas, pdl, stream, dev);
+  }
 }
 
 extern "C" w4_status w4_kv8_weigh(const void* q, size_t q_row_stride, int q_heads,
@@ -255,6 +857,6 @@ extern "C" w4_status w4_kv8_weigh(const void* q, size_t q_row_stride, int q_head
   const int pages = (p.bt.max_len + p.c.P - 1) / p.c.P;
   if (pages == 0) return W4_OK;
   return kv8::launch(kv8::weigh_simple_kernel,
-                     dim3((unsigned)pages, (unsigned)p.c.H, (unsigned)p.bt.B), 32 * kv8::kWarps, 0,
+                     dim3((unsigned)pages, (unsigned)p.c.H, (unsigned)p.bt.B), 128, 0,
                      (flags & W4_FLAG_PDL) != 0, stream, p);
 }

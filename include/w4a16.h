@@ -751,8 +751,7 @@ w4_status w4_kv8_append(const w4_kv8_cache *cache, const w4_kv8_batch *batch, co
  *   out[r][i] = sum_t p_t value[t],  p_t = exp(scale q.key[t]) / sum of them,
  *   lse[r][i] = log of that sum
  * over the keys t that row r sees; a row that sees none gives 0 and -inf.
- * Products are exact and sums fp32; p is rounded to fp16, scaled so that
- * only weights below 2^-28 of the row's largest lose bits.
+ * Products are exact and sums fp32; p is rounded to 11 significant bits.
  *
  * out         bf16 [rows][q_heads][head_dim], 16-byte aligned.
  * lse         fp32 [rows][q_heads], or NULL.
