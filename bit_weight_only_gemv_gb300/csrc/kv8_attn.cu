@@ -27,8 +27,9 @@
 #include <mutex>
 
 #include "gemv_host.h"
+#include "kv8_attn.h"
 #include "kv8_mma.cuh"
-#include "tc_common.cuh"
+#include "kv8_runs.cuh"
 
 namespace w4 {
 namespace kv8 {
@@ -89,31 +90,6 @@ struct AttnParams {
   int32_t* status;
 };
 
-// A row tile of a sequence: its rows' positions and the slices they see.
-struct Tile {
-  int lo, hi;        // first and one past the last visible token of any row
-  int pmin, pmax;    // positions of its first and last row
-  int slices;
-};
-
-__device__ __forceinline__ Tile tile_of(const AttnParams& p, const Seq& s, int rt, int rows, int sel_pages) {
-  Tile t;
-  const int R = s.n * p.G;
-  const int r0 = rt * rows, r1 = min(R, r0 + rows) - 1;
-  t.pmin = s.len - s.n + r0 / p.G;
-  t.pmax = s.len - s.n + r1 / p.G;
-  t.lo = p.window > 0 ? max(0, t.pmin + 1 - p.window) & ~(kSlice - 1) : 0;
-  t.hi = t.pmax + 1;
-  if (sel_pages >= 0) {
-    t.lo = 0;
-    t.slices = sel_pages * (p.c.P / kSlice);
-  } else {
-    t.slices = t.hi > t.lo ? (t.hi - t.lo + kSlice - 1) / kSlice : 0;
-  }
-  t.slices = max(1, t.slices);   // one empty slice: its rows are written too
-  return t;
-}
-
 // Pages chosen for a (sequence, head); a count that is none is 0 (refused later).
 __device__ __forceinline__ int chosen(const AttnParams& p, long long bh, bool* bad) {
   const int n = __ldg(p.n_sel + bh);
@@ -124,105 +100,27 @@ __device__ __forceinline__ int chosen(const AttnParams& p, long long bh, bool* b
   return n;
 }
 
+// A row tile over the whole sequence (pages < 0) or over `pages` chosen ones.
+__device__ __forceinline__ Tile unit_tile(const AttnParams& p, const Seq& s, int rt, int rows,
+                                          int pages) {
+  Tile t = tile_of(s, p.G, p.window, rt, rows, kSlice);
+  if (pages >= 0) {
+    t.lo = 0;
+    t.slices = max(1, pages * (p.c.P / kSlice));
+  }
+  return t;
+}
+
 // Slices of an entry: a sequence (all heads), or with chosen pages a
 // (sequence, head).
 __device__ __forceinline__ long long entry_slices(const AttnParams& p, int e, int rows) {
   const int b = p.sel == nullptr ? e : e / p.c.H;
   const Seq s = sequence(p.bt, p.c.P, b);
   if (!s.ok || s.n == 0) return 0;
+  if (p.sel == nullptr) return head_slices(s, p.G, p.window, rows, kSlice) * p.c.H;
   const int rts = (s.n * p.G + rows - 1) / rows;
-  long long sum = 0;
-  if (p.sel == nullptr) {
-    for (int rt = 0; rt < rts; ++rt) sum += tile_of(p, s, rt, rows, -1).slices;
-    return sum * p.c.H;
-  }
   bool bad = false;
-  const int n = chosen(p, e, &bad);
-  return (long long)tile_of(p, s, 0, rows, n).slices * rts;
-}
-
-__device__ __forceinline__ long long shfl_up64(long long v, int o) {
-  return __shfl_up_sync(0xffffffffu, v, o);
-}
-
-// This CTA's run [g0, g1) of the `total` slices, the entry that holds g0 and
-// the offset in it; *ctas: how many CTAs have one.  false: none.
-struct Run {
-  long long total, g0, g1, off;
-  int ctas, entry;
-};
-
-__device__ bool find_run(const AttnParams& p, int rows, long long* sm, Run* r) {
-  const int E = p.sel == nullptr ? p.bt.B : p.bt.B * p.c.H;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // sums of 32 entries a warp; the first chunk is kept for the search
-  long long first = 0, mine = 0;
-  const bool small = E <= 32;   // every warp by itself
-  if (small) {
-    first = lane < E ? entry_slices(p, lane, rows) : 0;
-    mine = first;
-  } else {
-    for (int e = tid; e < E; e += kThreads) mine += entry_slices(p, e, rows);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (!small) {
-    if (lane == 0) sm[warp] = mine;
-    __syncthreads();
-    mine = 0;
-    for (int w = 0; w < kWarps; ++w) mine += sm[w];
-    __syncthreads();
-  }
-  r->total = mine;
-  r->ctas = (int)min((long long)gridDim.x, (mine + kMinSlices - 1) / kMinSlices);
-  if ((int)blockIdx.x >= r->ctas) return false;
-  r->g0 = mine * blockIdx.x / r->ctas;
-  r->g1 = mine * (blockIdx.x + 1) / r->ctas;
-  if (small) {
-    long long inc = first;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = shfl_up64(inc, o);
-      if (lane >= o) inc += t;
-    }
-    const bool here = first > 0 && r->g0 >= inc - first && r->g0 < inc;
-    const int at = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-    r->entry = at;
-    r->off = r->g0 - __shfl_sync(0xffffffffu, inc - first, at);
-    return true;
-  }
-  long long base = 0;
-  for (int e0 = 0; e0 < E; e0 += kThreads) {
-    const long long w = e0 + tid < E ? entry_slices(p, e0 + tid, rows) : 0;
-    long long inc = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = shfl_up64(inc, o);
-      if (lane >= o) inc += t;
-    }
-    if (lane == 31) sm[warp] = inc;
-    __syncthreads();
-    long long all = 0;
-    for (int v = 0; v < kWarps; ++v) {
-      if (v < warp) inc += sm[v];
-      all += sm[v];
-    }
-    const bool here = w > 0 && r->g0 >= base + inc - w && r->g0 < base + inc;
-    if (here) {
-      sm[kWarps] = e0 + tid;
-      sm[kWarps + 1] = r->g0 - (base + inc - w);
-    }
-    const int found = __syncthreads_or(here);
-    if (found) {
-      r->entry = (int)sm[kWarps];
-      r->off = sm[kWarps + 1];
-      __syncthreads();
-      return true;
-    }
-    base += all;
-    __syncthreads();
-  }
-  return false;
+  return (long long)unit_tile(p, s, 0, rows, chosen(p, e, &bad)).slices * rts;
 }
 
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int tok, int h,
@@ -265,7 +163,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
     for (int b = tid; b < p.bt.B; b += kThreads)
       if (!sequence(p.bt, p.c.P, b).ok) report(p.status, W4_ERR_INDEX);
   Run run;
-  const bool any = find_run(p, kRows, scan, &run);
+  const bool any = find_run<kWarps>(
+      p.sel == nullptr ? p.bt.B : p.bt.B * p.c.H, kMinSlices,
+      [&](int e) { return entry_slices(p, e, kRows); }, scan, &run);
   __syncthreads();
   if (!any) return;
 
@@ -288,20 +188,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
     if (p.sel != nullptr) {
       h = entry - b * p.c.H;
       n_pages = chosen(p, entry, &bad);
-      t = tile_of(p, s, 0, kRows, n_pages);
+      t = unit_tile(p, s, 0, kRows, n_pages);
       rt = (int)(off / t.slices);
       sl0 = (int)(off - (long long)rt * t.slices);
-      t = tile_of(p, s, rt, kRows, n_pages);
+      t = unit_tile(p, s, rt, kRows, n_pages);
       left = (long long)t.slices * rts - off;
     } else {
-      long long per = 0;
-      for (int k = 0; k < rts; ++k) per += tile_of(p, s, k, kRows, -1).slices;
+      const long long per = head_slices(s, p.G, p.window, kRows, kSlice);
       h = (int)(off / per);
       long long rem = off - per * h;
-      t = tile_of(p, s, 0, kRows, -1);
+      t = unit_tile(p, s, 0, kRows, -1);
       while (rem >= t.slices) {
         rem -= t.slices;
-        t = tile_of(p, s, ++rt, kRows, -1);
+        t = unit_tile(p, s, ++rt, kRows, -1);
       }
       sl0 = (int)rem;
       left = per * p.c.H - off;
@@ -577,8 +476,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
     if (!whole) {
       // CTAs that hold a part of this unit: those of its first to its last slice
       const long long u0 = g - sl0, u1 = u0 + t.slices - 1;
-      const int c0 = (int)(((u0 + 1) * run.ctas - 1) / run.total);
-      const int c1 = (int)(((u1 + 1) * run.ctas - 1) / run.total);
+      const int c0 = run.holder(u0), c1 = run.holder(u1);
       int32_t* arrived = p.arrived + bh * p.rts + rt;
       __syncthreads();
       if (tid == 0) {
@@ -596,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
           bool none = false;
           // the first CTA's part began the unit, the others' run began inside it
           for (int c = c0; c <= c1; ++c) {
-            const int sl = 2 * c + (run.total * c / run.ctas <= u0 ? 1 : 0);
+            const int sl = 2 * c + (run.start(c) <= u0 ? 1 : 0);
             const float2 st = __ldcg(reinterpret_cast<const float2*>(p.part_stats) +
                                      (long long)sl * kRows + r);
             M = fmaxf(M, st.x);
@@ -606,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
           float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
           for (int c = c0; c <= c1; ++c) {
-            const int sl = 2 * c + (run.total * c / run.ctas <= u0 ? 1 : 0);
+            const int sl = 2 * c + (run.start(c) <= u0 ? 1 : 0);
             const float2 st = __ldcg(reinterpret_cast<const float2*>(p.part_stats) +
                                      (long long)sl * kRows + r);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(
@@ -666,21 +564,6 @@ Plan plan_token(const Cache& c, const Batch& b, int G, int sms) {
   pl.stats = up256((size_t)2 * pl.ctas * 8 * pl.nq * 8);
   pl.bytes = pl.arrived + pl.parts + pl.stats;
   return pl;
-}
-
-bool tensor_map(CUtensorMap* m, uint8_t* codes, const Cache& c, int rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tc::encoder();
-  if (enc == nullptr) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.P, (cuuint64_t)c.H,
-                              (cuuint64_t)c.num_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)c.D, (cuuint64_t)c.head_stride,
-                                 (cuuint64_t)c.page_stride};
-  const cuuint32_t box[4] = {(cuuint32_t)std::min(c.D, 128), (cuuint32_t)rows, 1, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, codes, dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE,
-             c.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int NQ>
@@ -761,6 +644,22 @@ __global__ void __launch_bounds__(128) weigh_simple_kernel(const WeighParams p) 
 }
 
 }  // namespace
+
+bool tensor_map(CUtensorMap* m, uint8_t* codes, const Cache& c, int rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tc::encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.P, (cuuint64_t)c.H,
+                              (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c.D, (cuuint64_t)c.head_stride,
+                                 (cuuint64_t)c.page_stride};
+  const cuuint32_t box[4] = {(cuuint32_t)std::min(c.D, 128), (cuuint32_t)rows, 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, codes, dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             c.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace kv8
 }  // namespace w4
 
@@ -775,6 +674,8 @@ extern "C" size_t w4_kv8_attn_workspace_bytes(const w4_kv8_cache* cache, const w
     return 0;
   DeviceInfo di;
   planning_device(&di);
+  if (max_sel == 0 && (long long)b.max_new * (q_heads / c.H) >= kv8::kChunkRows)
+    return kv8::chunk_workspace_bytes(c, b, q_heads / c.H, di.sms);
   return kv8::plan_token(c, b, q_heads / c.H, di.sms).bytes;
 }
 
@@ -799,6 +700,17 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
   DeviceInfo di;
   const bool have = current_device(&dev, &di);
   if (!have) planning_device(&di);
+  const bool pdl = (flags & W4_FLAG_PDL) != 0;
+  if (sel == nullptr && (long long)p.bt.max_new * (q_heads / p.c.H) >= kv8::kChunkRows) {
+    if (workspace == nullptr ||
+        workspace_bytes < kv8::chunk_workspace_bytes(p.c, p.bt, q_heads / p.c.H, di.sms))
+      return W4_ERR_WORKSPACE;
+    if (!have) return W4_ERR_DEVICE;
+    const kv8::ChunkArgs a = {static_cast<__nv_bfloat16*>(out), lse,
+                              static_cast<const __nv_bfloat16*>(q), (long long)q_row_stride,
+                              q_heads, scale, window, status_dev};
+    return kv8::chunk_attn(p.c, p.bt, a, workspace, di.sms, dev, pdl, stream);
+  }
   const kv8::Plan pl = kv8::plan_token(p.c, p.bt, q_heads / p.c.H, di.sms);
   if (workspace == nullptr || workspace_bytes < pl.bytes) return W4_ERR_WORKSPACE;
   if (!have) return W4_ERR_DEVICE;
@@ -824,7 +736,6 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
     note_cuda_error(cudaErrorInvalidValue);
     return W4_ERR_LAUNCH;
   }
-  const bool pdl = (flags & W4_FLAG_PDL) != 0;
   switch (p.c.D * 4 + pl.nq) {
     case 64 * 4 + 1: return kv8::launch_token<64, 1>(p, pl.ctas, pdl, stream, dev);
     case 64 * 4 + 2: return kv8::launch_token<64, 2>(p, pl.ctas, pdl, stream, dev);

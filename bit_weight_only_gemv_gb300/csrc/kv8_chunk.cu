@@ -1,0 +1,872 @@
+// Attention over the 8-bit cache for prompt chunks (many query rows on a key
+// head) on the 5th-generation tensor cores (tcgen05, sm_103a).
+//
+// The rows of a (sequence, key head) are its tokens times the group's query
+// heads, 128 to a tile.  A CTA takes one or two row tiles against a run of
+// key tiles, with a running maximum m and sum l:
+//
+//   S = Q K^T          kind::f16, bf16 operands (a code is exact in bf16)
+//   P = 2^(scale log2(e) ks S - m) vs
+//   O += P V           kind::tf32, P from tensor memory, codes exact
+//
+// P stays in tensor memory in S's own columns, as fp32 bits rounded to tf32:
+// 11 significant bits at every magnitude, so no weight is lost however far
+// below the row's largest it lies, and no conversion or packing is needed.  That
+// costs PV twice the tensor time of a 16-bit P; the softmax warps, not the
+// tensor cores, would then be the limit.  For the same reason m need not be
+// the maximum: it is the largest score of the row's first 32 keys, and moves
+// (with O and l rescaled) only when a score passes it by 2^64.
+//
+// Roles: four softmax warps per row tile (a thread owns a row, so maxima and
+// sums need no exchange), four warps that expand the codes (K to bf16, V to
+// fp32 transposed, both in the 128-byte-swizzled K-major layout), one warp
+// that issues the MMAs, one that issues the tiled copies of pages.  Two row
+// tiles take turns: while one's scores go through the softmax, the tensor
+// cores work for the other.  A unit of one row tile gives its key tiles to
+// the two softmax groups in turn and joins them at the end.
+//
+// Work is cut into equal runs of key tiles over all units, one run a CTA
+// (kv8_runs.cuh); parts of a cut unit meet in the workspace, joined in order
+// by the last CTA to arrive.  Every wait is bounded.
+#include <algorithm>
+#include <mutex>
+
+#include "gemv_host.h"
+#include "kv8_attn.h"
+#include "kv8_runs.cuh"
+
+namespace w4 {
+namespace kv8 {
+namespace {
+
+using tc::kWaitCycles;
+using tc::mma_commit;
+using tc::tc_fence_after;
+using tc::tc_fence_before;
+using tc::wait_bar;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kPass = 64.0f;        // log2 of how far a score may pass m
+constexpr int kRowTile = 128;
+constexpr int kRawStages = 2;
+constexpr int kMetaRing = 8;
+constexpr int kMinTiles = 2;          // key tiles of a CTA's run
+
+template <int D>
+struct Shape {
+  static constexpr int kGroups = D == 256 ? 1 : 2;   // softmax groups (and O accumulators)
+  static constexpr int kKeys = D == 256 ? 64 : 128;  // keys of a tile
+  static constexpr int kRows = kRowTile * kGroups;   // query rows of a unit
+  static constexpr int kSoftWarps = 4 * kGroups;
+  static constexpr int kConvWarp = kSoftWarps;       // four
+  static constexpr int kMmaWarp = kConvWarp + 4;
+  static constexpr int kCopyWarp = kMmaWarp + 1;
+  static constexpr int kWarps = kCopyWarp + 1;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kQTile = kRowTile * D * 2;    // bytes
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + kGroups * kQTile;
+  static constexpr int kV = kK + kKeys * D * 2;
+  static constexpr int kRaw = kV + kKeys * D * 4;
+  static constexpr int kRawBytes = 2 * kKeys * D;    // keys, then values
+  static constexpr int kMeta = kRaw + kRawStages * kRawBytes;   // [kMetaRing][8] (ks, vs)
+  static constexpr int kBars = kMeta + kMetaRing * 8 * 8;
+  static constexpr int kMisc = kBars + 32 * 8;
+  // more than half an SM's: each CTA holds all of its tensor memory
+  static constexpr int kSmem = kMisc + 256 + 1024 > 117248 ? kMisc + 256 + 1024 : 117248;
+  static_assert(kSmem <= 232448 && 2 * kSmem > 232448, "shared memory");
+  // tensor memory columns
+  static constexpr int kSCol = 0, kOCol = 2 * kKeys;
+  static_assert(kOCol + kGroups * D <= 512, "tensor memory");
+};
+
+// barriers
+enum {
+  kRawFull = 0,    // [2]
+  kRawEmpty = 2,   // [2]
+  kQReady = 4, kQFree, kKReady, kKFree, kVReady, kVFree,
+  kSFull = 10,     // [2] by S region
+  kPFull = 12,     // [2]
+  kODone = 14,     // [2] by group
+  kOFree = 16,     // [2]
+  kEpi = 18, kEpiGo,
+  kBarCount
+};
+
+struct ChunkParams {
+  CUtensorMap tm_k, tm_v;
+  Cache c;
+  Batch bt;
+  ChunkArgs a;
+  int G;
+  int rts;            // row tiles (units) of a (sequence, head), at most
+  int32_t* arrived;   // [B][H][rts], zero between calls
+  float* parts;       // [2 * CTAs][rows][D]
+  float* part_stats;  // [2 * CTAs][rows][2]: m, l (l = -1: refused)
+};
+
+// One unit of a run: a row tile (pair) of a (sequence, head), key tiles i0 .. i1 - 1 of it.
+struct Unit {
+  Seq s;
+  Tile t;
+  int b, h, rt, i0, i1, rows, R;   // rows: of this unit; R: of the (sequence, head)
+  long long u0;                    // item of the unit's tile 0
+  __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == t.slices; }
+  __device__ __forceinline__ int tiles() const { return i1 - i0; }
+};
+
+template <int D>
+__device__ __forceinline__ long long entry_tiles(const ChunkParams& p, int b) {
+  using S = Shape<D>;
+  const Seq s = sequence(p.bt, p.c.P, b);
+  if (!s.ok || s.n == 0) return 0;
+  return head_slices(s, p.G, p.a.window, S::kRows, S::kKeys) * p.c.H;
+}
+
+// Walks the units of a run; every role walks alike.
+struct Walk {
+  long long g, off;
+  int entry;
+};
+
+template <int D>
+__device__ __noinline__ bool next_unit(const ChunkParams& p, const Run& run, Walk& w, Unit& u) {
+  using S = Shape<D>;
+  if (w.g >= run.g1) return false;
+  u.b = w.entry;
+  u.s = sequence(p.bt, p.c.P, u.b);
+  u.R = u.s.n * p.G;
+  const long long per = head_slices(u.s, p.G, p.a.window, S::kRows, S::kKeys);
+  u.h = (int)(w.off / per);
+  long long rem = w.off - per * u.h;
+  u.rt = 0;
+  u.t = tile_of(u.s, p.G, p.a.window, 0, S::kRows, S::kKeys);
+  while (rem >= u.t.slices) {
+    rem -= u.t.slices;
+    u.t = tile_of(u.s, p.G, p.a.window, ++u.rt, S::kRows, S::kKeys);
+  }
+  u.rows = min(S::kRows, u.R - u.rt * S::kRows);
+  u.i0 = (int)rem;
+  u.i1 = (int)min((long long)u.t.slices, rem + run.g1 - w.g);
+  u.u0 = w.g - rem;
+  const long long step = u.i1 - u.i0;
+  w.g += step;
+  w.off += step;
+  if (w.off == per * p.c.H && w.g < run.g1) {
+    w.off = 0;
+    do ++w.entry;
+    while (entry_tiles<D>(p, w.entry) == 0);
+  }
+  return true;
+}
+
+// Codes of a word as bf16 pairs u - 128: byte u under 0x43 reads 128 + its
+// low seven bits once bit 7 is cleared; minus 128 where bit 7 was set, else minus 256.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t sel) {
+  const uint32_t t = __byte_perm(w, 0x43434343u, sel);
+  const uint32_t a = t & 0xFF7FFF7Fu;
+  const uint32_t b = (~t & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// K-major operand descriptor, rows of 128 bytes with 128-byte swizzle, 1024
+// bytes between 8-row groups.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void mma_ss_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31, %32};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
+      "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]),
+      "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]),
+      "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Multiply 32 columns from `col` on by this thread's factor.
+__device__ __forceinline__ void tmem_scale32(uint32_t col, float factor) {
+  float v[32];
+  tc::tmem_ld<32>(col, v);
+  tc::tmem_wait_ld<32>(v);
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] *= factor;
+  tmem_st32(col, v);
+}
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int tok, int h,
+                                       int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(tok), "r"(h), "r"(page), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ uint2 pack_bf16x4(const float* v, float f) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0] * f, v[1] * f);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v[2] * f, v[3] * f);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// A waiting position on a barrier: the parity of its next phase.
+struct Phase {
+  uint32_t n = 0;
+  __device__ __forceinline__ uint32_t next() { return n++ & 1u; }        // completions awaited in turn
+  __device__ __forceinline__ uint32_t before() { return (n++ & 1u) ^ 1u; }  // first one passes at once
+};
+
+template <int D>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
+    attn_chunk_kernel(const __grid_constant__ ChunkParams p) {
+  using S = Shape<D>;
+  constexpr int kKeys = S::kKeys, kGroups = S::kGroups;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+  uint8_t* sm = smem_raw + pad;
+  const uint32_t sb = smem_addr(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bars = sb + S::kBars;
+  auto bar = [&](int i) { return bars + 8 * i; };
+  float2* meta = reinterpret_cast<float2*>(sm + S::kMeta);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kMisc + 4);
+  volatile int* epi_flag = reinterpret_cast<volatile int*>(sm + S::kMisc + 8);
+  volatile int* refused = reinterpret_cast<volatile int*>(sm + S::kMisc + 16);   // [8] by unit
+  long long* scan = reinterpret_cast<long long*>(sm + S::kMisc + 64);
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kRawFull + i), 1);
+      mbar_init(bar(kRawEmpty + i), 4);
+      mbar_init(bar(kSFull + i), 1);
+      mbar_init(bar(kPFull + i), 4);
+      mbar_init(bar(kODone + i), 1);
+      mbar_init(bar(kOFree + i), 4);
+    }
+    mbar_init(bar(kQReady), 4);
+    mbar_init(bar(kQFree), 1);
+    mbar_init(bar(kKReady), 4);
+    mbar_init(bar(kKFree), 1);
+    mbar_init(bar(kVReady), 4);
+    mbar_init(bar(kVFree), 1);
+    mbar_init(bar(kEpi), S::kSoftWarps);
+    mbar_init(bar(kEpiGo), 1);
+    *abort_flag = 0;
+    for (int i = 0; i < 8; ++i) refused[i] = 0;
+    mbar_init_fence();
+  }
+  if (warp == S::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  if (blockIdx.x == 0)
+    for (int b = tid; b < p.bt.B; b += S::kThreads)
+      if (!sequence(p.bt, p.c.P, b).ok) report(p.a.status, W4_ERR_INDEX);
+  Run run;
+  const bool any = find_run<S::kWarps>(
+      p.bt.B, kMinTiles, [&](int e) { return entry_tiles<D>(p, e); }, scan, &run);
+  Walk walk = {any ? run.g0 : 0, any ? run.off : 0, any ? run.entry : 0};
+  if (!any) run.g1 = 0;
+  Unit u;
+  bool ok = true;
+  __syncthreads();
+
+  if (warp == S::kCopyWarp) {
+    // ------------------------------------------------------------- pages
+    const int box = min(p.c.P, kKeys);   // tokens of one copy
+    const int boxes = kKeys / box;
+    Phase empty[kRawStages];
+    int st = 0, serial = 0, unit = 0;
+    for (; ok && next_unit<D>(p, run, walk, u); ++unit) {
+      const int32_t* table = p.bt.table + (long long)u.b * p.bt.max_pages;
+      for (int i = u.i0; i < u.i1; ++i, ++serial) {
+        if (!wait_bar(bar(kRawEmpty + st), empty[st].before(), abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int tok = u.t.lo + i * kKeys + lane * box;
+        const bool want = lane < boxes && tok < u.t.hi;
+        int page = -1;
+        if (want) {
+          page = __ldg(table + tok / p.c.P);
+          if (page < 0 || page >= p.c.num_pages) {
+            page = -1;
+            refused[unit & 7] = 1;
+          }
+        }
+        if (lane < boxes) {
+          float2 m = make_float2(0.0f, 0.0f);
+          if (page >= 0) m = make_float2(p.c.ks[p.c.pair(page, u.h)], p.c.vs[p.c.pair(page, u.h)]);
+          for (int e = 0; e < box / 16; ++e) meta[(serial & 7) * 8 + lane * (box / 16) + e] = m;
+        }
+        const int n = __popc(__ballot_sync(0xffffffffu, page >= 0));
+        if (lane == 0) {
+          if (n > 0) mbar_arrive_expect_tx(bar(kRawFull + st), (uint32_t)(n * box * 2 * D));
+          else mbar_arrive(bar(kRawFull + st));
+        }
+        __syncwarp();
+        if (page >= 0) {
+          const uint32_t dst = sb + S::kRaw + st * S::kRawBytes;
+          const int row = tok % p.c.P;
+#pragma unroll
+          for (int x = 0; x < D; x += 128) {
+            const uint32_t o = x * kKeys + lane * box * (D < 128 ? D : 128);
+            tma_4d(dst + o, &p.tm_k, x, row, u.h, page, bar(kRawFull + st));
+            tma_4d(dst + kKeys * D + o, &p.tm_v, x, row, u.h, page, bar(kRawFull + st));
+          }
+        }
+        __syncwarp();
+        st ^= 1;
+      }
+    }
+    // the last copies land before the CTA may leave
+    if (!ok)
+      for (int i = 0; i < kRawStages; ++i)
+        mbar_wait_bounded(bar(kRawFull + i), (empty[i].n + 1) & 1u, kWaitCycles >> 4);
+  } else if (warp == S::kMmaWarp) {
+    // -------------------------------------------------------- MMA issuer
+    constexpr uint32_t kDescS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kKeys >> 3) << 17) |
+                                ((uint32_t)(kRowTile >> 4) << 24);
+    constexpr uint32_t kDescO = (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(D >> 3) << 17) |
+                                ((uint32_t)(kRowTile >> 4) << 24);
+    Phase q_ready, k_ready, v_ready, p_full[2], o_free[2];
+    bool issued = false;
+    uint32_t freed = 0;   // commits on kVFree
+    while (ok && next_unit<D>(p, run, walk, u)) {
+      const bool two = kGroups == 2 && u.rows > kRowTile;   // two row tiles
+      const int jobs = two ? 2 * u.tiles() : u.tiles();
+      if (!wait_bar(bar(kQReady), q_ready.next(), abort_flag)) {
+        ok = false;
+        break;
+      }
+      // S of job j: key tile j (j / 2 of two row tiles), S region j % 2
+      auto scores = [&](int j) {
+        const bool first = !two || (j & 1) == 0, last = !two || (j & 1) == 1;
+        if (first && !wait_bar(bar(kKReady), k_ready.next(), abort_flag)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t q = sb + S::kQ + (two ? (j & 1) * S::kQTile : 0);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss_f16(tmem + S::kSCol + (j & 1) * kKeys,
+                       desc_sw128(q + (k >> 2) * (kRowTile * 128) + (k & 3) * 32),
+                       desc_sw128(sb + S::kK + (k >> 2) * (kKeys * 128) + (k & 3) * 32), kDescS,
+                       k > 0);
+          mma_commit(bar(kSFull + (j & 1)));
+          if (last) mma_commit(bar(kKFree));
+          if (j == jobs - 1) mma_commit(bar(kQFree));
+        }
+        __syncwarp();
+        issued = true;
+        return true;
+      };
+      ok = scores(0) && (jobs < 2 || scores(1));
+      for (int j = 0; ok && j < jobs; ++j) {
+        const int r = j & 1, grp = kGroups == 2 ? r : 0;
+        const bool first = !two || r == 0, last = !two || r == 1;
+        if ((first && !wait_bar(bar(kVReady), v_ready.next(), abort_flag)) ||
+            (j < kGroups && !wait_bar(bar(kOFree + grp), o_free[grp].before(), abort_flag)) ||
+            !wait_bar(bar(kPFull + r), p_full[r].next(), abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 8; ++k)
+            mma_ts_tf32(tmem + S::kOCol + grp * D, tmem + S::kSCol + r * kKeys + 8 * k,
+                        desc_sw128(sb + S::kV + (k >> 2) * (D * 128) + (k & 3) * 32), kDescO,
+                        j >= kGroups || k > 0);
+          mma_commit(bar(kODone + grp));
+          if (last) mma_commit(bar(kVFree));
+        }
+        __syncwarp();
+        if (last) ++freed;
+        if (j + 2 < jobs) ok = scores(j + 2);
+      }
+    }
+    // the last commits land before the CTA may leave
+    if (ok) {
+      if (freed > 0) mbar_wait_bounded(bar(kVFree), (freed - 1) & 1u, kWaitCycles);
+    } else if (issued) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < (1 << 20)) {
+      }
+    }
+  } else if (warp >= S::kConvWarp) {
+    // ---------------------------------------------------------- expansion
+    const int w = warp - S::kConvWarp, ct = tid - 32 * S::kConvWarp;
+    Phase q_free, k_free, v_free, raw_full[kRawStages];
+    int st = 0;
+    while (ok && next_unit<D>(p, run, walk, u)) {
+      if (!wait_bar(bar(kQFree), q_free.before(), abort_flag)) {
+        ok = false;
+        break;
+      }
+      // query rows as they are; rows past the unit's are zero
+      const int tiles = u.rows > kRowTile ? 2 : 1;
+#pragma unroll 4
+      for (int x = ct; x < tiles * kRowTile * (D / 8); x += 128) {
+        const int r = x / (D / 8), ch = x % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < u.rows) {
+          const int row = u.rt * S::kRows + r;
+          v = __ldg(reinterpret_cast<const uint4*>(
+              p.a.q + (long long)(u.s.row0 + row / p.G) * p.a.q_stride +
+              (long long)(u.h * p.G + row % p.G) * D + ch * 8));
+        }
+        sts128(sb + S::kQ + (r >> 7) * S::kQTile + (ch >> 3) * (kRowTile * 128) + (r & 127) * 128 +
+                   (((ch & 7) ^ (r & 7)) << 4),
+               v.x, v.y, v.z, v.w);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kQReady));
+      for (int i = u.i0; i < u.i1; ++i) {
+        const uint32_t rawk = sb + S::kRaw + st * S::kRawBytes, rawv = rawk + kKeys * D;
+        if (!wait_bar(bar(kRawFull + st), raw_full[st].next(), abort_flag) ||
+            !wait_bar(bar(kKFree), k_free.before(), abort_flag)) {
+          ok = false;
+          break;
+        }
+        // keys: 8 rows by 4 chunks of 16 codes at a time (no bank conflicts
+        // on either side), 32 bytes of bf16 each
+#pragma unroll
+        for (int r8 = 0; r8 < kKeys / 32; ++r8) {
+          const int row = w * (kKeys / 4) + 8 * r8 + (lane & 7);
+#pragma unroll
+          for (int c0 = 0; c0 < D / 64; ++c0) {
+            const int c = 4 * c0 + (lane >> 3);
+            const uint4 v = lds128(
+                rawk + (D == 64 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4)
+                                : (c >> 3) * (kKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)));
+            const uint32_t to = sb + S::kK + (c >> 2) * (kKeys * 128) + row * 128;
+            const int e = 2 * (c & 3);
+            sts128(to + ((e ^ (row & 7)) << 4), codes_bf16(v.x, 0x4140), codes_bf16(v.x, 0x4342),
+                   codes_bf16(v.y, 0x4140), codes_bf16(v.y, 0x4342));
+            sts128(to + (((e + 1) ^ (row & 7)) << 4), codes_bf16(v.z, 0x4140),
+                   codes_bf16(v.z, 0x4342), codes_bf16(v.w, 0x4140), codes_bf16(v.w, 0x4342));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kKReady));
+        if (!wait_bar(bar(kVFree), v_free.before(), abort_flag)) {
+          ok = false;
+          break;
+        }
+        // values: four tokens of a channel side by side as fp32 (a byte under
+        // 0x4B0000 reads 2^23 + u); lanes start at different channels of
+        // their word so that the stores meet no bank conflict
+        constexpr int kWords = D == 64 ? 16 : 32;         // words of a raw row
+        constexpr int kSub = 32 / kWords;                 // token groups of a warp at a time
+#pragma unroll 2
+        for (int g0 = 0; g0 < kKeys / 16; g0 += kSub) {
+          const int tok = 4 * (w * (kKeys / 16) + g0 + lane / kWords), wd = lane % kWords;
+#pragma unroll
+          for (int x = 0; x < (D + 127) / 128; ++x) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = tok + e;
+              v[e] = lds32(rawv + (D == 64 ? t * 64 + (((wd >> 2) ^ ((t >> 1) & 3)) << 4)
+                                           : x * (kKeys * 128) + t * 128 + (((wd >> 2) ^ (t & 7)) << 4)) +
+                           (wd & 3) * 4);
+            }
+#pragma unroll
+            for (int dd = 0; dd < 4; ++dd) {
+              const int d = (dd + (lane >> 1)) & 3, ch = 128 * x + 4 * wd + d;
+              uint32_t f[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                f[e] = __float_as_uint(
+                    __uint_as_float(__byte_perm(v[e], 0x4B000000u, 0x7440 + d)) - 8388736.0f);
+              sts128(sb + S::kV + (tok >> 5) * (D * 128) + ch * 128 +
+                         ((((tok & 31) >> 2) ^ (ch & 7)) << 4),
+                     f[0], f[1], f[2], f[3]);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kVReady));
+          mbar_arrive(bar(kRawEmpty + st));
+        }
+        st ^= 1;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int grp = warp >> 2;                                     // 0 .. kGroups - 1
+    const int r = tid & 127;                                       // row in the tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ocol = tmem + lanes + S::kOCol + grp * D;
+    const float f = p.a.scale * kLog2e;
+    Phase s_full[2], o_done, epi, epi_go;
+    int serial = 0, unit = 0;   // key tiles and units walked
+    for (; ok && next_unit<D>(p, run, walk, u); ++unit) {
+      const bool two = kGroups == 2 && u.rows > kRowTile;
+      const int row = u.rt * S::kRows + (two ? grp * kRowTile : 0) + r;   // of the (sequence, head)
+      const int pos = u.s.len - u.s.n + min(row, u.R - 1) / p.G;
+      float m = 0.0f, l = 0.0f;
+      bool have = false;     // m is some score's
+      int done = 0;          // jobs of this group whose PV may be under way
+      for (int i = 0; i < u.tiles(); ++i) {
+        if (kGroups == 2 && !two && (i & 1) != grp) continue;   // the other group's tile
+        const int reg = kGroups == 2 ? grp : i & 1;
+        const uint32_t scol = tmem + lanes + S::kSCol + reg * kKeys;
+        const int tok0 = u.t.lo + (u.i0 + i) * kKeys;
+        const float2* mt = meta + ((serial + i) & 7) * 8;
+        if (!wait_bar(bar(kSFull + reg), s_full[reg].next(), abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool cut = __any_sync(0xffffffffu, tok0 + kKeys - 1 > pos ||
+                                                     (p.a.window > 0 && tok0 <= pos - p.a.window));
+#pragma unroll 1
+        for (int c0 = 0; c0 < kKeys; c0 += 32) {
+          float x[32];
+          tc::tmem_ld<32>(scol + c0, x);
+          const float2 m0 = mt[c0 / 16], m1 = mt[c0 / 16 + 1];
+          const float f0 = f * m0.x, f1 = f * m1.x;
+          tc::tmem_wait_ld<32>(x);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], e < 16 ? f0 : f1, -m);
+          if (cut) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int t = tok0 + c0 + e;
+              if (t > pos || (p.a.window > 0 && t <= pos - p.a.window)) x[e] = -INFINITY;
+            }
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, x[e]);
+          if (__any_sync(0xffffffffu, mx > (have ? kPass : -INFINITY))) {
+            const bool up = mx > (have ? kPass : -INFINITY);
+            // what was weighed against the old m: earlier columns, O and l
+            mx = ceilf(mx);   // whole, so that rescaling is exact
+            const float keep = up && have ? exp2_fast(-mx) : 1.0f;
+            if (__any_sync(0xffffffffu, keep != 1.0f)) {
+              tmem_wait_st();
+              for (int c = 0; c < c0; c += 32) tmem_scale32(scol + c, keep);
+              if (done > 0) {
+                // the last PV of this group has to be complete
+                if (!wait_bar(bar(kODone + grp), (o_done.n + done - 1) & 1u, abort_flag)) ok = false;
+                tc_fence_after();
+                for (int c = 0; c < D; c += 32) tmem_scale32(ocol + c, keep);
+              }
+              tmem_wait_st();
+            }
+            if (up) {
+              l *= keep;
+              m += mx;
+              have = true;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] -= mx;
+            }
+          }
+          float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            x[e] = exp2_fast(x[e]);
+            x[e + 1] = exp2_fast(x[e + 1]);
+            l0 += x[e];
+            l1 += x[e + 1];
+          }
+          l += l0 + l1;
+          // times the block's step, rounded to tf32 (the MMA drops 13 bits)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            x[e] = __uint_as_float(__float_as_uint(x[e] * (e < 16 ? m0.y : m1.y)) + 0x1000u);
+          tmem_st32(scol + c0, x);
+        }
+        if (!ok) break;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull + reg));
+        ++done;
+      }
+      serial += u.tiles();
+      if (!ok) break;
+      // ---------------------------------------------------------- epilogue
+      bool gave_up = false;
+      if (done > 0) {
+        // (with one group, scores of the last tile do not tell that the PV
+        // before the last is complete: in turn)
+        if (kGroups == 1 && done > 1 &&
+            !wait_bar(bar(kODone + grp), (o_done.n + done - 2) & 1u, abort_flag))
+          gave_up = true;
+        if (!wait_bar(bar(kODone + grp), (o_done.n + done - 1) & 1u, abort_flag)) gave_up = true;
+        o_done.n += done;
+        tc_fence_after();
+      }
+      if (gave_up) {
+        ok = false;
+        break;
+      }
+      const bool no = refused[unit & 7] != 0;
+      const bool direct = u.whole() && (two || kGroups == 1);
+      const int slot = 2 * blockIdx.x + (u.i0 == 0 ? 1 : 0);
+      const int prow = (kGroups == 2 ? grp * kRowTile : 0) + r;
+      const bool mine = row < u.R;
+      if (!have) m = -INFINITY;
+      const long long at = mine ? (long long)(u.s.row0 + row / p.G) * p.a.Hq + u.h * p.G + row % p.G : 0;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (done > 0) {
+          tc::tmem_ld<32>(ocol + c, o);
+          tc::tmem_wait_ld<32>(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+        }
+        if (direct) {
+          if (mine && !no) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              const uint2 a = pack_bf16x4(o + e, inv), b = pack_bf16x4(o + e + 4, inv);
+              *reinterpret_cast<uint4*>(p.a.out + at * D + c + e) = make_uint4(a.x, a.y, b.x, b.y);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(p.parts + ((long long)slot * S::kRows + prow) * D + c + e) =
+                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      // (a group without a tile in this unit holds up no PV)
+      if (lane == 0 && done > 0) mbar_arrive(bar(kOFree + grp));
+      if (direct) {
+        if (mine && !no && p.a.lse != nullptr)
+          p.a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+      } else {
+        *reinterpret_cast<float2*>(p.part_stats + ((long long)slot * S::kRows + prow) * 2) =
+            make_float2(m, no ? -1.0f : l);
+        __threadfence();
+      }
+      // all softmax warps have read `refused` and written their parts
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kEpi));
+      if (!wait_bar(bar(kEpi), epi.next(), abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (no && tid == 0) report(p.a.status, W4_ERR_INDEX);
+      int c0 = blockIdx.x, c1 = blockIdx.x;
+      if (tid == 0) {
+        refused[unit & 7] = 0;
+        int join = direct ? 0 : 1;
+        if (!u.whole()) {
+          c0 = run.holder(u.u0);
+          c1 = run.holder(u.u0 + u.t.slices - 1);
+          int32_t* arrived = p.arrived + ((long long)u.b * p.c.H + u.h) * p.rts + u.rt;
+          const int was = atomic_add_acq_rel_gpu(arrived, 1);
+          join = was == c1 - c0;
+          if (join) *arrived = 0;
+        }
+        *epi_flag = join;
+        mbar_arrive(bar(kEpiGo));
+      }
+      if (!wait_bar(bar(kEpiGo), epi_go.next(), abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (*epi_flag) {
+        if (!u.whole()) {
+          c0 = run.holder(u.u0);
+          c1 = run.holder(u.u0 + u.t.slices - 1);
+        }
+        __threadfence();
+        // of one row tile, each CTA holds two parts (one per group)
+        const int subs = kGroups == 2 && !two ? 2 : 1;
+        for (int x = tid; x < u.rows * (D / 4); x += 32 * S::kSoftWarps) {
+          const int rr = x / (D / 4), c4 = x % (D / 4);
+          float M = -INFINITY, L = 0.0f;
+          bool none = false;
+          auto part = [&](int c, int sub) {
+            return (long long)(2 * c + (run.start(c) <= u.u0 ? 1 : 0)) * S::kRows + rr + sub * kRowTile;
+          };
+          for (int c = c0; c <= c1; ++c)
+            for (int sub = 0; sub < subs; ++sub) {
+              const float2 s2 = __ldcg(reinterpret_cast<const float2*>(p.part_stats) + part(c, sub));
+              M = fmaxf(M, s2.x);
+              none |= s2.y < 0.0f;
+            }
+          if (none) continue;
+          float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int c = c0; c <= c1; ++c)
+            for (int sub = 0; sub < subs; ++sub) {
+              const long long q = part(c, sub);
+              const float2 s2 = __ldcg(reinterpret_cast<const float2*>(p.part_stats) + q);
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(p.parts + q * D + 4 * c4));
+              const float k = s2.x == -INFINITY ? (s2.y == 0.0f ? 0.0f : 1.0f) : exp2_fast(s2.x - M);
+              L += k * s2.y;
+              a.x += k * v.x;
+              a.y += k * v.y;
+              a.z += k * v.z;
+              a.w += k * v.w;
+            }
+          const int rw = u.rt * S::kRows + rr;
+          const long long to = (long long)(u.s.row0 + rw / p.G) * p.a.Hq + u.h * p.G + rw % p.G;
+          const float o4[4] = {a.x, a.y, a.z, a.w};
+          *reinterpret_cast<uint2*>(p.a.out + to * D + 4 * c4) =
+              pack_bf16x4(o4, L == 0.0f ? 0.0f : 1.0f / L);
+          if (c4 == 0 && p.a.lse != nullptr)
+            p.a.lse[to] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+        }
+      }
+    }
+  }
+  if (!ok) {
+    if (*abort_flag == 0) report(p.a.status, W4_ERR_TIMEOUT);
+    *abort_flag = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == S::kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ================================================================= host side
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+struct Plan {
+  int rows, rts;
+  size_t arrived, parts, stats, bytes;
+};
+
+Plan plan_chunk(const Cache& c, const Batch& b, int G, int sms) {
+  Plan pl;
+  pl.rows = c.D == 256 ? Shape<256>::kRows : Shape<128>::kRows;
+  pl.rts = (int)(((long long)b.max_new * G + pl.rows - 1) / pl.rows);
+  pl.arrived = up256((size_t)b.B * c.H * pl.rts * 4);
+  pl.parts = up256((size_t)2 * sms * pl.rows * c.D * 4);
+  pl.stats = up256((size_t)2 * sms * pl.rows * 8);
+  pl.bytes = pl.arrived + pl.parts + pl.stats;
+  return pl;
+}
+
+template <int D>
+w4_status launch_chunk(ChunkParams& p, int sms, int dev, bool pdl, w4_stream_t stream) {
+  using S = Shape<D>;
+  static std::mutex mu;
+  static bool done[64] = {};
+  if (dev < 0 || dev >= 64) return W4_ERR_DEVICE;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(
+          attn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+      if (e != cudaSuccess) {
+        note_cuda_error(e);
+        (void)cudaGetLastError();
+        return W4_ERR_LAUNCH;
+      }
+      done[dev] = true;
+    }
+  }
+  const int box = std::min(p.c.P, S::kKeys);
+  if (!tensor_map(&p.tm_k, p.c.kc, p.c, box) || !tensor_map(&p.tm_v, p.c.vc, p.c, box)) {
+    note_cuda_error(cudaErrorInvalidValue);
+    return W4_ERR_LAUNCH;
+  }
+  return launch(attn_chunk_kernel<D>, dim3((unsigned)sms), S::kThreads, S::kSmem, pdl, stream, p);
+}
+
+}  // namespace
+
+size_t chunk_workspace_bytes(const Cache& c, const Batch& b, int G, int sms) {
+  return plan_chunk(c, b, G, sms).bytes;
+}
+
+w4_status chunk_attn(const Cache& c, const Batch& b, const ChunkArgs& a, void* workspace, int sms,
+                     int dev, bool pdl, w4_stream_t stream) {
+  ChunkParams p = {};
+  p.c = c;
+  p.bt = b;
+  p.a = a;
+  p.G = a.Hq / c.H;
+  const Plan pl = plan_chunk(c, b, p.G, sms);
+  p.rts = pl.rts;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.arrived = reinterpret_cast<int32_t*>(ws);
+  p.parts = reinterpret_cast<float*>(ws + pl.arrived);
+  p.part_stats = reinterpret_cast<float*>(ws + pl.arrived + pl.parts);
+  switch (c.D) {
+    case 64: return launch_chunk<64>(p, sms, dev, pdl, stream);
+    case 128: return launch_chunk<128>(p, sms, dev, pdl, stream);
+    default: return launch_chunk<256>(p, sms, dev, pdl, stream);
+  }
+}
+
+}  // namespace kv8
+}  // namespace w4
