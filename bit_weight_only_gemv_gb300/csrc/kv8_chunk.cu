@@ -15,7 +15,7 @@
 // costs PV twice the tensor time of a 16-bit P; the softmax warps, not the
 // tensor cores, would then be the limit.  For the same reason m need not be
 // the maximum: it is the largest score of the row's first 32 keys, and moves
-// (with O and l rescaled) only when a score passes it by 2^64.
+// (with O and l rescaled) only when a score passes it by 2^60.
 //
 // Roles: four softmax warps per row tile (a thread owns a row, so maxima and
 // sums need no exchange), four warps that expand the codes (K to bf16, V to
@@ -26,8 +26,8 @@
 // the two softmax groups in turn and joins them at the end.
 //
 // Work is cut into equal runs of key tiles over all units, one run a CTA
-// (kv8_runs.cuh); parts of a cut unit meet in the workspace, joined in order
-// by the last CTA to arrive.  Every wait is bounded.
+// (kv8_runs.cuh); parts of a cut unit meet in the workspace and are joined in
+// order by a second small kernel.  Every wait is bounded.
 #include <algorithm>
 #include <mutex>
 
@@ -40,14 +40,15 @@ namespace kv8 {
 namespace {
 
 using tc::kWaitCycles;
-using tc::mma_commit;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
 using tc::wait_bar;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kPass = 64.0f;        // log2 of how far a score may pass m
+constexpr float kPass = 60.0f;        // log2 of how far a score may pass m
+constexpr float kFar = 1152921504606846976.0f;   // 2^60
+constexpr float kRound = 1.0f + 0.72f / 2048.0f;
 constexpr int kRowTile = 128;
 constexpr int kRawStages = 2;
 constexpr int kMetaRing = 8;
@@ -59,8 +60,9 @@ struct Shape {
   static constexpr int kKeys = D == 256 ? 64 : 128;  // keys of a tile
   static constexpr int kRows = kRowTile * kGroups;   // query rows of a unit
   static constexpr int kSoftWarps = 4 * kGroups;
-  static constexpr int kConvWarp = kSoftWarps;       // four
-  static constexpr int kMmaWarp = kConvWarp + 4;
+  static constexpr int kConvWarp = kSoftWarps;
+  static constexpr int kConvWarps = 6;               // 16 warps in all with two groups
+  static constexpr int kMmaWarp = kConvWarp + kConvWarps;
   static constexpr int kCopyWarp = kMmaWarp + 1;
   static constexpr int kWarps = kCopyWarp + 1;
   static constexpr int kThreads = 32 * kWarps;
@@ -85,12 +87,14 @@ struct Shape {
 enum {
   kRawFull = 0,    // [2]
   kRawEmpty = 2,   // [2]
-  kQReady = 4, kQFree, kKReady, kKFree, kVReady, kVFree,
-  kSFull = 10,     // [2] by S region
-  kPFull = 12,     // [2]
-  kODone = 14,     // [2] by group
-  kOFree = 16,     // [2]
-  kEpi = 18, kEpiGo,
+  kQReady = 4, kQFree, kKReady, kKFree,
+  kVReady = 8,     // [2] by half of the tile's keys
+  kVFree = 10,     // [2]
+  kSFull = 12,     // [2] by S region
+  kPFull = 14,     // [2]
+  kODone = 16,     // [2] by group
+  kOFree = 18,     // [2]
+  kEpi = 20,
   kBarCount
 };
 
@@ -101,9 +105,10 @@ struct ChunkParams {
   ChunkArgs a;
   int G;
   int rts;            // row tiles (units) of a (sequence, head), at most
-  int32_t* arrived;   // [B][H][rts], zero between calls
-  float* parts;       // [2 * CTAs][rows][D]
-  float* part_stats;  // [2 * CTAs][rows][2]: m, l (l = -1: refused)
+  long long* cut;     // [2 + B * H * rts]: total and CTAs of the runs, then each unit's
+                      // first item, -1 where the unit's outputs are written already
+  float* parts;       // [4 * CTAs][rows][D]
+  float* part_stats;  // [4 * CTAs][rows][2]: m, l (l = -1: refused)
 };
 
 // One unit of a run: a row tile (pair) of a (sequence, head), key tiles i0 .. i1 - 1 of it.
@@ -195,21 +200,56 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
          (1ull << 46) | (2ull << 61);
 }
 
+// The whole warp runs the issuing code, so that addresses and descriptors stay
+// in uniform registers; `leader` (one lane) issues.
 __device__ __forceinline__ void mma_ss_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t acc) {
+                                           uint32_t acc, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t acc) {
+                                            uint32_t acc, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
       : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar),
+      "r"(leader)
+      : "memory");
+}
+
+// Two fp32 values side by side (packed arithmetic: one instruction for both).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
@@ -232,6 +272,34 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// 2^(x factor - m) in place, 0 where a row sees no key (cut: some row does not
+// see some of the keys t0 .. t0 + 31); returns the sum.
+__device__ __forceinline__ float weights(float* x, float f0, float f1, float m, bool cut, int t0,
+                                         int pos, int window) {
+  const uint64_t a0 = pack2(f0, f0), a1 = pack2(f1, f1), c = pack2(-m, -m);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2)
+    unpack2(fma2(pack2(x[e], x[e + 1]), e < 16 ? a0 : a1, c), x[e], x[e + 1]);
+  if (cut) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const int t = t0 + e;
+      if (t > pos || (window > 0 && t <= pos - window)) x[e] = -INFINITY;
+    }
+  }
+  uint64_t s0 = 0, s1 = 0;   // two sums of pairs
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[e + k] = exp2_fast(x[e + k]);
+    s0 = add2(s0, pack2(x[e], x[e + 1]));
+    s1 = add2(s1, pack2(x[e + 2], x[e + 3]));
+  }
+  float a, b;
+  unpack2(add2(s0, s1), a, b);
+  return a + b;
 }
 
 // Multiply 32 columns from `col` on by this thread's factor.
@@ -266,6 +334,40 @@ struct Phase {
   __device__ __forceinline__ uint32_t before() { return (n++ & 1u) ^ 1u; }  // first one passes at once
 };
 
+// Four channels of one row from its parts, in order: part(k) is the row's
+// place in the k-th.
+template <int D, typename Part>
+__device__ __forceinline__ void join_row(const ChunkParams& p, const Seq& s, int h, int row, int c4,
+                                         int parts, Part part) {
+  const float2* stats = reinterpret_cast<const float2*>(p.part_stats);
+  float M = -INFINITY, L = 0.0f;
+  bool none = false;
+  for (int k = 0; k < parts; ++k) {
+    const float2 s2 = __ldcg(stats + part(k));
+    M = fmaxf(M, s2.x);
+    none |= s2.y < 0.0f;
+  }
+  if (none) return;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) {
+    const long long q = part(k);
+    const float2 s2 = __ldcg(stats + q);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p.parts + q * D + 4 * c4));
+    const float w = s2.x == -INFINITY ? (s2.y == 0.0f ? 0.0f : 1.0f) : exp2_fast(s2.x - M);
+    L += w * s2.y;
+    a.x += w * v.x;
+    a.y += w * v.y;
+    a.z += w * v.z;
+    a.w += w * v.w;
+  }
+  const long long to = (long long)(s.row0 + row / p.G) * p.a.Hq + h * p.G + row % p.G;
+  const float o4[4] = {a.x, a.y, a.z, a.w};
+  *reinterpret_cast<uint2*>(p.a.out + to * D + 4 * c4) =
+      pack_bf16x4(o4, L == 0.0f ? 0.0f : 1.0f / L);
+  if (c4 == 0 && p.a.lse != nullptr) p.a.lse[to] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     attn_chunk_kernel(const __grid_constant__ ChunkParams p) {
@@ -281,27 +383,25 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   float2* meta = reinterpret_cast<float2*>(sm + S::kMeta);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kMisc + 4);
-  volatile int* epi_flag = reinterpret_cast<volatile int*>(sm + S::kMisc + 8);
   volatile int* refused = reinterpret_cast<volatile int*>(sm + S::kMisc + 16);   // [8] by unit
   long long* scan = reinterpret_cast<long long*>(sm + S::kMisc + 64);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kRawFull + i), 1);
-      mbar_init(bar(kRawEmpty + i), 4);
+      mbar_init(bar(kRawEmpty + i), S::kConvWarps);
+      mbar_init(bar(kVReady + i), S::kConvWarps);
+      mbar_init(bar(kVFree + i), 1);
       mbar_init(bar(kSFull + i), 1);
       mbar_init(bar(kPFull + i), 4);
       mbar_init(bar(kODone + i), 1);
       mbar_init(bar(kOFree + i), 4);
     }
-    mbar_init(bar(kQReady), 4);
+    mbar_init(bar(kQReady), S::kConvWarps);
     mbar_init(bar(kQFree), 1);
-    mbar_init(bar(kKReady), 4);
+    mbar_init(bar(kKReady), S::kConvWarps);
     mbar_init(bar(kKFree), 1);
-    mbar_init(bar(kVReady), 4);
-    mbar_init(bar(kVFree), 1);
     mbar_init(bar(kEpi), S::kSoftWarps);
-    mbar_init(bar(kEpiGo), 1);
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) refused[i] = 0;
     mbar_init_fence();
@@ -316,7 +416,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;   // all 512 columns: they begin at 0
   pdl_wait();
   if (blockIdx.x == 0)
     for (int b = tid; b < p.bt.B; b += S::kThreads)
@@ -327,7 +427,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   Walk walk = {any ? run.g0 : 0, any ? run.off : 0, any ? run.entry : 0};
   if (!any) run.g1 = 0;
   Unit u;
-  bool ok = true;
+  bool ok = *tmem_slot == 0;
   __syncthreads();
 
   if (warp == S::kCopyWarp) {
@@ -388,9 +488,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                                 ((uint32_t)(kRowTile >> 4) << 24);
     constexpr uint32_t kDescO = (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(D >> 3) << 17) |
                                 ((uint32_t)(kRowTile >> 4) << 24);
-    Phase q_ready, k_ready, v_ready, p_full[2], o_free[2];
+    Phase q_ready, k_ready, v_ready[2], p_full[2], o_free[2];
     bool issued = false;
-    uint32_t freed = 0;   // commits on kVFree
+    uint32_t freed = 0;   // commits on the second half's kVFree
+    const uint32_t leader = lane == 0;
+    const uint64_t dq = desc_sw128(sb + S::kQ), dk = desc_sw128(sb + S::kK), dv = desc_sw128(sb + S::kV);
     while (ok && next_unit<D>(p, run, walk, u)) {
       const bool two = kGroups == 2 && u.rows > kRowTile;   // two row tiles
       const int jobs = two ? 2 * u.tiles() : u.tiles();
@@ -403,19 +505,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         const bool first = !two || (j & 1) == 0, last = !two || (j & 1) == 1;
         if (first && !wait_bar(bar(kKReady), k_ready.next(), abort_flag)) return false;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t q = sb + S::kQ + (two ? (j & 1) * S::kQTile : 0);
+        const uint64_t a0 = dq + (two ? (j & 1) * (S::kQTile / 16) : 0);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss_f16(tmem + S::kSCol + (j & 1) * kKeys,
-                       desc_sw128(q + (k >> 2) * (kRowTile * 128) + (k & 3) * 32),
-                       desc_sw128(sb + S::kK + (k >> 2) * (kKeys * 128) + (k & 3) * 32), kDescS,
-                       k > 0);
-          mma_commit(bar(kSFull + (j & 1)));
-          if (last) mma_commit(bar(kKFree));
-          if (j == jobs - 1) mma_commit(bar(kQFree));
-        }
-        __syncwarp();
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss_f16(tmem + S::kSCol + (j & 1) * kKeys,
+                     a0 + (k >> 2) * (kRowTile * 128 / 16) + (k & 3) * 2,
+                     dk + (k >> 2) * (kKeys * 128 / 16) + (k & 3) * 2, kDescS, k > 0, leader);
+        commit(bar(kSFull + (j & 1)), leader);
+        if (last) commit(bar(kKFree), leader);
+        if (j == jobs - 1) commit(bar(kQFree), leader);
         issued = true;
         return true;
       };
@@ -423,30 +521,32 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       for (int j = 0; ok && j < jobs; ++j) {
         const int r = j & 1, grp = kGroups == 2 ? r : 0;
         const bool first = !two || r == 0, last = !two || r == 1;
-        if ((first && !wait_bar(bar(kVReady), v_ready.next(), abort_flag)) ||
-            (j < kGroups && !wait_bar(bar(kOFree + grp), o_free[grp].before(), abort_flag)) ||
+        if ((j < kGroups && !wait_bar(bar(kOFree + grp), o_free[grp].before(), abort_flag)) ||
             !wait_bar(bar(kPFull + r), p_full[r].next(), abort_flag)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        if (lane == 0) {
 #pragma unroll
-          for (int k = 0; k < kKeys / 8; ++k)
+        for (int half = 0; half < 2; ++half) {
+          if (first && !wait_bar(bar(kVReady + half), v_ready[half].next(), abort_flag)) ok = false;
+          tc_fence_after();
+          if (!ok) break;
+#pragma unroll
+          for (int k = half * (kKeys / 16); k < (half + 1) * (kKeys / 16); ++k)
             mma_ts_tf32(tmem + S::kOCol + grp * D, tmem + S::kSCol + r * kKeys + 8 * k,
-                        desc_sw128(sb + S::kV + (k >> 2) * (D * 128) + (k & 3) * 32), kDescO,
-                        j >= kGroups || k > 0);
-          mma_commit(bar(kODone + grp));
-          if (last) mma_commit(bar(kVFree));
+                        dv + (k >> 2) * (D * 128 / 16) + (k & 3) * 2, kDescO, j >= kGroups || k > 0,
+                        leader);
+          if (half == 1) commit(bar(kODone + grp), leader);
+          if (last) commit(bar(kVFree + half), leader);
         }
-        __syncwarp();
+        if (!ok) break;
         if (last) ++freed;
         if (j + 2 < jobs) ok = scores(j + 2);
       }
     }
     // the last commits land before the CTA may leave
     if (ok) {
-      if (freed > 0) mbar_wait_bounded(bar(kVFree), (freed - 1) & 1u, kWaitCycles);
+      if (freed > 0) mbar_wait_bounded(bar(kVFree + 1), (freed - 1) & 1u, kWaitCycles);
     } else if (issued) {
       const long long t0 = clock64();
       while (clock64() - t0 < (1 << 20)) {
@@ -455,7 +555,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   } else if (warp >= S::kConvWarp) {
     // ---------------------------------------------------------- expansion
     const int w = warp - S::kConvWarp, ct = tid - 32 * S::kConvWarp;
-    Phase q_free, k_free, v_free, raw_full[kRawStages];
+    Phase q_free, k_free, v_free[2], raw_full[kRawStages];
     int st = 0;
     while (ok && next_unit<D>(p, run, walk, u)) {
       if (!wait_bar(bar(kQFree), q_free.before(), abort_flag)) {
@@ -465,7 +565,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       // query rows as they are; rows past the unit's are zero
       const int tiles = u.rows > kRowTile ? 2 : 1;
 #pragma unroll 4
-      for (int x = ct; x < tiles * kRowTile * (D / 8); x += 128) {
+      for (int x = ct; x < tiles * kRowTile * (D / 8); x += 32 * S::kConvWarps) {
         const int r = x / (D / 8), ch = x % (D / 8);
         uint4 v = make_uint4(0, 0, 0, 0);
         if (r < u.rows) {
@@ -490,9 +590,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         }
         // keys: 8 rows by 4 chunks of 16 codes at a time (no bank conflicts
         // on either side), 32 bytes of bf16 each
-#pragma unroll
-        for (int r8 = 0; r8 < kKeys / 32; ++r8) {
-          const int row = w * (kKeys / 4) + 8 * r8 + (lane & 7);
+#pragma unroll 2
+        for (int r8 = w; r8 < kKeys / 8; r8 += S::kConvWarps) {
+          const int row = 8 * r8 + (lane & 7);
 #pragma unroll
           for (int c0 = 0; c0 < D / 64; ++c0) {
             const int c = 4 * c0 + (lane >> 3);
@@ -510,48 +610,55 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kKReady));
-        if (!wait_bar(bar(kVFree), v_free.before(), abort_flag)) {
-          ok = false;
-          break;
-        }
         // values: four tokens of a channel side by side as fp32 (a byte under
         // 0x4B0000 reads 2^23 + u); lanes start at different channels of
         // their word so that the stores meet no bank conflict
         constexpr int kWords = D == 64 ? 16 : 32;         // words of a raw row
         constexpr int kSub = 32 / kWords;                 // token groups of a warp at a time
+        const uint64_t zero = pack2(-8388736.0f, -8388736.0f);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (!wait_bar(bar(kVFree + half), v_free[half].before(), abort_flag)) {
+            ok = false;
+            break;
+          }
 #pragma unroll 2
-        for (int g0 = 0; g0 < kKeys / 16; g0 += kSub) {
-          const int tok = 4 * (w * (kKeys / 16) + g0 + lane / kWords), wd = lane % kWords;
+          for (int g = w; g < kKeys / 8 / kSub; g += S::kConvWarps) {
+            const int tok = half * (kKeys / 2) + 4 * (g * kSub + lane / kWords), wd = lane % kWords;
 #pragma unroll
-          for (int x = 0; x < (D + 127) / 128; ++x) {
-            uint32_t v[4];
+            for (int x = 0; x < (D + 127) / 128; ++x) {
+              uint32_t v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int t = tok + e;
-              v[e] = lds32(rawv + (D == 64 ? t * 64 + (((wd >> 2) ^ ((t >> 1) & 3)) << 4)
-                                           : x * (kKeys * 128) + t * 128 + (((wd >> 2) ^ (t & 7)) << 4)) +
-                           (wd & 3) * 4);
-            }
+              for (int e = 0; e < 4; ++e) {
+                const int t = tok + e;
+                v[e] = lds32(rawv +
+                             (D == 64 ? t * 64 + (((wd >> 2) ^ ((t >> 1) & 3)) << 4)
+                                      : x * (kKeys * 128) + t * 128 + (((wd >> 2) ^ (t & 7)) << 4)) +
+                             (wd & 3) * 4);
+              }
 #pragma unroll
-            for (int dd = 0; dd < 4; ++dd) {
-              const int d = (dd + (lane >> 1)) & 3, ch = 128 * x + 4 * wd + d;
-              uint32_t f[4];
+              for (int dd = 0; dd < 4; ++dd) {
+                const int d = (dd + (lane >> 1)) & 3, ch = 128 * x + 4 * wd + d;
+                float f[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                f[e] = __float_as_uint(
-                    __uint_as_float(__byte_perm(v[e], 0x4B000000u, 0x7440 + d)) - 8388736.0f);
-              sts128(sb + S::kV + (tok >> 5) * (D * 128) + ch * 128 +
-                         ((((tok & 31) >> 2) ^ (ch & 7)) << 4),
-                     f[0], f[1], f[2], f[3]);
+                for (int e = 0; e < 4; e += 2)
+                  unpack2(add2(pack2(__uint_as_float(__byte_perm(v[e], 0x4B000000u, 0x7440 + d)),
+                                     __uint_as_float(__byte_perm(v[e + 1], 0x4B000000u, 0x7440 + d))),
+                               zero),
+                          f[e], f[e + 1]);
+                sts128(sb + S::kV + (tok >> 5) * (D * 128) + ch * 128 +
+                           ((((tok & 31) >> 2) ^ (ch & 7)) << 4),
+                       __float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                       __float_as_uint(f[3]));
+              }
             }
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kVReady + half));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kVReady));
-          mbar_arrive(bar(kRawEmpty + st));
-        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(bar(kRawEmpty + st));
         st ^= 1;
       }
     }
@@ -562,7 +669,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ocol = tmem + lanes + S::kOCol + grp * D;
     const float f = p.a.scale * kLog2e;
-    Phase s_full[2], o_done, epi, epi_go;
+    Phase s_full[2], o_done, epi;
     int serial = 0, unit = 0;   // key tiles and units walked
     for (; ok && next_unit<D>(p, run, walk, u); ++unit) {
       const bool two = kGroups == 2 && u.rows > kRowTile;
@@ -586,28 +693,32 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                                                      (p.a.window > 0 && tok0 <= pos - p.a.window));
 #pragma unroll 1
         for (int c0 = 0; c0 < kKeys; c0 += 32) {
-          float x[32];
-          tc::tmem_ld<32>(scol + c0, x);
+          float y[32];
+          tc::tmem_ld<32>(scol + c0, y);
           const float2 m0 = mt[c0 / 16], m1 = mt[c0 / 16 + 1];
-          const float f0 = f * m0.x, f1 = f * m1.x;
-          tc::tmem_wait_ld<32>(x);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], e < 16 ? f0 : f1, -m);
-          if (cut) {
+          tc::tmem_wait_ld<32>(y);
+          float sum = weights(y, f * m0.x, f * m1.x, m, cut, tok0 + c0, pos, p.a.window);
+          // a score far past m (its weight shows in the sum), or no m yet
+          if (__any_sync(0xffffffffu, !have || !(sum <= kFar))) {
+            tc::tmem_ld<32>(scol + c0, y);
+            tc::tmem_wait_ld<32>(y);
+            float mx = -INFINITY;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const int t = tok0 + c0 + e;
-              if (t > pos || (p.a.window > 0 && t <= pos - p.a.window)) x[e] = -INFINITY;
+              const bool sees = t <= pos && !(p.a.window > 0 && t <= pos - p.a.window);
+              mx = fmaxf(mx, sees ? y[e] * (e < 16 ? f * m0.x : f * m1.x) : -INFINITY);
             }
-          }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, x[e]);
-          if (__any_sync(0xffffffffu, mx > (have ? kPass : -INFINITY))) {
-            const bool up = mx > (have ? kPass : -INFINITY);
+            float keep = 1.0f;
+            if (!have) {
+              have = mx > -INFINITY;
+              m = have ? mx : 0.0f;
+            } else if (mx - m > kPass) {
+              const float up = ceilf(mx - m);   // whole, so that rescaling is exact
+              keep = exp2_fast(-up);
+              m += up;
+            }
             // what was weighed against the old m: earlier columns, O and l
-            mx = ceilf(mx);   // whole, so that rescaling is exact
-            const float keep = up && have ? exp2_fast(-mx) : 1.0f;
             if (__any_sync(0xffffffffu, keep != 1.0f)) {
               tmem_wait_st();
               for (int c = 0; c < c0; c += 32) tmem_scale32(scol + c, keep);
@@ -619,28 +730,19 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
               }
               tmem_wait_st();
             }
-            if (up) {
-              l *= keep;
-              m += mx;
-              have = true;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] -= mx;
-            }
+            l *= keep;
+            sum = weights(y, f * m0.x, f * m1.x, m, cut, tok0 + c0, pos, p.a.window);
           }
-          float l0 = 0.0f, l1 = 0.0f;
+          l += sum;
+          // times the block's step; the MMA drops 13 bits of what it reads,
+          // and the factor's last part makes that a rounding: the mean error is
+          // nil, and a weight of 11 bits stays what it is
+          const uint64_t v0 = pack2(m0.y * kRound, m0.y * kRound);
+          const uint64_t v1 = pack2(m1.y * kRound, m1.y * kRound);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            x[e] = exp2_fast(x[e]);
-            x[e + 1] = exp2_fast(x[e + 1]);
-            l0 += x[e];
-            l1 += x[e + 1];
-          }
-          l += l0 + l1;
-          // times the block's step, rounded to tf32 (the MMA drops 13 bits)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            x[e] = __uint_as_float(__float_as_uint(x[e] * (e < 16 ? m0.y : m1.y)) + 0x1000u);
-          tmem_st32(scol + c0, x);
+          for (int e = 0; e < 32; e += 2)
+            unpack2(mul2(pack2(y[e], y[e + 1]), e < 16 ? v0 : v1), y[e], y[e + 1]);
+          tmem_st32(scol + c0, y);
         }
         if (!ok) break;
         tmem_wait_st();
@@ -669,7 +771,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       }
       const bool no = refused[unit & 7] != 0;
       const bool direct = u.whole() && (two || kGroups == 1);
-      const int slot = 2 * blockIdx.x + (u.i0 == 0 ? 1 : 0);
+      // a whole unit of one row tile: the groups' parts meet right here, in
+      // two places of this CTA's own in turn
+      const bool pair = u.whole() && !direct;
+      const int slot = pair ? 2 * gridDim.x + 2 * blockIdx.x + (unit & 1)
+                            : 2 * blockIdx.x + (u.i0 == 0 ? 1 : 0);
       const int prow = (kGroups == 2 ? grp * kRowTile : 0) + r;
       const bool mine = row < u.R;
       if (!have) m = -INFINITY;
@@ -710,8 +816,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       } else {
         *reinterpret_cast<float2*>(p.part_stats + ((long long)slot * S::kRows + prow) * 2) =
             make_float2(m, no ? -1.0f : l);
-        __threadfence();
       }
+      // the unit's first CTA says where its parts are
+      if (tid == 0 && u.i0 == 0)
+        p.cut[2 + ((long long)u.b * p.c.H + u.h) * p.rts + u.rt] = u.whole() ? -1 : u.u0;
       // all softmax warps have read `refused` and written their parts
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kEpi));
@@ -719,70 +827,21 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         ok = false;
         break;
       }
-      if (no && tid == 0) report(p.a.status, W4_ERR_INDEX);
-      int c0 = blockIdx.x, c1 = blockIdx.x;
       if (tid == 0) {
+        if (no) report(p.a.status, W4_ERR_INDEX);
         refused[unit & 7] = 0;
-        int join = direct ? 0 : 1;
-        if (!u.whole()) {
-          c0 = run.holder(u.u0);
-          c1 = run.holder(u.u0 + u.t.slices - 1);
-          int32_t* arrived = p.arrived + ((long long)u.b * p.c.H + u.h) * p.rts + u.rt;
-          const int was = atomic_add_acq_rel_gpu(arrived, 1);
-          join = was == c1 - c0;
-          if (join) *arrived = 0;
-        }
-        *epi_flag = join;
-        mbar_arrive(bar(kEpiGo));
       }
-      if (!wait_bar(bar(kEpiGo), epi_go.next(), abort_flag)) {
-        ok = false;
-        break;
+      if (pair && !no) {
+        const long long base = (long long)slot * S::kRows;
+        for (int x = tid; x < u.rows * (D / 4); x += 32 * S::kSoftWarps)
+          join_row<D>(p, u.s, u.h, u.rt * S::kRows + x / (D / 4), x % (D / 4), 2, [&](int k) {
+            return base + x / (D / 4) + k * kRowTile;
+          });
       }
-      if (*epi_flag) {
-        if (!u.whole()) {
-          c0 = run.holder(u.u0);
-          c1 = run.holder(u.u0 + u.t.slices - 1);
-        }
-        __threadfence();
-        // of one row tile, each CTA holds two parts (one per group)
-        const int subs = kGroups == 2 && !two ? 2 : 1;
-        for (int x = tid; x < u.rows * (D / 4); x += 32 * S::kSoftWarps) {
-          const int rr = x / (D / 4), c4 = x % (D / 4);
-          float M = -INFINITY, L = 0.0f;
-          bool none = false;
-          auto part = [&](int c, int sub) {
-            return (long long)(2 * c + (run.start(c) <= u.u0 ? 1 : 0)) * S::kRows + rr + sub * kRowTile;
-          };
-          for (int c = c0; c <= c1; ++c)
-            for (int sub = 0; sub < subs; ++sub) {
-              const float2 s2 = __ldcg(reinterpret_cast<const float2*>(p.part_stats) + part(c, sub));
-              M = fmaxf(M, s2.x);
-              none |= s2.y < 0.0f;
-            }
-          if (none) continue;
-          float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int c = c0; c <= c1; ++c)
-            for (int sub = 0; sub < subs; ++sub) {
-              const long long q = part(c, sub);
-              const float2 s2 = __ldcg(reinterpret_cast<const float2*>(p.part_stats) + q);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(p.parts + q * D + 4 * c4));
-              const float k = s2.x == -INFINITY ? (s2.y == 0.0f ? 0.0f : 1.0f) : exp2_fast(s2.x - M);
-              L += k * s2.y;
-              a.x += k * v.x;
-              a.y += k * v.y;
-              a.z += k * v.z;
-              a.w += k * v.w;
-            }
-          const int rw = u.rt * S::kRows + rr;
-          const long long to = (long long)(u.s.row0 + rw / p.G) * p.a.Hq + u.h * p.G + rw % p.G;
-          const float o4[4] = {a.x, a.y, a.z, a.w};
-          *reinterpret_cast<uint2*>(p.a.out + to * D + 4 * c4) =
-              pack_bf16x4(o4, L == 0.0f ? 0.0f : 1.0f / L);
-          if (c4 == 0 && p.a.lse != nullptr)
-            p.a.lse[to] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
-        }
-      }
+    }
+    if (tid == 0 && blockIdx.x == 0) {
+      p.cut[0] = run.total;
+      p.cut[1] = run.ctas;
     }
   }
   if (!ok) {
@@ -793,7 +852,46 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == S::kMmaWarp)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*tmem_slot)
+                 : "memory");
+}
+
+// Joins the parts of cut units: one CTA per 16 rows.  Reading and adding
+// them all from one SM would take longer than computing them did.
+constexpr int kJoinRows = 16;
+constexpr int kJoinThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ ChunkParams p) {
+  using S = Shape<D>;
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kSlabs = S::kRows / kJoinRows;
+  const int rt = blockIdx.x / kSlabs, slab = blockIdx.x % kSlabs, h = blockIdx.y, b = blockIdx.z;
+  const Seq s = sequence(p.bt, p.c.P, b);
+  const int R = s.n * p.G, row0 = rt * S::kRows + slab * kJoinRows;
+  if (!s.ok || row0 >= R) return;
+  const long long u0 = p.cut[2 + ((long long)b * p.c.H + h) * p.rts + rt];
+  if (u0 < 0) return;
+  Run run;
+  run.total = p.cut[0];
+  run.ctas = (int)p.cut[1];
+  const Tile t = tile_of(s, p.G, p.a.window, rt, S::kRows, S::kKeys);
+  const int c0 = run.holder(u0), c1 = run.holder(u0 + t.slices - 1);
+  // of one row tile, each CTA holds two parts (one per softmax group)
+  const int subs = S::kGroups == 2 && R - rt * S::kRows <= kRowTile ? 2 : 1;
+  const int parts = (c1 - c0 + 1) * subs;
+#pragma unroll 2
+  for (int x = threadIdx.x; x < kJoinRows * (D / 4); x += kJoinThreads) {
+    const int r = x / (D / 4), c4 = x % (D / 4), row = row0 + r;
+    if (row >= R) break;
+    auto part = [&](int k) {
+      const int c = c0 + (subs == 2 ? k >> 1 : k), sub = subs == 2 ? k & 1 : 0;
+      return (long long)(2 * c + (run.start(c) <= u0 ? 1 : 0)) * S::kRows + slab * kJoinRows + r +
+             sub * kRowTile;
+    };
+    join_row<D>(p, s, h, row, c4, parts, part);
+  }
 }
 
 // ================================================================= host side
@@ -801,17 +899,17 @@ size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct Plan {
   int rows, rts;
-  size_t arrived, parts, stats, bytes;
+  size_t cut, parts, stats, bytes;
 };
 
 Plan plan_chunk(const Cache& c, const Batch& b, int G, int sms) {
   Plan pl;
   pl.rows = c.D == 256 ? Shape<256>::kRows : Shape<128>::kRows;
   pl.rts = (int)(((long long)b.max_new * G + pl.rows - 1) / pl.rows);
-  pl.arrived = up256((size_t)b.B * c.H * pl.rts * 4);
-  pl.parts = up256((size_t)2 * sms * pl.rows * c.D * 4);
-  pl.stats = up256((size_t)2 * sms * pl.rows * 8);
-  pl.bytes = pl.arrived + pl.parts + pl.stats;
+  pl.cut = up256(((size_t)b.B * c.H * pl.rts + 2) * 8);
+  pl.parts = up256((size_t)4 * sms * pl.rows * c.D * 4);
+  pl.stats = up256((size_t)4 * sms * pl.rows * 8);
+  pl.bytes = pl.cut + pl.parts + pl.stats;
   return pl;
 }
 
@@ -839,7 +937,12 @@ w4_status launch_chunk(ChunkParams& p, int sms, int dev, bool pdl, w4_stream_t s
     note_cuda_error(cudaErrorInvalidValue);
     return W4_ERR_LAUNCH;
   }
-  return launch(attn_chunk_kernel<D>, dim3((unsigned)sms), S::kThreads, S::kSmem, pdl, stream, p);
+  const w4_status st =
+      launch(attn_chunk_kernel<D>, dim3((unsigned)sms), S::kThreads, S::kSmem, pdl, stream, p);
+  if (st != W4_OK) return st;
+  return launch(attn_join_kernel<D>,
+                dim3((unsigned)(p.rts * (S::kRows / kJoinRows)), (unsigned)p.c.H, (unsigned)p.bt.B),
+                kJoinThreads, 0, true, stream, p);
 }
 
 }  // namespace
@@ -858,9 +961,9 @@ w4_status chunk_attn(const Cache& c, const Batch& b, const ChunkArgs& a, void* w
   const Plan pl = plan_chunk(c, b, p.G, sms);
   p.rts = pl.rts;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.arrived = reinterpret_cast<int32_t*>(ws);
-  p.parts = reinterpret_cast<float*>(ws + pl.arrived);
-  p.part_stats = reinterpret_cast<float*>(ws + pl.arrived + pl.parts);
+  p.cut = reinterpret_cast<long long*>(ws);
+  p.parts = reinterpret_cast<float*>(ws + pl.cut);
+  p.part_stats = reinterpret_cast<float*>(ws + pl.cut + pl.parts);
   switch (c.D) {
     case 64: return launch_chunk<64>(p, sms, dev, pdl, stream);
     case 128: return launch_chunk<128>(p, sms, dev, pdl, stream);
