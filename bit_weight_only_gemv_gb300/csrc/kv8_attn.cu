@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
           bool none = false;
           // the first CTA's part began the unit, the others' run began inside it
           for (int c = c0; c <= c1; ++c) {
-            const int sl = 2 * c + (run.start(c) <= u0 ? 1 : 0);
+            const int sl = c == c0 ? 2 * c + 1 : 2 * c;
             const float2 st = __ldcg(reinterpret_cast<const float2*>(p.part_stats) +
                                      (long long)sl * kRows + r);
             M = fmaxf(M, st.x);
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
           float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
           for (int c = c0; c <= c1; ++c) {
-            const int sl = 2 * c + (run.start(c) <= u0 ? 1 : 0);
+            const int sl = c == c0 ? 2 * c + 1 : 2 * c;
             const float2 st = __ldcg(reinterpret_cast<const float2*>(p.part_stats) +
                                      (long long)sl * kRows + r);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(
@@ -587,60 +587,6 @@ w4_status launch_token(const AttnParams& p, int ctas, bool pdl, w4_stream_t stre
   }
   return launch(attn_token_kernel<D, NQ>, dim3((unsigned)ctas), kThreads, Shape<D, NQ>::kSmem, pdl,
                 stream, p);
-}
-
-struct WeighParams {
-  Cache c;
-  Batch bt;
-  const __nv_bfloat16* q;
-  long long q_stride;
-  const float* lse;
-  int Hq, G;
-  float scale;
-  int window;
-  int32_t* status;
-};
-
-// One CTA per (page, head, sequence), one warp per token in turn.
-__global__ void __launch_bounds__(128) weigh_simple_kernel(const WeighParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lp = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int P = p.c.P, D = p.c.D, per = D / 32;
-  const Seq s = sequence(p.bt, P, b);
-  if (!s.ok) {
-    if (threadIdx.x == 0 && lp == 0) report(p.status, W4_ERR_INDEX);
-    return;
-  }
-  if (lp * P >= s.len) return;
-  const int page = __ldg(p.bt.table + (long long)b * p.bt.max_pages + lp);
-  if (page < 0 || page >= p.c.num_pages) {
-    if (threadIdx.x == 0) report(p.status, W4_ERR_INDEX);
-    return;
-  }
-  const float ks = p.c.ks[p.c.pair(page, h)];
-  const uint8_t* kc = p.c.kc + p.c.block(page, h);
-  for (int t = warp; t < P && lp * P + t < s.len; t += 4) {
-    const int kp = lp * P + t;
-    float sum = 0.0f;
-    for (int r = 0; r < s.n; ++r) {
-      const int pos = s.len - s.n + r;
-      if (kp > pos || (p.window > 0 && kp <= pos - p.window)) continue;
-      for (int g = 0; g < p.G; ++g) {
-        const __nv_bfloat16* q = p.q + (s.row0 + r) * p.q_stride + (long long)(h * p.G + g) * D;
-        float dot = 0.0f;
-        for (int d = 0; d < per; ++d)
-          dot += __bfloat162float(q[lane + 32 * d]) *
-                 (float)((int)kc[(long long)t * D + lane + 32 * d] - 128);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const float l = p.lse[(long long)(s.row0 + r) * p.Hq + h * p.G + g];
-        if (l != -INFINITY) sum += expf(dot * ks * p.scale - l);
-      }
-    }
-    if (lane == 0) p.c.weight[p.c.pair(page, h) * P + t] += sum;
-  }
 }
 
 }  // namespace
@@ -744,30 +690,4 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
     case 256 * 4 + 1: return kv8::launch_token<256, 1>(p, pl.ctas, pdl, stream, dev);
     default: return kv8::launch_token<256, 2>(p, pl.ctas, pdl, stream, dev);
   }
-}
-
-extern "C" w4_status w4_kv8_weigh(const void* q, size_t q_row_stride, int q_heads,
-                                  const float* lse, const w4_kv8_cache* cache,
-                                  const w4_kv8_batch* batch, float scale, int window,
-                                  int32_t* status_dev, unsigned flags, w4_stream_t stream) {
-  kv8::WeighParams p = {};
-  w4_status st = kv8::view(cache, batch, &p.c, &p.bt);
-  if (st != W4_OK) return st;
-  if (lse == nullptr || p.c.weight == nullptr || (flags & ~W4_FLAG_PDL) != 0 || window < 0)
-    return W4_ERR_ARG;
-  if ((st = kv8::check_q(q, q_row_stride, q_heads, p.c)) != W4_OK) return st;
-  if (kv8::misaligned(lse, 4)) return W4_ERR_ALIGN;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.q_stride = (long long)q_row_stride;
-  p.lse = lse;
-  p.Hq = q_heads;
-  p.G = q_heads / p.c.H;
-  p.scale = scale;
-  p.window = window;
-  p.status = status_dev;
-  const int pages = (p.bt.max_len + p.c.P - 1) / p.c.P;
-  if (pages == 0) return W4_OK;
-  return kv8::launch(kv8::weigh_simple_kernel,
-                     dim3((unsigned)pages, (unsigned)p.c.H, (unsigned)p.bt.B), 128, 0,
-                     (flags & W4_FLAG_PDL) != 0, stream, p);
 }

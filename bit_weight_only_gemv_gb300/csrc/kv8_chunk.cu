@@ -887,7 +887,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     if (row >= R) break;
     auto part = [&](int k) {
       const int c = c0 + (subs == 2 ? k >> 1 : k), sub = subs == 2 ? k & 1 : 0;
-      return (long long)(2 * c + (run.start(c) <= u0 ? 1 : 0)) * S::kRows + slab * kJoinRows + r +
+      // the first CTA's part began the unit, the others' runs began inside it
+      return (long long)(c == c0 ? 2 * c + 1 : 2 * c) * S::kRows + slab * kJoinRows + r +
              sub * kRowTile;
     };
     join_row<D>(p, s, h, row, c4, parts, part);

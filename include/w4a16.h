@@ -812,7 +812,9 @@ size_t w4_kv8_select_workspace_bytes(const w4_kv8_cache *cache, const w4_kv8_bat
  *   weight[t] += sum over rows r that see t and heads i of the group of
  *                exp(scale q_ri.key[t] - lse[r][i])
  * lse as written by w4_kv8_attn for the same rows (a row with lse = -inf
- * adds nothing).  flags: W4_FLAG_PDL.
+ * adds nothing).  A page id that is none leaves out its own tokens only.  A
+ * page belongs to one sequence of the call (two would race on its weights).
+ * flags: W4_FLAG_PDL.
  */
 w4_status w4_kv8_weigh(const void *q, size_t q_row_stride, int q_heads, const float *lse,
                        const w4_kv8_cache *cache, const w4_kv8_batch *batch, float scale,
