@@ -50,14 +50,14 @@ constexpr float kPass = 60.0f;        // log2 of how far a score may pass m
 constexpr float kFar = 1152921504606846976.0f;   // 2^60
 constexpr float kRound = 1.0f + 0.72f / 2048.0f;
 constexpr int kRowTile = 128;
-constexpr int kRawStages = 2;
-constexpr int kMetaRing = 8;
-constexpr int kMinTiles = 2;          // key tiles of a CTA's run
+constexpr int kKeys = 64;             // keys of a tile
+constexpr int kMetaRing = 16;         // tiles described ahead of their softmax
+constexpr int kUnitRing = 32;         // units of which a refusal is remembered
+constexpr int kMinTiles = 4;          // key tiles of a CTA's run
 
 template <int D>
 struct Shape {
   static constexpr int kGroups = D == 256 ? 1 : 2;   // softmax groups (and O accumulators)
-  static constexpr int kKeys = D == 256 ? 64 : 128;  // keys of a tile
   static constexpr int kRows = kRowTile * kGroups;   // query rows of a unit
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kConvWarp = kSoftWarps;
@@ -66,35 +66,47 @@ struct Shape {
   static constexpr int kCopyWarp = kMmaWarp + 1;
   static constexpr int kWarps = kCopyWarp + 1;
   static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kBuf = D == 256 ? 1 : 2;      // expanded tiles of K, and of V
+  static constexpr int kRaw = D == 256 ? 2 : 4;      // copied tiles of K, and of V
   static constexpr int kQTile = kRowTile * D * 2;    // bytes
+  static constexpr int kKTile = kKeys * D * 2;
+  static constexpr int kVTile = kKeys * D * 4;
+  static constexpr int kRawTile = kKeys * D;
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + kGroups * kQTile;
-  static constexpr int kV = kK + kKeys * D * 2;
-  static constexpr int kRaw = kV + kKeys * D * 4;
-  static constexpr int kRawBytes = 2 * kKeys * D;    // keys, then values
-  static constexpr int kMeta = kRaw + kRawStages * kRawBytes;   // [kMetaRing][8] (ks, vs)
-  static constexpr int kBars = kMeta + kMetaRing * 8 * 8;
-  static constexpr int kMisc = kBars + 32 * 8;
+  static constexpr int kV = kK + kBuf * kKTile;
+  static constexpr int kRawK = kV + kBuf * kVTile;
+  static constexpr int kRawV = kRawK + kRaw * kRawTile;
+  static constexpr int kMeta = kRawV + kRaw * kRawTile;   // [kMetaRing][4] (ks, vs) of 16 keys
+  static constexpr int kPages = kMeta + kMetaRing * 4 * 8;  // [kMetaRing][4]
+  static constexpr int kBars = kPages + kMetaRing * 4 * 4;
+  static constexpr int kMisc = kBars + 40 * 8;
+  static constexpr int kEnd = kMisc + 384 + 1024;
   // more than half an SM's: each CTA holds all of its tensor memory
-  static constexpr int kSmem = kMisc + 256 + 1024 > 117248 ? kMisc + 256 + 1024 : 117248;
+  static constexpr int kSmem = kEnd > 117248 ? kEnd : 117248;
   static_assert(kSmem <= 232448 && 2 * kSmem > 232448, "shared memory");
-  // tensor memory columns
-  static constexpr int kSCol = 0, kOCol = 2 * kKeys;
+  // tensor memory columns: S (and P) regions of a tile, then O
+  static constexpr int kRegions = 2 * kGroups;
+  static constexpr int kOCol = kRegions * kKeys;
   static_assert(kOCol + kGroups * D <= 512, "tensor memory");
 };
 
 // barriers
 enum {
-  kRawFull = 0,    // [2]
-  kRawEmpty = 2,   // [2]
-  kQReady = 4, kQFree, kKReady, kKFree,
-  kVReady = 8,     // [2] by half of the tile's keys
-  kVFree = 10,     // [2]
-  kSFull = 12,     // [2] by S region
-  kPFull = 14,     // [2]
-  kODone = 16,     // [2] by group
-  kOFree = 18,     // [2]
-  kEpi = 20,
+  kRawKFull = 0,   // [4] by stage
+  kRawKEmpty = 4,
+  kRawVFull = 8,
+  kRawVEmpty = 12,
+  kQReady = 16, kQFree,
+  kKReady = 18,    // [2] by buffer
+  kKFree = 20,
+  kVReady = 22,
+  kVFree = 24,
+  kSFull = 26,     // [4] by S region
+  kPFull = 30,
+  kODone = 34,     // [2] by group
+  kOFree = 36,
+  kEpi = 38,
   kBarCount
 };
 
@@ -126,7 +138,7 @@ __device__ __forceinline__ long long entry_tiles(const ChunkParams& p, int b) {
   using S = Shape<D>;
   const Seq s = sequence(p.bt, p.c.P, b);
   if (!s.ok || s.n == 0) return 0;
-  return head_slices(s, p.G, p.a.window, S::kRows, S::kKeys) * p.c.H;
+  return head_slices(s, p.G, p.a.window, S::kRows, kKeys) * p.c.H;
 }
 
 // Walks the units of a run; every role walks alike.
@@ -142,14 +154,14 @@ __device__ __noinline__ bool next_unit(const ChunkParams& p, const Run& run, Wal
   u.b = w.entry;
   u.s = sequence(p.bt, p.c.P, u.b);
   u.R = u.s.n * p.G;
-  const long long per = head_slices(u.s, p.G, p.a.window, S::kRows, S::kKeys);
+  const long long per = head_slices(u.s, p.G, p.a.window, S::kRows, kKeys);
   u.h = (int)(w.off / per);
   long long rem = w.off - per * u.h;
   u.rt = 0;
-  u.t = tile_of(u.s, p.G, p.a.window, 0, S::kRows, S::kKeys);
+  u.t = tile_of(u.s, p.G, p.a.window, 0, S::kRows, kKeys);
   while (rem >= u.t.slices) {
     rem -= u.t.slices;
-    u.t = tile_of(u.s, p.G, p.a.window, ++u.rt, S::kRows, S::kKeys);
+    u.t = tile_of(u.s, p.G, p.a.window, ++u.rt, S::kRows, kKeys);
   }
   u.rows = min(S::kRows, u.R - u.rt * S::kRows);
   u.i0 = (int)rem;
@@ -200,30 +212,30 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
          (1ull << 46) | (2ull << 61);
 }
 
-// The whole warp runs the issuing code, so that addresses and descriptors stay
-// in uniform registers; `leader` (one lane) issues.
+// The whole warp runs the issuing code and one elected lane issues: in uniform
+// code the operands stay in uniform registers and an MMA takes a few
+// instructions; under a branch on the lane it takes about twenty.
 __device__ __forceinline__ void mma_ss_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t acc, uint32_t leader) {
+                                           uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t acc, uint32_t leader) {
+                                            uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar, uint32_t leader) {
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          bar),
-      "r"(leader)
+          bar)
       : "memory");
 }
 
@@ -274,20 +286,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
-// 2^(x factor - m) in place, 0 where a row sees no key (cut: some row does not
-// see some of the keys t0 .. t0 + 31); returns the sum.
-__device__ __forceinline__ float weights(float* x, float f0, float f1, float m, bool cut, int t0,
-                                         int pos, int window) {
+// Bit e: column e of 32 is one of lo .. hi.  Opaque, so that the compiler
+// leaves the tests of its bits where they are: in blocks that few tiles enter.
+__device__ __forceinline__ uint32_t columns(int lo, int hi) {
+  uint32_t v = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1u;
+  if (lo > 0) v &= lo > 31 ? 0u : ~0u << lo;
+  asm volatile("" : "+r"(v));
+  return v;
+}
+
+// 2^(x factor - m) in place, 0 for the columns outside lo .. hi (cut: there
+// are some in the warp's rows); returns the sum.
+__device__ __forceinline__ float weights(float* x, float f0, float f1, float m, bool cut, int lo,
+                                         int hi) {
   const uint64_t a0 = pack2(f0, f0), a1 = pack2(f1, f1), c = pack2(-m, -m);
 #pragma unroll
   for (int e = 0; e < 32; e += 2)
     unpack2(fma2(pack2(x[e], x[e + 1]), e < 16 ? a0 : a1, c), x[e], x[e + 1]);
   if (cut) {
+    const uint32_t seen = columns(lo, hi);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const int t = t0 + e;
-      if (t > pos || (window > 0 && t <= pos - window)) x[e] = -INFINITY;
-    }
+    for (int e = 0; e < 32; ++e)
+      if (!(seen >> e & 1u)) x[e] = -INFINITY;
   }
   uint64_t s0 = 0, s1 = 0;   // two sums of pairs
 #pragma unroll
@@ -327,12 +347,19 @@ __device__ __forceinline__ uint2 pack_bf16x4(const float* v, float f) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// A waiting position on a barrier: the parity of its next phase.
-struct Phase {
-  uint32_t n = 0;
-  __device__ __forceinline__ uint32_t next() { return n++ & 1u; }        // completions awaited in turn
-  __device__ __forceinline__ uint32_t before() { return (n++ & 1u) ^ 1u; }  // first one passes at once
+// A constant as an argument.
+template <int N>
+struct Const {
+  static constexpr int value = N;
+  __device__ __forceinline__ constexpr operator int() const { return N; }
 };
+
+// Parity of the n-th use (from 0) of a ring of N barriers, and of the use
+// before it (the first passes at once).
+template <int N>
+__device__ __forceinline__ uint32_t use(uint32_t n) { return (n / N) & 1u; }
+template <int N>
+__device__ __forceinline__ uint32_t before(uint32_t n) { return ((n / N) & 1u) ^ 1u; }
 
 // Four channels of one row from its parts, in order: part(k) is the row's
 // place in the k-th.
@@ -372,7 +399,7 @@ template <int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     attn_chunk_kernel(const __grid_constant__ ChunkParams p) {
   using S = Shape<D>;
-  constexpr int kKeys = S::kKeys, kGroups = S::kGroups;
+  constexpr int kGroups = S::kGroups, kBuf = S::kBuf, kRaw = S::kRaw;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* sm = smem_raw + pad;
@@ -383,27 +410,19 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   float2* meta = reinterpret_cast<float2*>(sm + S::kMeta);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kMisc + 4);
-  volatile int* refused = reinterpret_cast<volatile int*>(sm + S::kMisc + 16);   // [8] by unit
-  long long* scan = reinterpret_cast<long long*>(sm + S::kMisc + 64);
+  volatile int* refused = reinterpret_cast<volatile int*>(sm + S::kMisc + 16);   // [kUnitRing]
+  long long* scan = reinterpret_cast<long long*>(sm + S::kMisc + 16 + 4 * kUnitRing);
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kRawFull + i), 1);
-      mbar_init(bar(kRawEmpty + i), S::kConvWarps);
-      mbar_init(bar(kVReady + i), S::kConvWarps);
-      mbar_init(bar(kVFree + i), 1);
-      mbar_init(bar(kSFull + i), 1);
-      mbar_init(bar(kPFull + i), 4);
-      mbar_init(bar(kODone + i), 1);
-      mbar_init(bar(kOFree + i), 4);
+    for (int i = 0; i < kBarCount; ++i) {
+      const bool conv = (i >= kRawKEmpty && i < kRawVFull) || i == kQReady ||
+                        (i >= kRawVEmpty && i < kQReady) || i == kKReady || i == kKReady + 1 ||
+                        i == kVReady || i == kVReady + 1;
+      const bool soft = (i >= kPFull && i < kODone) || i == kOFree || i == kOFree + 1;
+      mbar_init(bar(i), conv ? S::kConvWarps : soft ? 4 : i == kEpi ? S::kSoftWarps : 1);
     }
-    mbar_init(bar(kQReady), S::kConvWarps);
-    mbar_init(bar(kQFree), 1);
-    mbar_init(bar(kKReady), S::kConvWarps);
-    mbar_init(bar(kKFree), 1);
-    mbar_init(bar(kEpi), S::kSoftWarps);
     *abort_flag = 0;
-    for (int i = 0; i < 8; ++i) refused[i] = 0;
+    for (int i = 0; i < kUnitRing; ++i) refused[i] = 0;
     mbar_init_fence();
   }
   if (warp == S::kMmaWarp) {
@@ -432,122 +451,165 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 
   if (warp == S::kCopyWarp) {
     // ------------------------------------------------------------- pages
+    // Tiles of K run two ahead of those of V, as they are needed.
     const int box = min(p.c.P, kKeys);   // tokens of one copy
     const int boxes = kKeys / box;
-    Phase empty[kRawStages];
-    int st = 0, serial = 0, unit = 0;
-    for (; ok && next_unit<D>(p, run, walk, u); ++unit) {
+    int* pages = reinterpret_cast<int*>(sm + S::kPages);
+    uint32_t nk = 0, nv = 0;             // tiles copied
+    for (int unit = 0; ok && next_unit<D>(p, run, walk, u); ++unit) {
       const int32_t* table = p.bt.table + (long long)u.b * p.bt.max_pages;
-      for (int i = u.i0; i < u.i1; ++i, ++serial) {
-        if (!wait_bar(bar(kRawEmpty + st), empty[st].before(), abort_flag)) {
-          ok = false;
-          break;
-        }
-        const int tok = u.t.lo + i * kKeys + lane * box;
-        const bool want = lane < boxes && tok < u.t.hi;
+      const int n = u.tiles();
+      auto copy = [&](bool keys, int i, uint32_t serial) {
+        const int full = keys ? kRawKFull : kRawVFull, st = serial % kRaw;
+        if (!wait_bar(bar((keys ? kRawKEmpty : kRawVEmpty) + st), before<kRaw>(serial), abort_flag))
+          return false;
+        const int tok = u.t.lo + (u.i0 + i) * kKeys + lane * box;
+        const int at = (serial % kMetaRing) * 4 + lane * (box / 16);
         int page = -1;
-        if (want) {
-          page = __ldg(table + tok / p.c.P);
-          if (page < 0 || page >= p.c.num_pages) {
-            page = -1;
-            refused[unit & 7] = 1;
+        if (lane < boxes) {
+          if (!keys) {
+            page = pages[at];
+          } else {
+            float2 m = make_float2(0.0f, 0.0f);
+            if (tok < u.t.hi) {
+              page = __ldg(table + tok / p.c.P);
+              if (page < 0 || page >= p.c.num_pages) {
+                page = -1;
+                refused[unit % kUnitRing] = 1;
+              } else {
+                m = make_float2(p.c.ks[p.c.pair(page, u.h)], p.c.vs[p.c.pair(page, u.h)]);
+              }
+            }
+            for (int e = 0; e < box / 16; ++e) meta[at + e] = m;
+            pages[at] = page;
           }
         }
-        if (lane < boxes) {
-          float2 m = make_float2(0.0f, 0.0f);
-          if (page >= 0) m = make_float2(p.c.ks[p.c.pair(page, u.h)], p.c.vs[p.c.pair(page, u.h)]);
-          for (int e = 0; e < box / 16; ++e) meta[(serial & 7) * 8 + lane * (box / 16) + e] = m;
-        }
-        const int n = __popc(__ballot_sync(0xffffffffu, page >= 0));
+        const int c = __popc(__ballot_sync(0xffffffffu, page >= 0));
         if (lane == 0) {
-          if (n > 0) mbar_arrive_expect_tx(bar(kRawFull + st), (uint32_t)(n * box * 2 * D));
-          else mbar_arrive(bar(kRawFull + st));
+          if (c > 0) mbar_arrive_expect_tx(bar(full + st), (uint32_t)(c * box * D));
+          else mbar_arrive(bar(full + st));
         }
         __syncwarp();
         if (page >= 0) {
-          const uint32_t dst = sb + S::kRaw + st * S::kRawBytes;
-          const int row = tok % p.c.P;
+          const uint32_t dst = sb + (keys ? S::kRawK : S::kRawV) + st * S::kRawTile;
 #pragma unroll
-          for (int x = 0; x < D; x += 128) {
-            const uint32_t o = x * kKeys + lane * box * (D < 128 ? D : 128);
-            tma_4d(dst + o, &p.tm_k, x, row, u.h, page, bar(kRawFull + st));
-            tma_4d(dst + kKeys * D + o, &p.tm_v, x, row, u.h, page, bar(kRawFull + st));
-          }
+          for (int x = 0; x < D; x += 128)
+            tma_4d(dst + x * kKeys + lane * box * (D < 128 ? D : 128), keys ? &p.tm_k : &p.tm_v, x,
+                   tok % p.c.P, u.h, page, bar(full + st));
         }
         __syncwarp();
-        st ^= 1;
+        return true;
+      };
+      ok = copy(true, 0, nk++);
+      if (ok && n > 1) ok = copy(true, 1, nk++);
+      for (int i = 0; ok && i < n; ++i) {
+        ok = copy(false, i, nv++);
+        if (ok && i + 2 < n) ok = copy(true, i + 2, nk++);
       }
     }
-    // the last copies land before the CTA may leave
-    if (!ok)
-      for (int i = 0; i < kRawStages; ++i)
-        mbar_wait_bounded(bar(kRawFull + i), (empty[i].n + 1) & 1u, kWaitCycles >> 4);
+    // after a failure: what is in flight lands before the CTA leaves
+    if (!ok) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < (1 << 20)) {
+      }
+    }
   } else if (warp == S::kMmaWarp) {
     // -------------------------------------------------------- MMA issuer
     constexpr uint32_t kDescS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kKeys >> 3) << 17) |
                                 ((uint32_t)(kRowTile >> 4) << 24);
     constexpr uint32_t kDescO = (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(D >> 3) << 17) |
                                 ((uint32_t)(kRowTile >> 4) << 24);
-    Phase q_ready, k_ready, v_ready[2], p_full[2], o_free[2];
-    bool issued = false;
-    uint32_t freed = 0;   // commits on the second half's kVFree
-    const uint32_t leader = lane == 0;
+    // The jobs of a unit go round in steps whose S region, K and V buffers and
+    // row tile are compile-time constants: the descriptors are then a uniform
+    // base plus constants, and an MMA issues in a few instructions.
     const uint64_t dq = desc_sw128(sb + S::kQ), dk = desc_sw128(sb + S::kK), dv = desc_sw128(sb + S::kV);
-    while (ok && next_unit<D>(p, run, walk, u)) {
+    uint32_t units = 0;
+    uint32_t k_par = 0, v_par = 0, p_par = 0, o_par = 0;   // next parity of each barrier
+    int last_buf = -1;                                     // of the last commit on kVFree
+    auto take = [&](uint32_t& mask, int i) {
+      const uint32_t p = (mask >> i) & 1u;
+      mask ^= 1u << i;
+      return p;
+    };
+    for (; ok && next_unit<D>(p, run, walk, u); ++units) {
       const bool two = kGroups == 2 && u.rows > kRowTile;   // two row tiles
       const int jobs = two ? 2 * u.tiles() : u.tiles();
-      if (!wait_bar(bar(kQReady), q_ready.next(), abort_flag)) {
+      if (!wait_bar(bar(kQReady), use<1>(units), abort_flag)) {
         ok = false;
         break;
       }
-      // S of job j: key tile j (j / 2 of two row tiles), S region j % 2
-      auto scores = [&](int j) {
-        const bool first = !two || (j & 1) == 0, last = !two || (j & 1) == 1;
-        if (first && !wait_bar(bar(kKReady), k_ready.next(), abort_flag)) return false;
+      // S of a job: key tile in buffer kB, row tile kT, into region kR
+      auto scores = [&](auto kR, auto kB, auto kT, bool first, bool last, bool end) {
+        if (first && !wait_bar(bar(kKReady + kB), take(k_par, kB), abort_flag)) return false;
         tc_fence_after();
-        const uint64_t a0 = dq + (two ? (j & 1) * (S::kQTile / 16) : 0);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss_f16(tmem + S::kSCol + (j & 1) * kKeys,
-                     a0 + (k >> 2) * (kRowTile * 128 / 16) + (k & 3) * 2,
-                     dk + (k >> 2) * (kKeys * 128 / 16) + (k & 3) * 2, kDescS, k > 0, leader);
-        commit(bar(kSFull + (j & 1)), leader);
-        if (last) commit(bar(kKFree), leader);
-        if (j == jobs - 1) commit(bar(kQFree), leader);
-        issued = true;
+          mma_ss_f16(tmem + kR * kKeys,
+                     dq + kT * (S::kQTile / 16) + (k >> 2) * (kRowTile * 128 / 16) + (k & 3) * 2,
+                     dk + kB * (S::kKTile / 16) + (k >> 2) * (kKeys * 128 / 16) + (k & 3) * 2, kDescS,
+                     k > 0);
+        mma_commit(bar(kSFull + kR));
+        if (last) mma_commit(bar(kKFree + kB));
+        if (end) mma_commit(bar(kQFree));
         return true;
       };
-      ok = scores(0) && (jobs < 2 || scores(1));
-      for (int j = 0; ok && j < jobs; ++j) {
-        const int r = j & 1, grp = kGroups == 2 ? r : 0;
-        const bool first = !two || r == 0, last = !two || r == 1;
-        if ((j < kGroups && !wait_bar(bar(kOFree + grp), o_free[grp].before(), abort_flag)) ||
-            !wait_bar(bar(kPFull + r), p_full[r].next(), abort_flag)) {
-          ok = false;
-          break;
-        }
+      // O of a job: weights in region kR, value tile in buffer kB, group kG
+      auto values = [&](auto kR, auto kB, auto kG, bool begin, bool first, bool last) {
+        if (begin && !wait_bar(bar(kOFree + kG), take(o_par, kG) ^ 1u, abort_flag)) return false;
+        if (first && !wait_bar(bar(kVReady + kB), take(v_par, kB), abort_flag)) return false;
+        if (!wait_bar(bar(kPFull + kR), take(p_par, kR), abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t acc = begin ? 0u : 1u;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (first && !wait_bar(bar(kVReady + half), v_ready[half].next(), abort_flag)) ok = false;
-          tc_fence_after();
-          if (!ok) break;
-#pragma unroll
-          for (int k = half * (kKeys / 16); k < (half + 1) * (kKeys / 16); ++k)
-            mma_ts_tf32(tmem + S::kOCol + grp * D, tmem + S::kSCol + r * kKeys + 8 * k,
-                        dv + (k >> 2) * (D * 128 / 16) + (k & 3) * 2, kDescO, j >= kGroups || k > 0,
-                        leader);
-          if (half == 1) commit(bar(kODone + grp), leader);
-          if (last) commit(bar(kVFree + half), leader);
-        }
-        if (!ok) break;
-        if (last) ++freed;
-        if (j + 2 < jobs) ok = scores(j + 2);
+        for (int k = 0; k < kKeys / 8; ++k)
+          mma_ts_tf32(tmem + S::kOCol + kG * D, tmem + kR * kKeys + 8 * k,
+                      dv + kB * (S::kVTile / 16) + (k >> 2) * (D * 128 / 16) + (k & 3) * 2, kDescO,
+                      k > 0 ? 1u : acc);
+        mma_commit(bar(kODone + kG));
+        if (last) mma_commit(bar(kVFree + kB));
+        if (last) last_buf = kB;
+        return true;
+      };
+      if (two) {
+        // job j: key tile j / 2, row tile (and group) j % 2, region j % 4; scores four ahead
+        auto step = [&](auto kZ, int j, int at) {   // at: the job whose scores, or weights
+          constexpr int z = decltype(kZ)::value;
+          using R = Const<z>;
+          using B = Const<(z >> 1) % kBuf>;
+          using T = Const<z & 1>;
+          if (at >= jobs) return true;
+          if (j < 0) return scores(R(), B(), T(), (z & 1) == 0, (z & 1) == 1, at == jobs - 1);
+          return values(R(), B(), T(), at < 2, (z & 1) == 0, (z & 1) == 1);
+        };
+        ok = step(Const<0>(), -1, 0) && step(Const<1>(), -1, 1) && step(Const<2>(), -1, 2) &&
+             step(Const<3>(), -1, 3);
+        for (int j = 0; ok && j < jobs; j += 4)
+          ok = step(Const<0>(), 0, j) && step(Const<0>(), -1, j + 4) && step(Const<1>(), 0, j + 1) &&
+               step(Const<1>(), -1, j + 5) && step(Const<2>(), 0, j + 2) &&
+               step(Const<2>(), -1, j + 6) && step(Const<3>(), 0, j + 3) &&
+               step(Const<3>(), -1, j + 7);
+      } else {
+        // job j: key tile j, region j % 2; scores two ahead
+        auto step = [&](auto kZ, int j, int at) {
+          constexpr int z = decltype(kZ)::value;
+          using R = Const<z>;
+          using B = Const<z % kBuf>;
+          using G = Const<z % kGroups>;
+          if (at >= jobs) return true;
+          if (j < 0) return scores(R(), B(), Const<0>(), true, true, at == jobs - 1);
+          return values(R(), B(), G(), at < kGroups, true, true);
+        };
+        ok = step(Const<0>(), -1, 0) && step(Const<1>(), -1, 1);
+        for (int j = 0; ok && j < jobs; j += 2)
+          ok = step(Const<0>(), 0, j) && step(Const<0>(), -1, j + 2) && step(Const<1>(), 0, j + 1) &&
+               step(Const<1>(), -1, j + 3);
       }
     }
     // the last commits land before the CTA may leave
     if (ok) {
-      if (freed > 0) mbar_wait_bounded(bar(kVFree + 1), (freed - 1) & 1u, kWaitCycles);
-    } else if (issued) {
+      if (last_buf >= 0)
+        mbar_wait_bounded(bar(kVFree + last_buf), ((v_par >> last_buf) & 1u) ^ 1u, kWaitCycles);
+    } else {
       const long long t0 = clock64();
       while (clock64() - t0 < (1 << 20)) {
       }
@@ -555,112 +617,115 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   } else if (warp >= S::kConvWarp) {
     // ---------------------------------------------------------- expansion
     const int w = warp - S::kConvWarp, ct = tid - 32 * S::kConvWarp;
-    Phase q_free, k_free, v_free[2], raw_full[kRawStages];
-    int st = 0;
-    while (ok && next_unit<D>(p, run, walk, u)) {
-      if (!wait_bar(bar(kQFree), q_free.before(), abort_flag)) {
+    uint32_t nk = 0, nv = 0;             // tiles expanded
+    uint32_t kf_par = 3, vf_par = 3;     // next parity of each kKFree, kVFree (the first passes at once)
+    for (uint32_t units = 0; ok && next_unit<D>(p, run, walk, u); ++units) {
+      if (!wait_bar(bar(kQFree), before<1>(units), abort_flag)) {
         ok = false;
         break;
       }
       // query rows as they are; rows past the unit's are zero
-      const int tiles = u.rows > kRowTile ? 2 : 1;
-#pragma unroll 4
-      for (int x = ct; x < tiles * kRowTile * (D / 8); x += 32 * S::kConvWarps) {
+      const int qtiles = u.rows > kRowTile ? 2 : 1;
+      for (int x = ct; x < qtiles * kRowTile * (D / 8); x += 32 * S::kConvWarps) {
         const int r = x / (D / 8), ch = x % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < u.rows) {
-          const int row = u.rt * S::kRows + r;
-          v = __ldg(reinterpret_cast<const uint4*>(
-              p.a.q + (long long)(u.s.row0 + row / p.G) * p.a.q_stride +
-              (long long)(u.h * p.G + row % p.G) * D + ch * 8));
-        }
-        sts128(sb + S::kQ + (r >> 7) * S::kQTile + (ch >> 3) * (kRowTile * 128) + (r & 127) * 128 +
-                   (((ch & 7) ^ (r & 7)) << 4),
-               v.x, v.y, v.z, v.w);
+        const int row = u.rt * S::kRows + min(r, u.rows - 1);
+        const uint32_t dst = sb + S::kQ + (r >> 7) * S::kQTile + (ch >> 3) * (kRowTile * 128) +
+                             (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+        const __nv_bfloat16* src = p.a.q + (long long)(u.s.row0 + row / p.G) * p.a.q_stride +
+                                   (long long)(u.h * p.G + row % p.G) * D + ch * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                     "r"(r < u.rows ? 16 : 0)
+                     : "memory");
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kQReady));
-      for (int i = u.i0; i < u.i1; ++i) {
-        const uint32_t rawk = sb + S::kRaw + st * S::kRawBytes, rawv = rawk + kKeys * D;
-        if (!wait_bar(bar(kRawFull + st), raw_full[st].next(), abort_flag) ||
-            !wait_bar(bar(kKFree), k_free.before(), abort_flag)) {
-          ok = false;
-          break;
-        }
-        // keys: 8 rows by 4 chunks of 16 codes at a time (no bank conflicts
-        // on either side), 32 bytes of bf16 each
-#pragma unroll 2
-        for (int r8 = w; r8 < kKeys / 8; r8 += S::kConvWarps) {
-          const int row = 8 * r8 + (lane & 7);
+
+      // keys: 8 rows by 4 chunks of 16 codes at a time (no bank conflicts on
+      // either side), 32 bytes of bf16 each
+      auto keys = [&](int i) {
+        const uint32_t st = nk % kRaw, buf = i % kBuf;
+        if (!wait_bar(bar(kRawKFull + st), use<kRaw>(nk), abort_flag) ||
+            !wait_bar(bar(kKFree + buf), (kf_par >> buf) & 1u, abort_flag))
+          return false;
+        kf_par ^= 1u << buf;
+        const uint32_t raw = sb + S::kRawK + st * S::kRawTile, to0 = sb + S::kK + buf * S::kKTile;
 #pragma unroll
-          for (int c0 = 0; c0 < D / 64; ++c0) {
-            const int c = 4 * c0 + (lane >> 3);
-            const uint4 v = lds128(
-                rawk + (D == 64 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4)
-                                : (c >> 3) * (kKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)));
-            const uint32_t to = sb + S::kK + (c >> 2) * (kKeys * 128) + row * 128;
-            const int e = 2 * (c & 3);
-            sts128(to + ((e ^ (row & 7)) << 4), codes_bf16(v.x, 0x4140), codes_bf16(v.x, 0x4342),
-                   codes_bf16(v.y, 0x4140), codes_bf16(v.y, 0x4342));
-            sts128(to + (((e + 1) ^ (row & 7)) << 4), codes_bf16(v.z, 0x4140),
-                   codes_bf16(v.z, 0x4342), codes_bf16(v.w, 0x4140), codes_bf16(v.w, 0x4342));
+        for (int x = w; x < (kKeys / 8) * (D / 64); x += S::kConvWarps) {
+          const int row = 8 * (x % (kKeys / 8)) + (lane & 7), c = 4 * (x / (kKeys / 8)) + (lane >> 3);
+          const uint4 v = lds128(
+              raw + (D == 64 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4)
+                             : (c >> 3) * (kKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)));
+          const uint32_t to = to0 + (c >> 2) * (kKeys * 128) + row * 128;
+          const int e = 2 * (c & 3);
+          sts128(to + ((e ^ (row & 7)) << 4), codes_bf16(v.x, 0x4140), codes_bf16(v.x, 0x4342),
+                 codes_bf16(v.y, 0x4140), codes_bf16(v.y, 0x4342));
+          sts128(to + (((e + 1) ^ (row & 7)) << 4), codes_bf16(v.z, 0x4140),
+                 codes_bf16(v.z, 0x4342), codes_bf16(v.w, 0x4140), codes_bf16(v.w, 0x4342));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kKReady + buf));
+          mbar_arrive(bar(kRawKEmpty + st));
+        }
+        ++nk;
+        return true;
+      };
+      // values: four tokens of a channel side by side as fp32 (a byte under
+      // 0x4B0000 reads 2^23 + u); lanes start at different channels of their
+      // word so that the stores meet no bank conflict
+      auto vals = [&](int i) {
+        const uint32_t st = nv % kRaw, buf = i % kBuf;
+        if (!wait_bar(bar(kRawVFull + st), use<kRaw>(nv), abort_flag) ||
+            !wait_bar(bar(kVFree + buf), (vf_par >> buf) & 1u, abort_flag))
+          return false;
+        vf_par ^= 1u << buf;
+        const uint32_t raw = sb + S::kRawV + st * S::kRawTile, to0 = sb + S::kV + buf * S::kVTile;
+        constexpr int kWords = D == 64 ? 16 : 32;         // words of a raw row
+        constexpr int kSub = 32 / kWords;                 // token groups of a warp at a time
+        const uint64_t zero = pack2(-8388736.0f, -8388736.0f);
+#pragma unroll
+        for (int x = w; x < kKeys / 4 / kSub * ((D + 127) / 128); x += S::kConvWarps) {
+          const int g = x % (kKeys / 4 / kSub), half = x / (kKeys / 4 / kSub);
+          const int tok = 4 * (g * kSub + lane / kWords), wd = lane % kWords;
+          uint32_t v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = tok + e;
+            v[e] = lds32(raw +
+                         (D == 64 ? t * 64 + (((wd >> 2) ^ ((t >> 1) & 3)) << 4)
+                                  : half * (kKeys * 128) + t * 128 + (((wd >> 2) ^ (t & 7)) << 4)) +
+                         (wd & 3) * 4);
+          }
+#pragma unroll
+          for (int dd = 0; dd < 4; ++dd) {
+            const int d = (dd + (lane >> 1)) & 3, ch = 128 * half + 4 * wd + d;
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+              unpack2(add2(pack2(__uint_as_float(__byte_perm(v[e], 0x4B000000u, 0x7440 + d)),
+                                 __uint_as_float(__byte_perm(v[e + 1], 0x4B000000u, 0x7440 + d))),
+                           zero),
+                      f[e], f[e + 1]);
+            sts128(to0 + (tok >> 5) * (D * 128) + ch * 128 + ((((tok & 31) >> 2) ^ (ch & 7)) << 4),
+                   __float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                   __float_as_uint(f[3]));
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kKReady));
-        // values: four tokens of a channel side by side as fp32 (a byte under
-        // 0x4B0000 reads 2^23 + u); lanes start at different channels of
-        // their word so that the stores meet no bank conflict
-        constexpr int kWords = D == 64 ? 16 : 32;         // words of a raw row
-        constexpr int kSub = 32 / kWords;                 // token groups of a warp at a time
-        const uint64_t zero = pack2(-8388736.0f, -8388736.0f);
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (!wait_bar(bar(kVFree + half), v_free[half].before(), abort_flag)) {
-            ok = false;
-            break;
-          }
-#pragma unroll 2
-          for (int g = w; g < kKeys / 8 / kSub; g += S::kConvWarps) {
-            const int tok = half * (kKeys / 2) + 4 * (g * kSub + lane / kWords), wd = lane % kWords;
-#pragma unroll
-            for (int x = 0; x < (D + 127) / 128; ++x) {
-              uint32_t v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int t = tok + e;
-                v[e] = lds32(rawv +
-                             (D == 64 ? t * 64 + (((wd >> 2) ^ ((t >> 1) & 3)) << 4)
-                                      : x * (kKeys * 128) + t * 128 + (((wd >> 2) ^ (t & 7)) << 4)) +
-                             (wd & 3) * 4);
-              }
-#pragma unroll
-              for (int dd = 0; dd < 4; ++dd) {
-                const int d = (dd + (lane >> 1)) & 3, ch = 128 * x + 4 * wd + d;
-                float f[4];
-#pragma unroll
-                for (int e = 0; e < 4; e += 2)
-                  unpack2(add2(pack2(__uint_as_float(__byte_perm(v[e], 0x4B000000u, 0x7440 + d)),
-                                     __uint_as_float(__byte_perm(v[e + 1], 0x4B000000u, 0x7440 + d))),
-                               zero),
-                          f[e], f[e + 1]);
-                sts128(sb + S::kV + (tok >> 5) * (D * 128) + ch * 128 +
-                           ((((tok & 31) >> 2) ^ (ch & 7)) << 4),
-                       __float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                       __float_as_uint(f[3]));
-              }
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kVReady + half));
+        if (lane == 0) {
+          mbar_arrive(bar(kVReady + buf));
+          mbar_arrive(bar(kRawVEmpty + st));
         }
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(bar(kRawEmpty + st));
-        st ^= 1;
-      }
+        ++nv;
+        return true;
+      };
+      const int n = u.tiles();
+      ok = keys(0) && (n < 2 || keys(1));
+      for (int i = 0; ok && i < n; ++i) ok = vals(i) && (i + 2 >= n || keys(i + 2));
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -669,46 +734,53 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ocol = tmem + lanes + S::kOCol + grp * D;
     const float f = p.a.scale * kLog2e;
-    Phase s_full[2], o_done, epi;
-    int serial = 0, unit = 0;   // key tiles and units walked
+    uint32_t s_par = 0;                  // next parity of each region's barrier
+    uint32_t o_done = 0;                 // PVs of this group, units before this one
+    int serial = 0, unit = 0;            // key tiles and units walked
     for (; ok && next_unit<D>(p, run, walk, u); ++unit) {
       const bool two = kGroups == 2 && u.rows > kRowTile;
       const int row = u.rt * S::kRows + (two ? grp * kRowTile : 0) + r;   // of the (sequence, head)
       const int pos = u.s.len - u.s.n + min(row, u.R - 1) / p.G;
+      const int tok_lo = u.t.lo + u.i0 * kKeys, n = u.tiles(), win = p.a.window;
       float m = 0.0f, l = 0.0f;
       bool have = false;     // m is some score's
       int done = 0;          // jobs of this group whose PV may be under way
-      for (int i = 0; i < u.tiles(); ++i) {
-        if (kGroups == 2 && !two && (i & 1) != grp) continue;   // the other group's tile
-        const int reg = kGroups == 2 ? grp : i & 1;
-        const uint32_t scol = tmem + lanes + S::kSCol + reg * kKeys;
-        const int tok0 = u.t.lo + (u.i0 + i) * kKeys;
-        const float2* mt = meta + ((serial + i) & 7) * 8;
-        if (!wait_bar(bar(kSFull + reg), s_full[reg].next(), abort_flag)) {
+      const int step = kGroups == 2 && !two ? 2 : 1;               // the other group has the others
+      for (int i = step == 2 ? grp : 0; i < n; i += step) {
+        const int reg = two ? 2 * (i & 1) + grp : i & 1;
+        const uint32_t scol = tmem + lanes + reg * kKeys;
+        const int tok0 = tok_lo + i * kKeys;
+        const float2* mt = meta + ((serial + i) % kMetaRing) * 4;
+        if (!wait_bar(bar(kSFull + reg), (s_par >> reg) & 1u, abort_flag)) {
           ok = false;
           break;
         }
+        s_par ^= 1u << reg;
         tc_fence_after();
-        const bool cut = __any_sync(0xffffffffu, tok0 + kKeys - 1 > pos ||
-                                                     (p.a.window > 0 && tok0 <= pos - p.a.window));
+        // the tile's columns that the row sees
+        const int hi = pos - tok0, lo = win > 0 ? hi - win + 1 : 0;
+        const bool cut = __any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0);
 #pragma unroll 1
         for (int c0 = 0; c0 < kKeys; c0 += 32) {
           float y[32];
-          tc::tmem_ld<32>(scol + c0, y);
           const float2 m0 = mt[c0 / 16], m1 = mt[c0 / 16 + 1];
-          tc::tmem_wait_ld<32>(y);
-          float sum = weights(y, f * m0.x, f * m1.x, m, cut, tok0 + c0, pos, p.a.window);
-          // a score far past m (its weight shows in the sum), or no m yet
-          if (__any_sync(0xffffffffu, !have || !(sum <= kFar))) {
+          const float f0 = f * m0.x, f1 = f * m1.x;
+          float sum;
+#pragma unroll 1
+          for (bool again = false;; again = true) {
+            tc::tmem_ld<32>(scol + c0, y);
+            tc::tmem_wait_ld<32>(y);
+            sum = weights(y, f0, f1, m, cut, lo - c0, hi - c0);
+            // a score far past m shows in the sum (once m has moved, the sum
+            // is what it is: not a number, say)
+            if (again || !__any_sync(0xffffffffu, !have || !(sum <= kFar))) break;
             tc::tmem_ld<32>(scol + c0, y);
             tc::tmem_wait_ld<32>(y);
             float mx = -INFINITY;
+            const uint32_t seen = columns(lo - c0, hi - c0);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int t = tok0 + c0 + e;
-              const bool sees = t <= pos && !(p.a.window > 0 && t <= pos - p.a.window);
-              mx = fmaxf(mx, sees ? y[e] * (e < 16 ? f * m0.x : f * m1.x) : -INFINITY);
-            }
+            for (int e = 0; e < 32; ++e)
+              mx = fmaxf(mx, seen >> e & 1u ? y[e] * (e < 16 ? f0 : f1) : -INFINITY);
             float keep = 1.0f;
             if (!have) {
               have = mx > -INFINITY;
@@ -723,15 +795,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
               tmem_wait_st();
               for (int c = 0; c < c0; c += 32) tmem_scale32(scol + c, keep);
               if (done > 0) {
-                // the last PV of this group has to be complete
-                if (!wait_bar(bar(kODone + grp), (o_done.n + done - 1) & 1u, abort_flag)) ok = false;
+                // the last PV of this group has to be complete (the one before
+                // it is: these scores were issued after it)
+                if (!wait_bar(bar(kODone + grp), (o_done + done - 1) & 1u, abort_flag)) ok = false;
                 tc_fence_after();
                 for (int c = 0; c < D; c += 32) tmem_scale32(ocol + c, keep);
               }
               tmem_wait_st();
             }
             l *= keep;
-            sum = weights(y, f * m0.x, f * m1.x, m, cut, tok0 + c0, pos, p.a.window);
           }
           l += sum;
           // times the block's step; the MMA drops 13 bits of what it reads,
@@ -751,25 +823,19 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         if (lane == 0) mbar_arrive(bar(kPFull + reg));
         ++done;
       }
-      serial += u.tiles();
+      serial += n;
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
-      bool gave_up = false;
-      if (done > 0) {
-        // (with one group, scores of the last tile do not tell that the PV
-        // before the last is complete: in turn)
-        if (kGroups == 1 && done > 1 &&
-            !wait_bar(bar(kODone + grp), (o_done.n + done - 2) & 1u, abort_flag))
-          gave_up = true;
-        if (!wait_bar(bar(kODone + grp), (o_done.n + done - 1) & 1u, abort_flag)) gave_up = true;
-        o_done.n += done;
-        tc_fence_after();
-      }
-      if (gave_up) {
+      // (the last scores do not tell that the PV before the last is complete:
+      // in turn)
+      if ((done > 1 && !wait_bar(bar(kODone + grp), (o_done + done - 2) & 1u, abort_flag)) ||
+          (done > 0 && !wait_bar(bar(kODone + grp), (o_done + done - 1) & 1u, abort_flag))) {
         ok = false;
         break;
       }
-      const bool no = refused[unit & 7] != 0;
+      o_done += done;
+      tc_fence_after();
+      const bool no = refused[unit % kUnitRing] != 0;
       const bool direct = u.whole() && (two || kGroups == 1);
       // a whole unit of one row tile: the groups' parts meet right here, in
       // two places of this CTA's own in turn
@@ -823,13 +889,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       // all softmax warps have read `refused` and written their parts
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kEpi));
-      if (!wait_bar(bar(kEpi), epi.next(), abort_flag)) {
+      if (!wait_bar(bar(kEpi), use<1>(unit), abort_flag)) {
         ok = false;
         break;
       }
       if (tid == 0) {
         if (no) report(p.a.status, W4_ERR_INDEX);
-        refused[unit & 7] = 0;
+        refused[unit % kUnitRing] = 0;
       }
       if (pair && !no) {
         const long long base = (long long)slot * S::kRows;
@@ -876,7 +942,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   Run run;
   run.total = p.cut[0];
   run.ctas = (int)p.cut[1];
-  const Tile t = tile_of(s, p.G, p.a.window, rt, S::kRows, S::kKeys);
+  const Tile t = tile_of(s, p.G, p.a.window, rt, S::kRows, kKeys);
   const int c0 = run.holder(u0), c1 = run.holder(u0 + t.slices - 1);
   // of one row tile, each CTA holds two parts (one per softmax group)
   const int subs = S::kGroups == 2 && R - rt * S::kRows <= kRowTile ? 2 : 1;
@@ -933,7 +999,7 @@ w4_status launch_chunk(ChunkParams& p, int sms, int dev, bool pdl, w4_stream_t s
       done[dev] = true;
     }
   }
-  const int box = std::min(p.c.P, S::kKeys);
+  const int box = std::min(p.c.P, kKeys);
   if (!tensor_map(&p.tm_k, p.c.kc, p.c, box) || !tensor_map(&p.tm_v, p.c.vc, p.c, box)) {
     note_cuda_error(cudaErrorInvalidValue);
     return W4_ERR_LAUNCH;
