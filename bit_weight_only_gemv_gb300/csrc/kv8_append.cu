@@ -6,8 +6,9 @@
 // becomes s = max(s0, least power of two >= m / 127): a power of two, so that
 // the division value / s, the ratio s0 / s and code * step are exact and the
 // only rounding is the one to a whole code.  One pass finds m (and refuses
-// values that are not finite), a second one, served by L1, writes the codes;
-// older codes are touched only when the step grows.
+// values that are not finite), a second one, from registers or L1, writes the
+// codes; older codes are touched only when the step grows.  Latency bounds
+// it: the chain is lengths, then rows and page together, then the old step.
 #include "kv8.cuh"
 
 namespace w4 {
@@ -15,6 +16,17 @@ namespace kv8 {
 namespace {
 
 
+
+constexpr int kHeld = 4;   // input vectors a thread keeps between its two passes
+
+// Four codes times a ratio of steps.
+__device__ __forceinline__ uint32_t rescale4(uint32_t x, float ratio) {
+  uint32_t y = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    y |= to_code((float)((int)((x >> (8 * j)) & 0xFF) - 128) * ratio) << (8 * j);
+  return y;
+}
 
 __device__ __forceinline__ void unpack8(const uint4& w, float f[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -29,8 +41,7 @@ __global__ void __launch_bounds__(256) append_kernel(Cache c, Batch bt,
                                                      const __nv_bfloat16* __restrict__ k,
                                                      const __nv_bfloat16* __restrict__ v,
                                                      long long row_stride, int32_t* status) {
-  __shared__ float red[8];
-  __shared__ int bad_any;
+  __shared__ uint32_t red[8];
   __shared__ uint32_t lo_sm[256 / 2][4], hi_sm[256 / 2][4];   // [thread][2 words] halves
   pdl_launch_dependents();
   pdl_wait();
@@ -46,82 +57,80 @@ __global__ void __launch_bounds__(256) append_kernel(Cache c, Batch bt,
   const int p0 = lp * c.P;
   const int lo = max(first, p0), hi = min(s.len, p0 + c.P);
   if (lo >= hi) return;
-  const int page = __ldg(bt.table + (long long)b * bt.max_pages + lp);
-  if (page < 0 || page >= c.num_pages) {
-    if (threadIdx.x == 0) report(status, W4_ERR_INDEX);
-    return;
-  }
   const int tid = threadIdx.x, nth = blockDim.x;
-  if (tid == 0) bad_any = 0;
-  // rows lo .. hi - 1 of this head; 16-byte vectors of 8 values
+  // rows lo .. hi - 1 of this head; 16-byte vectors of 8 values, the first
+  // kHeld of a thread kept in registers, on their way before anything waits
   const int vecs = c.D / 8, col = tid % vecs, r0 = tid / vecs, rstep = nth / vecs;
   const __nv_bfloat16* src = (is_v ? v : k) +
                              (long long)(s.row0 + lo - (s.len - s.n)) * row_stride +
                              (long long)h * c.D + col * 8;
   const int rows = hi - lo;
+  uint4 held[kHeld];
+#pragma unroll
+  for (int z = 0; z < kHeld; ++z)
+    if (r0 + z * rstep < rows)
+      held[z] = __ldg(reinterpret_cast<const uint4*>(src + (r0 + z * rstep) * row_stride));
+  const int page = __ldg(bt.table + (long long)b * bt.max_pages + lp);
+  if (page < 0 || page >= c.num_pages) {
+    if (tid == 0) report(status, W4_ERR_INDEX);
+    return;
+  }
   const bool has_old = lo > p0;
   float* steps = is_v ? c.vs : c.ks;
   const float s0 = has_old ? steps[c.pair(page, h)] : 0.0f;
-  float m = 0.0f;
-  bool bad = false;
-  for (int r = r0; r < rows; r += rstep) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + r * row_stride));
-    float f[8];
-    unpack8(w, f);
+  // largest |value|; bf16 bits without the sign are in order, and those of
+  // infinities and NaN come last
+  uint32_t top = 0;
+  auto look = [&](const uint4& w) {
+    const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+    top = max(top, max(m & 0xFFFFu, m >> 16));
+  };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      bad |= !(fabsf(f[i]) <= 3.4e38f);   // infinities and NaN; bf16's largest is below 3.4e38
-      m = fmaxf(m, fabsf(f[i]));
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((tid & 31) == 0) red[tid >> 5] = m;
+  for (int z = 0; z < kHeld; ++z)
+    if (r0 + z * rstep < rows) look(held[z]);
+  for (int r = r0 + kHeld * rstep; r < rows; r += rstep)
+    look(__ldg(reinterpret_cast<const uint4*>(src + r * row_stride)));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((tid & 31) == 0) red[tid >> 5] = top;
   __syncthreads();
-  if (bad) bad_any = 1;
-  m = red[0];
-  for (int i = 1; i < nth / 32; ++i) m = fmaxf(m, red[i]);
-  __syncthreads();
-  if (bad_any) {
+  for (int i = 0; i < nth / 32; ++i) top = max(top, red[i]);
+  if (top >= 0x7F80u) {
     if (tid == 0) report(status, W4_ERR_VALUE);
     return;
   }
-  const float step = fmaxf(s0, pow2_step(m));
+  const float step = fmaxf(s0, pow2_step(__uint_as_float(top << 16)));
+  // a power of two (as the library's own steps are) divides by a product
+  const bool exact = (__float_as_uint(step) & 0x7FFFFFu) == 0;
+  const float inv = __fdiv_rn(1.0f, step);
   uint8_t* blk = (is_v ? c.vc : c.kc) + c.block(page, h);
-  uint32_t mn[8], mx[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    mn[i] = 255;
-    mx[i] = 0;
-  }
-  for (int r = r0; r < rows; r += rstep) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + r * row_stride));
+  uint32_t mn[2] = {~0u, ~0u}, mx[2] = {0, 0};   // by channel, four to a word
+  auto store = [&](const uint4& w, int r) {
     float f[8];
     unpack8(w, f);
     uint32_t out[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t u = to_code(__fdiv_rn(f[i], step));
-      mn[i] = min(mn[i], u);
-      mx[i] = max(mx[i], u);
-      out[i >> 2] |= u << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i)
+      out[i >> 2] |= to_code(exact ? f[i] * inv : __fdiv_rn(f[i], step)) << (8 * (i & 3));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mn[i] = __vminu4(mn[i], out[i]);
+      mx[i] = __vmaxu4(mx[i], out[i]);
     }
     *reinterpret_cast<uint2*>(blk + (long long)(lo - p0 + r) * c.D + col * 8) =
         make_uint2(out[0], out[1]);
-  }
+  };
+#pragma unroll
+  for (int z = 0; z < kHeld; ++z)
+    if (r0 + z * rstep < rows) store(held[z], r0 + z * rstep);
+  for (int r = r0 + kHeld * rstep; r < rows; r += rstep)
+    store(__ldg(reinterpret_cast<const uint4*>(src + r * row_stride)), r);
   const bool grow = has_old && step != s0;
   const float ratio = grow ? __fdiv_rn(s0, step) : 1.0f;
   if (grow) {
     const int words = (lo - p0) * c.D / 4;
     uint32_t* w = reinterpret_cast<uint32_t*>(blk);
-    for (int i = tid; i < words; i += nth) {
-      const uint32_t x = w[i];
-      uint32_t y = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        y |= to_code((float)((int)((x >> (8 * j)) & 0xFF) - 128) * ratio) << (8 * j);
-      w[i] = y;
-    }
+    for (int i = tid; i < words; i += nth) w[i] = rescale4(w[i], ratio);
   }
   if (tid == 0) steps[c.pair(page, h)] = step;
   if (is_v) {
@@ -132,57 +141,37 @@ __global__ void __launch_bounds__(256) append_kernel(Cache c, Batch bt,
   if (c.ranges == nullptr) return;
   // lowest and highest code of each channel: the threads of one column in
   // turn, then what the block held before
-  if (rstep > 1) {
-    // two 4-byte words of minima, two of maxima per thread
-    uint32_t a[2] = {0, 0}, z[2] = {0, 0};
+  uint32_t* lp_sm = &lo_sm[0][0];
+  uint32_t* hp_sm = &hi_sm[0][0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      a[i >> 2] |= mn[i] << (8 * (i & 3));
-      z[i >> 2] |= mx[i] << (8 * (i & 3));
-    }
-    uint32_t* lp_sm = &lo_sm[0][0];
-    uint32_t* hp_sm = &hi_sm[0][0];
-    lp_sm[2 * tid] = a[0];
-    lp_sm[2 * tid + 1] = a[1];
-    hp_sm[2 * tid] = z[0];
-    hp_sm[2 * tid + 1] = z[1];
-    __syncthreads();
-    for (int half = rstep >> 1; half > 0; half >>= 1) {   // rstep is a power of two
-      if (r0 < half) {
-        const int o = tid + half * vecs;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          lp_sm[2 * tid + i] = __vminu4(lp_sm[2 * tid + i], lp_sm[2 * o + i]);
-          hp_sm[2 * tid + i] = __vmaxu4(hp_sm[2 * tid + i], hp_sm[2 * o + i]);
-        }
-      }
-      __syncthreads();
-    }
-    if (r0 != 0) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mn[i] = (lp_sm[2 * tid + (i >> 2)] >> (8 * (i & 3))) & 0xFF;
-      mx[i] = (hp_sm[2 * tid + (i >> 2)] >> (8 * (i & 3))) & 0xFF;
-    }
+  for (int i = 0; i < 2; ++i) {
+    lp_sm[2 * tid + i] = mn[i];
+    hp_sm[2 * tid + i] = mx[i];
   }
+  __syncthreads();
+  if (r0 != 0) return;
+  for (int o = tid + vecs; o < nth; o += vecs)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mn[i] = __vminu4(mn[i], lp_sm[2 * o + i]);
+      mx[i] = __vmaxu4(mx[i], hp_sm[2 * o + i]);
+    }
   uint8_t* rg = c.ranges + c.pair(page, h) * 2 * c.D + col * 8;
   uint2* rlo = reinterpret_cast<uint2*>(rg);
   uint2* rhi = reinterpret_cast<uint2*>(rg + c.D);
-  uint32_t a[2] = {0, 0}, z[2] = {0, 0};
   const uint2 olo = has_old ? *rlo : make_uint2(~0u, ~0u), ohi = has_old ? *rhi : make_uint2(0, 0);
+  uint32_t l[2] = {olo.x, olo.y}, u[2] = {ohi.x, ohi.y};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t l = ((i < 4 ? olo.x : olo.y) >> (8 * (i & 3))) & 0xFF;
-    uint32_t u = ((i < 4 ? ohi.x : ohi.y) >> (8 * (i & 3))) & 0xFF;
+  for (int i = 0; i < 2; ++i) {
     if (grow) {   // rescaling is monotone: the range of the rescaled codes
-      l = to_code((float)((int)l - 128) * ratio);
-      u = to_code((float)((int)u - 128) * ratio);
+      l[i] = rescale4(l[i], ratio);
+      u[i] = rescale4(u[i], ratio);
     }
-    a[i >> 2] |= min(l, mn[i]) << (8 * (i & 3));
-    z[i >> 2] |= max(u, mx[i]) << (8 * (i & 3));
+    l[i] = __vminu4(l[i], mn[i]);
+    u[i] = __vmaxu4(u[i], mx[i]);
   }
-  *rlo = make_uint2(a[0], a[1]);
-  *rhi = make_uint2(z[0], z[1]);
+  *rlo = make_uint2(l[0], l[1]);
+  *rhi = make_uint2(u[0], u[1]);
 }
 
 }  // namespace

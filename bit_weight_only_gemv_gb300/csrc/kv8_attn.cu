@@ -210,32 +210,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
     const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
     const int R = s.n * p.G;
 
-    // --------------------------------------------------- query fragments
-    uint32_t q[NQ][D / 16][2];
-    float f[NQ][2];   // of this lane's two columns: scale log2(e) / the row's power of two
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int r = rt * kRows + 8 * n + i;
-      const __nv_bfloat16* row =
-          r < R ? p.q + (long long)(s.row0 + r / p.G) * p.q_stride + (long long)(h * p.G + r % p.G) * D
-                : nullptr;
-      const float down = load_query<D>(row, j, q[n]);
-      f[n][0] = __shfl_sync(0xffffffffu, down, 8 * j) * (p.scale * kLog2e);
-      f[n][1] = __shfl_sync(0xffffffffu, down, 8 * j + 4) * (p.scale * kLog2e);
-    }
-    float m[NQ][2], l[NQ][2], o[NQ][D / 16][4];
-    float vref = 0.0f;
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][c][e] = 0.0f;
-    }
-
-    // ------------------------------------------------- this warp's slices
+    // ------------------------- this warp's slices, the first on their way
     const int count = (sl1 - sl0 - warp + kWarps - 1) / kWarps;   // may be <= 0
     auto fill = [&](int k0) {   // descriptions k0 .. k0 + 31
       __syncwarp();
@@ -297,6 +272,31 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
     };
 #pragma unroll 1
     for (int k = 0; k < kStages; ++k) issue(k);
+    // --------------------------------------------------- query fragments
+    uint32_t q[NQ][D / 16][2];
+    float f[NQ][2];   // of this lane's two columns: scale log2(e) / the row's power of two
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int r = rt * kRows + 8 * n + i;
+      const __nv_bfloat16* row =
+          r < R ? p.q + (long long)(s.row0 + r / p.G) * p.q_stride + (long long)(h * p.G + r % p.G) * D
+                : nullptr;
+      const float down = load_query<D>(row, j, q[n]);
+      f[n][0] = __shfl_sync(0xffffffffu, down, 8 * j) * (p.scale * kLog2e);
+      f[n][1] = __shfl_sync(0xffffffffu, down, 8 * j + 4) * (p.scale * kLog2e);
+    }
+    float m[NQ][2], l[NQ][2], o[NQ][D / 16][4];
+    float vref = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][c][e] = 0.0f;
+    }
+
 #pragma unroll 1
     for (int k = 0; k < count; ++k) {
       if (!dead && !mbar_wait_bounded(bar0 + 8 * got, got_phase, kWait)) {

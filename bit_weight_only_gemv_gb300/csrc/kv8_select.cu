@@ -4,10 +4,14 @@
 //
 // Both choices are the same operation on a list of keys: the `count` largest,
 // ties from the lowest index on, given back in ascending index order.  Keys
-// are fp32 values mapped to uint32 in order; three radix passes (11, 11 and
-// 10 bits, a shared-memory histogram each) find the count-th largest key T
-// and how many keys equal to T are taken, then one ordered pass with prefix
-// sums writes the indexes.
+// are fp32 values mapped to uint32 in order.  Up to 16384 keys stay in the
+// registers of 1024 threads, consecutive ones in a thread: the count-th
+// largest key T is found two bits at a time by counting (16 rounds of one
+// barrier each; a histogram's atomics would pile up on the few exponents that
+// scores and weights have: measured 29 us against 9 for 1024 keys), then one
+// prefix sum gives every thread its place.  Longer lists are read from memory
+// again in three radix passes (11, 11 and 10 bits, a shared-memory histogram
+// each) and one ordered pass.
 #include "kv8.cuh"
 
 namespace w4 {
@@ -20,11 +24,18 @@ constexpr int kBins = 2048;
 // fp32 -> uint32 in the order of the values (-NaN lowest, NaN highest), below
 // kForced; -0 and 0 are one key.
 constexpr uint32_t kForced = 0xFFFFFFFFu;
+constexpr uint32_t kNoPage = 0x7FABCDEFu;   // a NaN no product gives
 __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t b = __float_as_uint(f);
   if (b == 0x80000000u) return 0x80000000u;
   return (b & 0x80000000u) ? ~b : min(b | 0x80000000u, kForced - 1);
 }
+
+// A constant as an argument.
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
 
 struct TopShared {
   uint32_t hist[kBins];
@@ -120,6 +131,66 @@ __device__ void top_indexes(TopShared& sh, int n, int count, Key key, Emit emit)
   }
 }
 
+// The same for keys in registers: thread t holds keys t * kPer .. of n (0 past
+// the end), kPer at most 16 and n at most 16384.  Calls emit(rank, k) for the
+// thread's k-th key.
+template <int kPer, typename Emit>
+__device__ void top_registers(TopShared& sh, const uint32_t (&key)[kPer], int n, int count, Emit emit) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int have = max(0, min(kPer, n - tid * kPer));
+  const bool all = count >= n;
+  // T: the largest value that at least `count` keys reach, two bits a round
+  uint32_t T = 0;
+  if (!all) {
+    uint32_t* counts = sh.hist;   // [2][32] packed counts of a warp, rounds in turn
+#pragma unroll 1
+    for (int bit = 30, odd = 0; bit >= 0; bit -= 2, odd ^= 32) {
+      const uint32_t c1 = T | 1u << bit, c2 = T | 2u << bit, c3 = T | 3u << bit;
+      uint32_t mine = 0;   // three counts of up to 512 a warp, ten bits each
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const uint32_t u = key[k];
+        mine += (k < have ? (u >= c1 ? 1u : 0u) + (u >= c2 ? 1u << 10 : 0u) + (u >= c3 ? 1u << 20 : 0u)
+                          : 0u);
+      }
+      mine = __reduce_add_sync(0xffffffffu, mine);
+      if (lane == 0) counts[odd + warp] = mine;
+      __syncthreads();
+      const uint32_t w = lane < (int)(blockDim.x >> 5) ? counts[odd + lane] : 0u;
+      const int n1 = (int)__reduce_add_sync(0xffffffffu, w & 1023u);
+      const int n2 = (int)__reduce_add_sync(0xffffffffu, w >> 10 & 1023u);
+      const int n3 = (int)__reduce_add_sync(0xffffffffu, w >> 20);
+      if (n3 >= count) T = c3;
+      else if (n2 >= count) T = c2;
+      else if (n1 >= count) T = c1;
+    }
+  }
+  // keys above T, and of those equal to T the first ones
+  uint32_t above = 0, equal = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if (k < have) {
+      if (all || key[k] > T) ++above;
+      else if (key[k] == T) ++equal;
+    }
+  __syncthreads();   // the counts have been read
+  uint32_t total;
+  const uint32_t ex = block_scan(above | equal << 16, sh.warp_sum, &total);
+  const int ties = count - (int)(total & 0xFFFFu);   // equal ones that are taken (all: none)
+  int rank = (int)(ex & 0xFFFFu), tie = (int)(ex >> 16);
+  rank += min(tie, ties);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if (k < have) {
+      if (all || key[k] > T) {
+        emit(rank++, k);
+      } else if (key[k] == T) {
+        if (tie < ties) emit(rank++, k);
+        ++tie;
+      }
+    }
+}
+
 // ------------------------------------------------------------------ select
 struct SelectParams {
   Cache c;
@@ -130,45 +201,21 @@ struct SelectParams {
   int32_t* sel;
   int32_t* n_sel;
   int max_sel, sink, recent;
-  float* scores;      // [B][H][max_pages]
-  int32_t* arrived;   // [B][H], zero between calls
+  float* scores;      // [B][H][scores_row]
+  long long scores_row;
   int chunk;          // pages scored by one CTA
   int32_t* status;
 };
 
-// One CTA scores `chunk` pages of a (sequence, head); the last of a
-// (sequence, head)'s CTAs to finish chooses.  A page's two range rows are 2 D
-// consecutive bytes: 16 bytes a lane, the codes made signed by one XOR, four
-// products an instruction; whole numbers below 2^24, so the sum's order does
-// not matter and its conversion is exact.
-__global__ void __launch_bounds__(kTopThreads) select_kernel(const SelectParams p) {
-  __shared__ TopShared sh;
-  __shared__ float part[32];
-  __shared__ __align__(16) int8_t qi[2][256];   // [down | up] rows, as the ranges are laid out
-  __shared__ int last;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Seq s = sequence(p.bt, p.c.P, b);
-  const int P = p.c.P, D = p.c.D;
-  int np = s.ok ? (s.len + P - 1) / P : -1;
-  if (np > p.bt.max_pages) np = -1;
-  if (np < 0) {
-    if (tid == 0 && blockIdx.x == 0) report(p.status, W4_ERR_INDEX);
-    return;
-  }
-  const int c0 = blockIdx.x * p.chunk, c1 = min(np, c0 + p.chunk);
-  const int ctas = max(1, (np + p.chunk - 1) / p.chunk);   // that take part
-  if ((int)blockIdx.x >= ctas) return;
-  // an entry in no use is refused before anything is written; each CTA
-  // checks its own pages and leaves a mark in the scores
-  const long long bh = (long long)b * p.c.H + h;
-  float* scores = p.scores + bh * p.bt.max_pages;
-  // the group's query rows: sums of their positive and negative parts
+// The query of a (sequence, head) as the pages are scored with: sums of the
+// group's positive and negative parts, 8 bits, [down | up] as the ranges lie.
+// part: one float per warp.
+__device__ void group_query(const SelectParams& p, const Seq& s, int h, float* part, int8_t (&qi)[2][256]) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, D = p.c.D;
   float up = 0.0f, down = 0.0f;
   if (tid < D && s.n > 0) {
     const __nv_bfloat16* q = p.q + (long long)s.row0 * p.q_stride + (long long)h * p.G * D + tid;
+#pragma unroll 8
     for (int g = 0; g < p.G; ++g) {
       const float x = __bfloat162float(q[g * D]);
       up += fmaxf(x, 0.0f);
@@ -188,49 +235,111 @@ __global__ void __launch_bounds__(kTopThreads) select_kernel(const SelectParams 
     qi[1][tid] = (int8_t)__float2int_rn(fminf(__fdiv_rn(up, step), 127.0f));
   }
   __syncthreads();
+}
+
+// Scores of `chunk` pages of a (sequence, head).  A page's two range rows are
+// 2 D consecutive bytes: 16 bytes a lane, the codes made signed by one XOR,
+// four products an instruction; whole numbers below 2^24, so the sum's order
+// does not matter and its conversion is exact.  The bytes of the ranges bound
+// it once there are enough of them; four pages a lane are in flight.
+constexpr int kScoreThreads = 256;
+
+__global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams p) {
+  __shared__ float part[kScoreThreads / 32];
+  __shared__ __align__(16) int8_t qi[2][256];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Seq s = sequence(p.bt, p.c.P, b);
+  const int P = p.c.P, D = p.c.D;
+  if (!s.ok) {
+    if (tid == 0 && blockIdx.x == 0 && h == 0) report(p.status, W4_ERR_INDEX);
+    return;
+  }
+  const int np = (s.len + P - 1) / P;
+  const int c0 = blockIdx.x * p.chunk, c1 = min(np, c0 + p.chunk);
+  if (c0 >= c1) return;
+  const long long bh = (long long)b * p.c.H + h;
+  float* scores = p.scores + bh * p.scores_row;
+  const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
+  group_query(p, s, h, part, qi);
   const int lanes = 2 * D / 16;             // lanes of a page: 8, 16 or 32
   const int sub = lane / lanes, l = lane % lanes;
-  const int row = l * 16 / D, off = l * 16 % D;
-  const int4 qw = *reinterpret_cast<const int4*>(&qi[row][off]);
-  const int per_warp = 32 / lanes;
-  const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
-  bool bad = false;
-  for (int i = c0 + warp * per_warp + sub; i - sub < c1; i += (kTopThreads / 32) * per_warp) {
-    const int page = i < c1 ? __ldg(table + i) : 0;
-    const bool ok = page >= 0 && page < p.c.num_pages;
-    bad |= !ok;
-    int acc = 0;
-    float ks = 0.0f;
-    if (ok && i < c1) {
-      const int4 r = __ldg(reinterpret_cast<const int4*>(p.c.ranges + p.c.pair(page, h) * 2 * D) + l);
-      ks = __ldg(p.c.ks + p.c.pair(page, h));
-      acc = __dp4a(r.x ^ (int)0x80808080, qw.x, acc);
-      acc = __dp4a(r.y ^ (int)0x80808080, qw.y, acc);
-      acc = __dp4a(r.z ^ (int)0x80808080, qw.z, acc);
-      acc = __dp4a(r.w ^ (int)0x80808080, qw.w, acc);
+  const int4 qw = *reinterpret_cast<const int4*>(&qi[l * 16 / D][l * 16 % D]);
+  const int per = kScoreThreads / lanes;    // pages of the CTA at a time
+  constexpr int kDeep = 4;
+  for (int i0 = c0 + warp * (32 / lanes); i0 < c1; i0 += kDeep * per) {
+    int4 r[kDeep];
+    float ks[kDeep];
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      const int i = i0 + k * per + sub;
+      int page = i < c1 ? __ldg(table + i) : 0;
+      const bool ok = page >= 0 && page < p.c.num_pages;
+      if (!ok) page = 0;
+      r[k] = __ldg(reinterpret_cast<const int4*>(p.c.ranges + p.c.pair(page, h) * 2 * D) + l);
+      // a page that is none: a mark that the choice refuses (no score is it)
+      ks[k] = ok ? __ldg(p.c.ks + p.c.pair(page, h)) : __uint_as_float(kNoPage);
     }
-    for (int o = lanes >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (l == 0 && i < c1) scores[i] = (float)acc * ks;
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      const int i = i0 + k * per + sub;
+      int acc = __dp4a(r[k].x ^ (int)0x80808080, qw.x, 0);
+      acc = __dp4a(r[k].y ^ (int)0x80808080, qw.y, acc);
+      acc = __dp4a(r[k].z ^ (int)0x80808080, qw.z, acc);
+      acc = __dp4a(r[k].w ^ (int)0x80808080, qw.w, acc);
+      for (int o = lanes >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      const float v = __float_as_uint(ks[k]) == kNoPage ? ks[k] : (float)acc * ks[k];
+      if (l == 0 && i < c1) scores[i] = v;
+    }
   }
-  if (bad) report(p.status, W4_ERR_INDEX);
-  const int any_bad = __syncthreads_or(bad);
-  if (tid == 0) {
-    // low half: CTAs that finished; high half: those that met a bad page
-    const int add = 1 + (any_bad ? 1 << 16 : 0);
-    const int was = atomic_add_acq_rel_gpu(p.arrived + bh, add);
-    last = (was & 0xFFFF) + 1 == ctas ? 1 + ((was + add) >> 16 != 0) : 0;
-    if (last) p.arrived[bh] = 0;
-  }
-  __syncthreads();
-  if (last != 1) return;   // not the last, or a page of the sequence is not one
+}
+
+// The choice of one (sequence, head).
+__global__ void __launch_bounds__(kTopThreads) choose_kernel(const SelectParams p) {
+  __shared__ TopShared sh;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const Seq s = sequence(p.bt, p.c.P, b);
+  if (!s.ok) return;   // said by the scores
+  const int np = (s.len + p.c.P - 1) / p.c.P;
+  const long long bh = (long long)b * p.c.H + h;
+  const float* scores = p.scores + bh * p.scores_row;
   const int count = min(np, p.max_sel);
   int32_t* sel = p.sel + bh * p.max_sel;
-  top_indexes(
-      sh, np, count,
-      [&](int i) {
-        return i < p.sink || i >= np - p.recent ? kForced : order_key(__ldcg(scores + i));
-      },
-      [&](int rank, int i) { sel[rank] = i; });
+  bool bad = false;
+  auto key = [&](int i) {
+    const float v = __ldcg(scores + i);
+    bad |= __float_as_uint(v) == kNoPage;
+    return i < p.sink || i >= np - p.recent ? kForced : order_key(v);
+  };
+  auto in_registers = [&](auto kPer) {
+    constexpr int per = decltype(kPer)::value;
+    uint32_t keys[per];
+#pragma unroll
+    for (int k = 0; k < per; ++k) keys[k] = tid * per + k < np ? key(tid * per + k) : 0u;
+    if (__syncthreads_or(bad)) return false;
+    top_registers<per>(sh, keys, np, count, [&](int rank, int k) { sel[rank] = tid * per + k; });
+    return true;
+  };
+  bool fine;
+  if (np <= kTopThreads) {
+    fine = in_registers(Const<1>());
+  } else if (np <= 4 * kTopThreads) {
+    fine = in_registers(Const<4>());
+  } else if (np <= 16 * kTopThreads) {
+    fine = in_registers(Const<16>());
+  } else {
+    for (int i = tid; i < np; i += kTopThreads) key(i);
+    fine = !__syncthreads_or(bad);
+    if (fine) top_indexes(sh, np, count, key, [&](int rank, int i) { sel[rank] = i; });
+  }
+  if (!fine) {
+    if (tid == 0) report(p.status, W4_ERR_INDEX);
+    return;
+  }
   for (int i = count + tid; i < p.max_sel; i += kTopThreads) sel[i] = -1;
   if (tid == 0) p.n_sel[bh] = count;
 }
@@ -244,13 +353,16 @@ struct EvictParams {
   int32_t* kept;
   int32_t* new_lens;
   int budget, sink, recent;
-  uint32_t* keys;     // [B][H][max_len rounded up]
+  int32_t* go;        // [B][H]
+  uint32_t* keys;     // [B][H][keys_row]: of sequences too long for registers
   long long keys_row;
   int32_t* status;
 };
 
-// One CTA per (sequence, head): the kept positions.  keys[0] afterwards tells
-// the gather whether there are any (kForced) or the sequence was refused (0).
+// One CTA per (sequence, head): the kept positions.  Sixteen consecutive
+// tokens lie in one page: a thread that holds that many reads them as four
+// 16-byte words.  go[b][h] tells the gather whether there are any (1) or the
+// sequence was refused (0).
 __global__ void __launch_bounds__(kTopThreads) evict_top_kernel(const EvictParams p) {
   __shared__ TopShared sh;
   pdl_launch_dependents();
@@ -259,109 +371,166 @@ __global__ void __launch_bounds__(kTopThreads) evict_top_kernel(const EvictParam
   const int P = p.c.P;
   const int len = __ldg(p.bt.lens + b);
   const long long bh = (long long)b * p.c.H + h;
-  uint32_t* keys = p.keys + bh * p.keys_row;
   const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
-  const bool in = len >= 0 && len <= p.bt.max_len;
-  bool bad = !in;
-  if (in) {
-    for (int t = tid; t < len; t += kTopThreads) {
+  bool bad = len < 0 || len > p.bt.max_len;
+  const int n = bad ? 0 : len, count = min(n, p.budget);
+  int32_t* kept = p.kept + bh * p.budget;
+  auto in_registers = [&](auto kPer) {
+    constexpr int per = decltype(kPer)::value;
+    uint32_t keys[per];
+    const int t0 = tid * per;
+#pragma unroll
+    for (int k = 0; k < per; ++k) keys[k] = 0u;
+    if (t0 < n) {
+      const int page = __ldg(table + t0 / P);
+      if (page < 0 || page >= p.c.num_pages) {
+        bad = true;
+      } else {
+        const float* w = p.c.weight + p.c.pair(page, h) * P + t0 % P;
+        float v[per];
+        if (per == 16 && (reinterpret_cast<uintptr_t>(p.c.weight) & 15) == 0) {
+#pragma unroll
+          for (int k = 0; k < per; k += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(w + k);
+            v[k] = x.x;
+            v[k + 1] = x.y;
+            v[k + 2] = x.z;
+            v[k + 3] = x.w;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < per; ++k) v[k] = w[k];
+        }
+#pragma unroll
+        for (int k = 0; k < per; ++k)
+          if (t0 + k < n)
+            keys[k] = t0 + k < p.sink || t0 + k >= n - p.recent ? kForced : order_key(v[k]);
+      }
+    }
+    if (__syncthreads_or(bad)) return false;
+    top_registers<per>(sh, keys, n, count, [&](int rank, int k) { kept[rank] = t0 + k; });
+    return true;
+  };
+  bool fine;
+  if (n <= 4 * kTopThreads) {
+    fine = in_registers(Const<4>());
+  } else if (n <= 16 * kTopThreads) {
+    fine = in_registers(Const<16>());
+  } else {
+    uint32_t* keys = p.keys + bh * p.keys_row;
+    for (int t = tid; t < n; t += kTopThreads) {
       const int page = __ldg(table + t / P);
       uint32_t u = kForced;
       if (page < 0 || page >= p.c.num_pages)
         bad = true;
-      else if (t >= p.sink && t < len - p.recent)
+      else if (t >= p.sink && t < n - p.recent)
         u = order_key(p.c.weight[p.c.pair(page, h) * P + t % P]);
       keys[t] = u;
     }
+    fine = !__syncthreads_or(bad);
+    if (fine)
+      top_indexes(
+          sh, n, count, [&](int i) { return keys[i]; },
+          [&](int rank, int i) { kept[rank] = i; });
   }
-  bad = __syncthreads_or(bad);
-  if (bad) {
-    if (tid == 0) {
-      report(p.status, W4_ERR_INDEX);
-      keys[0] = 0u;   // the gather's sign that this (sequence, head) is left alone
-    }
-    return;
+  if (tid == 0) {
+    p.go[bh] = fine;
+    if (!fine) report(p.status, W4_ERR_INDEX);
+    if (fine && h == 0) p.new_lens[b] = count;
   }
-  const int count = min(len, p.budget);
-  int32_t* kept = p.kept + bh * p.budget;
-  top_indexes(
-      sh, len, count, [&](int i) { return keys[i]; },
-      [&](int rank, int i) { kept[rank] = i; });
+  if (!fine) return;
   for (int i = count + tid; i < p.budget; i += kTopThreads) kept[i] = -1;
-  if (h == 0 && tid == 0) p.new_lens[b] = count;
-  __syncthreads();
-  if (tid == 0) keys[0] = kForced;
 }
 
-// One CTA per (destination page, head, sequence): the block's tokens, its
-// steps, then the codes rescaled, 16 bytes a thread.
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p) {
-  __shared__ long long src_blk[128];   // byte offset of each token's codes
-  __shared__ float src_ks[128], src_vs[128];
-  __shared__ float steps[2];
-  __shared__ __align__(16) uint8_t lo_sm[256 * 16], hi_sm[256 * 16];
+// One warp per (destination page, head, sequence): its tokens' places and
+// steps, then the codes, rescaled where the token's step is not the block's,
+// 16 bytes a lane and four rows in flight for keys and values each.  No
+// barriers: the bytes moved bound it.
+constexpr int kMoveWarps = 4;
+
+__global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const EvictParams p) {
+  struct Token {
+    long long from;   // byte offset of its codes
+    float ks, vs;     // step ratios
+  };
+  __shared__ Token tokens[kMoveWarps][128];
   pdl_launch_dependents();
   pdl_wait();
-  const int j = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = blockIdx.x * kMoveWarps + warp, h = blockIdx.y, b = blockIdx.z;
   const int P = p.c.P, D = p.c.D;
   const long long bh = (long long)b * p.c.H + h;
-  if (__ldcg(p.keys + bh * p.keys_row) != kForced) return;   // refused before
+  if (j >= p.dst_pages || __ldcg(p.go + bh) != 1) return;   // refused before
   const int count = min(__ldg(p.bt.lens + b), p.budget);
   const int n = min(P, count - j * P);
   if (n <= 0) return;
   const int dst = __ldg(p.dst_table + (long long)b * p.dst_pages + j);
   if (dst < 0 || dst >= p.c.num_pages) {
-    if (tid == 0) report(p.status, W4_ERR_INDEX);
+    if (lane == 0) report(p.status, W4_ERR_INDEX);
     return;
   }
-  if (tid < n) {
-    const int t = __ldcg(p.kept + bh * p.budget + (long long)j * P + tid);
+  Token* tk = tokens[warp];
+  float mk = 0.0f, mv = 0.0f;
+  for (int i = lane; i < n; i += 32) {
+    const int t = __ldcg(p.kept + bh * p.budget + (long long)j * P + i);
     const int page = __ldg(p.bt.table + (long long)b * p.bt.max_pages + t / P);   // checked before
-    src_blk[tid] = p.c.block(page, h) + (long long)(t % P) * D;
-    src_ks[tid] = p.c.ks[p.c.pair(page, h)];
-    src_vs[tid] = p.c.vs[p.c.pair(page, h)];
-    p.c.weight[p.c.pair(dst, h) * P + tid] = p.c.weight[p.c.pair(page, h) * P + t % P];
+    const long long pr = p.c.pair(page, h);
+    const Token x = {p.c.block(page, h) + (long long)(t % P) * D, p.c.ks[pr], p.c.vs[pr]};
+    p.c.weight[p.c.pair(dst, h) * P + i] = p.c.weight[pr * P + t % P];
+    mk = fmaxf(mk, x.ks);
+    mv = fmaxf(mv, x.vs);
+    tk[i] = x;
   }
-  __syncthreads();
-  if (tid < 64) {   // one warp each for keys and values
-    const float* s = tid < 32 ? src_ks : src_vs;
-    float m = 0.0f;
-    for (int i = tid & 31; i < n; i += 32) m = fmaxf(m, s[i]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) steps[tid >> 5] = m;
+  for (int o = 16; o > 0; o >>= 1) {
+    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
   }
-  __syncthreads();
-  if (tid == 0) {
-    p.c.ks[p.c.pair(dst, h)] = steps[0];
-    p.c.vs[p.c.pair(dst, h)] = steps[1];
+  for (int i = lane; i < n; i += 32) {   // steps to ratios
+    tk[i].ks = mk > 0.0f ? __fdiv_rn(tk[i].ks, mk) : 0.0f;
+    tk[i].vs = mv > 0.0f ? __fdiv_rn(tk[i].vs, mv) : 0.0f;
   }
-  const int vecs = D / 16, col = tid % vecs, r0 = tid / vecs, rstep = 256 / vecs;
-  const long long to = p.c.block(dst, h);
+  if (lane == 0) {
+    p.c.ks[p.c.pair(dst, h)] = mk;
+    p.c.vs[p.c.pair(dst, h)] = mv;
+  }
+  __syncwarp();
+  const int vecs = D / 16, col = lane % vecs, r0 = lane / vecs, rstep = 32 / vecs;
+  const long long to = p.c.block(dst, h) + col * 16;
   uint32_t lo[4] = {~0u, ~0u, ~0u, ~0u}, hi[4] = {0, 0, 0, 0};
+  auto rescaled = [](uint4 w, float ratio) {
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    if (ratio != 1.0f) {
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    const uint8_t* src = kv ? p.c.vc : p.c.kc;
-    uint8_t* out = (kv ? p.c.vc : p.c.kc) + to;
-    const float step = steps[kv];
-    for (int r = r0; r < n; r += rstep) {
-      uint4 w = *reinterpret_cast<const uint4*>(src + src_blk[r] + col * 16);
-      const float s0 = kv ? src_vs[r] : src_ks[r];
-      uint32_t x[4] = {w.x, w.y, w.z, w.w};
-      if (s0 != step) {
-        const float ratio = step > 0.0f ? __fdiv_rn(s0, step) : 0.0f;
+      for (int i = 0; i < 4; ++i) {
+        uint32_t y = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t y = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            y |= to_code((float)((int)((x[i] >> (8 * e)) & 0xFF) - 128) * ratio) << (8 * e);
-          x[i] = y;
-        }
+        for (int e = 0; e < 4; ++e)
+          y |= to_code((float)((int)((x[i] >> (8 * e)) & 0xFF) - 128) * ratio) << (8 * e);
+        x[i] = y;
       }
-      *reinterpret_cast<uint4*>(out + (long long)r * D + col * 16) =
-          make_uint4(x[0], x[1], x[2], x[3]);
-      if (kv == 0) {
+    }
+    return make_uint4(x[0], x[1], x[2], x[3]);
+  };
+  constexpr int kDeep = 4;
+  for (int r = r0; r < n; r += kDeep * rstep) {
+    uint4 k[kDeep], v[kDeep];
+#pragma unroll
+    for (int z = 0; z < kDeep; ++z) {
+      if (r + z * rstep < n) {
+        const long long from = tk[r + z * rstep].from + col * 16;
+        k[z] = __ldcs(reinterpret_cast<const uint4*>(p.c.kc + from));
+        v[z] = __ldcs(reinterpret_cast<const uint4*>(p.c.vc + from));
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < kDeep; ++z) {
+      const int rr = r + z * rstep;
+      if (rr < n) {
+        const uint4 a = rescaled(k[z], tk[rr].ks), c = rescaled(v[z], tk[rr].vs);
+        *reinterpret_cast<uint4*>(p.c.kc + to + (long long)rr * D) = a;
+        *reinterpret_cast<uint4*>(p.c.vc + to + (long long)rr * D) = c;
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           lo[i] = __vminu4(lo[i], x[i]);
@@ -371,31 +540,24 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p) {
     }
   }
   if (p.c.ranges == nullptr) return;
-  uint4* ls = reinterpret_cast<uint4*>(lo_sm);
-  uint4* hs = reinterpret_cast<uint4*>(hi_sm);
-  ls[tid] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  hs[tid] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  __syncthreads();
-  if (tid < 2 * vecs) {
-    const bool is_hi = tid >= vecs;
-    const uint4* s = is_hi ? hs : ls;
-    uint4 a = s[col];
-    for (int r = 1; r < rstep; ++r) {
-      const uint4 o = s[r * vecs + col];
-      a.x = is_hi ? __vmaxu4(a.x, o.x) : __vminu4(a.x, o.x);
-      a.y = is_hi ? __vmaxu4(a.y, o.y) : __vminu4(a.y, o.y);
-      a.z = is_hi ? __vmaxu4(a.z, o.z) : __vminu4(a.z, o.z);
-      a.w = is_hi ? __vmaxu4(a.w, o.w) : __vminu4(a.w, o.w);
+  for (int o = vecs; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = __vminu4(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+      hi[i] = __vmaxu4(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
     }
-    *(reinterpret_cast<uint4*>(p.c.ranges + p.c.pair(dst, h) * 2 * D) + tid) = a;
+  if (r0 == 0) {
+    uint4* rg = reinterpret_cast<uint4*>(p.c.ranges + p.c.pair(dst, h) * 2 * D) + col;
+    rg[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    rg[vecs] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   }
 }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-size_t select_scores_bytes(const Cache& c, const Batch& b) {
-  return up256((size_t)b.B * c.H * b.max_pages * 4);
-}
+long long scores_row(const Batch& b) { return (b.max_pages + 3) / 4 * 4; }
+
+long long evict_row(const Batch& b) { return (b.max_len + 63) / 64 * 64; }
 
 }  // namespace
 }  // namespace kv8
@@ -408,7 +570,7 @@ extern "C" size_t w4_kv8_select_workspace_bytes(const w4_kv8_cache* cache,
   kv8::Cache c;
   kv8::Batch b;
   if (kv8::view(cache, batch, &c, &b) != W4_OK) return 0;
-  return kv8::up256((size_t)b.B * c.H * 4) + kv8::select_scores_bytes(c, b);
+  return kv8::up256((size_t)b.B * c.H * kv8::scores_row(b) * 4);
 }
 
 extern "C" w4_status w4_kv8_select(int32_t* sel, int32_t* n_sel, int max_sel, int sink, int recent,
@@ -437,17 +599,21 @@ extern "C" w4_status w4_kv8_select(int32_t* sel, int32_t* n_sel, int max_sel, in
   p.max_sel = max_sel;
   p.sink = sink;
   p.recent = recent;
-  p.arrived = static_cast<int32_t*>(workspace);
-  p.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                      kv8::up256((size_t)p.bt.B * p.c.H * 4));
-  const int pages = max(1, (p.bt.max_len + p.c.P - 1) / p.c.P);
-  p.chunk = 1024;
-  while ((pages + p.chunk - 1) / p.chunk > 16384) p.chunk *= 2;   // `arrived` counts in 16 bits
+  p.scores = static_cast<float*>(workspace);
+  p.scores_row = kv8::scores_row(p.bt);
   p.status = status_dev;
-  return kv8::launch(kv8::select_kernel,
-                     dim3((unsigned)((pages + p.chunk - 1) / p.chunk), (unsigned)p.c.H,
-                          (unsigned)p.bt.B),
-                     kv8::kTopThreads, 0, (flags & W4_FLAG_PDL) != 0, stream, p);
+  // about four CTAs an SM, of at least 32 and at most 1024 pages
+  const int pages = max(1, (p.bt.max_len + p.c.P - 1) / p.c.P);
+  const long long most = (long long)pages * p.c.H * p.bt.B;
+  p.chunk = 32;
+  while (p.chunk < 1024 && most / p.chunk > 600) p.chunk *= 2;
+  st = kv8::launch(kv8::score_kernel,
+                   dim3((unsigned)((pages + p.chunk - 1) / p.chunk), (unsigned)p.c.H,
+                        (unsigned)p.bt.B),
+                   kv8::kScoreThreads, 0, (flags & W4_FLAG_PDL) != 0, stream, p);
+  if (st != W4_OK) return st;
+  return kv8::launch(kv8::choose_kernel, dim3((unsigned)p.c.H, (unsigned)p.bt.B), kv8::kTopThreads,
+                     0, true, stream, p);
 }
 
 extern "C" size_t w4_kv8_evict_workspace_bytes(const w4_kv8_cache* cache,
@@ -455,7 +621,7 @@ extern "C" size_t w4_kv8_evict_workspace_bytes(const w4_kv8_cache* cache,
   kv8::Cache c;
   kv8::Batch b;
   if (kv8::view(cache, batch, &c, &b) != W4_OK || budget < 1) return 0;
-  return (size_t)b.B * c.H * kv8::up256((size_t)(b.max_len + 1) * 4);
+  return kv8::up256((size_t)b.B * c.H * 4) + (size_t)b.B * c.H * kv8::evict_row(b) * 4;
 }
 
 extern "C" w4_status w4_kv8_evict(const int32_t* dst_table, int32_t* kept, int32_t* new_lens,
@@ -483,15 +649,17 @@ extern "C" w4_status w4_kv8_evict(const int32_t* dst_table, int32_t* kept, int32
   p.budget = budget;
   p.sink = sink;
   p.recent = recent;
-  p.keys = static_cast<uint32_t*>(workspace);
-  p.keys_row = (long long)(kv8::up256((size_t)(p.bt.max_len + 1) * 4) / 4);
+  p.go = static_cast<int32_t*>(workspace);
+  p.keys = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) +
+                                       kv8::up256((size_t)p.bt.B * p.c.H * 4));
+  p.keys_row = kv8::evict_row(p.bt);
   p.status = status_dev;
   w4_status r = kv8::launch(kv8::evict_top_kernel, dim3((unsigned)p.c.H, (unsigned)p.bt.B),
                             kv8::kTopThreads, 0, (flags & W4_FLAG_PDL) != 0, stream, p);
   if (r != W4_OK) return r;
-  const int most = min(budget, max(1, p.bt.max_len));
+  const int pages = (min(budget, max(1, p.bt.max_len)) + p.c.P - 1) / p.c.P;
   return kv8::launch(kv8::evict_move_kernel,
-                     dim3((unsigned)((most + p.c.P - 1) / p.c.P), (unsigned)p.c.H,
-                          (unsigned)p.bt.B),
-                     256, 0, true, stream, p);
+                     dim3((unsigned)((pages + kv8::kMoveWarps - 1) / kv8::kMoveWarps),
+                          (unsigned)p.c.H, (unsigned)p.bt.B),
+                     32 * kv8::kMoveWarps, 0, true, stream, p);
 }
