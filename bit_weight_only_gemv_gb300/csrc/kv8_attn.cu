@@ -242,11 +242,23 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
             bad = true;
           } else {
             d.page = page;
-            d.ks = __ldg(p.c.ks + p.c.pair(page, h));
-            d.vs = __ldg(p.c.vs + p.c.pair(page, h));
           }
         }
         meta[k & (kRing - 1)] = d;
+      }
+      __syncwarp();
+    };
+    // their steps, once the copies of the first are on their way
+    auto fill_steps = [&](int k0) {
+      const int k = k0 + lane;
+      if (k < count) {
+        Meta& d = meta[k & (kRing - 1)];
+        if (d.page >= 0) {
+          const long long at = p.c.pair(d.page, h);
+          const float ks = __ldg(p.c.ks + at), vs = __ldg(p.c.vs + at);
+          d.ks = ks;
+          d.vs = vs;
+        }
       }
       __syncwarp();
     };
@@ -269,9 +281,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
         }
       }
       if (++put == kStages) put = 0;
+      if (k > 0 && (k & 31) == 0) fill_steps(k);
     };
 #pragma unroll 1
     for (int k = 0; k < kStages; ++k) issue(k);
+    fill_steps(0);
     // --------------------------------------------------- query fragments
     uint32_t q[NQ][D / 16][2];
     float f[NQ][2];   // of this lane's two columns: scale log2(e) / the row's power of two

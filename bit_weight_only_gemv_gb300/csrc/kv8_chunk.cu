@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 
 // Joins the parts of cut units: one CTA per 16 rows.  Reading and adding
 // them all from one SM would take longer than computing them did.
-constexpr int kJoinRows = 16;
+constexpr int kJoinRows = 4;
 constexpr int kJoinThreads = 128;
 
 template <int D>

@@ -45,9 +45,14 @@ struct Run {
 
   // the CTA whose run holds item g
   __device__ __forceinline__ int holder(long long g) const {
+    if (total <= kNarrow) return (int)(((uint32_t)(g + 1) * (uint32_t)ctas - 1) / (uint32_t)total);
     return (int)(((g + 1) * ctas - 1) / total);
   }
-  __device__ __forceinline__ long long start(int c) const { return total * c / ctas; }
+  __device__ __forceinline__ long long start(int c) const {
+    if (total <= kNarrow) return (uint32_t)total * (uint32_t)c / (uint32_t)ctas;
+    return total * c / ctas;
+  }
+  static constexpr long long kNarrow = 1 << 22;   // times at most 1023 CTAs: 32 bits do
 };
 
 // Every thread of the CTA calls (kWarps warps; sm: kWarps + 2 words of shared

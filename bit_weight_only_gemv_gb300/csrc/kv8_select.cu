@@ -5,13 +5,11 @@
 // Both choices are the same operation on a list of keys: the `count` largest,
 // ties from the lowest index on, given back in ascending index order.  Keys
 // are fp32 values mapped to uint32 in order.  Up to 16384 keys stay in the
-// registers of 1024 threads, consecutive ones in a thread: the count-th
-// largest key T is found two bits at a time by counting (16 rounds of one
-// barrier each; a histogram's atomics would pile up on the few exponents that
-// scores and weights have: measured 29 us against 9 for 1024 keys), then one
-// prefix sum gives every thread its place.  Longer lists are read from memory
-// again in three radix passes (11, 11 and 10 bits, a shared-memory histogram
-// each) and one ordered pass.
+// registers, consecutive ones in a thread.  Three radix passes (11, 11 and 10
+// bits, a shared-memory histogram each) find the count-th largest key T and
+// how many keys equal to T are taken, then one prefix sum gives every thread
+// its place.  Longer lists are read from memory in each pass and written in
+// rounds.
 #include "kv8.cuh"
 
 namespace w4 {
@@ -67,6 +65,50 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
   return base + inc - v;
 }
 
+// The count-th largest key (there are more than `count`), and in *ties how
+// many of the keys equal to it belong to the `count`.  keys(add) calls
+// add(key) for every key that the thread sees, the same ones each time.
+template <typename Keys>
+__device__ uint32_t threshold(TopShared& sh, int count, Keys keys, int* ties) {
+  const int tid = threadIdx.x, nth = blockDim.x;
+  uint32_t prefix = 0, mask = 0, remaining = (uint32_t)count;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int bins = pass == 2 ? 1024 : 2048;
+    for (int i = tid; i < bins; i += nth) sh.hist[i] = 0;
+    __syncthreads();
+    keys([&](uint32_t u) {
+      if ((u & mask) == prefix) atomicAdd(&sh.hist[(u >> shift) & (bins - 1)], 1u);
+    });
+    __syncthreads();
+    // from the highest bin down: the one where the running count reaches
+    // `remaining`; a thread owns `per` consecutive bins
+    const int per = (bins + nth - 1) / nth;
+    uint32_t mine = 0;
+    for (int j = 0; j < per; ++j)
+      if (tid * per + j < bins) mine += sh.hist[bins - 1 - tid * per - j];
+    uint32_t total;
+    uint32_t before = block_scan(mine, sh.warp_sum, &total);
+    if (before < remaining && before + mine >= remaining) {
+      for (int j = 0; j < per; ++j) {
+        const uint32_t c = sh.hist[bins - 1 - tid * per - j];
+        if (before < remaining && before + c >= remaining) {
+          sh.prefix = prefix | ((uint32_t)(bins - 1 - tid * per - j) << shift);
+          sh.remaining = remaining - before;
+        }
+        before += c;
+      }
+    }
+    __syncthreads();
+    prefix = sh.prefix;
+    remaining = sh.remaining;
+    mask |= (uint32_t)(bins - 1) << shift;
+    __syncthreads();
+  }
+  *ties = (int)remaining;
+  return prefix;
+}
+
 // Calls emit(rank, index) for the `count` largest of key(0) .. key(n - 1)
 // (count <= n), rank ascending with the index.  Every thread of the CTA calls.
 template <typename Key, typename Emit>
@@ -74,43 +116,14 @@ __device__ void top_indexes(TopShared& sh, int n, int count, Key key, Emit emit)
   const int tid = threadIdx.x, nth = blockDim.x;
   uint32_t T = 0, ties = 0;   // threshold key, and how many equal ones are taken
   if (count < n) {
-    uint32_t prefix = 0, mask = 0, remaining = (uint32_t)count;
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const int bins = pass == 2 ? 1024 : 2048;
-      for (int i = tid; i < bins; i += nth) sh.hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < n; i += nth) {
-        const uint32_t u = key(i);
-        if ((u & mask) == prefix) atomicAdd(&sh.hist[(u >> shift) & (bins - 1)], 1u);
-      }
-      __syncthreads();
-      // from the highest bin down: the bin where the running count reaches
-      // `remaining`.  Thread t owns bins top, top - 1 (of its pair).
-      const int per = bins / kTopThreads > 0 ? bins / kTopThreads : 1;
-      uint32_t mine = 0;
-      if (tid * per < bins)
-        for (int j = 0; j < per; ++j) mine += sh.hist[bins - 1 - tid * per - j];
-      uint32_t total;
-      uint32_t before = block_scan(mine, sh.warp_sum, &total);
-      if (tid * per < bins) {
-        for (int j = 0; j < per; ++j) {
-          const uint32_t c = sh.hist[bins - 1 - tid * per - j];
-          if (before < remaining && before + c >= remaining) {
-            sh.prefix = prefix | ((uint32_t)(bins - 1 - tid * per - j) << shift);
-            sh.remaining = remaining - before;
-          }
-          before += c;
-        }
-      }
-      __syncthreads();
-      prefix = sh.prefix;
-      remaining = sh.remaining;
-      mask |= (uint32_t)(bins - 1) << shift;
-      __syncthreads();
-    }
-    T = prefix;
-    ties = remaining;
+    int t = 0;
+    T = threshold(
+        sh, count,
+        [&](auto add) {
+          for (int i = tid; i < n; i += nth) add(key(i));
+        },
+        &t);
+    ties = (uint32_t)t;
   }
   // ordered pass: rounds of nth consecutive indexes
   uint32_t taken = 0, seen_ties = 0;
@@ -132,39 +145,23 @@ __device__ void top_indexes(TopShared& sh, int n, int count, Key key, Emit emit)
 }
 
 // The same for keys in registers: thread t holds keys t * kPer .. of n (0 past
-// the end), kPer at most 16 and n at most 16384.  Calls emit(rank, k) for the
-// thread's k-th key.
+// the end), at most 16384 in all.  Calls emit(rank, k) for the thread's k-th key.
 template <int kPer, typename Emit>
 __device__ void top_registers(TopShared& sh, const uint32_t (&key)[kPer], int n, int count, Emit emit) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int have = max(0, min(kPer, n - tid * kPer));
   const bool all = count >= n;
-  // T: the largest value that at least `count` keys reach, two bits a round
   uint32_t T = 0;
-  if (!all) {
-    uint32_t* counts = sh.hist;   // [2][32] packed counts of a warp, rounds in turn
-#pragma unroll 1
-    for (int bit = 30, odd = 0; bit >= 0; bit -= 2, odd ^= 32) {
-      const uint32_t c1 = T | 1u << bit, c2 = T | 2u << bit, c3 = T | 3u << bit;
-      uint32_t mine = 0;   // three counts of up to 512 a warp, ten bits each
+  int ties = 0;   // keys equal to T that are taken
+  if (!all)
+    T = threshold(
+        sh, count,
+        [&](auto add) {
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const uint32_t u = key[k];
-        mine += (k < have ? (u >= c1 ? 1u : 0u) + (u >= c2 ? 1u << 10 : 0u) + (u >= c3 ? 1u << 20 : 0u)
-                          : 0u);
-      }
-      mine = __reduce_add_sync(0xffffffffu, mine);
-      if (lane == 0) counts[odd + warp] = mine;
-      __syncthreads();
-      const uint32_t w = lane < (int)(blockDim.x >> 5) ? counts[odd + lane] : 0u;
-      const int n1 = (int)__reduce_add_sync(0xffffffffu, w & 1023u);
-      const int n2 = (int)__reduce_add_sync(0xffffffffu, w >> 10 & 1023u);
-      const int n3 = (int)__reduce_add_sync(0xffffffffu, w >> 20);
-      if (n3 >= count) T = c3;
-      else if (n2 >= count) T = c2;
-      else if (n1 >= count) T = c1;
-    }
-  }
+          for (int k = 0; k < kPer; ++k)
+            if (k < have) add(key[k]);
+        },
+        &ties);
   // keys above T, and of those equal to T the first ones
   uint32_t above = 0, equal = 0;
 #pragma unroll
@@ -173,10 +170,8 @@ __device__ void top_registers(TopShared& sh, const uint32_t (&key)[kPer], int n,
       if (all || key[k] > T) ++above;
       else if (key[k] == T) ++equal;
     }
-  __syncthreads();   // the counts have been read
   uint32_t total;
   const uint32_t ex = block_scan(above | equal << 16, sh.warp_sum, &total);
-  const int ties = count - (int)(total & 0xFFFFu);   // equal ones that are taken (all: none)
   int rank = (int)(ex & 0xFFFFu), tie = (int)(ex >> 16);
   rank += min(tie, ties);
 #pragma unroll
@@ -263,25 +258,33 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
   const long long bh = (long long)b * p.c.H + h;
   float* scores = p.scores + bh * p.scores_row;
   const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
-  group_query(p, s, h, part, qi);
   const int lanes = 2 * D / 16;             // lanes of a page: 8, 16 or 32
   const int sub = lane / lanes, l = lane % lanes;
-  const int4 qw = *reinterpret_cast<const int4*>(&qi[l * 16 / D][l * 16 % D]);
   const int per = kScoreThreads / lanes;    // pages of the CTA at a time
   constexpr int kDeep = 4;
-  for (int i0 = c0 + warp * (32 / lanes); i0 < c1; i0 += kDeep * per) {
-    int4 r[kDeep];
-    float ks[kDeep];
+  int4 r[kDeep];
+  float ks[kDeep];
+  auto load = [&](int i0) {
+    int page[kDeep];
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
       const int i = i0 + k * per + sub;
-      int page = i < c1 ? __ldg(table + i) : 0;
-      const bool ok = page >= 0 && page < p.c.num_pages;
-      if (!ok) page = 0;
-      r[k] = __ldg(reinterpret_cast<const int4*>(p.c.ranges + p.c.pair(page, h) * 2 * D) + l);
-      // a page that is none: a mark that the choice refuses (no score is it)
-      ks[k] = ok ? __ldg(p.c.ks + p.c.pair(page, h)) : __uint_as_float(kNoPage);
+      page[k] = i < c1 ? __ldg(table + i) : 0;
     }
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      const bool ok = page[k] >= 0 && page[k] < p.c.num_pages;
+      if (!ok) page[k] = 0;
+      r[k] = __ldg(reinterpret_cast<const int4*>(p.c.ranges + p.c.pair(page[k], h) * 2 * D) + l);
+      // a page that is none: a mark that the choice refuses (no score is it)
+      ks[k] = ok ? __ldg(p.c.ks + p.c.pair(page[k], h)) : __uint_as_float(kNoPage);
+    }
+  };
+  int i0 = c0 + warp * (32 / lanes);
+  load(i0);                                 // on their way while the query is summed
+  group_query(p, s, h, part, qi);
+  const int4 qw = *reinterpret_cast<const int4*>(&qi[l * 16 / D][l * 16 % D]);
+  while (true) {
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
       const int i = i0 + k * per + sub;
@@ -293,6 +296,9 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
       const float v = __float_as_uint(ks[k]) == kNoPage ? ks[k] : (float)acc * ks[k];
       if (l == 0 && i < c1) scores[i] = v;
     }
+    i0 += kDeep * per;
+    if (i0 >= c1) break;
+    load(i0);
   }
 }
 
@@ -325,14 +331,13 @@ __global__ void __launch_bounds__(kTopThreads) choose_kernel(const SelectParams 
     return true;
   };
   bool fine;
-  if (np <= kTopThreads) {
-    fine = in_registers(Const<1>());
-  } else if (np <= 4 * kTopThreads) {
+  const int nth = blockDim.x;
+  if (np <= 4 * nth) {
     fine = in_registers(Const<4>());
-  } else if (np <= 16 * kTopThreads) {
+  } else if (np <= 16 * nth) {
     fine = in_registers(Const<16>());
   } else {
-    for (int i = tid; i < np; i += kTopThreads) key(i);
+    for (int i = tid; i < np; i += nth) key(i);
     fine = !__syncthreads_or(bad);
     if (fine) top_indexes(sh, np, count, key, [&](int rank, int i) { sel[rank] = i; });
   }
@@ -340,7 +345,7 @@ __global__ void __launch_bounds__(kTopThreads) choose_kernel(const SelectParams 
     if (tid == 0) report(p.status, W4_ERR_INDEX);
     return;
   }
-  for (int i = count + tid; i < p.max_sel; i += kTopThreads) sel[i] = -1;
+  for (int i = count + tid; i < p.max_sel; i += nth) sel[i] = -1;
   if (tid == 0) p.n_sel[bh] = count;
 }
 
@@ -412,13 +417,14 @@ __global__ void __launch_bounds__(kTopThreads) evict_top_kernel(const EvictParam
     return true;
   };
   bool fine;
-  if (n <= 4 * kTopThreads) {
+  const int nth = blockDim.x;
+  if (n <= 4 * nth) {
     fine = in_registers(Const<4>());
-  } else if (n <= 16 * kTopThreads) {
+  } else if (n <= 16 * nth) {
     fine = in_registers(Const<16>());
   } else {
     uint32_t* keys = p.keys + bh * p.keys_row;
-    for (int t = tid; t < n; t += kTopThreads) {
+    for (int t = tid; t < n; t += nth) {
       const int page = __ldg(table + t / P);
       uint32_t u = kForced;
       if (page < 0 || page >= p.c.num_pages)
@@ -439,7 +445,7 @@ __global__ void __launch_bounds__(kTopThreads) evict_top_kernel(const EvictParam
     if (fine && h == 0) p.new_lens[b] = count;
   }
   if (!fine) return;
-  for (int i = count + tid; i < p.budget; i += kTopThreads) kept[i] = -1;
+  for (int i = count + tid; i < p.budget; i += nth) kept[i] = -1;
 }
 
 // One warp per (destination page, head, sequence): its tokens' places and
@@ -555,6 +561,10 @@ __global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const Evict
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
+// Threads of a choice among n keys: a small CTA's barriers are cheaper, and
+// 1024 threads hold 16 keys each at most.
+int choice_threads(int n) { return n <= 1024 ? 256 : n <= 8192 ? 512 : kTopThreads; }
+
 long long scores_row(const Batch& b) { return (b.max_pages + 3) / 4 * 4; }
 
 long long evict_row(const Batch& b) { return (b.max_len + 63) / 64 * 64; }
@@ -602,18 +612,18 @@ extern "C" w4_status w4_kv8_select(int32_t* sel, int32_t* n_sel, int max_sel, in
   p.scores = static_cast<float*>(workspace);
   p.scores_row = kv8::scores_row(p.bt);
   p.status = status_dev;
-  // about four CTAs an SM, of at least 32 and at most 1024 pages
+  // about eight CTAs an SM, of at least 32 and at most 1024 pages
   const int pages = max(1, (p.bt.max_len + p.c.P - 1) / p.c.P);
   const long long most = (long long)pages * p.c.H * p.bt.B;
   p.chunk = 32;
-  while (p.chunk < 1024 && most / p.chunk > 600) p.chunk *= 2;
+  while (p.chunk < 1024 && most / p.chunk > 1400) p.chunk *= 2;
   st = kv8::launch(kv8::score_kernel,
                    dim3((unsigned)((pages + p.chunk - 1) / p.chunk), (unsigned)p.c.H,
                         (unsigned)p.bt.B),
                    kv8::kScoreThreads, 0, (flags & W4_FLAG_PDL) != 0, stream, p);
   if (st != W4_OK) return st;
-  return kv8::launch(kv8::choose_kernel, dim3((unsigned)p.c.H, (unsigned)p.bt.B), kv8::kTopThreads,
-                     0, true, stream, p);
+  return kv8::launch(kv8::choose_kernel, dim3((unsigned)p.c.H, (unsigned)p.bt.B),
+                     kv8::choice_threads(pages), 0, true, stream, p);
 }
 
 extern "C" size_t w4_kv8_evict_workspace_bytes(const w4_kv8_cache* cache,
@@ -655,7 +665,7 @@ extern "C" w4_status w4_kv8_evict(const int32_t* dst_table, int32_t* kept, int32
   p.keys_row = kv8::evict_row(p.bt);
   p.status = status_dev;
   w4_status r = kv8::launch(kv8::evict_top_kernel, dim3((unsigned)p.c.H, (unsigned)p.bt.B),
-                            kv8::kTopThreads, 0, (flags & W4_FLAG_PDL) != 0, stream, p);
+                            kv8::choice_threads(p.bt.max_len), 0, (flags & W4_FLAG_PDL) != 0, stream, p);
   if (r != W4_OK) return r;
   const int pages = (min(budget, max(1, p.bt.max_len)) + p.c.P - 1) / p.c.P;
   return kv8::launch(kv8::evict_move_kernel,

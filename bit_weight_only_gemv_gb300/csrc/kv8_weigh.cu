@@ -115,6 +115,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
     const int R = s.n * p.G;
     const int count = (sl1 - sl0 - warp + kWarps - 1) / kWarps;
+    auto fill_steps = [&](int k0) {   // of descriptions k0 .. k0 + 31
+      const int k = k0 + lane;
+      if (k < count) {
+        Meta& d = meta[k & (kRing - 1)];
+        if (d.page >= 0) d.ks = __ldg(p.c.ks + p.c.pair(d.page, h));
+      }
+      __syncwarp();
+    };
     auto issue = [&](int k) {
       if (k >= count || dead) return;
       if ((k & 31) == 0) {   // descriptions of the next 32 slices
@@ -128,7 +136,6 @@ __global__ void __launch_bounds__(kThreads, 2)
               report(p.status, W4_ERR_INDEX);
             } else {
               d.page = page;
-              d.ks = __ldg(p.c.ks + p.c.pair(page, h));
             }
           }
           meta[kk & (kRing - 1)] = d;
@@ -148,9 +155,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if (++put == kStages) put = 0;
+      if (k > 0 && (k & 31) == 0) fill_steps(k);   // once its first copy is on its way
     };
 #pragma unroll 1
     for (int k = 0; k < kStages; ++k) issue(k);
+    fill_steps(0);
     uint32_t q[NQ][D / 16][2];
     float f[NQ][2], lse2[NQ][2];
 #pragma unroll

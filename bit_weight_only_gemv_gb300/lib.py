@@ -770,8 +770,16 @@ def _kv8_bytes(t) -> int:
 
 def _kv8_call(fn, name, args, keep):
     """call(pdl=False, stream=None) that enqueues fn(*args) again."""
+    dev = keep[0].device.index
+    if dev is None:
+        dev = torch.cuda.current_device()
+    raw = torch._C._cuda_getCurrentRawStream   # current_stream() builds an object each time
+
     def call(pdl: bool = False, stream=None):
-        _check(fn(*args, W4_FLAG_PDL if pdl else 0, _stream(stream)), name)
+        code = fn(*args, W4_FLAG_PDL if pdl else 0,
+                  raw(dev) if stream is None else stream.cuda_stream)
+        if code:
+            _check(code, name)
 
     call.tensors = keep
     return call
