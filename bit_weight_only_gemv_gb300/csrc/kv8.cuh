@@ -77,10 +77,12 @@ w4_status check_q(const void* q, size_t q_row_stride, int q_heads, const Cache& 
 
 inline bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
-// host: launch with or without the programmatic-dependent attribute.
+// host: launch as a programmatic dependent of the previous kernel in the
+// stream.  Every kernel here waits for that one before it reads or writes
+// anything, so this is always right, and hides the launch and the set-up.
 template <typename... KArgs, typename... Args>
-w4_status launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, bool pdl,
-                 w4_stream_t stream, Args... args) {
+w4_status launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, w4_stream_t stream,
+                 Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
@@ -90,7 +92,7 @@ w4_status launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, bo
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
   if (e != cudaSuccess) {
     note_cuda_error(e);

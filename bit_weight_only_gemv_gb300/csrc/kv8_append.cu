@@ -247,7 +247,7 @@ extern "C" w4_status w4_kv8_append(const w4_kv8_cache* cache, const w4_kv8_batch
   const long long nt = (b.max_new + c.P - 2) / c.P + 1;
   const int threads = b.max_new == 1 ? 64 : 256;
   return kv8::launch(kv8::append_kernel, dim3((unsigned)nt, (unsigned)c.H, (unsigned)(2 * b.B)),
-                     threads, 0, (flags & W4_FLAG_PDL) != 0, stream, c, b,
+                     threads, 0, stream, c, b,
                      static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
                      (long long)row_stride, status_dev);
 }

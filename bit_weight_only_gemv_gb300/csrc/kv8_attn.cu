@@ -189,13 +189,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
       h = entry - b * p.c.H;
       n_pages = chosen(p, entry, &bad);
       t = unit_tile(p, s, 0, kRows, n_pages);
-      rt = (int)(off / t.slices);
+      rt = quotient(off, t.slices);
       sl0 = (int)(off - (long long)rt * t.slices);
       t = unit_tile(p, s, rt, kRows, n_pages);
       left = (long long)t.slices * rts - off;
     } else {
       const long long per = head_slices(s, p.G, p.window, kRows, kSlice);
-      h = (int)(off / per);
+      h = quotient(off, per);
       long long rem = off - per * h;
       t = unit_tile(p, s, 0, kRows, -1);
       while (rem >= t.slices) {
@@ -210,6 +210,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
     const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
     const int R = s.n * p.G;
 
+    uint2 raw[NQ][D / 16];   // query rows, on their way
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int r = rt * kRows + 8 * n + i;
+      load_query<D>(r < R ? p.q + (long long)(s.row0 + r / p.G) * p.q_stride +
+                                (long long)(h * p.G + r % p.G) * D
+                          : nullptr,
+                    j, raw[n]);
+    }
     // ------------------------- this warp's slices, the first on their way
     const int count = (sl1 - sl0 - warp + kWarps - 1) / kWarps;   // may be <= 0
     auto fill = [&](int k0) {   // descriptions k0 .. k0 + 31
@@ -291,11 +300,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
     float f[NQ][2];   // of this lane's two columns: scale log2(e) / the row's power of two
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const int r = rt * kRows + 8 * n + i;
-      const __nv_bfloat16* row =
-          r < R ? p.q + (long long)(s.row0 + r / p.G) * p.q_stride + (long long)(h * p.G + r % p.G) * D
-                : nullptr;
-      const float down = load_query<D>(row, j, q[n]);
+      const float down = scale_query<D>(raw[n], q[n]);
       f[n][0] = __shfl_sync(0xffffffffu, down, 8 * j) * (p.scale * kLog2e);
       f[n][1] = __shfl_sync(0xffffffffu, down, 8 * j + 4) * (p.scale * kLog2e);
     }
@@ -507,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
           float M = -INFINITY, L = 0.0f;
           bool none = false;
           // the first CTA's part began the unit, the others' run began inside it
+#pragma unroll 8
           for (int c = c0; c <= c1; ++c) {
             const int sl = c == c0 ? 2 * c + 1 : 2 * c;
             const float2 st = __ldcg(reinterpret_cast<const float2*>(p.part_stats) +
@@ -581,7 +587,7 @@ Plan plan_token(const Cache& c, const Batch& b, int G, int sms) {
 }
 
 template <int D, int NQ>
-w4_status launch_token(const AttnParams& p, int ctas, bool pdl, w4_stream_t stream, int dev) {
+w4_status launch_token(const AttnParams& p, int ctas, w4_stream_t stream, int dev) {
   static std::mutex mu;
   static bool done[64] = {};
   if (dev < 0 || dev >= 64) return W4_ERR_DEVICE;
@@ -599,7 +605,7 @@ w4_status launch_token(const AttnParams& p, int ctas, bool pdl, w4_stream_t stre
       done[dev] = true;
     }
   }
-  return launch(attn_token_kernel<D, NQ>, dim3((unsigned)ctas), kThreads, Shape<D, NQ>::kSmem, pdl,
+  return launch(attn_token_kernel<D, NQ>, dim3((unsigned)ctas), kThreads, Shape<D, NQ>::kSmem,
                 stream, p);
 }
 
@@ -660,7 +666,6 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
   DeviceInfo di;
   const bool have = current_device(&dev, &di);
   if (!have) planning_device(&di);
-  const bool pdl = (flags & W4_FLAG_PDL) != 0;
   if (sel == nullptr && (long long)p.bt.max_new * (q_heads / p.c.H) >= kv8::kChunkRows) {
     if (workspace == nullptr ||
         workspace_bytes < kv8::chunk_workspace_bytes(p.c, p.bt, q_heads / p.c.H, di.sms))
@@ -669,7 +674,7 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
     const kv8::ChunkArgs a = {static_cast<__nv_bfloat16*>(out), lse,
                               static_cast<const __nv_bfloat16*>(q), (long long)q_row_stride,
                               q_heads, scale, window, status_dev};
-    return kv8::chunk_attn(p.c, p.bt, a, workspace, di.sms, dev, pdl, stream);
+    return kv8::chunk_attn(p.c, p.bt, a, workspace, di.sms, dev, stream);
   }
   const kv8::Plan pl = kv8::plan_token(p.c, p.bt, q_heads / p.c.H, di.sms);
   if (workspace == nullptr || workspace_bytes < pl.bytes) return W4_ERR_WORKSPACE;
@@ -697,11 +702,11 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
     return W4_ERR_LAUNCH;
   }
   switch (p.c.D * 4 + pl.nq) {
-    case 64 * 4 + 1: return kv8::launch_token<64, 1>(p, pl.ctas, pdl, stream, dev);
-    case 64 * 4 + 2: return kv8::launch_token<64, 2>(p, pl.ctas, pdl, stream, dev);
-    case 128 * 4 + 1: return kv8::launch_token<128, 1>(p, pl.ctas, pdl, stream, dev);
-    case 128 * 4 + 2: return kv8::launch_token<128, 2>(p, pl.ctas, pdl, stream, dev);
-    case 256 * 4 + 1: return kv8::launch_token<256, 1>(p, pl.ctas, pdl, stream, dev);
-    default: return kv8::launch_token<256, 2>(p, pl.ctas, pdl, stream, dev);
+    case 64 * 4 + 1: return kv8::launch_token<64, 1>(p, pl.ctas, stream, dev);
+    case 64 * 4 + 2: return kv8::launch_token<64, 2>(p, pl.ctas, stream, dev);
+    case 128 * 4 + 1: return kv8::launch_token<128, 1>(p, pl.ctas, stream, dev);
+    case 128 * 4 + 2: return kv8::launch_token<128, 2>(p, pl.ctas, stream, dev);
+    case 256 * 4 + 1: return kv8::launch_token<256, 1>(p, pl.ctas, stream, dev);
+    default: return kv8::launch_token<256, 2>(p, pl.ctas, stream, dev);
   }
 }

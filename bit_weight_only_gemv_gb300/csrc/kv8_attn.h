@@ -28,7 +28,7 @@ struct ChunkArgs {
 
 size_t chunk_workspace_bytes(const Cache& c, const Batch& b, int G, int sms);
 w4_status chunk_attn(const Cache& c, const Batch& b, const ChunkArgs& a, void* workspace,
-                     int sms, int dev, bool pdl, w4_stream_t stream);
+                     int sms, int dev, w4_stream_t stream);
 
 }  // namespace kv8
 }  // namespace w4

@@ -981,7 +981,7 @@ Plan plan_chunk(const Cache& c, const Batch& b, int G, int sms) {
 }
 
 template <int D>
-w4_status launch_chunk(ChunkParams& p, int sms, int dev, bool pdl, w4_stream_t stream) {
+w4_status launch_chunk(ChunkParams& p, int sms, int dev, w4_stream_t stream) {
   using S = Shape<D>;
   static std::mutex mu;
   static bool done[64] = {};
@@ -1005,11 +1005,11 @@ w4_status launch_chunk(ChunkParams& p, int sms, int dev, bool pdl, w4_stream_t s
     return W4_ERR_LAUNCH;
   }
   const w4_status st =
-      launch(attn_chunk_kernel<D>, dim3((unsigned)sms), S::kThreads, S::kSmem, pdl, stream, p);
+      launch(attn_chunk_kernel<D>, dim3((unsigned)sms), S::kThreads, S::kSmem, stream, p);
   if (st != W4_OK) return st;
   return launch(attn_join_kernel<D>,
                 dim3((unsigned)(p.rts * (S::kRows / kJoinRows)), (unsigned)p.c.H, (unsigned)p.bt.B),
-                kJoinThreads, 0, true, stream, p);
+                kJoinThreads, 0, stream, p);
 }
 
 }  // namespace
@@ -1019,7 +1019,7 @@ size_t chunk_workspace_bytes(const Cache& c, const Batch& b, int G, int sms) {
 }
 
 w4_status chunk_attn(const Cache& c, const Batch& b, const ChunkArgs& a, void* workspace, int sms,
-                     int dev, bool pdl, w4_stream_t stream) {
+                     int dev, w4_stream_t stream) {
   ChunkParams p = {};
   p.c = c;
   p.bt = b;
@@ -1032,9 +1032,9 @@ w4_status chunk_attn(const Cache& c, const Batch& b, const ChunkArgs& a, void* w
   p.parts = reinterpret_cast<float*>(ws + pl.cut);
   p.part_stats = reinterpret_cast<float*>(ws + pl.cut + pl.parts);
   switch (c.D) {
-    case 64: return launch_chunk<64>(p, sms, dev, pdl, stream);
-    case 128: return launch_chunk<128>(p, sms, dev, pdl, stream);
-    default: return launch_chunk<256>(p, sms, dev, pdl, stream);
+    case 64: return launch_chunk<64>(p, sms, dev, stream);
+    case 128: return launch_chunk<128>(p, sms, dev, stream);
+    default: return launch_chunk<256>(p, sms, dev, stream);
   }
 }
 

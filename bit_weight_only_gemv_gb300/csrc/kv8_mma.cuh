@@ -78,19 +78,25 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // = (lane / 4, lane % 4) holds row i; its D / 4 channels are, for each
 // 128-channel half of the head (or all 64), the 16-byte chunks of codes that
 // the same j reads from a key row: 2j and 2j + 1 of eight, or j of four.
-// Step s of 16 channels multiplies word s of those.  `row` null: zeros.
-// Returns the row's down factor.
+// Step s of 16 channels multiplies word s of those.  `row` null: zeros.  The
+// loads are apart from their use, so that other chains run in between.
 template <int D>
-__device__ __forceinline__ float load_query(const __nv_bfloat16* row, int j, uint32_t (&b)[D / 16][2]) {
-  uint2 raw[D / 16];
-  float m = 0.0f;
+__device__ __forceinline__ void load_query(const __nv_bfloat16* row, int j, uint2 (&raw)[D / 16]) {
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
     const int ch = D == 64 ? 16 * j + 4 * s : 128 * (s / 8) + 32 * j + 4 * (s % 8);
     raw[s] = row == nullptr ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(row + ch));
+  }
+}
+
+// The loaded row as fragments; returns the row's down factor.
+template <int D>
+__device__ __forceinline__ float scale_query(const uint2 (&raw)[D / 16], uint32_t (&b)[D / 16][2]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s)
     m = fmaxf(m, fmaxf(fmaxf(fabsf(bf16_lo(raw[s].x)), fabsf(bf16_hi(raw[s].x))),
                        fmaxf(fabsf(bf16_lo(raw[s].y)), fabsf(bf16_hi(raw[s].y)))));
-  }
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
   float up, down;

@@ -15,13 +15,18 @@ struct Tile {
   int slices;
 };
 
+// a / b, whose quotient fits an int.
+__device__ __forceinline__ int quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
+}
+
 // Rows rt * rows .. of the n G query rows that a key head has in a sequence.
 __device__ __forceinline__ Tile tile_of(const Seq& s, int G, int window, int rt, int rows, int slice) {
   Tile t;
   const int R = s.n * G;
   const int r0 = rt * rows, r1 = min(R, r0 + rows) - 1;
-  t.pmin = s.len - s.n + r0 / G;
-  t.pmax = s.len - s.n + r1 / G;
+  t.pmin = s.len - s.n + (s.n == 1 ? 0 : r0 / G);
+  t.pmax = s.len - s.n + (s.n == 1 ? 0 : r1 / G);
   t.lo = window > 0 ? max(0, t.pmin + 1 - window) / slice * slice : 0;
   t.hi = t.pmax + 1;
   // at least one slice, if an empty one: the rows are written too

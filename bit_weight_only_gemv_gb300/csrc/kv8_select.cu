@@ -620,10 +620,10 @@ extern "C" w4_status w4_kv8_select(int32_t* sel, int32_t* n_sel, int max_sel, in
   st = kv8::launch(kv8::score_kernel,
                    dim3((unsigned)((pages + p.chunk - 1) / p.chunk), (unsigned)p.c.H,
                         (unsigned)p.bt.B),
-                   kv8::kScoreThreads, 0, (flags & W4_FLAG_PDL) != 0, stream, p);
+                   kv8::kScoreThreads, 0, stream, p);
   if (st != W4_OK) return st;
   return kv8::launch(kv8::choose_kernel, dim3((unsigned)p.c.H, (unsigned)p.bt.B),
-                     kv8::choice_threads(pages), 0, true, stream, p);
+                     kv8::choice_threads(pages), 0, stream, p);
 }
 
 extern "C" size_t w4_kv8_evict_workspace_bytes(const w4_kv8_cache* cache,
@@ -665,11 +665,11 @@ extern "C" w4_status w4_kv8_evict(const int32_t* dst_table, int32_t* kept, int32
   p.keys_row = kv8::evict_row(p.bt);
   p.status = status_dev;
   w4_status r = kv8::launch(kv8::evict_top_kernel, dim3((unsigned)p.c.H, (unsigned)p.bt.B),
-                            kv8::choice_threads(p.bt.max_len), 0, (flags & W4_FLAG_PDL) != 0, stream, p);
+                            kv8::choice_threads(p.bt.max_len), 0, stream, p);
   if (r != W4_OK) return r;
   const int pages = (min(budget, max(1, p.bt.max_len)) + p.c.P - 1) / p.c.P;
   return kv8::launch(kv8::evict_move_kernel,
                      dim3((unsigned)((pages + kv8::kMoveWarps - 1) / kv8::kMoveWarps),
                           (unsigned)p.c.H, (unsigned)p.bt.B),
-                     32 * kv8::kMoveWarps, 0, true, stream, p);
+                     32 * kv8::kMoveWarps, 0, stream, p);
 }

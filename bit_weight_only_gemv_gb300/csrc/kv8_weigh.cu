@@ -110,10 +110,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   while (g < run.g1 && !dead) {
     const Seq s = sequence(p.bt, p.c.P, b);
     const Tile t = tile_of(s, p.G, p.window, 0, kRows, kSlice);   // one row tile
-    const int h = (int)(off / t.slices), sl0 = (int)(off - (long long)h * t.slices);
+    const int h = quotient(off, t.slices), sl0 = (int)(off - (long long)h * t.slices);
     const int sl1 = (int)min((long long)t.slices, sl0 + (run.g1 - g));
     const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
     const int R = s.n * p.G;
+    uint2 raw[NQ][D / 16];   // query rows, on their way
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int r = 8 * n + i;
+      load_query<D>(r < R ? p.q + (long long)(s.row0 + r / p.G) * p.q_stride +
+                                (long long)(h * p.G + r % p.G) * D
+                          : nullptr,
+                    j, raw[n]);
+    }
     const int count = (sl1 - sl0 - warp + kWarps - 1) / kWarps;
     auto fill_steps = [&](int k0) {   // of descriptions k0 .. k0 + 31
       const int k = k0 + lane;
@@ -164,11 +173,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float f[NQ][2], lse2[NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const int r = 8 * n + i;
-      const __nv_bfloat16* row =
-          r < R ? p.q + (long long)(s.row0 + r / p.G) * p.q_stride + (long long)(h * p.G + r % p.G) * D
-                : nullptr;
-      const float down = load_query<D>(row, j, q[n]);
+      const float down = scale_query<D>(raw[n], q[n]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         f[n][c] = __shfl_sync(0xffffffffu, down, 8 * j + 4 * c) * (p.scale * kLog2e);
@@ -423,7 +428,7 @@ w4_status allow_smem(K kern, int smem, int dev, bool* done) {
 }
 
 template <int D, int NQ>
-w4_status launch_token(WeighParams& p, int sms, bool pdl, w4_stream_t stream, int dev) {
+w4_status launch_token(WeighParams& p, int sms, w4_stream_t stream, int dev) {
   static bool done[64] = {};
   if (!tensor_map(&p.tm_k, p.c.kc, p.c, kSlice)) {
     note_cuda_error(cudaErrorInvalidValue);
@@ -431,12 +436,12 @@ w4_status launch_token(WeighParams& p, int sms, bool pdl, w4_stream_t stream, in
   }
   const w4_status st = allow_smem(weigh_token_kernel<D, NQ>, Shape<D>::kSmem, dev, done);
   if (st != W4_OK) return st;
-  return launch(weigh_token_kernel<D, NQ>, dim3((unsigned)(2 * sms)), kThreads, Shape<D>::kSmem, pdl,
+  return launch(weigh_token_kernel<D, NQ>, dim3((unsigned)(2 * sms)), kThreads, Shape<D>::kSmem,
                 stream, p);
 }
 
 template <int D>
-w4_status launch_chunk(const WeighParams& p, bool pdl, w4_stream_t stream, int dev) {
+w4_status launch_chunk(const WeighParams& p, w4_stream_t stream, int dev) {
   constexpr int kSub = D == 256 ? 1 : 2;   // 128 registers of fragments are too many
   constexpr int kSmem = kChunk * D * 2 + kChunk * 4;
   static bool done[64] = {};
@@ -446,7 +451,7 @@ w4_status launch_chunk(const WeighParams& p, bool pdl, w4_stream_t stream, int d
   return launch(weigh_chunk_kernel<D, kSub>,
                 dim3((unsigned)((p.bt.max_len + tokens - 1) / tokens), (unsigned)p.c.H,
                      (unsigned)p.bt.B),
-                kThreads, kSmem, pdl, stream, p);
+                kThreads, kSmem, stream, p);
 }
 
 }  // namespace
@@ -478,21 +483,20 @@ extern "C" w4_status w4_kv8_weigh(const void* q, size_t q_row_stride, int q_head
   p.window = window;
   p.status = status_dev;
   if (p.bt.max_len == 0) return W4_OK;
-  const bool pdl = (flags & W4_FLAG_PDL) != 0;
   const long long rows = (long long)p.bt.max_new * p.G;
   if (rows > 16) {
     switch (p.c.D) {
-      case 64: return kv8::launch_chunk<64>(p, pdl, stream, dev);
-      case 128: return kv8::launch_chunk<128>(p, pdl, stream, dev);
-      default: return kv8::launch_chunk<256>(p, pdl, stream, dev);
+      case 64: return kv8::launch_chunk<64>(p, stream, dev);
+      case 128: return kv8::launch_chunk<128>(p, stream, dev);
+      default: return kv8::launch_chunk<256>(p, stream, dev);
     }
   }
   switch (p.c.D * 4 + (rows <= 8 ? 1 : 2)) {
-    case 64 * 4 + 1: return kv8::launch_token<64, 1>(p, di.sms, pdl, stream, dev);
-    case 64 * 4 + 2: return kv8::launch_token<64, 2>(p, di.sms, pdl, stream, dev);
-    case 128 * 4 + 1: return kv8::launch_token<128, 1>(p, di.sms, pdl, stream, dev);
-    case 128 * 4 + 2: return kv8::launch_token<128, 2>(p, di.sms, pdl, stream, dev);
-    case 256 * 4 + 1: return kv8::launch_token<256, 1>(p, di.sms, pdl, stream, dev);
-    default: return kv8::launch_token<256, 2>(p, di.sms, pdl, stream, dev);
+    case 64 * 4 + 1: return kv8::launch_token<64, 1>(p, di.sms, stream, dev);
+    case 64 * 4 + 2: return kv8::launch_token<64, 2>(p, di.sms, stream, dev);
+    case 128 * 4 + 1: return kv8::launch_token<128, 1>(p, di.sms, stream, dev);
+    case 128 * 4 + 2: return kv8::launch_token<128, 2>(p, di.sms, stream, dev);
+    case 256 * 4 + 1: return kv8::launch_token<256, 1>(p, di.sms, stream, dev);
+    default: return kv8::launch_token<256, 2>(p, di.sms, stream, dev);
   }
 }

@@ -683,6 +683,9 @@ w4_status w4a16_gemv_chain_task_plan(const w4_gemv_task *tasks, int n_tasks, int
  *     pages are not read.  A new row at a negative position (an empty
  *     sequence of a padded batch) is stored nowhere and sees nothing.
  *   - Calls are deterministic: no sum's order depends on timing.
+ *   - Every kernel is launched as a programmatic dependent and waits for the
+ *     kernel before it in the stream before it reads or writes anything:
+ *     W4_FLAG_PDL is accepted and changes nothing.
  *   - Codes past a sequence's length may hold anything.
  */
 typedef struct w4_kv8_cache {
