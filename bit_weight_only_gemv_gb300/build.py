@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4a16.so")
 SOURCES = ["gemv.cu", "chain.cu", "gemv_tc.cu", "gemm_tc.cu", "gather.cu", "quant.cu",
            "slot_pool.cu", "dev_pool.cu", "kv8_append.cu", "kv8_select.cu", "kv8_attn.cu",
-           "kv8_chunk.cu", "kv8_weigh.cu"]
+           "kv8_chunk.cu", "kv8_weigh.cu", "kv8_weigh_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -52,6 +52,7 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
                    os.path.join(CSRC, "tc_common.cuh"), os.path.join(CSRC, "pointer_view.h"),
                    os.path.join(CSRC, "kv8.cuh"), os.path.join(CSRC, "kv8_mma.cuh"),
                    os.path.join(CSRC, "kv8_attn.h"), os.path.join(CSRC, "kv8_runs.cuh"),
+                   os.path.join(CSRC, "kv8_tc.cuh"),
                    os.path.join(os.path.dirname(PKG), "include", "w4a16.h")]
     if not force and os.path.exists(LIB):
         newest = max(os.path.getmtime(d) for d in deps)

@@ -69,6 +69,17 @@ __device__ __forceinline__ uint32_t to_code(float v) {
   return (uint32_t)(__float2int_rn(fminf(fmaxf(v, -128.0f), 127.0f)) + 128);
 }
 
+// Codes of a word as bf16 pairs u - 128: byte u under 0x43 reads 128 + its
+// low seven bits once bit 7 is cleared; minus 128 where bit 7 was set, else minus 256.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t sel) {
+  const uint32_t t = __byte_perm(w, 0x43434343u, sel);
+  const uint32_t a = t & 0xFF7FFF7Fu;
+  const uint32_t b = (~t & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // host: W4_OK and the kernels' view, or the argument error.
 w4_status view(const w4_kv8_cache* c, const w4_kv8_batch* b, Cache* cv, Batch* bv);
 

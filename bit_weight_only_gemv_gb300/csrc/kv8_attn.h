@@ -26,6 +26,22 @@ struct ChunkArgs {
   int32_t* status;
 };
 
+struct WeighParams {
+  CUtensorMap tm_k;
+  Cache c;
+  Batch bt;
+  const __nv_bfloat16* q;
+  long long q_stride;
+  const float* lse;
+  int Hq, G;
+  float scale;
+  int window;
+  int32_t* status;
+};
+
+// w4_kv8_weigh for many query rows on a key head (kv8_weigh_tc.cu).
+w4_status weigh_many(const WeighParams& p, int dev, w4_stream_t stream);
+
 size_t chunk_workspace_bytes(const Cache& c, const Batch& b, int G, int sms);
 w4_status chunk_attn(const Cache& c, const Batch& b, const ChunkArgs& a, void* workspace,
                      int sms, int dev, w4_stream_t stream);

@@ -30,19 +30,6 @@ constexpr int kRing = 64;
 constexpr int kMinSlices = 16;
 constexpr long long kWait = 1LL << 31;   // about a second
 
-struct WeighParams {
-  CUtensorMap tm_k;
-  Cache c;
-  Batch bt;
-  const __nv_bfloat16* q;
-  long long q_stride;
-  const float* lse;
-  int Hq, G;
-  float scale;
-  int window;
-  int32_t* status;
-};
-
 // ------------------------------------------------------------ few rows
 template <int D>
 struct Shape {
@@ -245,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ------------------------------------------------------------ many rows
 constexpr int kChunk = 128;   // query rows in shared memory at a time
+constexpr long long kManyRows = 128;   // above: the tcgen05 kernel
 
 __device__ __forceinline__ void mma_bf16(float d[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -252,18 +240,6 @@ __device__ __forceinline__ void mma_bf16(float d[4], const uint32_t (&a)[4], uin
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Two codes as a bf16 pair u - 128 (sel picks the bytes): byte u under 0x43
-// reads 128 + its low seven bits once bit 7 is cleared; minus 128 where bit 7
-// was set, else minus 256.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t sel) {
-  const uint32_t t = __byte_perm(w, 0x43434343u, sel);
-  const uint32_t a = t & 0xFF7FFF7Fu;
-  const uint32_t b = (~t & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // One CTA per (block of tokens, head, sequence); kSub 16-token slices a warp.
@@ -484,6 +460,7 @@ extern "C" w4_status w4_kv8_weigh(const void* q, size_t q_row_stride, int q_head
   p.status = status_dev;
   if (p.bt.max_len == 0) return W4_OK;
   const long long rows = (long long)p.bt.max_new * p.G;
+  if (rows > kv8::kManyRows) return kv8::weigh_many(p, dev, stream);
   if (rows > 16) {
     switch (p.c.D) {
       case 64: return kv8::launch_chunk<64>(p, stream, dev);
