@@ -12,7 +12,8 @@
 // every warp held 32 tokens' keys as legacy MMA fragments: 123 us at 2 x 256
 // rows of 32 heads on 8k keys; this one 50 us).
 //
-// Roles: four warps per key tile that exponentiate and add, six that bring the
+// Roles: eight warps per key tile that exponentiate and add (a thread has a
+// token and half of the columns), six that bring the
 // query tiles in (two per buffer, so that several are on their way), one that issues
 // the MMAs.  Every wait is bounded.
 #include <algorithm>
@@ -38,7 +39,7 @@ template <int D>
 struct Shape {
   static constexpr int kTiles = D == 256 ? 1 : 2;   // key tiles of a CTA
   static constexpr int kBufs = D == 256 ? 2 : 3;    // query tiles in shared memory
-  static constexpr int kLoadWarp = 4 * kTiles;
+  static constexpr int kLoadWarp = 8 * kTiles;      // weights: four warps a key tile and half of the columns
   static constexpr int kLoadWarps = 6;
   static constexpr int kPerBuf = kLoadWarps / kBufs;
   static constexpr int kMmaWarp = kLoadWarp + kLoadWarps;
@@ -48,7 +49,8 @@ struct Shape {
   static constexpr int kLse = kQ + kBufs * kBytes;  // [kLseRing][kTile]
   static constexpr int kBars = kLse + kLseRing * kTile * 4;
   static constexpr int kMisc = kBars + 16 * 8;
-  static constexpr int kEnd = kMisc + 64 + 1024;
+  static constexpr int kSums = kMisc + 64;          // [kTiles][kTile]: the second halves' sums
+  static constexpr int kEnd = kSums + kTiles * kTile * 4 + 1024;
   // more than half an SM's: each CTA holds all of its tensor memory
   static constexpr int kSmem = kEnd > 117248 ? kEnd : 117248;
   static_assert(kSmem <= 232448 && 2 * kSmem > 232448, "shared memory");
@@ -62,9 +64,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   using S = Shape<D>;
   constexpr int kTiles = S::kTiles, kBufs = S::kBufs;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
-  uint8_t* sm = smem_raw + pad;
-  const uint32_t sb = smem_addr(sm);
+  uint8_t* sm = smem_raw;
+  const uint32_t sb = smem_addr(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](int i) { return sb + S::kBars + 8 * i; };
   float* lse = reinterpret_cast<float*>(sm + S::kLse);   // minus log2(e) lse; -inf: adds nothing
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(kSFull + i), 1);
-      mbar_init(bar(kSFree + i), 4);
+      mbar_init(bar(kSFree + i), 8);
     }
     *abort_flag = 0;
     mbar_init_fence();
@@ -131,8 +132,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   constexpr uint32_t tmem = 0;   // all 512 columns: they begin at 0
-  bool ok = __syncthreads_and(*tmem_slot == 0) != 0;
+  bool ok = __syncthreads_and(*tmem_slot == 0 && (sb & 1023u) == 0) != 0;
 
+  float* sums = reinterpret_cast<float*>(sm + S::kSums);
+  // of a thread that adds a token's weight in the end: its first half, its place
+  float sum = 0.0f;
+  int page = -1, from = 0;
+  long long at = 0;
+  bool mine = false;
   if (warp == S::kMmaWarp) {
     // -------------------------------------------------------- MMA issuer
     constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTile >> 3) << 17) |
@@ -201,10 +208,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     }
   } else {
     // -------------------------------------------------------- the weights
-    const int z = warp >> 2;
+    const int z = (warp >> 2) % kTiles, half = warp / (4 * kTiles);
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int tok = blk0 + z * kTile + (tid & 127);
-    int page = -1;
     float f = 0.0f;
     if (tok < s.len) {
       page = __ldg(table + tok / p.c.P);
@@ -216,7 +222,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       }
     }
     const uint64_t ff = pack2(f, f);
-    float sum = 0.0f;
     for (int t = 0; t < qtiles; ++t) {
       const int par = t & 1, r0 = r_lo + t * kTile;
       if (!wait_bar(bar(kSFull + 2 * par + z), (uint32_t)(t >> 1) & 1u, abort_flag)) {
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       const bool cut = __any_sync(0xffffffffu, lo > 0 || hi < kTile - 1);
       const float* nl = lse + (t % kLseRing) * kTile;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kTile; c0 += 32) {
+      for (int c0 = half * (kTile / 2); c0 < (half + 1) * (kTile / 2); c0 += 32) {
         float x[32];
         tc::tmem_ld<32>(tmem + lanes + (2 * par + z) * kTile + c0, x);
         float4 l4[8];
@@ -268,7 +273,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kSFree + 2 * par + z));
     }
-    if (ok && page >= 0) p.c.weight[p.c.pair(page, h) * p.c.P + tok % p.c.P] += sum;
+    if (half == 1) sums[z * kTile + (tid & 127)] = sum;
+    mine = ok && half == 0 && page >= 0;
+    if (mine) at = p.c.pair(page, h) * p.c.P + tok % p.c.P;
+    if (mine) from = z * kTile + (tid & 127);
   }
   if (!ok) {
     if (*abort_flag == 0) report(p.status, W4_ERR_TIMEOUT);
@@ -277,6 +285,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (mine && *abort_flag == 0) p.c.weight[at] += sum + sums[from];
   if (warp == S::kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*tmem_slot)
                  : "memory");
