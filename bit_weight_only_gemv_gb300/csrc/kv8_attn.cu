@@ -221,7 +221,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
     }
     // ------------------------- this warp's slices, the first on their way
     const int count = (sl1 - sl0 - warp + kWarps - 1) / kWarps;   // may be <= 0
-    auto fill = [&](int k0) {   // descriptions k0 .. k0 + 31
+    // descriptions k0 .. k0 + 31; the steps' loads set out before the first
+    // copies (behind them they would queue) and are waited for after them
+    float ks = 0.0f, vs = 0.0f;
+    auto fill = [&](int k0) {
       __syncwarp();
       const int k = k0 + lane;
       if (k < count) {
@@ -251,23 +254,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
             bad = true;
           } else {
             d.page = page;
+            ks = __ldg(p.c.ks + p.c.pair(page, h));
+            vs = __ldg(p.c.vs + p.c.pair(page, h));
           }
         }
         meta[k & (kRing - 1)] = d;
       }
       __syncwarp();
     };
-    // their steps, once the copies of the first are on their way
     auto fill_steps = [&](int k0) {
       const int k = k0 + lane;
       if (k < count) {
-        Meta& d = meta[k & (kRing - 1)];
-        if (d.page >= 0) {
-          const long long at = p.c.pair(d.page, h);
-          const float ks = __ldg(p.c.ks + at), vs = __ldg(p.c.vs + at);
-          d.ks = ks;
-          d.vs = vs;
-        }
+        meta[k & (kRing - 1)].ks = ks;
+        meta[k & (kRing - 1)].vs = vs;
       }
       __syncwarp();
     };

@@ -56,6 +56,19 @@ constexpr int kMetaRing = 16;         // tiles described ahead of their softmax
 constexpr int kUnitRing = 32;         // units of which a refusal is remembered
 constexpr int kMinTiles = 4;          // key tiles of a CTA's run
 
+// The same for roles that work ahead of the others: they leave the issue slots
+// to those while they wait.
+__device__ __forceinline__ bool wait_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    __nanosleep(64);
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag != 0) return false;
+    if (clock64() - t0 > kWaitCycles) return false;
+  }
+}
+
 template <int D>
 struct Shape {
   static constexpr int kGroups = D == 256 ? 1 : 2;   // softmax groups (and O accumulators)
@@ -345,7 +358,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       const int n = u.tiles();
       auto copy = [&](bool keys, int i, uint32_t serial) {
         const int full = keys ? kRawKFull : kRawVFull, st = serial % kRaw;
-        if (!wait_bar(bar((keys ? kRawKEmpty : kRawVEmpty) + st), before<kRaw>(serial), abort_flag))
+        if (!wait_idle(bar((keys ? kRawKEmpty : kRawVEmpty) + st), before<kRaw>(serial), abort_flag))
           return false;
         const int tok = u.t.lo + (u.i0 + i) * kKeys + lane * box;
         const int at = (serial % kMetaRing) * 4 + lane * (box / 16);
@@ -501,25 +514,40 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
   } else if (warp >= S::kConvWarp) {
     // ---------------------------------------------------------- expansion
     const int w = warp - S::kConvWarp, ct = tid - 32 * S::kConvWarp;
+    constexpr int kQThreads = 128;       // that copy query rows (a power of two)
     uint32_t nk = 0, nv = 0;             // tiles expanded
     uint32_t kf_par = 3, vf_par = 3;     // next parity of each kKFree, kVFree (the first passes at once)
     for (uint32_t units = 0; ok && next_unit<D>(p, run, walk, u); ++units) {
-      if (!wait_bar(bar(kQFree), before<1>(units), abort_flag)) {
+      if (!wait_idle(bar(kQFree), before<1>(units), abort_flag)) {
         ok = false;
         break;
       }
       // query rows as they are; rows past the unit's are zero
       const int qtiles = u.rows > kRowTile ? 2 : 1;
-      for (int x = ct; x < qtiles * kRowTile * (D / 8); x += 32 * S::kConvWarps) {
-        const int r = x / (D / 8), ch = x % (D / 8);
-        const int row = u.rt * S::kRows + min(r, u.rows - 1);
-        const uint32_t dst = sb + S::kQ + (r >> 7) * S::kQTile + (ch >> 3) * (kRowTile * 128) +
-                             (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
-        const __nv_bfloat16* src = p.a.q + (long long)(u.s.row0 + row / p.G) * p.a.q_stride +
-                                   (long long)(u.h * p.G + row % p.G) * D + ch * 8;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                     "r"(r < u.rows ? 16 : 0)
-                     : "memory");
+      // (a thread keeps its 16-byte column and finds the next row's token and
+      // head by addition)
+      if (ct < kQThreads) {
+        constexpr int kStep = kQThreads / (D / 8);   // rows
+        const int ch = ct % (D / 8);
+        int r = ct / (D / 8), row = u.rt * S::kRows + r;
+        int t = row / p.G, g = row - t * p.G;
+        const __nv_bfloat16* src = p.a.q + (long long)(u.s.row0 + t) * p.a.q_stride +
+                                   (long long)(u.h * p.G + g) * D + ch * 8;
+#pragma unroll 4
+        for (; r < qtiles * kRowTile; r += kStep) {
+          const bool in = r < u.rows;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           sb + S::kQ + (r >> 7) * S::kQTile + (ch >> 3) * (kRowTile * 128) +
+                           (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                       "l"(in ? src : p.a.q), "r"(in ? 16 : 0)
+                       : "memory");
+          g += kStep;
+          src += kStep * D;
+          while (g >= p.G) {
+            g -= p.G;
+            src += p.a.q_stride - (long long)p.G * D;
+          }
+        }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
@@ -530,8 +558,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       // either side), 32 bytes of bf16 each
       auto keys = [&](int i) {
         const uint32_t st = nk % kRaw, buf = i % kBuf;
-        if (!wait_bar(bar(kRawKFull + st), use<kRaw>(nk), abort_flag) ||
-            !wait_bar(bar(kKFree + buf), (kf_par >> buf) & 1u, abort_flag))
+        if (!wait_idle(bar(kRawKFull + st), use<kRaw>(nk), abort_flag) ||
+            !wait_idle(bar(kKFree + buf), (kf_par >> buf) & 1u, abort_flag))
           return false;
         kf_par ^= 1u << buf;
         const uint32_t raw = sb + S::kRawK + st * S::kRawTile, to0 = sb + S::kK + buf * S::kKTile;
@@ -562,8 +590,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       // word so that the stores meet no bank conflict
       auto vals = [&](int i) {
         const uint32_t st = nv % kRaw, buf = i % kBuf;
-        if (!wait_bar(bar(kRawVFull + st), use<kRaw>(nv), abort_flag) ||
-            !wait_bar(bar(kVFree + buf), (vf_par >> buf) & 1u, abort_flag))
+        if (!wait_idle(bar(kRawVFull + st), use<kRaw>(nv), abort_flag) ||
+            !wait_idle(bar(kVFree + buf), (vf_par >> buf) & 1u, abort_flag))
           return false;
         vf_par ^= 1u << buf;
         const uint32_t raw = sb + S::kRawV + st * S::kRawTile, to0 = sb + S::kV + buf * S::kVTile;

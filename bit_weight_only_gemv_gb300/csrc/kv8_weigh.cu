@@ -111,12 +111,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                     j, raw[n]);
     }
     const int count = (sl1 - sl0 - warp + kWarps - 1) / kWarps;
-    auto fill_steps = [&](int k0) {   // of descriptions k0 .. k0 + 31
-      const int k = k0 + lane;
-      if (k < count) {
-        Meta& d = meta[k & (kRing - 1)];
-        if (d.page >= 0) d.ks = __ldg(p.c.ks + p.c.pair(d.page, h));
-      }
+    // the steps' loads set out before the first copies (behind them they would
+    // queue) and are waited for after them
+    float ks = 0.0f;
+    auto fill_steps = [&](int k0) {
+      if (k0 + lane < count) meta[(k0 + lane) & (kRing - 1)].ks = ks;
       __syncwarp();
     };
     auto issue = [&](int k) {
@@ -132,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               report(p.status, W4_ERR_INDEX);
             } else {
               d.page = page;
+              ks = __ldg(p.c.ks + p.c.pair(page, h));
             }
           }
           meta[kk & (kRing - 1)] = d;
