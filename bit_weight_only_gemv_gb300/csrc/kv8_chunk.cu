@@ -707,8 +707,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
               tmem_wait_st();
               for (int c = 0; c < c0; c += 32) tmem_scale32(scol + c, keep);
               if (done > 0) {
-                // the last PV of this group has to be complete (the one before
-                // it is: these scores were issued after it)
+                // the last PV of this group has to be complete
                 if (!wait_bar(bar(kODone + grp), (o_done + done - 1) & 1u, abort_flag)) ok = false;
                 tc_fence_after();
                 for (int c = 0; c < D; c += 32) tmem_scale32(ocol + c, keep);
@@ -731,6 +730,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
+        // A wait tells phases apart by one bit: the PV before this one is seen
+        // to complete before this one may begin (it has had the whole softmax).
+        if (done > 0 && !wait_bar(bar(kODone + grp), (o_done + done - 1) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kPFull + reg));
         ++done;
@@ -738,10 +743,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       serial += n;
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
-      // (the last scores do not tell that the PV before the last is complete:
-      // in turn)
-      if ((done > 1 && !wait_bar(bar(kODone + grp), (o_done + done - 2) & 1u, abort_flag)) ||
-          (done > 0 && !wait_bar(bar(kODone + grp), (o_done + done - 1) & 1u, abort_flag))) {
+      if (done > 0 && !wait_bar(bar(kODone + grp), (o_done + done - 1) & 1u, abort_flag)) {
         ok = false;
         break;
       }
