@@ -60,7 +60,7 @@ struct Shape {
   static constexpr int kStats = kMeta + kWarps * kRing * 16;  // [kWarps][kRows] (m, l)
   static constexpr int kBars = kStats + kWarps * kRows * 8;
   static constexpr int kMisc = kBars + kWarps * kStages * 8;
-  static constexpr int kSmem = kMisc + 128 + 1024;            // and alignment
+  static constexpr int kSmem = kMisc + 16 + 8 * (2 * kWarps + 2) + 1024;   // and alignment
 };
 
 struct Meta {
@@ -113,12 +113,13 @@ __device__ __forceinline__ Tile unit_tile(const AttnParams& p, const Seq& s, int
 
 // Slices of an entry: a sequence (all heads), or with chosen pages a
 // (sequence, head).
-__device__ __forceinline__ long long entry_slices(const AttnParams& p, int e, int rows) {
+__device__ __forceinline__ long long entry_slices(const AttnParams& p, int e, int rows, int* units) {
   const int b = p.sel == nullptr ? e : e / p.c.H;
   const Seq s = sequence(p.bt, p.c.P, b);
   if (!s.ok || s.n == 0) return 0;
-  if (p.sel == nullptr) return head_slices(s, p.G, p.window, rows, kSlice) * p.c.H;
   const int rts = (s.n * p.G + rows - 1) / rows;
+  *units += p.sel == nullptr ? rts * p.c.H : rts;
+  if (p.sel == nullptr) return head_slices(s, p.G, p.window, rows, kSlice) * p.c.H;
   bool bad = false;
   return (long long)unit_tile(p, s, 0, rows, chosen(p, e, &bad)).slices * rts;
 }
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
   Run run;
   const bool any = find_run<kWarps>(
       p.sel == nullptr ? p.bt.B : p.bt.B * p.c.H, kMinSlices,
-      [&](int e) { return entry_slices(p, e, kRows); }, scan, &run);
+      [&](int e, int* units) { return entry_slices(p, e, kRows, units); }, scan, &run);
   __syncthreads();
   if (!any) return;
 
@@ -555,8 +556,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
     off += step;
     if (step == left && g < run.g1) {
       off = 0;
+      int none = 0;
       do ++entry;
-      while (entry_slices(p, entry, kRows) == 0);
+      while (entry_slices(p, entry, kRows, &none) == 0);
     }
   }
   if (dead) {   // copies still in flight land before the CTA leaves

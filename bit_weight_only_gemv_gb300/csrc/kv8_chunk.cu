@@ -95,7 +95,7 @@ struct Shape {
   static constexpr int kPages = kMeta + kMetaRing * 4 * 8;  // [kMetaRing][4]
   static constexpr int kBars = kPages + kMetaRing * 4 * 4;
   static constexpr int kMisc = kBars + 40 * 8;
-  static constexpr int kEnd = kMisc + 384 + 1024;
+  static constexpr int kEnd = kMisc + 512 + 1024;
   // more than half an SM's: each CTA holds all of its tensor memory
   static constexpr int kSmem = kEnd > 117248 ? kEnd : 117248;
   static_assert(kSmem <= 232448 && 2 * kSmem > 232448, "shared memory");
@@ -148,10 +148,11 @@ struct Unit {
 };
 
 template <int D>
-__device__ __forceinline__ long long entry_tiles(const ChunkParams& p, int b) {
+__device__ __forceinline__ long long entry_tiles(const ChunkParams& p, int b, int* units) {
   using S = Shape<D>;
   const Seq s = sequence(p.bt, p.c.P, b);
   if (!s.ok || s.n == 0) return 0;
+  *units += (s.n * p.G + S::kRows - 1) / S::kRows * p.c.H;
   return head_slices(s, p.G, p.a.window, S::kRows, kKeys) * p.c.H;
 }
 
@@ -186,8 +187,9 @@ __device__ __noinline__ bool next_unit(const ChunkParams& p, const Run& run, Wal
   w.off += step;
   if (w.off == per * p.c.H && w.g < run.g1) {
     w.off = 0;
+    int none = 0;
     do ++w.entry;
-    while (entry_tiles<D>(p, w.entry) == 0);
+    while (entry_tiles<D>(p, w.entry, &none) == 0);
   }
   return true;
 }
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       if (!sequence(p.bt, p.c.P, b).ok) report(p.a.status, W4_ERR_INDEX);
   Run run;
   const bool any = find_run<S::kWarps>(
-      p.bt.B, kMinTiles, [&](int e) { return entry_tiles<D>(p, e); }, scan, &run);
+      p.bt.B, kMinTiles, [&](int e, int* units) { return entry_tiles<D>(p, e, units); }, scan, &run);
   Walk walk = {any ? run.g0 : 0, any ? run.off : 0, any ? run.entry : 0};
   if (!any) run.g1 = 0;
   Unit u;

@@ -38,7 +38,7 @@ struct Shape {
   static constexpr int kMeta = kWarps * kStages * kStageBytes;   // [kWarps][kRing] Meta
   static constexpr int kBars = kMeta + kWarps * kRing * 16;
   static constexpr int kMisc = kBars + kWarps * kStages * 8;
-  static constexpr int kSmem = kMisc + 128 + 1024;
+  static constexpr int kSmem = kMisc + 8 * (2 * kWarps + 2) + 1024;
 };
 
 struct Meta {
@@ -80,9 +80,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (blockIdx.x == 0)
     for (int b = tid; b < p.bt.B; b += kThreads)
       if (!sequence(p.bt, p.c.P, b).ok) report(p.status, W4_ERR_INDEX);
-  auto weight = [&](int b) -> long long {
+  auto weight = [&](int b, int* units) -> long long {
     const Seq s = sequence(p.bt, p.c.P, b);
-    return s.ok && s.n > 0 ? head_slices(s, p.G, p.window, kRows, kSlice) * p.c.H : 0;
+    if (!s.ok || s.n == 0) return 0;
+    *units += p.c.H;   // one row tile
+    return head_slices(s, p.G, p.window, kRows, kSlice) * p.c.H;
   };
   Run run;
   const bool any = find_run<kWarps>(p.bt.B, kMinSlices, weight, scan, &run);
@@ -222,8 +224,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     off += step;
     if (off == (long long)t.slices * p.c.H && g < run.g1) {
       off = 0;
+      int none = 0;
       do ++b;
-      while (weight(b) == 0);
+      while (weight(b, &none) == 0);
     }
   }
   if (dead)   // copies still in flight land before the CTA leaves
