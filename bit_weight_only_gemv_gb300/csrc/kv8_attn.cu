@@ -577,7 +577,11 @@ struct Plan {
 Plan plan_token(const Cache& c, const Batch& b, int G, int sms) {
   Plan pl;
   const long long rows = (long long)b.max_new * G;
-  pl.nq = rows <= 8 ? 1 : 2;
+  // Two column tiles read the keys once for 16 rows, but from 128 channels on
+  // their accumulators do not fit the registers of two CTAs an SM: 16 rows on
+  // 16 x 16k keys of 128 channels 74 us against 64 with one, of 256 channels
+  // 124 against 117; of 64 channels 39 against 47.
+  pl.nq = c.D == 64 && rows > 8 ? 2 : 1;
   pl.rts = (int)((rows + 8 * pl.nq - 1) / (8 * pl.nq));
   pl.ctas = sms * (c.D == 256 ? 1 : 2);
   pl.arrived = up256((size_t)b.B * c.H * pl.rts * 4);
@@ -641,7 +645,7 @@ extern "C" size_t w4_kv8_attn_workspace_bytes(const w4_kv8_cache* cache, const w
     return 0;
   DeviceInfo di;
   planning_device(&di);
-  if (max_sel == 0 && (long long)b.max_new * (q_heads / c.H) >= kv8::kChunkRows)
+  if (max_sel == 0 && (long long)b.max_new * (q_heads / c.H) >= kv8::chunk_rows(c.D))
     return kv8::chunk_workspace_bytes(c, b, q_heads / c.H, di.sms);
   return kv8::plan_token(c, b, q_heads / c.H, di.sms).bytes;
 }
@@ -667,7 +671,7 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
   DeviceInfo di;
   const bool have = current_device(&dev, &di);
   if (!have) planning_device(&di);
-  if (sel == nullptr && (long long)p.bt.max_new * (q_heads / p.c.H) >= kv8::kChunkRows) {
+  if (sel == nullptr && (long long)p.bt.max_new * (q_heads / p.c.H) >= kv8::chunk_rows(p.c.D)) {
     if (workspace == nullptr ||
         workspace_bytes < kv8::chunk_workspace_bytes(p.c, p.bt, q_heads / p.c.H, di.sms))
       return W4_ERR_WORKSPACE;
@@ -706,8 +710,6 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
     case 64 * 4 + 1: return kv8::launch_token<64, 1>(p, pl.ctas, stream, dev);
     case 64 * 4 + 2: return kv8::launch_token<64, 2>(p, pl.ctas, stream, dev);
     case 128 * 4 + 1: return kv8::launch_token<128, 1>(p, pl.ctas, stream, dev);
-    case 128 * 4 + 2: return kv8::launch_token<128, 2>(p, pl.ctas, stream, dev);
-    case 256 * 4 + 1: return kv8::launch_token<256, 1>(p, pl.ctas, stream, dev);
-    default: return kv8::launch_token<256, 2>(p, pl.ctas, stream, dev);
+    default: return kv8::launch_token<256, 1>(p, pl.ctas, stream, dev);
   }
 }

@@ -9,7 +9,10 @@ namespace w4 {
 namespace kv8 {
 
 // Query rows on a key head from which a call takes the prompt-chunk kernel.
-constexpr int kChunkRows = 17;
+// Measured, row tiles of 8 or 16 in the token kernel against tiles of 128: 64
+// rows of 128-channel heads on 2 x 8k keys 45 and 55 us, 96 rows 61 and 55, 128
+// rows 76 and 57; of 256-channel heads on 4 x 4k keys 32 rows 39 and 54, 64 rows 62 and 55.
+constexpr long long chunk_rows(int D) { return D == 256 ? 49 : 81; }
 
 // The tensor map of one side's codes: bytes [page][head][token][channel], boxes of
 // `rows` tokens by 128 channels (64 for 64-channel heads), swizzled.
