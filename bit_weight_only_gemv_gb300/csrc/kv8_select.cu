@@ -55,14 +55,16 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
   __syncthreads();   // earlier readers of warp_sum are done
   if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  uint32_t base = 0, all = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-    const uint32_t s = warp_sum[w];
-    if (w < warp) base += s;
-    all += s;
+  // every warp sums the warps' sums by itself
+  uint32_t w = lane < (int)(blockDim.x >> 5) ? warp_sum[lane] : 0u;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += t;
   }
-  *total = all;
-  return base + inc - v;
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const uint32_t base = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  return (warp > 0 ? base : 0u) + inc - v;
 }
 
 // The count-th largest key (there are more than `count`), and in *ties how
