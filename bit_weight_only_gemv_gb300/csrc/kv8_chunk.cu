@@ -12,13 +12,13 @@
 // P stays in tensor memory in S's own columns, as fp32 bits rounded to tf32:
 // 11 significant bits at every magnitude, so no weight is lost however far
 // below the row's largest it lies, and no conversion or packing is needed.  That
-// costs PV twice the tensor time of a 16-bit P; the softmax warps, not the
-// tensor cores, would then be the limit.  For the same reason m need not be
+// costs PV twice the tensor time of a 16-bit P; as the softmax warps are the
+// limit, little of that shows.  For the same reason m need not be
 // the maximum: it is the largest score of the row's first 32 keys, and moves
 // (with O and l rescaled) only when a score passes it by 2^60.
 //
 // Roles: four softmax warps per row tile (a thread owns a row, so maxima and
-// sums need no exchange), four warps that expand the codes (K to bf16, V to
+// sums need no exchange), six warps that expand the codes (K to bf16, V to
 // fp32 transposed, both in the 128-byte-swizzled K-major layout), one warp
 // that issues the MMAs, one that issues the tiled copies of pages.  Two row
 // tiles take turns: while one's scores go through the softmax, the tensor
@@ -28,6 +28,13 @@
 // Work is cut into equal runs of key tiles over all units, one run a CTA
 // (kv8_runs.cuh); parts of a cut unit meet in the workspace and are joined in
 // order by a second small kernel.  Every wait is bounded.
+//
+// 256 rows of 32 heads on 8 of 128 channels against 16k keys: 110 us, 0.62
+// PFLOP/s.  Of about 3400 cycles per 64 keys a softmax group computes 2300 (four
+// warps, one per scheduler, beside the expansion and the issuing), the tensor
+// cores 1792 for both groups; one issuing warp keeps up (one per group: 133 us), and
+// neither 64 scores in registers at once (121 us) nor 128-key tiles (145 us)
+// were faster.
 #include <algorithm>
 #include <mutex>
 

@@ -7,10 +7,15 @@
 //
 // Few rows on a key head (single tokens): the bytes of the keys bound it;
 // equal runs of 16-token slices over all sequences, each warp streaming its
-// own through a ring of tiled copies, query fragments in registers.
-// More rows (prompt chunks): a warp keeps its tokens' keys as fragments in
-// registers, converted once, and walks all query rows, which the CTA brings
-// into shared memory 128 at a time in fragment order; the MMAs bound it.
+// own through a ring of tiled copies, query fragments in registers.  8
+// sequences of up to 16k tokens, 32 heads on 8 of 128 channels: 25.9 us, 3.8
+// TB/s; about 10 us of that are the start (lengths, page ids, first copies), the
+// rest runs at 6 TB/s.
+// Up to 128 rows: a warp keeps its tokens' keys as fragments in registers,
+// converted once, and walks all query rows, which the CTA brings into shared
+// memory 128 at a time in fragment order; the legacy MMAs bound it (20 rows
+// on 2 x 8k keys 12.7 us, 128 rows 23.2).  Beyond that kv8_weigh_tc.cu (23.6 and
+// 24.3 us at those sizes, 27.5 against 37.1 at 256 rows).
 #include <algorithm>
 #include <mutex>
 
@@ -206,8 +211,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         a0 += __shfl_xor_sync(0xffffffffu, a0, 2);
         a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
         if (j == 0) {
-          // one addition to each weight, which nothing here waits for (the
-          // old weights' way back would bound the slice: 29 us against 20)
+          // one addition to each weight, which nothing here waits for (loading
+          // the old weight first: 30.8 us against 29.0 at 8 x 16k keys)
           if (d.tok + i < s.len) atomicAdd(w, a0);
           if (d.tok + i + 8 < s.len) atomicAdd(w + 8, a1);
         }

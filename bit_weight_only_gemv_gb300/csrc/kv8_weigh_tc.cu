@@ -8,9 +8,13 @@
 // exchange.  A CTA expands the keys of 256 tokens (128 of 256-channel heads)
 // to bf16 once and takes all query rows that see one of them past, 128 at a
 // time: two row tiles' keys share each query tile, which halves what the
-// queries cost in L2 traffic (measured bound of the first form, in which
-// every warp held 32 tokens' keys as legacy MMA fragments: 123 us at 2 x 256
-// rows of 32 heads on 8k keys; this one 50 us).
+// queries cost in L2 traffic.
+//
+// 2 x 256 rows of 32 heads on 8 of 128 channels, 8k keys: 51 us, 0.45 PFLOP/s
+// (keys as legacy MMA fragments in every warp: 120 us).  A CTA's start (page
+// ids, keys, expansion: about 6 us, 3.4 times over on 152 SMs) and about 2200
+// cycles a query tile against 1024 of MMAs make that up; smaller CTAs, two an SM, hide more
+// of the start and lose more on the queries (59 us).
 //
 // Roles: eight warps per key tile that exponentiate and add (a thread has a
 // token and half of the columns), six that bring the
