@@ -30,7 +30,7 @@ struct ChunkArgs {
 };
 
 struct WeighParams {
-  CUtensorMap tm_k;
+  CUtensorMap tm;   // of the keys (single tokens) or the query rows (many rows)
   Cache c;
   Batch bt;
   const __nv_bfloat16* q;
@@ -43,7 +43,7 @@ struct WeighParams {
 };
 
 // w4_kv8_weigh for many query rows on a key head (kv8_weigh_tc.cu).
-w4_status weigh_many(const WeighParams& p, int dev, w4_stream_t stream);
+w4_status weigh_many(WeighParams& p, int sms, int dev, w4_stream_t stream);
 
 size_t chunk_workspace_bytes(const Cache& c, const Batch& b, int G, int sms);
 w4_status chunk_attn(const Cache& c, const Batch& b, const ChunkArgs& a, void* workspace,

@@ -11,11 +11,10 @@
 // sequences of up to 16k tokens, 32 heads on 8 of 128 channels: 25.9 us, 3.8
 // TB/s; about 10 us of that are the start (lengths, page ids, first copies), the
 // rest runs at 6 TB/s.
-// Up to 128 rows: a warp keeps its tokens' keys as fragments in registers,
+// Up to 64 rows: a warp keeps its tokens' keys as fragments in registers,
 // converted once, and walks all query rows, which the CTA brings into shared
-// memory 128 at a time in fragment order; the legacy MMAs bound it (20 rows
-// on 2 x 8k keys 12.7 us, 128 rows 23.2).  Beyond that kv8_weigh_tc.cu (23.6 and
-// 24.3 us at those sizes, 27.5 against 37.1 at 256 rows).
+// memory in fragment order; the legacy MMAs bound it (2 x 8k keys, 8 heads of
+// 128 channels: 20 rows 12.7 us, 64 rows 16.3).  Beyond that kv8_weigh_tc.cu.
 #include <algorithm>
 #include <mutex>
 
@@ -154,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           mbar_arrive_expect_tx(bar, S::kStageBytes);
 #pragma unroll
           for (int x = 0; x < D; x += 128)
-            tma_4d(st + x * kSlice, &p.tm_k, x, d.tok & (p.c.P - 1), h, d.page, bar);
+            tma_4d(st + x * kSlice, &p.tm, x, d.tok & (p.c.P - 1), h, d.page, bar);
         }
       }
       if (++put == kStages) put = 0;
@@ -239,8 +238,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // ------------------------------------------------------------ many rows
-constexpr int kChunk = 128;   // query rows in shared memory at a time
-constexpr long long kManyRows = 128;   // above: the tcgen05 kernel
+// The most rows of this kernel; above, kv8_weigh_tc.cu.  2 x 8k keys, 8 heads
+// of 64 and 128 channels, 4 of 256: 64 rows 13.5, 16.3 and 15.2 us here and 12.7,
+// 18.5 and 14.9 there; 96 rows 16.2, 20.1 and 20.7 against 12.7, 18.5 and 14.9.
+constexpr int kManyRows = 64;
 
 __device__ __forceinline__ void mma_bf16(float d[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // [tile of 8 rows][D / 32][lane] 16 bytes: the lane's four column registers
   // of two steps of 16 channels
   const uint32_t qs = smem_addr(smem_raw);
-  float* lse2 = reinterpret_cast<float*>(smem_raw + kChunk * D * 2);
+  float* lse2 = reinterpret_cast<float*>(smem_raw + kManyRows * D * 2);
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kTokens = kWarps * kSub * kSlice;
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int R = s.n * p.G;
   // rows that see some token of the block: positions from blk0 on, and within the window
   int t_lo = max(0, blk0 - first), t_hi = s.n;
-  if (p.window > 0) t_hi = min(s.n, blk0 + kTokens - 1 + p.window - first);
+  if (p.window > 0) t_hi = (int)min((long long)s.n, (long long)blk0 + kTokens - 1 + p.window - first);
   if (t_lo >= t_hi) return;
   const int r_lo = t_lo * p.G, r_hi = t_hi * p.G;
 
@@ -316,68 +317,65 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
-  for (int r0 = r_lo; r0 < r_hi; r0 += kChunk) {
-    const int n = min(kChunk, r_hi - r0), tiles = (n + 7) / 8;
-    __syncthreads();   // the rows before have been read
-    for (int x = tid; x < tiles * 8 * (D / 8); x += kThreads) {
-      // 8 channels (16 bytes) of a row: two steps of one lane
-      const int r = x / (D / 8), c8 = x % (D / 8), chunk = c8 >> 1;
-      // the chunk's lane and its place among the lane's chunks
-      const int jj = D == 64 ? chunk : (chunk & 7) >> 1;
-      const int c = D == 64 ? 0 : 2 * (chunk >> 3) + (chunk & 1);
-      const uint32_t dst =
-          qs + (((r >> 3) * (D / 32) + 2 * c + (c8 & 1)) * 32 + (r & 7) * 4 + jj) * 16;
-      const int row = min(r0 + r, R - 1);
-      const __nv_bfloat16* src = p.q + (long long)(s.row0 + row / p.G) * p.q_stride +
-                                 (long long)(h * p.G + row % p.G) * D + c8 * 8;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  const int n = r_hi - r_lo, tiles = (n + 7) / 8;
+  for (int x = tid; x < tiles * 8 * (D / 8); x += kThreads) {
+    // 8 channels (16 bytes) of a row: two steps of one lane
+    const int r = x / (D / 8), c8 = x % (D / 8), chunk = c8 >> 1;
+    // the chunk's lane and its place among the lane's chunks
+    const int jj = D == 64 ? chunk : (chunk & 7) >> 1;
+    const int c = D == 64 ? 0 : 2 * (chunk >> 3) + (chunk & 1);
+    const uint32_t dst =
+        qs + (((r >> 3) * (D / 32) + 2 * c + (c8 & 1)) * 32 + (r & 7) * 4 + jj) * 16;
+    const int row = min(r_lo + r, R - 1);
+    const __nv_bfloat16* src = p.q + (long long)(s.row0 + row / p.G) * p.q_stride +
+                               (long long)(h * p.G + row % p.G) * D + c8 * 8;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  }
+  for (int r = tid; r < tiles * 8; r += kThreads) {
+    float l = INFINITY;   // adds nothing
+    if (r < n) {
+      const int row = r_lo + r;
+      l = p.lse[(long long)(s.row0 + row / p.G) * p.Hq + h * p.G + row % p.G] * kLog2e;
+      if (l == -INFINITY) l = INFINITY;
     }
-    for (int r = tid; r < tiles * 8; r += kThreads) {
-      float l = INFINITY;   // adds nothing
-      if (r < n) {
-        const int row = r0 + r;
-        l = p.lse[(long long)(s.row0 + row / p.G) * p.Hq + h * p.G + row % p.G] * kLog2e;
-        if (l == -INFINITY) l = INFINITY;
-      }
-      lse2[r] = l;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
+    lse2[r] = l;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
 #pragma unroll 1
-    for (int t = 0; t < tiles; ++t) {
-      float x[kSub][4];
+  for (int t = 0; t < tiles; ++t) {
+    float x[kSub][4];
 #pragma unroll
-      for (int z = 0; z < kSub; ++z)
+    for (int z = 0; z < kSub; ++z)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[z][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) x[z][e] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        const uint4 q = lds128(qs + ((t * (D / 32) + k) * 32 + lane) * 16);
-#pragma unroll
-        for (int z = 0; z < kSub; ++z) {
-          mma_bf16(x[z], a[z][2 * k], q.x, q.y);
-          mma_bf16(x[z], a[z][2 * k + 1], q.z, q.w);
-        }
-      }
-      const float2 l = *reinterpret_cast<const float2*>(lse2 + 8 * t + 2 * j);
-      const int pmin = first + (r0 + 8 * t) / p.G;
-      const int pmax = first + min(R - 1, r0 + 8 * t + 7) / p.G;
+    for (int k = 0; k < D / 32; ++k) {
+      const uint4 q = lds128(qs + ((t * (D / 32) + k) * 32 + lane) * 16);
 #pragma unroll
       for (int z = 0; z < kSub; ++z) {
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = exp2_fast(fmaf(x[z][e], f[z], (e & 1) ? -l.y : -l.x));
-        if (tok[z] + kSlice - 1 > pmin || (p.window > 0 && tok[z] <= pmax - p.window)) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int pos = first + min(R - 1, r0 + 8 * t + 2 * j + (e & 1)) / p.G;
-            const int k = tok[z] + i + 8 * (e >> 1);
-            if (k > pos || (p.window > 0 && k <= pos - p.window)) y[e] = 0.0f;
-          }
-        }
-        sum[z][0] += y[0] + y[1];
-        sum[z][1] += y[2] + y[3];
+        mma_bf16(x[z], a[z][2 * k], q.x, q.y);
+        mma_bf16(x[z], a[z][2 * k + 1], q.z, q.w);
       }
+    }
+    const float2 l = *reinterpret_cast<const float2*>(lse2 + 8 * t + 2 * j);
+    const int pmin = first + (r_lo + 8 * t) / p.G;
+    const int pmax = first + min(R - 1, r_lo + 8 * t + 7) / p.G;
+#pragma unroll
+    for (int z = 0; z < kSub; ++z) {
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = exp2_fast(fmaf(x[z][e], f[z], (e & 1) ? -l.y : -l.x));
+      if (tok[z] + kSlice - 1 > pmin || (p.window > 0 && tok[z] <= pmax - p.window)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int pos = first + min(R - 1, r_lo + 8 * t + 2 * j + (e & 1)) / p.G;
+          const int k = tok[z] + i + 8 * (e >> 1);
+          if (k > pos || (p.window > 0 && k <= pos - p.window)) y[e] = 0.0f;
+        }
+      }
+      sum[z][0] += y[0] + y[1];
+      sum[z][1] += y[2] + y[3];
     }
   }
 #pragma unroll
@@ -414,7 +412,7 @@ w4_status allow_smem(K kern, int smem, int dev, bool* done) {
 template <int D, int NQ>
 w4_status launch_token(WeighParams& p, int sms, w4_stream_t stream, int dev) {
   static bool done[64] = {};
-  if (!tensor_map(&p.tm_k, p.c.kc, p.c, kSlice)) {
+  if (!tensor_map(&p.tm, p.c.kc, p.c, kSlice)) {
     note_cuda_error(cudaErrorInvalidValue);
     return W4_ERR_LAUNCH;
   }
@@ -427,7 +425,7 @@ w4_status launch_token(WeighParams& p, int sms, w4_stream_t stream, int dev) {
 template <int D>
 w4_status launch_chunk(const WeighParams& p, w4_stream_t stream, int dev) {
   constexpr int kSub = D == 256 ? 1 : 2;   // 128 registers of fragments are too many
-  constexpr int kSmem = kChunk * D * 2 + kChunk * 4;
+  constexpr int kSmem = kManyRows * D * 2 + kManyRows * 4;
   static bool done[64] = {};
   const w4_status st = allow_smem(weigh_chunk_kernel<D, kSub>, kSmem, dev, done);
   if (st != W4_OK) return st;
@@ -468,7 +466,7 @@ extern "C" w4_status w4_kv8_weigh(const void* q, size_t q_row_stride, int q_head
   p.status = status_dev;
   if (p.bt.max_len == 0) return W4_OK;
   const long long rows = (long long)p.bt.max_new * p.G;
-  if (rows > kv8::kManyRows) return kv8::weigh_many(p, dev, stream);
+  if (rows > kv8::kManyRows) return kv8::weigh_many(p, di.sms, dev, stream);
   if (rows > 16) {
     switch (p.c.D) {
       case 64: return kv8::launch_chunk<64>(p, stream, dev);
