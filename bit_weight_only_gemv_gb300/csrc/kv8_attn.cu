@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
               bad = true;
             } else {
               d.tok = lp * p.c.P + (sl - e * per) * kSlice;
-              read = d.tok < t.hi && !(p.window > 0 && d.tok + kSlice + p.window <= t.pmin + 1);
+              read = d.tok < t.hi && !(p.window > 0 && d.tok + kSlice <= (long long)t.pmin + 1 - p.window);
             }
           }
         } else {

@@ -27,7 +27,7 @@ __device__ __forceinline__ Tile tile_of(const Seq& s, int G, int window, int rt,
   const int r0 = rt * rows, r1 = min(R, r0 + rows) - 1;
   t.pmin = s.len - s.n + (s.n == 1 ? 0 : r0 / G);
   t.pmax = s.len - s.n + (s.n == 1 ? 0 : r1 / G);
-  t.lo = window > 0 ? max(0, t.pmin + 1 - window) / slice * slice : 0;
+  t.lo = window > 0 ? (int)max(0LL, (long long)t.pmin + 1 - window) / slice * slice : 0;
   t.hi = t.pmax + 1;
   // at least one slice, if an empty one: the rows are written too
   t.slices = max(1, t.hi > t.lo ? (t.hi - t.lo + slice - 1) / slice : 0);

@@ -227,3 +227,33 @@ def test_decode_loop_example(cuda_lib):
     ref = kv8.attn_ref(a["cache"], a["table"], a["lens"], None, a["q"], layer.scale, 0, a["sel"],
                        a["n_sel"])
     check_attn(a["out"], ref[1], ref, 64)
+
+
+@pytest.mark.parametrize("news,D", [(None, 128), ([5, 9], 64), ([30, 20], 128), ([70, 90], 256)])
+def test_window_beyond_every_length(cuda_lib, news, D):
+    """A window as long as the type allows is none at all."""
+    c = Case(71, [300, 190], news, 2, D, 16, 4)
+    c.to_gpu()
+    plain = c.attn()
+    wide = c.attn(window=2 ** 31 - 1)
+    assert status(c) == 0
+    assert np.array_equal(plain[0], wide[0]) and np.array_equal(plain[1], wide[1])
+    got = []
+    for window in (0, 2 ** 31 - 1):
+        c.to_gpu()
+        lib.kv8_weigh(c.dev, c.batch, c.gpu_q(), torch.from_numpy(plain[1]).float().cuda(), c.scale,
+                      window, c.status)
+        assert status(c) == 0
+        got.append(c.dev_arrays()["weight"])
+    assert np.array_equal(got[0], got[1])
+
+
+@pytest.mark.parametrize("G", [3, 5, 48, 128])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_weigh_many_rows_of_odd_groups(cuda_lib, G, D):
+    """Query tiles of whole tokens: groups that do not divide 128, several units a CTA."""
+    c = Case(72 + G, [40, 700, 0, 333, 129], [40, 3, 0, 33, 1], 2, D, 32, G)
+    c.to_gpu()
+    weigh_and_check(c)
+    c.to_gpu()
+    weigh_and_check(c, 100)
