@@ -471,8 +471,10 @@ w4_status launch_many(WeighParams& p, int sms, int dev, w4_stream_t stream) {
   if (enc == nullptr ||
       enc(&p.tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.q), dims, strides,
           box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+    note_cuda_error(cudaErrorInvalidValue);
     return W4_ERR_LAUNCH;
+  }
   const int tokens = kTile * S::kTiles;
   const long long units = (long long)((p.bt.max_len + tokens - 1) / tokens) * p.c.H * p.bt.B;
   return launch(weigh_many_kernel<D>, dim3((unsigned)std::min<long long>(units, sms)), S::kThreads,

@@ -257,3 +257,27 @@ def test_weigh_many_rows_of_odd_groups(cuda_lib, G, D):
     weigh_and_check(c)
     c.to_gpu()
     weigh_and_check(c, 100)
+
+
+@pytest.mark.parametrize("news", [None, [9, 4], [60, 33]])
+@pytest.mark.parametrize("D", [64, 256])
+def test_query_rows_with_gaps(cuda_lib, news, D):
+    """A row stride that no head's size divides: the same bits as dense rows."""
+    c = Case(75, [200, 90], news, 2, D, 16, 3)
+    c.to_gpu()
+    q = c.gpu_q()
+    n = q.shape[1] * D
+    wide = torch.full((q.shape[0], n + 8), float("nan"), dtype=q.dtype, device=q.device)
+    wide[:, :n] = q.view(-1, n)
+    gaps = wide[:, :n].unflatten(1, (q.shape[1], D))
+    dense, spread = c.attn(), c.attn(q=gaps)
+    assert status(c) == 0
+    assert np.array_equal(dense[0], spread[0]) and np.array_equal(dense[1], spread[1])
+    got = []
+    for x in (q, gaps):
+        c.to_gpu()
+        lib.kv8_weigh(c.dev, c.batch, x, torch.from_numpy(dense[1]).float().cuda(), c.scale, 0,
+                      c.status)
+        assert status(c) == 0
+        got.append(c.dev_arrays()["weight"])
+    assert np.array_equal(got[0], got[1])
