@@ -340,10 +340,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // only now that the tensor memory is held: a dependent that allocates some
+  // and shares the SM could else take columns first and wait for this grid,
+  // while this CTA's allocation waits for those columns
+  pdl_launch_dependents();
   constexpr uint32_t tmem = 0;   // all 512 columns: they begin at 0
   pdl_wait();
   if (blockIdx.x == 0)

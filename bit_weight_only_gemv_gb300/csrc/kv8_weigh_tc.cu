@@ -179,11 +179,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     sts128(sb + S::kQ + i * (kTile * 128) + r * 128 + (x & 7) * 16, 0, 0, 0, 0);
   }
   fence_proxy_async_smem();
-  pdl_launch_dependents();
-  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // only now that the tensor memory is held (as in kv8_chunk.cu)
+  pdl_launch_dependents();
+  pdl_wait();
   constexpr uint32_t tmem = 0;   // all 512 columns: they begin at 0
   bool ok = __syncthreads_and(*tmem_slot == 0 && (sb & 1023u) == 0) != 0;
 
