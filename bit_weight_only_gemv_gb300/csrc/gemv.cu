@@ -100,7 +100,7 @@ struct GemvParams {
   int x_slots;                         // activation rows staged per CTA (per MR row)
   int nst;                             // pipeline stages
   int tile_bytes, code_pitch, step_pitch, step_off;
-  int* ws_count;                       // [B] at the start of the workspace
+  int* ws_count;                       // [B] in the workspace's head
   float* ws_partial;                   // [B][nch][RB][MR] after it
   int32_t* status;
   int gated;                           // x rows are [gate K | up K]: the product takes silu(gate) * up
@@ -1100,7 +1100,8 @@ bool make_plan(int MR, int N, int K, int n_items, int allow_split, int x_per_ite
   const long long step_chunk = (long long)pl.nsw * pl.CL * pl.T * 18;
   const int cps_max = (int)std::max<long long>(1, kTileMax / step_chunk);
   int split = 1;
-  if (allow_split && pl.nch > 1 && 2 * g1 < target) {
+  // (a counter for each block fits the workspace's head)
+  if (allow_split && pl.nch > 1 && 2 * g1 < target && blocks <= W4_WORKSPACE_HEAD / 4) {
     split = (int)std::min<long long>(pl.nch, (target + blocks - 1) / blocks);
     split = std::max(split, (pl.nch + cps_max - 1) / cps_max);
   }
@@ -1208,9 +1209,10 @@ bool make_plan(int MR, int N, int K, int n_items, int allow_split, int x_per_ite
   if (routed_dyn_ok)
     pl.dyn = (long long)n_items * ((N + pl.RB - 1) / pl.RB) >= 2LL * pl.ctas;
   if (pl.S > 1) {
-    // counters first, partials after them
+    // counters in the head, partials after it: what a call leaves there never
+    // lies where a call of another shape counts
     const size_t part = (size_t)pl.B * pl.nch * pl.RB * MR * sizeof(float);
-    pl.ws_part_off = ((size_t)pl.B * sizeof(int) + 255) & ~size_t(255);
+    pl.ws_part_off = W4_WORKSPACE_HEAD;
     pl.ws_bytes = pl.ws_part_off + part;
   }
   *out = pl;
@@ -1883,10 +1885,14 @@ extern "C" w4_status w4a16_gemv_id_scaled(void* y, const void* qw_base, size_t q
 // library, for callers that cannot allocate device memory themselves (see
 // w4a16_gemv_static_scratch in w4a16.h).  Every GPU that loads the library
 // holds this array until the process exits.
-static __device__ __align__(256) unsigned char w4_static_scratch[W4_STATIC_SCRATCH_BYTES];
+static __device__ __align__(256) unsigned char
+    w4_static_scratch[W4_WORKSPACE_HEAD + W4_STATIC_SCRATCH_BYTES];
 
 namespace w4 {
 namespace {
+
+// The most scratch that a call may take of the array.
+constexpr size_t kStaticMost = W4_WORKSPACE_HEAD + W4_STATIC_SCRATCH_BYTES - 256;
 
 // Device address of w4_static_scratch on device `dev` (the host-side name is
 // only a stand-in).  Looked up once per device, with that device current.
@@ -1929,7 +1935,7 @@ extern "C" w4_status w4a16_gemv_static_scratch(void* y, const void* qw, const vo
     // every launch of this call must fit the fixed array: check before any work
     // (the plain plans: balanced runs are not taken here)
     const size_t need = tc_workspace(M, N, K, di.sms, false);
-    if (need > (size_t)W4_STATIC_SCRATCH_BYTES) return W4_ERR_WORKSPACE;
+    if (need > kStaticMost) return W4_ERR_WORKSPACE;
     void* base = nullptr;
     if (need > 0) {
       cudaError_t e = static_scratch_address(dev, &base);
@@ -1949,7 +1955,7 @@ extern "C" w4_status w4a16_gemv_static_scratch(void* y, const void* qw, const vo
   for (int m0 = 0; m0 < M; m0 += mr_cap) {
     Plan pm;
     if (!cached_plan(std::min(mr_cap, M - m0), N, K, 1, 1, 0, false, di, &pm)) return W4_ERR_SHAPE;
-    if (pm.ws_bytes > (size_t)W4_STATIC_SCRATCH_BYTES) return W4_ERR_WORKSPACE;
+    if (pm.ws_bytes > kStaticMost) return W4_ERR_WORKSPACE;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for (int m0 = 0; m0 < M; m0 += mr_cap) {

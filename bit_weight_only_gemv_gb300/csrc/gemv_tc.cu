@@ -174,8 +174,8 @@ __device__ __forceinline__ bool wait_flag_gpu(const int* f, volatile int* abort_
 }
 
 // Row `tid`'s prefix from slot blockIdx.x - 1 (the previous CTA's part of
-// this tile), its M values read once and cleared: the workspace is left
-// zero-filled, as every completed call leaves it.
+// this tile), its M values read once and cleared: slots may reach into the
+// workspace's head, which every completed call leaves zero.
 template <int MC>
 __device__ __forceinline__ void take_prefix(const TcParams& p, int tid, float* v) {
   float* slot = p.sk_prefix + (long long)(blockIdx.x - 1) * p.M * kRows + tid;
@@ -776,7 +776,7 @@ bool tc_plan(int M, int N, int K, int sms, TcPlan* out, bool allow_sk) {
   for (int per_sm = 1; per_sm <= 2; ++per_sm) {
     const int target = per_sm * std::max(1, sms);
     int S = 1;
-    if (2 * pl.tiles <= std::max(1, sms)) S = std::max(1, std::min(pl.slices, target / pl.tiles));
+    if (2 * pl.tiles <= std::min(std::max(1, sms), W4_WORKSPACE_HEAD / 4)) S = std::max(1, std::min(pl.slices, target / pl.tiles));
     pl.sps = (pl.slices + S - 1) / S;
     pl.S = (pl.slices + pl.sps - 1) / pl.sps;
     pl.units = pl.tiles * pl.S;
@@ -798,7 +798,8 @@ bool tc_plan(int M, int N, int K, int sms, TcPlan* out, bool allow_sk) {
   // allocation for the first to finish (all 512 columns are taken)
   if (pl.per_sm == 1) pl.smem = std::max(pl.smem, 232448 / 2 + 1024);
   if (pl.S > 1) {
-    pl.ws_part_off = ((size_t)pl.tiles * sizeof(int) + 255) & ~size_t(255);
+    // (S > 1 needs fewer tiles than SMs: their counters fit the head)
+    pl.ws_part_off = W4_WORKSPACE_HEAD;
     pl.ws_bytes = pl.ws_part_off + (size_t)pl.slices * M * N * sizeof(float);
   }
   // Balanced runs when whole tiles divide badly over the CTAs: the busiest

@@ -102,6 +102,9 @@ typedef enum w4_status {
                                      read after it) */
 
 #define W4_GROUP 32        /* codes per group along K */
+/* Leading bytes of a workspace that hold counters and flags, zero between
+ * calls; sums and lists that a call leaves behind lie past them. */
+#define W4_WORKSPACE_HEAD 4096
 #define W4_MAX_K 65536     /* largest supported K */
 /* Largest batch of activation rows per call: a prompt chunk of 256 tokens
  * (page "Gemma 4 on a 4 GB GPU in Plain PyTorch", section "Step 6 — Read
@@ -146,10 +149,13 @@ const char *w4_last_cuda_error(void);
  * N          >= 1 output rows.
  * K          multiple of 32, 32 .. W4_MAX_K.
  * workspace  device scratch of at least w4a16_gemv_workspace_bytes(M, N, K)
- *            bytes (16-byte aligned), or NULL when that is 0.  It must be
- *            zero-filled before its first use; every call that completes
- *            without a device-side error leaves it zero-filled again.  Calls
- *            that may run concurrently need separate workspaces.  On the
+ *            bytes (16-byte aligned), or NULL when that is 0.  Its first
+ *            W4_WORKSPACE_HEAD bytes must be zero-filled before the first
+ *            use; every call that completes without a device-side error
+ *            leaves them zero again, and no call asks anything of the rest:
+ *            one buffer, the largest call's, serves calls of any shapes in
+ *            turn.  Calls that may run concurrently need separate
+ *            workspaces.  On the
  *            tensor-core small-batch path a call whose row tiles do not
  *            divide evenly over the CTAs uses the workspace for balanced runs
  *            (w4_plan_info.dynamic_windows); given less (or NULL) it runs the
@@ -250,9 +256,9 @@ w4_status w4a16_gemv_prefetch_l2(void *y, const void *qw, const void *st, const 
  * device buffers; the call allocates nothing (no cudaMalloc / cudaFree and
  * no allocating library routine).
  *
- *  - A shape whose split-K plan needs more than W4_STATIC_SCRATCH_BYTES of
- *    scratch (w4a16_gemv_workspace_bytes(M, N, K)) returns W4_ERR_WORKSPACE
- *    before any work is enqueued.
+ *  - A shape whose split-K plan needs more than W4_STATIC_SCRATCH_BYTES - 256
+ *    of scratch past the counters (w4a16_gemv_workspace_bytes(M, N, K) -
+ *    W4_WORKSPACE_HEAD) returns W4_ERR_WORKSPACE before any work is enqueued.
  *  - The first call on each device looks up the array's device address
  *    (cudaGetSymbolAddress) with that device current; make that first call
  *    before any stream capture.
