@@ -7,6 +7,12 @@
 namespace w4 {
 namespace kv8 {
 
+// The start of every call's workspace: arrival counters of the token kernel,
+// one a CTA, zero between calls.  Nothing else is ever written there, so one
+// buffer serves calls of every kind and shape in turn.
+constexpr size_t kHeadBytes = W4_WORKSPACE_HEAD;
+constexpr int kHeadCounters = (int)(kHeadBytes / 4);
+
 struct Cache {
   uint8_t* kc;
   uint8_t* vc;

@@ -89,8 +89,7 @@ struct AttnParams {
   const int32_t* sel;
   const int32_t* n_sel;
   int max_sel;
-  int rts;            // row tiles of a (sequence, head), at most
-  int32_t* arrived;   // [B][H][rts], zero between calls
+  int32_t* arrived;   // [CTAs], zero between calls: of the unit whose first part the CTA has
   float* parts;       // [2 * CTAs][rows][D]
   float* part_stats;  // [2 * CTAs][rows][2]: m, l (l = -1: refused)
   int32_t* status;
@@ -502,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
       // CTAs that hold a part of this unit: those of its first to its last slice
       const long long u0 = g - sl0, u1 = u0 + t.slices - 1;
       const int c0 = run.holder(u0), c1 = run.holder(u1);
-      int32_t* arrived = p.arrived + bh * p.rts + rt;
+      // a CTA has the first part of one cut unit at most: its last
+      int32_t* arrived = p.arrived + c0;
       __syncthreads();
       if (tid == 0) {
         const int was = atomic_add_acq_rel_gpu(arrived, 1);
@@ -576,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct Plan {
-  int nq, rts, ctas;
-  size_t arrived, parts, stats, bytes;
+  int nq, ctas;
+  size_t parts, stats, bytes;
 };
 
 Plan plan_token(const Cache& c, const Batch& b, int G, int sms) {
@@ -588,12 +588,10 @@ Plan plan_token(const Cache& c, const Batch& b, int G, int sms) {
   // 16 x 16k keys of 128 channels 74 us against 64 with one, of 256 channels
   // 124 against 117; of 64 channels 39 against 47.
   pl.nq = c.D == 64 && rows > 8 ? 2 : 1;
-  pl.rts = (int)((rows + 8 * pl.nq - 1) / (8 * pl.nq));
-  pl.ctas = sms * (c.D == 256 ? 1 : 2);
-  pl.arrived = up256((size_t)b.B * c.H * pl.rts * 4);
+  pl.ctas = std::min(sms * (c.D == 256 ? 1 : 2), kHeadCounters);
   pl.parts = up256((size_t)2 * pl.ctas * 8 * pl.nq * c.D * 4);
   pl.stats = up256((size_t)2 * pl.ctas * 8 * pl.nq * 8);
-  pl.bytes = pl.arrived + pl.parts + pl.stats;
+  pl.bytes = kHeadBytes + pl.parts + pl.stats;
   return pl;
 }
 
@@ -702,11 +700,10 @@ extern "C" w4_status w4_kv8_attn(void* out, float* lse, const void* q, size_t q_
   p.n_sel = n_sel;
   p.max_sel = max_sel;
   p.status = status_dev;
-  p.rts = pl.rts;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.arrived = reinterpret_cast<int32_t*>(ws);
-  p.parts = reinterpret_cast<float*>(ws + pl.arrived);
-  p.part_stats = reinterpret_cast<float*>(ws + pl.arrived + pl.parts);
+  p.parts = reinterpret_cast<float*>(ws + kv8::kHeadBytes);
+  p.part_stats = reinterpret_cast<float*>(ws + kv8::kHeadBytes + pl.parts);
   if (!kv8::tensor_map(&p.tm_k, p.c.kc, p.c, kv8::kSlice) ||
       !kv8::tensor_map(&p.tm_v, p.c.vc, p.c, kv8::kSlice)) {
     note_cuda_error(cudaErrorInvalidValue);

@@ -905,7 +905,7 @@ Plan plan_chunk(const Cache& c, const Batch& b, int G, int sms) {
   pl.cut = up256(((size_t)b.B * c.H * pl.rts + 2) * 8);
   pl.parts = up256((size_t)4 * sms * pl.rows * c.D * 4);
   pl.stats = up256((size_t)4 * sms * pl.rows * 8);
-  pl.bytes = pl.cut + pl.parts + pl.stats;
+  pl.bytes = kHeadBytes + pl.cut + pl.parts + pl.stats;
   return pl;
 }
 
@@ -956,7 +956,7 @@ w4_status chunk_attn(const Cache& c, const Batch& b, const ChunkArgs& a, void* w
   p.G = a.Hq / c.H;
   const Plan pl = plan_chunk(c, b, p.G, sms);
   p.rts = pl.rts;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(workspace) + kHeadBytes;
   p.cut = reinterpret_cast<long long*>(ws);
   p.parts = reinterpret_cast<float*>(ws + pl.cut);
   p.part_stats = reinterpret_cast<float*>(ws + pl.cut + pl.parts);

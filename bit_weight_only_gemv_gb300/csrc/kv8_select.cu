@@ -584,7 +584,7 @@ extern "C" size_t w4_kv8_select_workspace_bytes(const w4_kv8_cache* cache,
   kv8::Cache c;
   kv8::Batch b;
   if (kv8::view(cache, batch, &c, &b) != W4_OK) return 0;
-  return kv8::up256((size_t)b.B * c.H * kv8::scores_row(b) * 4);
+  return kv8::kHeadBytes + kv8::up256((size_t)b.B * c.H * kv8::scores_row(b) * 4);
 }
 
 extern "C" w4_status w4_kv8_select(int32_t* sel, int32_t* n_sel, int max_sel, int sink, int recent,
@@ -613,7 +613,7 @@ extern "C" w4_status w4_kv8_select(int32_t* sel, int32_t* n_sel, int max_sel, in
   p.max_sel = max_sel;
   p.sink = sink;
   p.recent = recent;
-  p.scores = static_cast<float*>(workspace);
+  p.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kv8::kHeadBytes);
   p.scores_row = kv8::scores_row(p.bt);
   p.status = status_dev;
   // about eight CTAs an SM, of at least 32 and at most 1024 pages
@@ -635,7 +635,8 @@ extern "C" size_t w4_kv8_evict_workspace_bytes(const w4_kv8_cache* cache,
   kv8::Cache c;
   kv8::Batch b;
   if (kv8::view(cache, batch, &c, &b) != W4_OK || budget < 1) return 0;
-  return kv8::up256((size_t)b.B * c.H * 4) + (size_t)b.B * c.H * kv8::evict_row(b) * 4;
+  return kv8::kHeadBytes + kv8::up256((size_t)b.B * c.H * 4) +
+         (size_t)b.B * c.H * kv8::evict_row(b) * 4;
 }
 
 extern "C" w4_status w4_kv8_evict(const int32_t* dst_table, int32_t* kept, int32_t* new_lens,
@@ -663,9 +664,9 @@ extern "C" w4_status w4_kv8_evict(const int32_t* dst_table, int32_t* kept, int32
   p.budget = budget;
   p.sink = sink;
   p.recent = recent;
-  p.go = static_cast<int32_t*>(workspace);
-  p.keys = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) +
-                                       kv8::up256((size_t)p.bt.B * p.c.H * 4));
+  uint8_t* ws = static_cast<uint8_t*>(workspace) + kv8::kHeadBytes;
+  p.go = reinterpret_cast<int32_t*>(ws);
+  p.keys = reinterpret_cast<uint32_t*>(ws + kv8::up256((size_t)p.bt.B * p.c.H * 4));
   p.keys_row = kv8::evict_row(p.bt);
   p.status = status_dev;
   w4_status r = kv8::launch(kv8::evict_top_kernel, dim3((unsigned)p.c.H, (unsigned)p.bt.B),

@@ -773,9 +773,11 @@ w4_status w4_kv8_append(const w4_kv8_cache *cache, const w4_kv8_batch *batch, co
  *             w4_kv8_select): the row sees tokens of those pages only.  One row per
  *             sequence (W4_ERR_SHAPE otherwise).  An entry outside the
  *             sequence's pages or a count outside 0 .. max_sel: W4_ERR_INDEX.
- * workspace   w4_kv8_attn_workspace_bytes(...) bytes, 16-byte aligned,
- *             zero-filled before its first use and left ready for the next call; not
- *             shared by calls that may overlap.
+ * workspace   w4_kv8_attn_workspace_bytes(...) bytes, 16-byte aligned, its first
+ *             W4_WORKSPACE_HEAD bytes zero-filled before the first use and
+ *             left zero; nothing is asked of the rest.  One buffer, the
+ *             largest call's, serves w4_kv8 and w4a16_gemv calls of every kind
+ *             and shape in turn; calls that may overlap need one each.
  * flags       W4_FLAG_PDL.
  */
 w4_status w4_kv8_attn(void *out, float *lse, const void *q, size_t q_row_stride, int q_heads,

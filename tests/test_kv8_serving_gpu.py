@@ -64,3 +64,73 @@ def test_chunk_kernels_and_products_as_dependents_of_one_another(cuda_lib, D):
     # twenty times what one call adds, but for the fp32 sums' roundings
     bound = 21 * 2.0 ** -23 * c.dev.tensors[5].double() + 1e-12
     assert bool((torch.abs(many - 20 * added) <= 20 * bound).all())
+
+
+def test_one_workspace_for_every_call(cuda_lib):
+    """A product, then prompt chunks, single tokens, more sequences, selections and evictions in
+    turn on one buffer, zero-filled once: each leaves it ready for the next."""
+    def made(seed, lens, news, H, D, P, G, spare=3):
+        c = Case(seed, lens, news, H, D, P, G, spare=spare)
+        c.fix_ranges()
+        c.to_gpu()
+        return c, kv8.attn_ref(c.cache, c.table, c.lens, c.offsets, c.q, c.scale)
+
+    chunk = made(1, [700], [100], 1, 128, 32, 2)
+    rows64 = made(2, [900, 260], [90, 33], 2, 64, 16, 3)
+    token = made(3, [4000], None, 1, 128, 32, 8, spare=40)
+    many = made(4, [int(x) for x in np.random.default_rng(4).integers(1, 1500, 70)], None, 2, 128,
+                64, 12)
+    wide = made(6, [3000, 2000], None, 2, 256, 16, 4)
+    pairs = made(7, [2500, 800], [5, 4], 2, 128, 16, 8)
+    sparse = made(5, [6000, 900], None, 2, 64, 16, 4)
+    sel_want, n_want = kv8.select_ref(sparse[0].cache, sparse[0].table, sparse[0].lens, sparse[0].q,
+                                      200, 1, 1)
+    budget = 1100
+    dst = token[0].free[:-(-budget // 32)][None].copy()
+    cases = (chunk, rows64, token, many, wide, pairs, sparse)
+    w = lib.quantize(torch.randn((300, 512), device="cuda") * 0.05)
+    x = torch.randn((5, 512), device="cuda").to(torch.bfloat16)
+    need = max([lib.kv8_attn_workspace_bytes(c.dev, c.batch, c.H * c.G) for c, _ in cases]
+               + [lib.kv8_attn_workspace_bytes(sparse[0].dev, sparse[0].batch, 8, max_sel=200),
+                  lib.kv8_select_workspace_bytes(sparse[0].dev, sparse[0].batch),
+                  lib.kv8_evict_workspace_bytes(token[0].dev, token[0].batch, budget),
+                  lib.workspace_bytes(5, 300, 512)])
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+
+    def attend(case, sel=None, n_sel=None, ref=None):
+        c = case[0]
+        q = c.gpu_q()
+        out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+        lse = torch.full(q.shape[:2], float("nan"), dtype=torch.float32, device="cuda")
+        lib.kv8_attn(c.dev, c.batch, q, c.scale, out, lse, 0, sel, n_sel, ws, c.status)
+        assert status(c) == 0
+        check_attn(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref or case[1], c.D)
+
+    def choose():
+        c = sparse[0]
+        sel, n_sel = lib.kv8_select(c.dev, c.batch, c.gpu_q(), 200, 1, 1, ws, c.status)
+        assert status(c) == 0
+        assert np.array_equal(sel.cpu().numpy(), sel_want)
+        assert np.array_equal(n_sel.cpu().numpy(), n_want)
+        attend(sparse, sel, n_sel, kv8.attn_ref(c.cache, c.table, c.lens, None, c.q, c.scale, 0,
+                                                sel_want, n_want))
+
+    def evict():
+        c = token[0]
+        want, kept, _ = kv8.evict_ref(c.cache, c.table, c.lens, dst, budget, 4, 16)
+        got, _ = lib.kv8_evict(c.dev, c.batch, budget, torch.from_numpy(dst).cuda(), 4, 16, ws,
+                               c.status)
+        assert status(c) == 0
+        assert np.array_equal(got.cpu().numpy(), kept)
+        got = c.dev_arrays()
+        assert all(np.array_equal(got[n], want[n]) for n in want)
+
+    alone = lib.gemv(*w, x, workspace=torch.zeros_like(ws), status=chunk[0].status)
+
+    def product():
+        assert torch.equal(lib.gemv(*w, x, workspace=ws, status=chunk[0].status), alone)
+
+    for step in (product, chunk, token, many, choose, token, evict, wide, product, rows64, sparse,
+                 pairs, many, evict, product, token, choose, chunk, wide):
+        step() if callable(step) else attend(step)
+    assert not bool(ws[:4096].any())
