@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           });
       }
     }
-    if (tid == 0 && blockIdx.x == 0) {
+    if (tid == 0 && blockIdx.x == 0) {   // also when a wait ran out
       p.cut[0] = run.total;
       p.cut[1] = run.ctas;
     }
@@ -872,6 +872,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   run.total = p.cut[0];
   run.ctas = (int)p.cut[1];
   const Tile t = tile_of(s, p.G, p.a.window, rt, S::kRows, kKeys);
+  // a unit whose CTA gave up waiting has no start of this call's: whatever
+  // stands there may not be taken for parts (the status says W4_ERR_TIMEOUT)
+  if (!run.holds(u0, t.slices)) return;
   const int c0 = run.holder(u0), c1 = run.holder(u0 + t.slices - 1);
   // of one row tile, each CTA holds two parts (one per softmax group)
   const int subs = S::kGroups == 2 && R - rt * S::kRows <= kRowTile ? 2 : 1;

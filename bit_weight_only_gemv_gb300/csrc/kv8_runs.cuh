@@ -49,13 +49,18 @@ struct Run {
   int ctas, entry;
 
   // the CTA whose run holds item g
-  __device__ __forceinline__ int holder(long long g) const {
+  __host__ __device__ __forceinline__ int holder(long long g) const {
     if (total <= kNarrow) return (int)(((uint32_t)(g + 1) * (uint32_t)ctas - 1) / (uint32_t)total);
     return (int)(((g + 1) * ctas - 1) / total);
   }
-  __device__ __forceinline__ long long start(int c) const {
+  __host__ __device__ __forceinline__ long long start(int c) const {
     if (total <= kNarrow) return (uint32_t)total * (uint32_t)c / (uint32_t)ctas;
     return total * c / ctas;
+  }
+  // items u0 .. u0 + n - 1 are all of the runs' (a number read back from
+  // memory: a call that gave up may have left another one's there)
+  __host__ __device__ __forceinline__ bool holds(long long u0, int n) const {
+    return u0 >= 0 && n <= total && u0 <= total - n;
   }
   static constexpr long long kNarrow = 1 << 22;   // times at most 1023 CTAs: 32 bits do
 };

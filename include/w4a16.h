@@ -693,6 +693,9 @@ w4_status w4a16_gemv_chain_task_plan(const w4_gemv_task *tasks, int n_tasks, int
  *     kernel before it in the stream before it reads or writes anything:
  *     W4_FLAG_PDL is accepted and changes nothing.
  *   - Codes past a sequence's length may hold anything.
+ *   - A wait inside a kernel that exceeds about a second: W4_ERR_TIMEOUT in
+ *     *status_dev.  The call's outputs may then hold anything, and the
+ *     workspace's head is to be zeroed again.
  */
 typedef struct w4_kv8_cache {
     void *kc, *vc;       /* uint8 [num_pages][kv_heads][page_tokens][head_dim]: tokens and
