@@ -21,14 +21,15 @@ namespace {
 constexpr int kTopThreads = 1024;
 constexpr int kBins = 2048;
 
-// fp32 -> uint32 in the order of the values (-NaN lowest, NaN highest), below
-// kForced; -0 and 0 are one key.
+// fp32 -> uint32 in the order of the values, below kForced; -0 and 0 are one
+// key, and every NaN, of either sign, is the highest.
 constexpr uint32_t kForced = 0xFFFFFFFFu;
 constexpr uint32_t kNoPage = 0x7FABCDEFu;   // a NaN no product gives
 __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t b = __float_as_uint(f);
   if (b == 0x80000000u) return 0x80000000u;
-  return (b & 0x80000000u) ? ~b : min(b | 0x80000000u, kForced - 1);
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return kForced - 1;
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
 // A constant as an argument.

@@ -853,7 +853,7 @@ w4_status w4_kv8_weigh(const void *q, size_t q_row_stride, int q_heads, const fl
  *             past the count.
  * new_lens    int32 [batch]: min(len, budget); not the lens array itself.
  * budget      >= max(1, sink + recent).
- * A NaN weight counts as the largest.  Needs weight.  offsets and rows are
+ * A NaN weight, of either sign, counts as the largest.  Needs weight.  offsets and rows are
  * not used.  workspace, flags: as w4_kv8_attn.
  */
 w4_status w4_kv8_evict(const int32_t *dst_table, int32_t *kept, int32_t *new_lens, int budget,
