@@ -270,6 +270,19 @@ __device__ __forceinline__ uint32_t use(uint32_t n) { return (n / N) & 1u; }
 template <int N>
 __device__ __forceinline__ uint32_t before(uint32_t n) { return ((n / N) & 1u) ^ 1u; }
 
+// A part's m and l against its largest weight, not against an m that may lie
+// 2^60 below it, so that the join's factors reach as far down as fp32 does: l's
+// power of two is that weight, or above it by the weights' number.  Returns
+// the factor that brings the part's values along.
+__device__ __forceinline__ float settle(float2& s) {
+  const int e = (int)(__float_as_uint(s.y) >> 23 & 0xFF) - 127;
+  if (e <= 0 || e >= 127) return 1.0f;
+  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+  s.x += (float)e;
+  s.y *= f;
+  return f;
+}
+
 // Four channels of one row from its parts, in order: part(k) is the row's
 // place in the k-th.
 template <int D, typename Part>
@@ -708,17 +721,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               mx = fmaxf(mx, seen >> e & 1u ? y[e] * (e < 16 ? f0 : f1) : -INFINITY);
-            float keep = 1.0f;
+            float up = 0.0f;
             if (!have) {
               have = mx > -INFINITY;
               m = have ? mx : 0.0f;
             } else if (mx - m > kPass) {
-              const float up = ceilf(mx - m);   // whole, so that rescaling is exact
-              keep = exp2_fast(-up);
+              up = ceilf(mx - m);   // whole, so that rescaling is exact
               m += up;
+              up = fminf(up, 252.0f);
             }
-            // what was weighed against the old m: earlier columns, O and l
-            if (__any_sync(0xffffffffu, keep != 1.0f)) {
+            // what was weighed against the old m: earlier columns, O and l.  Twice
+            // where m moves further than one factor reaches: what stands 2^60 above
+            // the old m shows down to 2^-126 of the new one.
+            while (__any_sync(0xffffffffu, up > 0.0f)) {
+              const float keep = exp2_fast(-fminf(up, 126.0f));
+              up = fmaxf(up - 126.0f, 0.0f);
+              l *= keep;
               tmem_wait_st();
               for (int c = 0; c < c0; c += 32) tmem_scale32(scol + c, keep);
               if (done > 0) {
@@ -729,7 +747,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
               }
               tmem_wait_st();
             }
-            l *= keep;
           }
           l += sum;
           // times the block's step; the MMA drops 13 bits of what it reads,
@@ -776,6 +793,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       if (!have) m = -INFINITY;
       const long long at = mine ? (long long)(u.s.row0 + row / p.G) * p.a.Hq + u.h * p.G + row % p.G : 0;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      float2 kept = make_float2(m, l);
+      const float part_scale = direct ? inv : settle(kept);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -798,7 +817,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(p.parts + ((long long)slot * S::kRows + prow) * D + c + e) =
-                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                make_float4(o[e] * part_scale, o[e + 1] * part_scale, o[e + 2] * part_scale,
+                            o[e + 3] * part_scale);
         }
       }
       tc_fence_before();
@@ -810,7 +830,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           p.a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
       } else {
         *reinterpret_cast<float2*>(p.part_stats + ((long long)slot * S::kRows + prow) * 2) =
-            make_float2(m, no ? -1.0f : l);
+            make_float2(kept.x, no ? -1.0f : kept.y);
       }
       // the unit's first CTA says where its parts are
       if (tid == 0 && u.i0 == 0)
