@@ -683,11 +683,16 @@ w4_status w4a16_gemv_chain_task_plan(const w4_gemv_task *tasks, int n_tasks, int
  *     kv_heads).
  *   - A length or row count that is negative, a length over max_len or the
  *     table's pages, more new rows than max_new, rows outside the packed
- *     ones, a page id outside [0, num_pages) that is read: W4_ERR_INDEX in
- *     *status_dev, and what belongs to that sequence (of a page id: that
- *     sequence and head) is left unwritten.  Table entries past a sequence's
- *     pages are not read.  A new row at a negative position (an empty
- *     sequence of a padded batch) is stored nowhere and sees nothing.
+ *     ones: W4_ERR_INDEX in *status_dev, and what belongs to that sequence is
+ *     left unwritten.
+ *   - A page id outside [0, num_pages): W4_ERR_INDEX as well.  Of that
+ *     sequence, w4_kv8_append stores the tokens of every other page;
+ *     w4_kv8_attn leaves the rows that see a token of the page unwritten, and
+ *     may leave other rows of the same head; w4_kv8_weigh leaves out the page's
+ *     tokens; w4_kv8_select and w4_kv8_evict write nothing.  Table entries past
+ *     a sequence's pages are not read.
+ *   - A new row at a negative position (an empty sequence of a padded batch)
+ *     is stored nowhere and sees nothing.
  *   - Calls are deterministic: no sum's order depends on timing.
  *   - Every kernel is launched as a programmatic dependent and waits for the
  *     kernel before it in the stream before it reads or writes anything:

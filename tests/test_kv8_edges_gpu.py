@@ -82,3 +82,80 @@ def test_attn_light_tokens_keep_their_bits(cuda_lib, new, D, length, order):
     out, lse = c.attn()
     assert status(c) == 0
     check_attn(out, lse, ref, D)
+
+
+def good_or_unwritten(c, out, lse, ref, blind):
+    """Rows `blind` (bool [rows]) unwritten, every other one right, or unwritten in all channels of
+    one head."""
+    assert np.isnan(out[blind]).all() and np.isnan(lse[blind]).all()
+    left = np.isnan(lse)
+    assert np.array_equal(left, np.isnan(out).all(-1)) and np.array_equal(left, np.isnan(out).any(-1))
+    rows, heads = np.nonzero(~left)
+    check_attn(out[rows, heads], lse[rows, heads], [x[rows, heads] for x in ref], c.D)
+    return left
+
+
+@pytest.mark.parametrize("long", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [3, 100])
+def test_attn_rows_that_see_a_bad_page_stay_unwritten(cuda_lib, new, D, long):
+    """A page that is none among the new tokens' own: rows before it do not see it.  Few rows (the
+    token kernel) and many (several row tiles of the chunk kernel), units whole and cut."""
+    length = (5000 if long else 300) + new
+    c = Case(7 * D + new, [150, length, 90], [2, new, 2], 2, D, 16, 8)
+    ref = kv8.attn_ref(c.cache, c.table, c.lens, c.offsets, c.q, c.scale)
+    first = length - new
+    pos = np.full(c.rows, -1)
+    pos[2:2 + new] = first + np.arange(new)
+    for page in (0, (first + new * 3 // 5) // 16, (length - 1) // 16):
+        keep = c.table[1, page]
+        c.table[1, page] = c.cache["ks"].shape[0] if page else -3
+        c.to_gpu()
+        blind = pos >= page * 16
+        left = good_or_unwritten(c, *c.attn(), ref, blind)
+        assert status(c) == ERR
+        assert not left[:2].any() and not left[2 + new:].any()   # other sequences
+        if new == 100 and 16 < page < (length - 1) // 16:        # row tiles before the page
+            assert not left[2:2 + 16].any()
+        c.table[1, page] = keep
+    c.to_gpu()
+    c.batch.tensors[1][1] = length + 1                           # a length past the bound
+    left = good_or_unwritten(c, *c.attn(), ref, pos >= 0)
+    assert status(c) == ERR
+    assert not left[:2].any() and not left[2 + new:].any()
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_attn_refusals_among_thousands_of_units(cuda_lib, D):
+    """Many units a CTA, a third of them with a page that is none: the others' bits as without."""
+    B = 700
+    rng = np.random.default_rng(D)
+    c = Case(D, [int(x) for x in rng.integers(1, 50, B)], None, 8, D, 16, 128)
+    c.to_gpu()
+    out, lse = c.attn()
+    assert status(c) == 0 and not np.isnan(out).any()
+    bad = rng.random(B) < 0.33
+    for b in np.flatnonzero(bad):
+        c.table[b, rng.integers(0, -(-c.lens[b] // 16))] = 1 << 30
+    c.to_gpu()
+    out2, lse2 = c.attn()
+    assert status(c) == ERR
+    assert np.isnan(out2[bad]).all() and np.isnan(lse2[bad]).all()
+    assert np.array_equal(out[~bad], out2[~bad]) and np.array_equal(lse[~bad], lse2[~bad])
+
+
+def test_append_stores_all_but_a_bad_page(cuda_lib):
+    c = Case(8, [100, 70], [80, 30], 2, 64, 16)
+    c.fix_ranges([20, 40])
+    k, v = (bf16_round(c.rng.normal(size=(c.rows, 2, 64))) for _ in range(2))
+    want = kv8.append_ref(c.cache, c.table, c.lens, c.offsets, k, v)
+    page = c.table[0, 3]
+    for n in want:
+        want[n][page] = c.cache[n][page]
+    c.table[0, 3] = -1
+    c.to_gpu()
+    lib.kv8_append(c.dev, c.batch, *(torch.from_numpy(x).cuda().to(torch.bfloat16) for x in (k, v)),
+                   c.status)
+    assert status(c) == ERR
+    got = c.dev_arrays()
+    assert all(np.array_equal(got[n], want[n]) for n in want)
