@@ -671,7 +671,10 @@ w4_status w4a16_gemv_chain_task_plan(const w4_gemv_task *tasks, int n_tasks, int
  *
  * The library's writers (w4_kv8_append, w4_kv8_evict) choose steps that are
  * powers of two, so rescaling a block and reading it back round nowhere but
- * in the codes; the readers take any finite step.
+ * in the codes; the readers take any step from 0 to 2^30 (values to 2^37, whose
+ * sums stay in fp32's range at any length and spread of the scores).  Larger
+ * steps, which w4_kv8_append writes for larger values, are read as they are, but
+ * a prompt chunk's sums may then overflow.
  *
  * Conventions beside those at the top of this file:
  *   - `offsets` packs the sequences' new (query) rows: rows offsets[b] ..
@@ -768,7 +771,10 @@ w4_status w4_kv8_append(const w4_kv8_cache *cache, const w4_kv8_batch *batch, co
  *   out[r][i] = sum_t p_t value[t],  p_t = exp(scale q.key[t]) / sum of them,
  *   lse[r][i] = log of that sum
  * over the keys t that row r sees; a row that sees none gives 0 and -inf.
- * Products are exact and sums fp32; p is rounded to 11 significant bits.
+ * Products are exact and sums fp32; p is rounded to 11 significant bits, down to
+ * 2^-118 of the row's largest p (and, for a prompt chunk, as long as that
+ * ratio times the block's value step is at least 2^-126).  What is lighter may
+ * count as nothing.
  *
  * out         bf16 [rows][q_heads][head_dim], 16-byte aligned.
  * lse         fp32 [rows][q_heads], or NULL.

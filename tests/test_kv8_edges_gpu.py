@@ -159,3 +159,27 @@ def test_append_stores_all_but_a_bad_page(cuda_lib):
     assert status(c) == ERR
     got = c.dev_arrays()
     assert all(np.array_equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("vstep", [0.0, 2.0 ** -100, 2.0 ** -6 * 1.3, 2.0 ** 30])
+@pytest.mark.parametrize("rise", [0, 59, 110])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [None, 30])
+def test_attn_steps_at_the_ends_of_their_range(cuda_lib, new, D, rise, vstep):
+    """Thousands of tokens 2^rise above the first ones, in values of every allowed size: below
+    what moves the chunk kernel's maximum, and above."""
+    n = 2500
+    c = Case(17, [n], None if new is None else [new], 1, D, 64, 8)
+    c.cache["kc"][:] = 128
+    c.cache["ks"][:] = 2.0 ** 30
+    c.cache["vs"][:] = vstep
+    pos = np.arange(n)
+    c.cache["kc"][c.table[0, pos // 64], 0, pos % 64, 0] = np.where(pos < 40, 128, 128 + rise)
+    c.q[:] = 0
+    c.q[:, :, 0] = 2.0 ** -30
+    c.scale = float(np.log(2.0))
+    c.to_gpu()
+    ref = kv8.attn_ref(c.cache, c.table, c.lens, c.offsets, c.q, c.scale)
+    out, lse = c.attn()
+    assert status(c) == 0
+    check_attn(out, lse, ref, D)
