@@ -39,6 +39,9 @@ struct WeighParams {
   int Hq, G;
   float scale;
   int window;
+  const int32_t* sel;     // chosen pages (single tokens), or NULL
+  const int32_t* n_sel;
+  int max_sel;
   int32_t* status;
 };
 

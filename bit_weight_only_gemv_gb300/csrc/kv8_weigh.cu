@@ -7,7 +7,8 @@
 //
 // Few rows on a key head (single tokens): the bytes of the keys bound it;
 // equal runs of 16-token slices over all sequences, each warp streaming its
-// own through a ring of tiled copies, query fragments in registers.  8
+// own through a ring of tiled copies, query fragments in registers; also over
+// chosen pages.  8
 // sequences of up to 16k tokens, 32 heads on 8 of 128 channels: 25.9 us, 3.8
 // TB/s; about 10 us of that are the start (lengths, page ids, first copies), the
 // rest runs at 6 TB/s.
@@ -61,7 +62,12 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
       : "memory");
 }
 
-template <int D, int NQ>
+// kSel: over the pages of p.sel, one row a sequence.  A run's entries are then
+// (sequence, head) pairs, and groups of more query rows than a tile go through
+// the same slices tile by tile, so that a token's additions keep their order.
+// 16 sequences, 128 pages of 32 tokens each out of up to 1024, 32 heads on 8 of 128
+// channels: 20.2 us (the whole cache 73.7).
+template <int D, int NQ, bool kSel>
 __global__ void __launch_bounds__(kThreads, 2)
     weigh_token_kernel(const __grid_constant__ WeighParams p) {
   using S = Shape<D>;
@@ -84,14 +90,24 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (blockIdx.x == 0)
     for (int b = tid; b < p.bt.B; b += kThreads)
       if (!sequence(p.bt, p.c.P, b).ok) report(p.status, W4_ERR_INDEX);
-  auto weight = [&](int b, int* units) -> long long {
-    const Seq s = sequence(p.bt, p.c.P, b);
+  const int per = p.c.P / kSlice;
+  auto weight = [&](int e, int* units) -> long long {
+    const Seq s = sequence(p.bt, p.c.P, kSel ? e / p.c.H : e);
     if (!s.ok || s.n == 0) return 0;
+    if (kSel) {
+      const int n = __ldg(p.n_sel + e);
+      if (n <= 0 || n > p.max_sel) {
+        if (n != 0 && blockIdx.x == 0) report(p.status, W4_ERR_INDEX);
+        return 0;
+      }
+      *units += 1;
+      return (long long)n * per;
+    }
     *units += p.c.H;   // one row tile
     return head_slices(s, p.G, p.window, kRows, kSlice) * p.c.H;
   };
   Run run;
-  const bool any = find_run<kWarps>(p.bt.B, kMinSlices, weight, scan, &run);
+  const bool any = find_run<kWarps>(kSel ? p.bt.B * p.c.H : p.bt.B, kMinSlices, weight, scan, &run);
   __syncthreads();
   if (!any) return;
 
@@ -99,138 +115,155 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t got_phase = 0;
   bool dead = false;
   long long g = run.g0, off = run.off;
-  int b = run.entry;
+  int entry = run.entry;
   while (g < run.g1 && !dead) {
+    const int b = kSel ? entry / p.c.H : entry;
     const Seq s = sequence(p.bt, p.c.P, b);
-    const Tile t = tile_of(s, p.G, p.window, 0, kRows, kSlice);   // one row tile
-    const int h = quotient(off, t.slices), sl0 = (int)(off - (long long)h * t.slices);
+    Tile t = tile_of(s, p.G, p.window, 0, kRows, kSlice);   // one row tile
+    if (kSel) t.slices = __ldg(p.n_sel + entry) * per;
+    const int h = kSel ? entry - b * p.c.H : quotient(off, t.slices);
+    const int sl0 = kSel ? (int)off : (int)(off - (long long)h * t.slices);
     const int sl1 = (int)min((long long)t.slices, sl0 + (run.g1 - g));
     const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
     const int R = s.n * p.G;
-    uint2 raw[NQ][D / 16];   // query rows, on their way
+#pragma unroll 1
+    for (int r0 = 0; r0 < (kSel ? R : 1) && !dead; r0 += kRows) {   // dense: one row tile
+      uint2 raw[NQ][D / 16];   // query rows, on their way
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int r = 8 * n + i;
-      load_query<D>(r < R ? p.q + (long long)(s.row0 + r / p.G) * p.q_stride +
-                                (long long)(h * p.G + r % p.G) * D
-                          : nullptr,
-                    j, raw[n]);
-    }
-    const int count = (sl1 - sl0 - warp + kWarps - 1) / kWarps;
-    // the steps' loads set out before the first copies (behind them they would
-    // queue) and are waited for after them
-    float ks = 0.0f;
-    auto fill_steps = [&](int k0) {
-      if (k0 + lane < count) meta[(k0 + lane) & (kRing - 1)].ks = ks;
-      __syncwarp();
-    };
-    auto issue = [&](int k) {
-      if (k >= count || dead) return;
-      if ((k & 31) == 0) {   // descriptions of the next 32 slices
-        __syncwarp();
-        const int kk = k + lane;
-        if (kk < count) {
-          Meta d = {-1, t.lo + (sl0 + warp + kWarps * kk) * kSlice, 0.0f, 0};
-          if (d.tok < t.hi) {
-            const int page = __ldg(table + d.tok / p.c.P);
-            if (page < 0 || page >= p.c.num_pages) {
-              report(p.status, W4_ERR_INDEX);
-            } else {
-              d.page = page;
-              ks = __ldg(p.c.ks + p.c.pair(page, h));
-            }
-          }
-          meta[kk & (kRing - 1)] = d;
-        }
-        __syncwarp();
+      for (int n = 0; n < NQ; ++n) {
+        const int r = (kSel ? r0 : 0) + 8 * n + i;
+        load_query<D>(r < R ? p.q + (long long)(s.row0 + r / p.G) * p.q_stride +
+                                  (long long)(h * p.G + r % p.G) * D
+                            : nullptr,
+                      j, raw[n]);
       }
-      if (lane == 0) {
+      const int count = (sl1 - sl0 - warp + kWarps - 1) / kWarps;
+      // the steps' loads set out before the first copies (behind them they would
+      // queue) and are waited for after them
+      float ks = 0.0f;
+      auto fill_steps = [&](int k0) {
+        if (k0 + lane < count) meta[(k0 + lane) & (kRing - 1)].ks = ks;
+        __syncwarp();
+      };
+      auto issue = [&](int k) {
+        if (k >= count || dead) return;
+        if ((k & 31) == 0) {   // descriptions of the next 32 slices
+          __syncwarp();
+          const int kk = k + lane;
+          if (kk < count) {
+            const int sl = sl0 + warp + kWarps * kk;
+            Meta d = {-1, t.lo + sl * kSlice, 0.0f, 0};
+            bool read = d.tok < t.hi;
+            if (kSel) {
+              const int lp = __ldg(p.sel + (long long)entry * p.max_sel + sl / per);
+              read = lp >= 0 && (long long)lp * p.c.P < s.len;
+              if (!read) report(p.status, W4_ERR_INDEX);
+              d.tok = read ? lp * p.c.P + sl % per * kSlice : 0;
+              read &= d.tok < t.hi &&
+                      !(p.window > 0 && d.tok + kSlice <= (long long)t.pmin + 1 - p.window);
+            }
+            if (read) {
+              const int page = __ldg(table + d.tok / p.c.P);
+              if (page < 0 || page >= p.c.num_pages) {
+                report(p.status, W4_ERR_INDEX);
+              } else {
+                d.page = page;
+                ks = __ldg(p.c.ks + p.c.pair(page, h));
+              }
+            }
+            meta[kk & (kRing - 1)] = d;
+          }
+          __syncwarp();
+        }
+        if (lane == 0) {
+          const Meta d = meta[k & (kRing - 1)];
+          const uint32_t bar = bar0 + 8 * put, st = stage0 + put * S::kStageBytes;
+          if (d.page < 0) {
+            mbar_arrive(bar);
+          } else {
+            mbar_arrive_expect_tx(bar, S::kStageBytes);
+#pragma unroll
+            for (int x = 0; x < D; x += 128)
+              tma_4d(st + x * kSlice, &p.tm, x, d.tok & (p.c.P - 1), h, d.page, bar);
+          }
+        }
+        if (++put == kStages) put = 0;
+        if (k > 0 && (k & 31) == 0) fill_steps(k);   // once its first copy is on its way
+      };
+#pragma unroll 1
+      for (int k = 0; k < kStages; ++k) issue(k);
+      fill_steps(0);
+      uint32_t q[NQ][D / 16][2];
+      float f[NQ][2], lse2[NQ][2];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const float down = scale_query<D>(raw[n], q[n]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          f[n][c] = __shfl_sync(0xffffffffu, down, 8 * j + 4 * c) * (p.scale * kLog2e);
+          const int rc = (kSel ? r0 : 0) + 8 * n + 2 * j + c;
+          float l = INFINITY;   // adds nothing
+          if (rc < R) {
+            l = p.lse[(long long)(s.row0 + rc / p.G) * p.Hq + h * p.G + rc % p.G] * kLog2e;
+            if (l == -INFINITY) l = INFINITY;
+          }
+          lse2[n][c] = l;
+        }
+      }
+#pragma unroll 1
+      for (int k = 0; k < count; ++k) {
+        if (!mbar_wait_bounded(bar0 + 8 * got, got_phase, kWait)) {
+          dead = true;
+          if (lane == 0) report(p.status, W4_ERR_TIMEOUT);
+          break;
+        }
         const Meta d = meta[k & (kRing - 1)];
-        const uint32_t bar = bar0 + 8 * put, st = stage0 + put * S::kStageBytes;
-        if (d.page < 0) {
-          mbar_arrive(bar);
-        } else {
-          mbar_arrive_expect_tx(bar, S::kStageBytes);
+        if (d.page >= 0) {
+          float* w = p.c.weight + p.c.pair(d.page, h) * p.c.P + (d.tok & (p.c.P - 1)) + i;
+          float x[NQ][4];
+          key_scores<D, NQ>(stage0 + got * S::kStageBytes, i, j, q, x);
+          const bool cut = d.tok + kSlice - 1 > t.pmin || (p.window > 0 && d.tok <= t.pmax - p.window);
+          float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
-          for (int x = 0; x < D; x += 128)
-            tma_4d(st + x * kSlice, &p.tm, x, d.tok & (p.c.P - 1), h, d.page, bar);
-        }
-      }
-      if (++put == kStages) put = 0;
-      if (k > 0 && (k & 31) == 0) fill_steps(k);   // once its first copy is on its way
-    };
-#pragma unroll 1
-    for (int k = 0; k < kStages; ++k) issue(k);
-    fill_steps(0);
-    uint32_t q[NQ][D / 16][2];
-    float f[NQ][2], lse2[NQ][2];
+          for (int n = 0; n < NQ; ++n)
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const float down = scale_query<D>(raw[n], q[n]);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        f[n][c] = __shfl_sync(0xffffffffu, down, 8 * j + 4 * c) * (p.scale * kLog2e);
-        const int rc = 8 * n + 2 * j + c;
-        float l = INFINITY;   // adds nothing
-        if (rc < R) {
-          l = p.lse[(long long)(s.row0 + rc / p.G) * p.Hq + h * p.G + rc % p.G] * kLog2e;
-          if (l == -INFINITY) l = INFINITY;
-        }
-        lse2[n][c] = l;
-      }
-    }
-#pragma unroll 1
-    for (int k = 0; k < count; ++k) {
-      if (!mbar_wait_bounded(bar0 + 8 * got, got_phase, kWait)) {
-        dead = true;
-        if (lane == 0) report(p.status, W4_ERR_TIMEOUT);
-        break;
-      }
-      const Meta d = meta[k & (kRing - 1)];
-      if (d.page >= 0) {
-        float* w = p.c.weight + p.c.pair(d.page, h) * p.c.P + (d.tok & (p.c.P - 1)) + i;
-        float x[NQ][4];
-        key_scores<D, NQ>(stage0 + got * S::kStageBytes, i, j, q, x);
-        const bool cut = d.tok + kSlice - 1 > t.pmin || (p.window > 0 && d.tok <= t.pmax - p.window);
-        float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float y = exp2_fast(fmaf(x[n][e], d.ks * f[n][e & 1], -lse2[n][e & 1]));
-            if (cut) {
-              const int r = min(R - 1, 8 * n + 2 * j + (e & 1));
-              const int pos = s.len - s.n + r / p.G, tok = d.tok + i + 8 * (e >> 1);
-              if (tok > pos || (p.window > 0 && tok <= pos - p.window)) y = 0.0f;
+            for (int e = 0; e < 4; ++e) {
+              float y = exp2_fast(fmaf(x[n][e], d.ks * f[n][e & 1], -lse2[n][e & 1]));
+              if (cut) {
+                // (chosen pages: one row a sequence, the last position)
+                const int r = kSel ? 0 : min(R - 1, 8 * n + 2 * j + (e & 1));
+                const int pos = s.len - s.n + r / p.G, tok = d.tok + i + 8 * (e >> 1);
+                if (tok > pos || (p.window > 0 && tok <= pos - p.window)) y = 0.0f;
+              }
+              (e < 2 ? a0 : a1) += y;
             }
-            (e < 2 ? a0 : a1) += y;
+          a0 += __shfl_xor_sync(0xffffffffu, a0, 1);
+          a1 += __shfl_xor_sync(0xffffffffu, a1, 1);
+          a0 += __shfl_xor_sync(0xffffffffu, a0, 2);
+          a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
+          if (j == 0) {
+            // one addition to each weight, which nothing here waits for (loading
+            // the old weight first: 30.8 us against 29.0 at 8 x 16k keys)
+            if (d.tok + i < s.len) atomicAdd(w, a0);
+            if (d.tok + i + 8 < s.len) atomicAdd(w + 8, a1);
           }
-        a0 += __shfl_xor_sync(0xffffffffu, a0, 1);
-        a1 += __shfl_xor_sync(0xffffffffu, a1, 1);
-        a0 += __shfl_xor_sync(0xffffffffu, a0, 2);
-        a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
-        if (j == 0) {
-          // one addition to each weight, which nothing here waits for (loading
-          // the old weight first: 30.8 us against 29.0 at 8 x 16k keys)
-          if (d.tok + i < s.len) atomicAdd(w, a0);
-          if (d.tok + i + 8 < s.len) atomicAdd(w + 8, a1);
         }
+        __syncwarp();
+        if (++got == kStages) {
+          got = 0;
+          got_phase ^= 1u;
+        }
+        issue(k + kStages);
       }
-      __syncwarp();
-      if (++got == kStages) {
-        got = 0;
-        got_phase ^= 1u;
-      }
-      issue(k + kStages);
     }
     const long long step = sl1 - sl0;
     g += step;
     off += step;
-    if (off == (long long)t.slices * p.c.H && g < run.g1) {
+    if (off == (long long)t.slices * (kSel ? 1 : p.c.H) && g < run.g1) {
       off = 0;
       int none = 0;
-      do ++b;
-      while (weight(b, &none) == 0);
+      do ++entry;
+      while (weight(entry, &none) == 0);
     }
   }
   if (dead)   // copies still in flight land before the CTA leaves
@@ -409,16 +442,16 @@ w4_status allow_smem(K kern, int smem, int dev, bool* done) {
   return W4_OK;
 }
 
-template <int D, int NQ>
+template <int D, int NQ, bool kSel>
 w4_status launch_token(WeighParams& p, int sms, w4_stream_t stream, int dev) {
   static bool done[64] = {};
   if (!tensor_map(&p.tm, p.c.kc, p.c, kSlice)) {
     note_cuda_error(cudaErrorInvalidValue);
     return W4_ERR_LAUNCH;
   }
-  const w4_status st = allow_smem(weigh_token_kernel<D, NQ>, Shape<D>::kSmem, dev, done);
+  const w4_status st = allow_smem(weigh_token_kernel<D, NQ, kSel>, Shape<D>::kSmem, dev, done);
   if (st != W4_OK) return st;
-  return launch(weigh_token_kernel<D, NQ>, dim3((unsigned)(2 * sms)), kThreads, Shape<D>::kSmem,
+  return launch(weigh_token_kernel<D, NQ, kSel>, dim3((unsigned)(2 * sms)), kThreads, Shape<D>::kSmem,
                 stream, p);
 }
 
@@ -446,13 +479,25 @@ extern "C" w4_status w4_kv8_weigh(const void* q, size_t q_row_stride, int q_head
                                   const float* lse, const w4_kv8_cache* cache,
                                   const w4_kv8_batch* batch, float scale, int window,
                                   int32_t* status_dev, unsigned flags, w4_stream_t stream) {
+  return w4_kv8_weigh_pages(q, q_row_stride, q_heads, lse, cache, batch, scale, window, nullptr,
+                            nullptr, 0, status_dev, flags, stream);
+}
+
+extern "C" w4_status w4_kv8_weigh_pages(const void* q, size_t q_row_stride, int q_heads,
+                                        const float* lse, const w4_kv8_cache* cache,
+                                        const w4_kv8_batch* batch, float scale, int window,
+                                        const int32_t* sel, const int32_t* n_sel, int max_sel,
+                                        int32_t* status_dev, unsigned flags, w4_stream_t stream) {
   kv8::WeighParams p = {};
   w4_status st = kv8::view(cache, batch, &p.c, &p.bt);
   if (st != W4_OK) return st;
-  if (lse == nullptr || p.c.weight == nullptr || (flags & ~W4_FLAG_PDL) != 0 || window < 0)
+  if (lse == nullptr || p.c.weight == nullptr || (flags & ~W4_FLAG_PDL) != 0 || window < 0 ||
+      (sel == nullptr) != (n_sel == nullptr) || (sel != nullptr && max_sel < 1))
     return W4_ERR_ARG;
   if ((st = kv8::check_q(q, q_row_stride, q_heads, p.c)) != W4_OK) return st;
-  if (kv8::misaligned(lse, 4)) return W4_ERR_ALIGN;
+  if (sel != nullptr && (p.bt.max_new != 1 || max_sel > (1 << 24))) return W4_ERR_SHAPE;
+  if (kv8::misaligned(lse, 4) || kv8::misaligned(sel, 4) || kv8::misaligned(n_sel, 4))
+    return W4_ERR_ALIGN;
   int dev = -1;
   DeviceInfo di;
   if (!current_device(&dev, &di)) return W4_ERR_DEVICE;
@@ -463,9 +508,23 @@ extern "C" w4_status w4_kv8_weigh(const void* q, size_t q_row_stride, int q_head
   p.G = q_heads / p.c.H;
   p.scale = scale;
   p.window = window;
+  p.sel = sel;
+  p.n_sel = n_sel;
+  p.max_sel = max_sel;
   p.status = status_dev;
   if (p.bt.max_len == 0) return W4_OK;
   const long long rows = (long long)p.bt.max_new * p.G;
+  const int one = rows <= 8 ? 1 : 0;
+  if (sel != nullptr) {
+    switch (p.c.D * 2 + one) {
+      case 64 * 2 + 1: return kv8::launch_token<64, 1, true>(p, di.sms, stream, dev);
+      case 64 * 2: return kv8::launch_token<64, 2, true>(p, di.sms, stream, dev);
+      case 128 * 2 + 1: return kv8::launch_token<128, 1, true>(p, di.sms, stream, dev);
+      case 128 * 2: return kv8::launch_token<128, 2, true>(p, di.sms, stream, dev);
+      case 256 * 2 + 1: return kv8::launch_token<256, 1, true>(p, di.sms, stream, dev);
+      default: return kv8::launch_token<256, 2, true>(p, di.sms, stream, dev);
+    }
+  }
   if (rows > kv8::kManyRows) return kv8::weigh_many(p, di.sms, dev, stream);
   if (rows > 16) {
     switch (p.c.D) {
@@ -474,12 +533,12 @@ extern "C" w4_status w4_kv8_weigh(const void* q, size_t q_row_stride, int q_head
       default: return kv8::launch_chunk<256>(p, stream, dev);
     }
   }
-  switch (p.c.D * 4 + (rows <= 8 ? 1 : 2)) {
-    case 64 * 4 + 1: return kv8::launch_token<64, 1>(p, di.sms, stream, dev);
-    case 64 * 4 + 2: return kv8::launch_token<64, 2>(p, di.sms, stream, dev);
-    case 128 * 4 + 1: return kv8::launch_token<128, 1>(p, di.sms, stream, dev);
-    case 128 * 4 + 2: return kv8::launch_token<128, 2>(p, di.sms, stream, dev);
-    case 256 * 4 + 1: return kv8::launch_token<256, 1>(p, di.sms, stream, dev);
-    default: return kv8::launch_token<256, 2>(p, di.sms, stream, dev);
+  switch (p.c.D * 2 + one) {
+    case 64 * 2 + 1: return kv8::launch_token<64, 1, false>(p, di.sms, stream, dev);
+    case 64 * 2: return kv8::launch_token<64, 2, false>(p, di.sms, stream, dev);
+    case 128 * 2 + 1: return kv8::launch_token<128, 1, false>(p, di.sms, stream, dev);
+    case 128 * 2: return kv8::launch_token<128, 2, false>(p, di.sms, stream, dev);
+    case 256 * 2 + 1: return kv8::launch_token<256, 1, false>(p, di.sms, stream, dev);
+    default: return kv8::launch_token<256, 2, false>(p, di.sms, stream, dev);
   }
 }

@@ -42,8 +42,8 @@ EXPORTS = ("w4_status_str", "w4_abi_version", "w4_last_cuda_error", "w4a16_gemv"
            "w4a16_gemv_chain_workspace_bytes", "w4a16_gemv_chain_plan",
            "w4a16_gemv_chain_task_plan", "w4a16_gemv_id_plan", "w4a16_gemv_prefetch_l2",
            "w4a16_gemv_plan_flags", "w4_kv8_append", "w4_kv8_attn", "w4_kv8_attn_workspace_bytes",
-           "w4_kv8_select", "w4_kv8_select_workspace_bytes", "w4_kv8_weigh", "w4_kv8_evict",
-           "w4_kv8_evict_workspace_bytes")
+           "w4_kv8_select", "w4_kv8_select_workspace_bytes", "w4_kv8_weigh", "w4_kv8_weigh_pages",
+           "w4_kv8_evict", "w4_kv8_evict_workspace_bytes")
 W4_TASK_SILU_MUL = 1
 W4_MAX_L2_RANGES = 4
 CHAIN_MAX_TASKS = 320
@@ -194,6 +194,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4_kv8_select_workspace_bytes.argtypes = [cp, bp]
     lib.w4_kv8_weigh.restype = i32
     lib.w4_kv8_weigh.argtypes = [vp, sz, i32, vp, cp, bp, f32, i32, vp, u32, vp]
+    lib.w4_kv8_weigh_pages.restype = i32
+    lib.w4_kv8_weigh_pages.argtypes = [vp, sz, i32, vp, cp, bp, f32, i32, vp, vp, i32, vp, u32, vp]
     lib.w4_kv8_evict.restype = i32
     lib.w4_kv8_evict.argtypes = [vp, vp, vp, i32, i32, i32, cp, bp, vp, sz, vp, u32, vp]
     lib.w4_kv8_evict_workspace_bytes.restype = sz
@@ -824,6 +826,21 @@ def kv8_append(cache: KV8Cache, batch: KV8Batch, k: torch.Tensor, v: torch.Tenso
     bind_kv8_append(cache, batch, k, v, status)(pdl, stream)
 
 
+def _kv8_sel(cache: KV8Cache, batch: KV8Batch, sel, n_sel) -> int:
+    """max_sel of a selection (0: none)."""
+    if sel is None and n_sel is None:
+        return 0
+    if sel is None or n_sel is None:
+        raise ValueError("sel and n_sel go together")
+    _need(sel, torch.int32, "sel")
+    _need(n_sel, torch.int32, "n_sel")
+    max_sel = sel.shape[-1]
+    if tuple(sel.shape) != (batch.batch, cache.kv_heads, max_sel) or \
+            tuple(n_sel.shape) != (batch.batch, cache.kv_heads):
+        raise ValueError("sel must be [batch, kv_heads, max_sel] and n_sel [batch, kv_heads]")
+    return max_sel
+
+
 def bind_kv8_attn(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: float,
                   out: torch.Tensor, lse: torch.Tensor = None, window: int = 0,
                   sel: torch.Tensor = None, n_sel: torch.Tensor = None,
@@ -838,16 +855,7 @@ def bind_kv8_attn(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, scale: floa
         _need(lse, torch.float32, "lse")
         if tuple(lse.shape) != (rows, q_heads):
             raise ValueError("lse must be [rows, q_heads]")
-    max_sel = 0
-    if sel is not None or n_sel is not None:
-        if sel is None or n_sel is None:
-            raise ValueError("sel and n_sel go together")
-        _need(sel, torch.int32, "sel")
-        _need(n_sel, torch.int32, "n_sel")
-        max_sel = sel.shape[-1]
-        if tuple(sel.shape) != (batch.batch, cache.kv_heads, max_sel) or \
-                tuple(n_sel.shape) != (batch.batch, cache.kv_heads):
-            raise ValueError("sel must be [batch, kv_heads, max_sel] and n_sel [batch, kv_heads]")
+    max_sel = _kv8_sel(cache, batch, sel, n_sel)
     bs = batch.struct(rows)
     args = (_ptr(out), _ptr(lse), _ptr(q), stride, q_heads, ctypes.byref(cache.struct),
             ctypes.byref(bs), scale, window, _ptr(sel), _ptr(n_sel), max_sel, _ptr(workspace),
@@ -899,24 +907,32 @@ def kv8_select(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, max_sel: int, 
 
 
 def bind_kv8_weigh(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, lse: torch.Tensor,
-                   scale: float, window: int = 0, status: torch.Tensor = None):
-    """w4_kv8_weigh with its arguments marshalled once: returns call(pdl=False, stream=None)."""
+                   scale: float, window: int = 0, status: torch.Tensor = None,
+                   sel: torch.Tensor = None, n_sel: torch.Tensor = None):
+    """w4_kv8_weigh (over the pages of sel / n_sel if given: w4_kv8_weigh_pages) with its arguments
+    marshalled once: returns call(pdl=False, stream=None)."""
     stride, rows = _kv8_rows(q, "q", None, cache.head_dim)
     _need(lse, torch.float32, "lse")
     if tuple(lse.shape) != (rows, q.shape[1]):
         raise ValueError("lse must be [rows, q_heads]")
     bs = batch.struct(rows)
     args = (_ptr(q), stride, q.shape[1], _ptr(lse), ctypes.byref(cache.struct), ctypes.byref(bs),
-            scale, window, _ptr(status))
-    return _kv8_call(load().w4_kv8_weigh, "w4_kv8_weigh", args,
-                     (cache, batch, bs, q, lse, status))
+            scale, window)
+    max_sel = _kv8_sel(cache, batch, sel, n_sel)
+    if max_sel == 0 and sel is None:
+        return _kv8_call(load().w4_kv8_weigh, "w4_kv8_weigh", (*args, _ptr(status)),
+                         (cache, batch, bs, q, lse, status))
+    return _kv8_call(load().w4_kv8_weigh_pages, "w4_kv8_weigh_pages",
+                     (*args, _ptr(sel), _ptr(n_sel), max_sel, _ptr(status)),
+                     (cache, batch, bs, q, lse, sel, n_sel, status))
 
 
 def kv8_weigh(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, lse: torch.Tensor, scale: float,
-              window: int = 0, status: torch.Tensor = None, pdl: bool = False, stream=None):
+              window: int = 0, status: torch.Tensor = None, pdl: bool = False, stream=None,
+              sel: torch.Tensor = None, n_sel: torch.Tensor = None):
     """Add the attention weight that each cached token receives from the new rows to
-    cache.weight (lse as given by kv8_attn for the same rows)."""
-    bind_kv8_weigh(cache, batch, q, lse, scale, window, status)(pdl, stream)
+    cache.weight (lse as given by kv8_attn for the same rows, with the same selection)."""
+    bind_kv8_weigh(cache, batch, q, lse, scale, window, status, sel, n_sel)(pdl, stream)
 
 
 def bind_kv8_evict(cache: KV8Cache, batch: KV8Batch, dst_table: torch.Tensor, kept: torch.Tensor,

@@ -114,10 +114,10 @@ class Layer:
         lse = torch.empty((1, self.hq), dtype=torch.float32, device="cuda")
         out = lib.kv8_attn(self.cache, self.one, q, self.scale, lse=lse, sel=sel, n_sel=n_sel,
                            workspace=self.ws_attn, status=self.status)
-        # weights over the whole cache against the chosen pages' sum: what a
-        # page that was not chosen would have had counts too
-        lib.kv8_weigh(self.cache, self.one, q, lse, self.scale, status=self.status)
-        self.last = dict(q=q, sel=sel, n_sel=n_sel, out=out)
+        # the tokens of pages that were not chosen received nothing
+        lib.kv8_weigh(self.cache, self.one, q, lse, self.scale, status=self.status, sel=sel,
+                      n_sel=n_sel)
+        self.last = dict(q=q, sel=sel, n_sel=n_sel, out=out, lse=lse)
         return self._product(self.o, out.view(1, -1))
 
     def _kept_pages(self):
@@ -140,10 +140,12 @@ class Layer:
         """The cache and the last step on the host (for checks)."""
         t = self.cache.tensors
         last = self.last
-        return dict(cache={n: x.cpu().numpy() for n, x in zip(("kc", "vc", "ks", "vs"), t)},
+        names = ("kc", "vc", "ks", "vs", "ranges", "weight")
+        return dict(cache={n: x.cpu().numpy() for n, x in zip(names, t)},
                     table=self.table.cpu().numpy(), lens=self.lens.cpu().numpy(),
                     q=last["q"].double().cpu().numpy(), sel=last["sel"].cpu().numpy(),
-                    n_sel=last["n_sel"].cpu().numpy(), out=last["out"].double().cpu().numpy())
+                    n_sel=last["n_sel"].cpu().numpy(), out=last["out"].double().cpu().numpy(),
+                    lse=last["lse"].double().cpu().numpy())
 
 
 def main():

@@ -836,14 +836,26 @@ size_t w4_kv8_select_workspace_bytes(const w4_kv8_cache *cache, const w4_kv8_bat
  *
  *   weight[t] += sum over rows r that see t and heads i of the group of
  *                exp(scale q_ri.key[t] - lse[r][i])
- * lse as written by w4_kv8_attn for the same rows (a row with lse = -inf
- * adds nothing).  A page id that is none leaves out its own tokens only.  A
- * page belongs to one sequence of the call (two would race on its weights).
+ * lse as written by w4_kv8_attn for the same rows over the same tokens, so
+ * that a row and head add 1 in all (a row with lse = -inf adds nothing).  A page
+ * id that is none leaves out its own tokens only.  A page belongs to one
+ * sequence of the call (two would race on its weights).
  * flags: W4_FLAG_PDL.
  */
 w4_status w4_kv8_weigh(const void *q, size_t q_row_stride, int q_heads, const float *lse,
                        const w4_kv8_cache *cache, const w4_kv8_batch *batch, float scale,
                        int window, int32_t *status_dev, unsigned flags, w4_stream_t stream);
+
+/*
+ * w4_kv8_weigh_pages — the same over chosen pages: lse as written by
+ * w4_kv8_attn with this selection.  sel, n_sel, max_sel as there; an entry
+ * outside the sequence's pages is left out, a count outside 0 .. max_sel adds
+ * nothing (W4_ERR_INDEX both).  Without a selection: w4_kv8_weigh.
+ */
+w4_status w4_kv8_weigh_pages(const void *q, size_t q_row_stride, int q_heads, const float *lse,
+                             const w4_kv8_cache *cache, const w4_kv8_batch *batch, float scale,
+                             int window, const int32_t *sel, const int32_t *n_sel, int max_sel,
+                             int32_t *status_dev, unsigned flags, w4_stream_t stream);
 
 /*
  * w4_kv8_evict — keep the `budget` tokens of most weight, in fresh pages.

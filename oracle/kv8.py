@@ -111,7 +111,7 @@ def attn_ref(cache, table, lens, offsets, q, scale, window=0, sel=None, n_sel=No
     return out, lse, spread, reach
 
 
-def weigh_ref(cache, table, lens, offsets, q, lse, scale, window=0):
+def weigh_ref(cache, table, lens, offsets, q, lse, scale, window=0, sel=None, n_sel=None):
     """(weight, reach): the accumulated weights fp64, and the bound's sum over what was added of
     weight times scale sum |q key|."""
     rows, Hq, D = q.shape
@@ -123,8 +123,9 @@ def weigh_ref(cache, table, lens, offsets, q, lse, scale, window=0):
             k = values(cache["kc"], cache["ks"], table[b], length, h)
             t = np.arange(length)
             page, slot = table[b, t // P] if length else t, t % P
+            pages = None if sel is None else sel[b, h, :n_sel[b, h]]
             for r in range(n):
-                see = visible(length - n + r, length, window)
+                see = visible(length - n + r, length, window, pages, P)
                 for g in range(h * G, h * G + G):
                     l = lse[row0 + r, g]
                     if not see.any() or l == -np.inf:

@@ -7,7 +7,7 @@ import torch
 
 from oracle import kv8
 from bit_weight_only_gemv_gb300 import lib
-from _kv8 import Case, check_attn
+from _kv8 import Case, check_attn, score_error
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,136 @@ def test_one_workspace_for_every_call(cuda_lib):
                  pairs, many, evict, product, token, choose, chunk, wide):
         step() if callable(step) else attend(step)
     assert not bool(ws[:4096].any())
+
+
+def weigh_chosen(c, q, sel, n_sel, window=0):
+    """(weights after one kv8_weigh over the chosen pages, reference, its reach, log-sums)."""
+    want_sel, want_n = sel.cpu().numpy(), n_sel.cpu().numpy()
+    _, lse, _, _ = kv8.attn_ref(c.cache, c.table, c.lens, c.offsets, c.q, c.scale, window, want_sel,
+                                want_n)
+    lse = lse.astype(np.float32)
+    want, reach = kv8.weigh_ref(c.cache, c.table, c.lens, c.offsets, c.q, lse.astype(np.float64),
+                                c.scale, window, want_sel, want_n)
+    lib.kv8_weigh(c.dev, c.batch, q, torch.from_numpy(lse).cuda(), c.scale, window, c.status,
+                  sel=sel, n_sel=n_sel)
+    return want, reach, lse
+
+
+@pytest.mark.parametrize("lens,H,D,P,G,max_sel,window", [
+    ([1], 1, 64, 16, 1, 1, 0),
+    ([700, 30, 1, 0], 2, 128, 16, 4, 9, 0),
+    ([5000], 2, 256, 16, 8, 40, 0),
+    ([1000, 2000], 3, 64, 32, 12, 20, 0),
+    ([900, 333], 2, 128, 128, 20, 3, 0),                  # a group of several row tiles
+    ([600], 1, 256, 64, 71, 5, 0),
+    ([3000, 77], 1, 64, 16, 128, 100, 0),
+    ([2000, 500], 2, 128, 32, 3, 16, 300),                # pages before the window add nothing
+    ([9000] * 40, 1, 64, 16, 2, 30, 0),                   # more entries than a warp looks at
+])
+def test_weigh_over_chosen_pages(cuda_lib, lens, H, D, P, G, max_sel, window):
+    c = Case(sum(lens) + D, lens, None, H, D, P, G)
+    c.fix_ranges()
+    c.to_gpu()
+    ws = c.scratch(lib.kv8_select_workspace_bytes(c.dev, c.batch))
+    q = c.gpu_q()
+    sel, n_sel = lib.kv8_select(c.dev, c.batch, q, max_sel, 0, 1, ws, c.status)
+    first = None
+    for _ in range(2):
+        c.to_gpu()
+        want, reach, _ = weigh_chosen(c, q, sel, n_sel, window)
+        assert status(c) == 0
+        got = c.dev_arrays()["weight"]
+        # as for the weights over the whole cache: the exponent's error, then fp32 sums
+        added = want - c.cache["weight"]
+        tol = score_error(D, reach) + 2.0 ** -20 * added + 2.0 ** -22 * want + G * 2.0 ** -24 * added
+        assert np.all(np.abs(got - want) <= tol)
+        untouched = added == 0
+        assert np.array_equal(got[untouched], c.cache["weight"][untouched])
+        assert first is None or np.array_equal(first, got)
+        first = got
+
+
+def test_weigh_over_chosen_pages_refusals(cuda_lib):
+    """Entries outside the sequence's pages are left out, a count that is none adds nothing, a
+    page that is none leaves out its tokens; the rest is right."""
+    err = lib.STATUS_CODE["W4_ERR_INDEX"]
+    c = Case(33, [100, 90, 80, 70], None, 1, 64, 16, 2)
+    c.to_gpu()
+    q = c.gpu_q()
+    good = torch.tensor([[[0, 3, -1, -1]], [[0, 1, 2, 3]], [[1, 2, 4, -1]], [[2, 3, -1, -1]]],
+                        dtype=torch.int32, device="cuda")
+    n_good = torch.tensor([[2], [4], [3], [2]], dtype=torch.int32, device="cuda")
+    want, reach, lse = weigh_chosen(c, q, good, n_good)
+    assert status(c) == 0
+    for bad_sel, bad_n, lost in (([0, 3, 7, -1], 3, None), ([0, 3, -2, -1], 3, None),
+                                 ([0, 3, -1, -1], 5, 0), ([0, 3, -1, -1], -1, 0)):
+        c.to_gpu()
+        sel, n_sel = good.clone(), n_good.clone()
+        sel[0, 0] = torch.tensor(bad_sel, dtype=torch.int32)
+        n_sel[0, 0] = bad_n
+        lib.kv8_weigh(c.dev, c.batch, q, torch.from_numpy(lse).cuda(), c.scale, 0, c.status, sel=sel,
+                      n_sel=n_sel)
+        assert status(c) == err
+        got, ref = c.dev_arrays()["weight"], want.copy()
+        if lost is not None:
+            ref[c.table[lost]] = c.cache["weight"][c.table[lost]]
+        assert np.allclose(got, ref, rtol=1e-4, atol=1e-6)
+    page = c.table[1, 2]
+    c.table[1, 2] = -5
+    c.to_gpu()
+    lib.kv8_weigh(c.dev, c.batch, q, torch.from_numpy(lse).cuda(), c.scale, 0, c.status, sel=good,
+                  n_sel=n_good)
+    assert status(c) == err
+    ref = want.copy()
+    ref[page] = c.cache["weight"][page]
+    assert np.allclose(c.dev_arrays()["weight"], ref, rtol=1e-4, atol=1e-6)
+
+
+def test_decode_loop_weights_and_evictions(cuda_lib):
+    """The example's loop step by step: each step adds one per query head to the chosen pages'
+    tokens, by the definition, and an eviction keeps what the definition keeps."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "kv8_decode.py")
+    spec = importlib.util.spec_from_file_location("kv8_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer = example.Layer(hidden=512, q_heads=8, kv_heads=2, head_dim=64, page_tokens=16,
+                          max_len=160, budget=96, keep_pages=4, seed=2)
+    x = layer.tokens(100 + 70)
+    layer.prompt(x[:100])
+    before = layer.cache.tensors[5].cpu().numpy()
+    assert np.allclose(before.sum((0, 2)), 100 * 4, rtol=1e-4)
+    was, lens, table = None, None, None
+    for i in range(70):
+        evictions = layer.evictions
+        layer.step(x[100 + i:101 + i])
+        torch.cuda.synchronize()
+        assert int(layer.status.item()) == 0
+        a = layer.arrays()
+        base = before
+        if layer.evictions > evictions:
+            # the step cut the cache first, then stored its token
+            kept_pages = np.array(layer.used[:6], np.int32)[None]
+            cut, _, n = kv8.evict_ref(was, table, lens, kept_pages, 96, layer.sink, layer.recent)
+            assert n[0] == 96
+            for name in ("kc", "vc", "ks", "vs", "ranges"):
+                assert np.array_equal(a["cache"][name][kept_pages[0]], cut[name][kept_pages[0]])
+            base = cut["weight"]
+        page, slot = a["table"][0, (layer.length - 1) // 16], (layer.length - 1) % 16
+        base = base.copy()
+        base[page, :, slot] = 0                       # the new token starts at nothing
+        ref = kv8.attn_ref(a["cache"], a["table"], a["lens"], None, a["q"], layer.scale, 0, a["sel"],
+                           a["n_sel"])
+        check_attn(a["out"], a["lse"], ref, 64)
+        want, reach = kv8.weigh_ref(dict(a["cache"], weight=base), a["table"], a["lens"], None,
+                                    a["q"], a["lse"], layer.scale, 0, a["sel"], a["n_sel"])
+        got, added = a["cache"]["weight"], want - base
+        tol = score_error(64, reach) + 2.0 ** -20 * added + 2.0 ** -22 * want + \
+            4 * 2.0 ** -24 * added
+        live = a["table"][0, :len(layer.used)]
+        assert np.all(np.abs(got - want)[live] <= tol[live])
+        assert np.allclose((got.astype(np.float64) - base)[live].sum((0, 2)), 4, rtol=1e-4)
+        before, was, lens, table = got, a["cache"], a["lens"], a["table"]
+    assert layer.evictions >= 1
