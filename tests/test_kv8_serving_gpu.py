@@ -267,3 +267,40 @@ def test_decode_loop_weights_and_evictions(cuda_lib):
         assert np.allclose((got.astype(np.float64) - base)[live].sum((0, 2)), 4, rtol=1e-4)
         before, was, lens, table = got, a["cache"], a["lens"], a["table"]
     assert layer.evictions >= 1
+
+
+@pytest.mark.parametrize("D,P,budget", [(128, 16, 200), (64, 32, 333), (256, 16, 90), (128, 64, 400)])
+def test_attention_after_an_eviction_is_that_of_the_kept_tokens(cuda_lib, D, P, budget):
+    """Against the source's own tokens at the kept positions.  Blocks have steps s, 2 s and 4 s and
+    codes 128 + 4 n, so that rescaling to a block's largest step moves no value."""
+    c = Case(52 + D, [700], None, 2, D, P, 4, spare=-(-budget // P) + 1)
+    for codes, steps, base in (("kc", "ks", 2.0 ** -9), ("vc", "vs", 2.0 ** -5)):
+        c.cache[codes] = (c.rng.integers(-31, 32, c.cache[codes].shape) * 4 + 128).astype(np.uint8)
+        c.cache[steps] = (base * 2.0 ** c.rng.integers(0, 3, c.cache[steps].shape)).astype(np.float32)
+    c.fix_ranges()
+    c.to_gpu()
+    pages = -(-budget // P)
+    dst = torch.from_numpy(c.free[:pages][None].copy()).cuda()
+    ws = c.scratch(max(lib.kv8_evict_workspace_bytes(c.dev, c.batch, budget),
+                       lib.kv8_attn_workspace_bytes(c.dev, c.batch, 8)))
+    kept, new_lens = lib.kv8_evict(c.dev, c.batch, budget, dst, 4, 8, ws, c.status)
+    assert status(c) == 0 and new_lens.tolist() == [budget]
+    kept = kept.cpu().numpy()[0]
+    batch = lib.KV8Batch(dst, new_lens, max_len=budget)
+    lse = torch.full((1, 8), float("nan"), device="cuda")
+    out = lib.kv8_attn(c.dev, batch, c.gpu_q(), c.scale, lse=lse, workspace=ws, status=c.status)
+    assert status(c) == 0
+    # the kept tokens of each head as a sequence of their own in a cache of one-token steps
+    ref = [np.zeros((1, 8, D)), np.zeros((1, 8)), np.zeros((1, 8, D)), np.zeros((1, 8))]
+    for h in range(2):
+        assert kept[h, -1] == 699 and np.all(np.diff(kept[h]) > 0)
+        k, v = (kv8.values(c.cache[x], c.cache[y], c.table[0], 700, h)[kept[h]]
+                for x, y in (("kc", "ks"), ("vc", "vs")))
+        for g in range(4 * h, 4 * h + 4):
+            s = c.scale * (k @ c.q[0, g])
+            p = np.exp(s - s.max())
+            ref[1][0, g] = s.max() + np.log(p.sum())
+            p /= p.sum()
+            ref[0][0, g], ref[2][0, g] = p @ v, p @ np.abs(v)
+            ref[3][0, g] = c.scale * (np.abs(k) @ np.abs(c.q[0, g])).max()
+    check_attn(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, D)
