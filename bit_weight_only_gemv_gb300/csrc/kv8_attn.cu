@@ -51,7 +51,10 @@ constexpr float kHalfNormal = 6.103515625e-05f;   // 2^-14, fp16's least normal 
 constexpr float kLevel = 536870912.0f;            // 2^29: from there to 2^15, well in range
 constexpr float kLeast = 7.5e-37f;                // above 2^-120: five ranges reach it
 constexpr long long kWait = 1LL << 31;   // about a second
-constexpr int kMinSlices = 16;           // of a CTA's run: two a warp
+// Slices of a CTA's run, at least (two a warp): one token on 2k keys, 32 heads on
+// 8 of 128 channels 11.5 us (4: 13.9, 8: 11.8, 32: 13.8), on 16k keys of one head
+// 20.0 (8: 29.5, 32: 17.4), 8 on 1k 18.1 (8: 17.8, 32: 21.2).
+constexpr int kMinSlices = 16;
 
 template <int D, int NQ>
 struct Shape {

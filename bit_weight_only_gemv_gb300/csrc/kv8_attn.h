@@ -9,10 +9,15 @@ namespace w4 {
 namespace kv8 {
 
 // Query rows on a key head from which a call takes the prompt-chunk kernel.
-// Measured, row tiles of 8 or 16 in the token kernel against tiles of 128: 64
-// rows of 128-channel heads on 2 x 8k keys 45 and 55 us, 96 rows 61 and 55, 128
-// rows 76 and 57; of 256-channel heads on 4 x 4k keys 32 rows 39 and 54, 64 rows 62 and 55.
-constexpr long long chunk_rows(int D) { return D == 256 ? 49 : 81; }
+// Measured, row tiles of 8 or 16 in the token kernel against tiles of 128, on 2
+// sequences of up to 8k keys / 16 of up to 1k, 8 heads (4 of 256 channels), us:
+//    64 channels: 96 rows 38 and 43 / 42 and 45, 112 rows 41 and 43 / 45 and 45,
+//                 128 rows 44 and 44 / 50 and 45
+//   128 channels: 64 rows 45 and 58 / 50 and 57, 80 rows 53 and 58 / 61 and 58,
+//                 96 rows 60 and 58 / 71 and 58
+//   256 channels: 48 rows 41 and 56 / 46 and 44, 64 rows 46 and 57 / 55 and 45,
+//                 96 rows 60 and 57 / 71 and 45
+constexpr long long chunk_rows(int D) { return D == 256 ? 49 : D == 128 ? 81 : 113; }
 
 // The tensor map of one side's codes: bytes [page][head][token][channel], boxes of
 // `rows` tokens by 128 channels (64 for 64-channel heads), swizzled.

@@ -61,9 +61,10 @@ constexpr int kRowTile = 128;
 constexpr int kKeys = 64;             // keys of a tile
 constexpr int kMetaRing = 16;         // tiles described ahead of their softmax
 constexpr int kUnitRing = 32;         // units of which a refusal is remembered
-// Key tiles of a CTA's run, at least: 64 rows of 16 heads on 2 of 64 channels
-// against 4k keys 28.6 us (2: 34.5, 8: 28.6, 16: 37.1), 40 rows of 8 on 4 of 256
-// against 1000 29.4 (2: 28.8, 8: 34.3, 16: 37.0).
+// Key tiles of a CTA's run, at least: 128 rows of 8 heads on 2 of 64 channels
+// against 4k keys 31.6 us (2: 48.5, 8: 28.4, 16: 33.4), 64 rows of 16 on 4 of 256
+// against 1000 28.8 (2: 28.5, 8: 33.4, 16: 35.6), 256 rows of 16 on 4 of 128 against
+// 2000 32.4 (2: 34.7, 8: 34.2, 16: 42.3).
 constexpr int kMinTiles = 4;
 
 // The same for roles that work ahead of the others: they leave the issue slots
@@ -871,7 +872,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                  : "memory");
 }
 
-// Joins the parts of cut units: one CTA per 16 rows.  Reading and adding
+// Joins the parts of cut units: one CTA per 4 rows.  Reading and adding
 // them all from one SM would take longer than computing them did.
 constexpr int kJoinRows = 4;
 constexpr int kJoinThreads = 128;

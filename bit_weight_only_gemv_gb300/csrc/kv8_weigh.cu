@@ -12,7 +12,7 @@
 // sequences of up to 16k tokens, 32 heads on 8 of 128 channels: 25.9 us, 3.8
 // TB/s; about 10 us of that are the start (lengths, page ids, first copies), the
 // rest runs at 6 TB/s.
-// Up to 64 rows: a warp keeps its tokens' keys as fragments in registers,
+// Up to 64 rows (48 but for 128 channels): a warp keeps its tokens' keys as fragments in registers,
 // converted once, and walks all query rows, which the CTA brings into shared
 // memory in fragment order; the legacy MMAs bound it (2 x 8k keys, 8 heads of
 // 128 channels: 20 rows 12.7 us, 64 rows 16.3).  Beyond that kv8_weigh_tc.cu.
@@ -32,6 +32,9 @@ constexpr int kSlice = 16;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRing = 64;
+// Slices of a CTA's run, at least (two a warp): one token on 2k keys, 32 heads on
+// 8 of 128 channels 6.4 us (8: 5.7, 32: 8.0), on 16k keys of one head 6.7 (8: 6.1,
+// 32: 8.1), 8 on 1k 9.4 (8: 9.1, 32: 12.0).
 constexpr int kMinSlices = 16;
 constexpr long long kWait = 1LL << 31;   // about a second
 
@@ -242,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           a0 += __shfl_xor_sync(0xffffffffu, a0, 2);
           a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
           if (j == 0) {
-            // one addition to each weight, which nothing here waits for (loading
-            // the old weight first: 30.8 us against 29.0 at 8 x 16k keys)
+            // one addition to each weight, which nothing here waits for (when 8 x
+            // 16k keys took 29.0 us, loading the old weight first cost 30.8)
             if (d.tok + i < s.len) atomicAdd(w, a0);
             if (d.tok + i + 8 < s.len) atomicAdd(w + 8, a1);
           }
@@ -271,10 +274,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // ------------------------------------------------------------ many rows
-// The most rows of this kernel; above, kv8_weigh_tc.cu.  2 x 8k keys, 8 heads
-// of 64 and 128 channels, 4 of 256: 64 rows 13.5, 16.3 and 15.2 us here and 12.7,
-// 18.5 and 14.9 there; 96 rows 16.2, 20.1 and 20.7 against 12.7, 18.5 and 14.9.
+// The most rows of this kernel, and of it at a head size; above, kv8_weigh_tc.cu.
+// 2 x 8k keys, 8 heads of 64 and 128 channels, 4 of 256: 48 rows 12.4, 14.7 and
+// 14.5 us here and 12.8, 18.7 and 15.1 there; 64 rows 13.5, 16.2 and 16.4 against
+// 12.8, 18.6 and 15.2; 96 rows 16.2, 20.1 and 20.7 against 12.8, 18.7 and 15.2.
 constexpr int kManyRows = 64;
+constexpr int many_rows(int D) { return D == 128 ? kManyRows : 48; }
 
 __device__ __forceinline__ void mma_bf16(float d[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -525,7 +530,7 @@ extern "C" w4_status w4_kv8_weigh_pages(const void* q, size_t q_row_stride, int 
       default: return kv8::launch_token<256, 2, true>(p, di.sms, stream, dev);
     }
   }
-  if (rows > kv8::kManyRows) return kv8::weigh_many(p, di.sms, dev, stream);
+  if (rows > kv8::many_rows(p.c.D)) return kv8::weigh_many(p, di.sms, dev, stream);
   if (rows > 16) {
     switch (p.c.D) {
       case 64: return kv8::launch_chunk<64>(p, stream, dev);

@@ -290,7 +290,7 @@ def test_attention_after_an_eviction_is_that_of_the_kept_tokens(cuda_lib, D, P, 
     lse = torch.full((1, 8), float("nan"), device="cuda")
     out = lib.kv8_attn(c.dev, batch, c.gpu_q(), c.scale, lse=lse, workspace=ws, status=c.status)
     assert status(c) == 0
-    # the kept tokens of each head as a sequence of their own in a cache of one-token steps
+    # attention of each head over its kept tokens
     ref = [np.zeros((1, 8, D)), np.zeros((1, 8)), np.zeros((1, 8, D)), np.zeros((1, 8))]
     for h in range(2):
         assert kept[h, -1] == 699 and np.all(np.diff(kept[h]) > 0)
