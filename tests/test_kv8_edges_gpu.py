@@ -183,3 +183,74 @@ def test_attn_steps_at_the_ends_of_their_range(cuda_lib, new, D, rise, vstep):
     out, lse = c.attn()
     assert status(c) == 0
     check_attn(out, lse, ref, D)
+
+
+def moved(c, layout):
+    """The case's cache with its pages and heads elsewhere: gaps that no head's size divides, or
+    all pages of a head side by side."""
+    n, H, P, D = c.cache["kc"].shape
+    out = []
+    for name in ("kc", "vc"):
+        if layout == "gaps":
+            strides = (H * (P * D + 16) + 48, P * D + 16, D, 1)
+            size = strides[0] * n
+        else:
+            strides = (P * D, n * P * D + 32, D, 1)
+            size = strides[1] * H
+        t = torch.as_strided(torch.full((size,), 77, dtype=torch.uint8, device="cuda"),
+                             (n, H, P, D), strides)
+        t.copy_(torch.from_numpy(c.cache[name]))
+        out.append(t)
+    rest = c.dev.tensors
+    c.dev = lib.KV8Cache(*out, rest[2], rest[3], ranges=rest[4], weight=rest[5])
+
+
+@pytest.mark.parametrize("layout", ["gaps", "heads first"])
+@pytest.mark.parametrize("D,P,news", [(64, 16, None), (128, 32, [1, 40]), (256, 128, [30, 9]),
+                                      (64, 64, [70, 3]), (128, 16, None)])
+def test_pages_and_heads_anywhere(cuda_lib, D, P, news, layout):
+    """Every operator on strides other than the dense ones."""
+    c = Case(5 + D, [150, 333], news, 3, D, P, 4, spare=8)
+    before = [150, 333] if news is None else [150 - news[0], 333 - news[1]]
+    c.fix_ranges([n - (news is None) for n in before])
+    k, v = (bf16_round(c.rng.normal(size=(c.rows, 3, D))) for _ in range(2))
+    c.to_gpu()
+    moved(c, layout)
+    want = kv8.append_ref(c.cache, c.table, c.lens, c.offsets, k, v)
+    lib.kv8_append(c.dev, c.batch, *(torch.from_numpy(x).cuda().to(torch.bfloat16) for x in (k, v)),
+                   c.status)
+    assert status(c) == 0
+    got = c.dev_arrays()
+    assert all(np.array_equal(got[n], want[n]) for n in want)
+    c.cache = want
+    ref = kv8.attn_ref(c.cache, c.table, c.lens, c.offsets, c.q, c.scale)
+    out, lse = c.attn()
+    assert status(c) == 0
+    check_attn(out, lse, ref, D)
+    lse = ref[1].astype(np.float32)
+    after, reach = kv8.weigh_ref(c.cache, c.table, c.lens, c.offsets, c.q, lse.astype(np.float64),
+                                 c.scale)
+    lib.kv8_weigh(c.dev, c.batch, c.gpu_q(), torch.from_numpy(lse).cuda(), c.scale, 0, c.status)
+    assert status(c) == 0
+    weight = c.dev_arrays()["weight"]
+    added = after - c.cache["weight"]
+    assert np.all(np.abs(weight - after) <= score_error(D, reach) + 2.0 ** -20 * added +
+                  2.0 ** -22 * after + c.max_new * 4 * 2.0 ** -24 * added)
+    c.cache["weight"] = weight
+    if news is None:
+        ws = c.scratch(lib.kv8_select_workspace_bytes(c.dev, c.batch))
+        sel, n_sel = lib.kv8_select(c.dev, c.batch, c.gpu_q(), 5, 1, 1, ws, c.status)
+        want_sel, want_n = kv8.select_ref(c.cache, c.table, c.lens, c.q, 5, 1, 1)
+        assert np.array_equal(sel.cpu().numpy(), want_sel)
+        out, lse = c.attn(sel=sel, n_sel=n_sel)
+        assert status(c) == 0
+        check_attn(out, lse, kv8.attn_ref(c.cache, c.table, c.lens, None, c.q, c.scale, 0, want_sel,
+                                          want_n), D)
+    pages = -(-48 // P)
+    dst = c.free[:2 * pages].reshape(2, pages).copy()
+    want, kept, _ = kv8.evict_ref(c.cache, c.table, c.lens, dst, 48, 2, 8)
+    ws = c.scratch(lib.kv8_evict_workspace_bytes(c.dev, c.batch, 48))
+    got_kept, _ = lib.kv8_evict(c.dev, c.batch, 48, torch.from_numpy(dst).cuda(), 2, 8, ws, c.status)
+    assert status(c) == 0 and np.array_equal(got_kept.cpu().numpy(), kept)
+    got = c.dev_arrays()
+    assert all(np.array_equal(got[n], want[n]) for n in want)

@@ -304,3 +304,56 @@ def test_attention_after_an_eviction_is_that_of_the_kept_tokens(cuda_lib, D, P, 
             ref[0][0, g], ref[2][0, g] = p @ v, p @ np.abs(v)
             ref[3][0, g] = c.scale * (np.abs(k) @ np.abs(c.q[0, g])).max()
     check_attn(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, D)
+
+
+@pytest.mark.parametrize("D,G", [(128, 4), (64, 128)])
+def test_steps_that_grow_from_call_to_call_in_one_graph(cuda_lib, D, G):
+    """Append and attention as dependents of one another, token after token: every call of one
+    graph sees the steps and codes that the call before it has just rewritten."""
+    B, steps, H = 40, 24, 2
+    c = Case(61, [3] * B, None, H, D, 32, G)
+    rng = c.rng
+    c.fix_ranges()
+    table = c.table
+    c.to_gpu()
+    start = [t.clone() for t in c.dev.tensors]
+    calls, outs, rows = [], [], []
+    ws = None
+    for i in range(steps):
+        size = 2.0 ** (i % 7 + i // 3) * 0.01
+        k, v = (torch.from_numpy(rng.normal(size=(B, H, D)) * size).cuda().to(torch.bfloat16)
+                for _ in range(2))
+        q = (torch.from_numpy(rng.normal(size=(B, H * G, D)) / (1 + size)).cuda()).to(torch.bfloat16)
+        batch = lib.KV8Batch(c.batch.tensors[0], torch.full((B,), 4 + i, dtype=torch.int32,
+                                                            device="cuda"), max_len=4 + steps)
+        if ws is None:
+            ws = c.scratch(lib.kv8_attn_workspace_bytes(c.dev, batch, H * G))
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        calls += [lib.bind_kv8_append(c.dev, batch, k, v, c.status),
+                  lib.bind_kv8_attn(c.dev, batch, q, c.scale, out, lse=lse, workspace=ws,
+                                    status=c.status)]
+        outs.append((out, lse))
+        rows.append([x.double().cpu().numpy() for x in (k, v, q)])
+    calls[-1]()                                       # (first use of each kernel, outside the graph)
+    calls[-2]()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call in calls:
+            call(pdl=True)
+    for _ in range(3):
+        for t, s in zip(c.dev.tensors, start):
+            t.copy_(s)
+        graph.replay()
+        assert status(c) == 0
+        first = [(o.clone(), x.clone()) for o, x in outs]
+    cache = c.cache
+    for i, (k, v, q) in enumerate(rows):
+        lens = np.full(B, 4 + i)
+        cache = kv8.append_ref(cache, table, lens, None, k, v)
+        some = slice(0, B, 7)                         # (every seventh sequence: the reference is slow)
+        ref = kv8.attn_ref(cache, table[some], lens[some], None, q[some], c.scale)
+        out, lse = (x.double().cpu().numpy()[some] for x in first[i])
+        check_attn(out, lse, ref, D)
+    got = c.dev_arrays()
+    assert all(np.array_equal(got[n], cache[n]) for n in ("kc", "vc", "ks", "vs", "ranges"))
