@@ -29,7 +29,7 @@
 // (kv8_runs.cuh); parts of a cut unit meet in the workspace and are joined in
 // order by a second small kernel.  Every wait is bounded.
 //
-// 256 rows of 32 heads on 8 of 128 channels against 16k keys: 110 us, 0.62
+// 256 rows of 32 heads on 8 of 128 channels against 16k keys: 112 us, 0.61
 // PFLOP/s.  Of about 3400 cycles per 64 keys a softmax group computes 2300 (four
 // warps, one per scheduler, beside the expansion and the issuing), the tensor
 // cores 1792 for both groups; one issuing warp keeps up (one per group: 133 us), and
