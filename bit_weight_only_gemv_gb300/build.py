@@ -19,7 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4a16.so")
 SOURCES = ["gemv.cu", "chain.cu", "gemv_tc.cu", "gemm_tc.cu", "gather.cu", "quant.cu",
            "slot_pool.cu", "dev_pool.cu", "kv8_append.cu", "kv8_select.cu", "kv8_attn.cu",
-           "kv8_chunk.cu", "kv8_weigh.cu", "kv8_weigh_tc.cu"]
+           "kv8_chunk.cu", "kv8_weigh.cu", "kv8_weigh_tc.cu", "kv8_pages.cu", "route.cu",
+           "logits.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

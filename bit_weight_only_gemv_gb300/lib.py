@@ -43,7 +43,9 @@ EXPORTS = ("w4_status_str", "w4_abi_version", "w4_last_cuda_error", "w4a16_gemv"
            "w4a16_gemv_chain_task_plan", "w4a16_gemv_id_plan", "w4a16_gemv_prefetch_l2",
            "w4a16_gemv_plan_flags", "w4_kv8_append", "w4_kv8_attn", "w4_kv8_attn_workspace_bytes",
            "w4_kv8_select", "w4_kv8_select_workspace_bytes", "w4_kv8_weigh", "w4_kv8_weigh_pages",
-           "w4_kv8_evict", "w4_kv8_evict_workspace_bytes")
+           "w4_kv8_evict", "w4_kv8_evict_workspace_bytes", "w4_route", "w4_moe_combine",
+           "w4_logits_adjust", "w4_kv8_fork", "w4_kv8_reserve", "w4_kv8_compact",
+           "w4_kv8_pages_workspace_bytes")
 W4_TASK_SILU_MUL = 1
 W4_MAX_L2_RANGES = 4
 CHAIN_MAX_TASKS = 320
@@ -102,6 +104,22 @@ class KV8BatchStruct(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
                 ("offsets", ctypes.c_void_p), ("batch", ctypes.c_int), ("max_pages", ctypes.c_int),
                 ("rows", ctypes.c_int), ("max_new", ctypes.c_int), ("max_len", ctypes.c_int)]
+
+
+class RouterStruct(ctypes.Structure):
+    """struct w4_router of include/w4a16.h."""
+    _fields_ = [("experts", ctypes.c_int), ("top_k", ctypes.c_int), ("groups", ctypes.c_int),
+                ("top_groups", ctypes.c_int), ("group_best", ctypes.c_int),
+                ("score", ctypes.c_int), ("renorm", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class LogitRulesStruct(ctypes.Structure):
+    """struct w4_logit_rules of include/w4a16.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("tokens", "lens", "prompt", "repetition",
+                                               "presence", "frequency", "bias_ids", "bias",
+                                               "n_bias", "mask", "mask_rows")] + \
+               [(n, ctypes.c_size_t) for n in ("token_stride", "bias_stride", "mask_stride")] + \
+               [(n, ctypes.c_int) for n in ("max_tokens", "max_bias", "num_masks")]
 
 
 _lib = None
@@ -200,6 +218,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4_kv8_evict.argtypes = [vp, vp, vp, i32, i32, i32, cp, bp, vp, sz, vp, u32, vp]
     lib.w4_kv8_evict_workspace_bytes.restype = sz
     lib.w4_kv8_evict_workspace_bytes.argtypes = [cp, bp, i32]
+    lib.w4_route.restype = i32
+    lib.w4_route.argtypes = [vp, vp, ctypes.POINTER(RouterStruct), vp, i32, sz, vp, i32, vp, u32, vp]
+    lib.w4_moe_combine.restype = i32
+    lib.w4_moe_combine.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, u32, vp]
+    lib.w4_logits_adjust.restype = i32
+    lib.w4_logits_adjust.argtypes = [vp, i32, sz, i32, i32, ctypes.POINTER(LogitRulesStruct), vp,
+                                     u32, vp]
+    lib.w4_kv8_fork.restype = i32
+    lib.w4_kv8_fork.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, cp, i32, vp, sz, vp,
+                                u32, vp]
+    lib.w4_kv8_reserve.restype = i32
+    lib.w4_kv8_reserve.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, sz, vp, u32, vp]
+    lib.w4_kv8_compact.restype = i32
+    lib.w4_kv8_compact.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, cp, i32, vp, sz, vp, u32, vp]
+    lib.w4_kv8_pages_workspace_bytes.restype = sz
+    lib.w4_kv8_pages_workspace_bytes.argtypes = [i32, i32]
     _lib = lib
     return lib
 
@@ -966,3 +1000,320 @@ def kv8_evict(cache: KV8Cache, batch: KV8Batch, budget: int, dst_table: torch.Te
     bind_kv8_evict(cache, batch, dst_table, kept, new_lens, sink, recent, workspace,
                    status)(pdl, stream)
     return kept, new_lens
+
+
+# ------------------------------------------------------------------ pages of the cache
+def _same_device(*tensors):
+    """The tensors' device, which must be the current one (a call launches there)."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError("all tensors of a call must be on one device")
+    dev = devs.pop()
+    if dev.type != "cuda" or dev.index not in (None, torch.cuda.current_device()):
+        raise ValueError(f"the tensors are on {dev}, which is not the current CUDA device")
+    return dev
+
+
+def _caches(caches):
+    """An array of w4_kv8_cache of one cache or several."""
+    caches = [caches] if isinstance(caches, KV8Cache) else list(caches)
+    if not caches:
+        raise ValueError("at least one cache is needed")
+    return caches, (KV8CacheStruct * len(caches))(*[c.struct for c in caches])
+
+
+def _kv8_table(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor):
+    for t, name in ((table, "table"), (lens, "lens"), (refs, "refs")):
+        _need(t, torch.int32, name)
+    if table.dim() != 2 or lens.shape != (table.shape[0],) or refs.dim() != 1:
+        raise ValueError("table must be [batch, max_pages], lens [batch] and refs [pages]")
+
+
+def kv8_pages_workspace_bytes(batch: int, num_pages: int) -> int:
+    """Scratch of kv8_fork, kv8_reserve and kv8_compact calls of up to `batch` rows (old or new)
+    on a pool of num_pages pages."""
+    return int(load().w4_kv8_pages_workspace_bytes(batch, num_pages))
+
+
+def bind_kv8_fork(caches, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                  parents: torch.Tensor, new_table: torch.Tensor, new_lens: torch.Tensor,
+                  new_refs: torch.Tensor, workspace: torch.Tensor, status: torch.Tensor = None):
+    """w4_kv8_fork with its arguments marshalled once: returns call(pdl=False, stream=None).
+    caches: a KV8Cache or several of one shape (a model's layers)."""
+    caches, arr = _caches(caches)
+    _kv8_table(table, lens, refs)
+    _kv8_table(new_table, new_lens, new_refs)
+    _need(parents, torch.int32, "parents")
+    if refs.shape != (caches[0].pages,) or new_refs.shape != refs.shape:
+        raise ValueError("refs and new_refs must be [pages]")
+    if new_table.shape[1] != table.shape[1] or parents.shape != new_lens.shape:
+        raise ValueError("new_table must be [new_batch, max_pages] and parents [new_batch]")
+    _same_device(*[c.tensors[0] for c in caches], table, lens, refs, parents, new_table, new_lens,
+                 new_refs, workspace, status)
+    args = (_ptr(new_table), _ptr(new_lens), _ptr(new_refs), new_table.shape[0], _ptr(parents),
+            _ptr(table), _ptr(lens), _ptr(refs), *table.shape, arr, len(caches), _ptr(workspace),
+            _kv8_bytes(workspace), _ptr(status))
+    return _kv8_call(load().w4_kv8_fork, "w4_kv8_fork", args,
+                     (table, caches, lens, refs, parents, new_table, new_lens, new_refs, workspace,
+                      status))
+
+
+def kv8_fork(caches, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+             parents: torch.Tensor, workspace: torch.Tensor, status: torch.Tensor = None,
+             pdl: bool = False, stream=None):
+    """(new_table, new_lens, new_refs): row b goes on from row parents[b] of the old table (-1:
+    it is empty); the pages that rows will write to are their own.  Entries past a row's pages
+    are -1."""
+    shape = (parents.numel(), table.shape[1])
+    new_table = torch.full(shape, -1, dtype=torch.int32, device=table.device)
+    new_lens, new_refs = torch.empty_like(parents), torch.empty_like(refs)
+    _on(stream, new_table, new_lens, new_refs)
+    bind_kv8_fork(caches, table, lens, refs, parents, new_table, new_lens, new_refs, workspace,
+                  status)(pdl, stream)
+    return new_table, new_lens, new_refs
+
+
+def _on(stream, *tensors):
+    """Fresh tensors whose first use is on another stream than the one they were allocated (and
+    filled) on: that stream waits for the current one, and the memory is not reused before it is
+    done."""
+    if stream is None or stream == torch.cuda.current_stream():
+        return
+    stream.wait_stream(torch.cuda.current_stream())
+    for t in tensors:
+        t.record_stream(stream)
+
+
+def bind_kv8_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                     page_tokens: int, grow: torch.Tensor = None, workspace: torch.Tensor = None,
+                     status: torch.Tensor = None):
+    """w4_kv8_reserve with its arguments marshalled once: returns call(pdl=False, stream=None)."""
+    _kv8_table(table, lens, refs)
+    if grow is not None:
+        _need(grow, torch.int32, "grow")
+        if grow.shape != lens.shape:
+            raise ValueError("grow must be [batch]")
+    _same_device(table, lens, refs, grow, workspace, status)
+    args = (_ptr(table), _ptr(lens), _ptr(refs), _ptr(grow), *table.shape, refs.shape[0],
+            page_tokens, _ptr(workspace), _kv8_bytes(workspace), _ptr(status))
+    return _kv8_call(load().w4_kv8_reserve, "w4_kv8_reserve", args,
+                     (table, lens, refs, grow, workspace, status))
+
+
+def kv8_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_tokens: int,
+                grow: torch.Tensor = None, workspace: torch.Tensor = None,
+                status: torch.Tensor = None, pdl: bool = False, stream=None):
+    """lens += grow (None: one token for each row that has any), with pages for the new tokens, in
+    place."""
+    bind_kv8_reserve(table, lens, refs, page_tokens, grow, workspace, status)(pdl, stream)
+
+
+def bind_kv8_compact(caches, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                     new_table: torch.Tensor, new_refs: torch.Tensor, used: torch.Tensor,
+                     workspace: torch.Tensor, status: torch.Tensor = None):
+    """w4_kv8_compact with its arguments marshalled once: returns call(pdl=False, stream=None)."""
+    caches, arr = _caches(caches)
+    _kv8_table(table, lens, refs)
+    _kv8_table(new_table, lens, new_refs)
+    _need(used, torch.int32, "used")
+    if refs.shape != (caches[0].pages,) or new_refs.shape != refs.shape or used.numel() != 1:
+        raise ValueError("refs and new_refs must be [pages] and used [1]")
+    if new_table.shape != table.shape:
+        raise ValueError("new_table must have the shape of table")
+    _same_device(*[c.tensors[0] for c in caches], table, lens, refs, new_table, new_refs, used,
+                 workspace, status)
+    args = (_ptr(new_table), _ptr(new_refs), _ptr(used), _ptr(table), _ptr(lens), _ptr(refs),
+            *table.shape, arr, len(caches), _ptr(workspace), _kv8_bytes(workspace), _ptr(status))
+    return _kv8_call(load().w4_kv8_compact, "w4_kv8_compact", args,
+                     (table, caches, lens, refs, new_table, new_refs, used, workspace, status))
+
+
+def kv8_compact(caches, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                workspace: torch.Tensor, status: torch.Tensor = None, pdl: bool = False,
+                stream=None):
+    """(new_table, new_refs, used): the pages in use moved to the lowest numbers.  Entries past a
+    row's pages are -1."""
+    new_table, new_refs = torch.full_like(table, -1), torch.empty_like(refs)
+    used = torch.empty((1,), dtype=torch.int32, device=table.device)
+    _on(stream, new_table, new_refs, used)
+    bind_kv8_compact(caches, table, lens, refs, new_table, new_refs, used, workspace,
+                     status)(pdl, stream)
+    return new_table, new_refs, used
+
+
+# ------------------------------------------------------------------ routing and logits
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}   # W4_TYPE_*
+
+
+def _float_rows(t: torch.Tensor, name: str):
+    """(W4_TYPE_*, row stride) of [rows, n] logits, dense within a row."""
+    if not t.is_cuda or t.dtype not in _TYPES:
+        raise ValueError(f"{name} must be a CUDA tensor of bfloat16 or float32")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, n], each row dense")
+    return _TYPES[t.dtype], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class Router:
+    """How tokens choose experts (struct w4_router): scores "softmax" or "sigmoid" of the logits;
+    with groups > 1 only experts of the top_groups groups whose group_best largest scores sum
+    highest; weights scale * score, divided by the chosen scores' sum with renorm."""
+
+    def __init__(self, experts: int, top_k: int, groups: int = 1, top_groups: int = 1,
+                 group_best: int = 2, score: str = "softmax", renorm: bool = True,
+                 scale: float = 1.0):
+        if score not in ("softmax", "sigmoid"):
+            raise ValueError('score must be "softmax" or "sigmoid"')
+        self.experts, self.top_k = experts, top_k
+        self.struct = RouterStruct(experts, top_k, groups, top_groups, group_best,
+                                   int(score == "sigmoid"), int(renorm), scale)
+
+
+def bind_route(router: Router, logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+               bias: torch.Tensor = None, status: torch.Tensor = None):
+    """w4_route with its arguments marshalled once: returns call(pdl=False, stream=None)."""
+    kind, stride = _float_rows(logits, "logits")
+    _need(ids, torch.int32, "ids")
+    _need(weights, torch.float32, "weights")
+    if logits.shape[1] != router.experts:
+        raise ValueError("logits must be [rows, experts]")
+    if tuple(ids.shape) != (logits.shape[0], router.top_k) or weights.shape != ids.shape:
+        raise ValueError("ids and weights must be [rows, top_k]")
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if bias.shape != (router.experts,):
+            raise ValueError("bias must be [experts]")
+    _same_device(logits, ids, weights, bias, status)
+    args = (_ptr(ids), _ptr(weights), ctypes.byref(router.struct), _ptr(logits), kind, stride,
+            _ptr(bias), logits.shape[0], _ptr(status))
+    return _kv8_call(load().w4_route, "w4_route", args,
+                     (logits, ids, weights, bias, status, router))
+
+
+def route(router: Router, logits: torch.Tensor, bias: torch.Tensor = None,
+          status: torch.Tensor = None, pdl: bool = False, stream=None):
+    """(ids, weights): int32 and fp32 [rows, top_k], the experts of each row of logits [rows,
+    experts] (bf16 or fp32), by score + bias."""
+    shape = (logits.shape[0], router.top_k)
+    ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    _on(stream, ids, weights)
+    bind_route(router, logits, ids, weights, bias, status)(pdl, stream)
+    return ids, weights
+
+
+def bind_moe_combine(y: torch.Tensor, weights: torch.Tensor, out: torch.Tensor,
+                     add: torch.Tensor = None, ids: torch.Tensor = None, num_experts: int = 0,
+                     status: torch.Tensor = None):
+    """w4_moe_combine with its arguments marshalled once: returns call(pdl=False, stream=None)."""
+    _need(y, torch.bfloat16, "y")
+    _need(weights, torch.float32, "weights")
+    _need(out, torch.bfloat16, "out")
+    if y.dim() != 2 or weights.dim() != 2 or y.shape[0] != weights.numel() or \
+            tuple(out.shape) != (weights.shape[0], y.shape[1]):
+        raise ValueError("weights must be [rows, top_k], y [rows * top_k, N] and out [rows, N]")
+    if add is not None:
+        _need(add, torch.bfloat16, "add")
+        if add.shape != out.shape:
+            raise ValueError("add must be [rows, N]")
+    if ids is not None:
+        _need(ids, torch.int32, "ids")
+        if ids.numel() != weights.numel():
+            raise ValueError("ids must be [rows, top_k]")
+    _same_device(y, weights, out, add, ids, status)
+    args = (_ptr(out), _ptr(y), _ptr(weights), _ptr(ids), num_experts, _ptr(add),
+            *weights.shape, y.shape[1], _ptr(status))
+    return _kv8_call(load().w4_moe_combine, "w4_moe_combine", args,
+                     (y, weights, out, add, ids, status))
+
+
+def moe_combine(y: torch.Tensor, weights: torch.Tensor, out: torch.Tensor = None,
+                add: torch.Tensor = None, ids: torch.Tensor = None, num_experts: int = 0,
+                status: torch.Tensor = None, pdl: bool = False, stream=None) -> torch.Tensor:
+    """out[t] = add[t] + sum_j weights[t, j] * y[t * top_k + j] (y as gemv_id writes it)."""
+    if out is None:
+        out = torch.empty((weights.shape[0], y.shape[1]), dtype=torch.bfloat16, device=y.device)
+        _on(stream, out)
+    bind_moe_combine(y, weights, out, add, ids, num_experts, status)(pdl, stream)
+    return out
+
+
+class LogitRules:
+    """What w4_logits_adjust does to each row (struct w4_logit_rules); None where there is no such
+    rule.
+
+    tokens int32 [rows, max_tokens] with lens int32 [rows]: the histories; prompt int32 [rows]:
+    how many of their tokens, from the first on, were the prompt.  repetition, presence,
+    frequency: fp32 [rows].  bias_ids int32 and bias fp32 [rows, max_bias], n_bias int32 [rows]
+    (None: all).  mask int32 or uint32 [masks, words]: bit v % 32 of word v / 32 allows token v;
+    mask_rows int32 [rows]: each row's mask, -1: none (None: row b's is b).  The tensors may
+    change between calls, in place."""
+
+    def __init__(self, tokens: torch.Tensor = None, lens: torch.Tensor = None,
+                 prompt: torch.Tensor = None, repetition: torch.Tensor = None,
+                 presence: torch.Tensor = None, frequency: torch.Tensor = None,
+                 bias_ids: torch.Tensor = None, bias: torch.Tensor = None,
+                 n_bias: torch.Tensor = None, mask: torch.Tensor = None,
+                 mask_rows: torch.Tensor = None):
+        if (tokens is None) != (lens is None) or (bias_ids is None) != (bias is None):
+            raise ValueError("tokens go with lens, and bias_ids with bias")
+        per_row = (("lens", lens, torch.int32), ("prompt", prompt, torch.int32),
+                   ("repetition", repetition, torch.float32),
+                   ("presence", presence, torch.float32),
+                   ("frequency", frequency, torch.float32), ("n_bias", n_bias, torch.int32),
+                   ("mask_rows", mask_rows, torch.int32))
+        for name, t, dtype in per_row:
+            if t is not None:
+                _need(t, dtype, name)
+                if t.dim() != 1:
+                    raise ValueError(f"{name} must be [rows]")
+        lists = (("tokens", tokens, (torch.int32,)), ("bias_ids", bias_ids, (torch.int32,)),
+                 ("bias", bias, (torch.float32,)), ("mask", mask, (torch.int32, torch.uint32)))
+        strides, widths = {}, {}
+        for name, t, dtypes in lists:
+            strides[name] = widths[name] = 0
+            if t is None:
+                continue
+            if not t.is_cuda or t.dtype not in dtypes or t.dim() != 2 or \
+                    (t.shape[1] > 1 and t.stride(1) != 1):
+                raise ValueError(f"{name} must be a CUDA tensor [rows, n] of {dtypes[0]}, each "
+                                 "row dense")
+            widths[name] = t.shape[1]
+            strides[name] = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+        if bias is not None and (bias.shape != bias_ids.shape or
+                                 strides["bias"] != strides["bias_ids"]):
+            raise ValueError("bias_ids and bias must have the same shape and row stride")
+        self.row_counts = {t.shape[0] for t in (tokens, bias_ids, *(t for _, t, _ in per_row))
+                           if t is not None}
+        self.words = widths["mask"]
+        self.masks = 0 if mask is None else mask.shape[0]
+        self.per_row_mask = mask is not None and mask_rows is None
+        self.tensors = (tokens, lens, prompt, repetition, presence, frequency, bias_ids, bias,
+                        n_bias, mask, mask_rows)
+        self.struct = LogitRulesStruct(*[None if t is None else t.data_ptr() for t in self.tensors],
+                                       strides["tokens"], strides["bias"], strides["mask"],
+                                       widths["tokens"], widths["bias"], self.masks)
+
+
+def bind_adjust_logits(logits: torch.Tensor, rules: LogitRules, status: torch.Tensor = None):
+    """w4_logits_adjust with its arguments marshalled once: returns call(pdl=False,
+    stream=None)."""
+    kind, stride = _float_rows(logits, "logits")
+    rows, V = logits.shape
+    if rules.row_counts - {rows}:
+        raise ValueError(f"the rules are for {sorted(rules.row_counts)} rows, the logits have {rows}")
+    if rules.masks and rules.words < (V + 31) // 32:
+        raise ValueError("mask must hold a bit for each token")
+    if rules.per_row_mask and rules.masks < rows:
+        raise ValueError("mask must have a row for each row of logits")
+    _same_device(logits, *rules.tensors, status)
+    args = (_ptr(logits), kind, stride, rows, V, ctypes.byref(rules.struct), _ptr(status))
+    return _kv8_call(load().w4_logits_adjust, "w4_logits_adjust", args, (logits, rules, status))
+
+
+def adjust_logits(logits: torch.Tensor, rules: LogitRules, status: torch.Tensor = None,
+                  pdl: bool = False, stream=None) -> torch.Tensor:
+    """Penalties for repeated tokens, biases and masks on logits [rows, V] (bf16 or fp32), in
+    place."""
+    bind_adjust_logits(logits, rules, status)(pdl, stream)
+    return logits

@@ -887,6 +887,236 @@ w4_status w4_kv8_evict(const int32_t *dst_table, int32_t *kept, int32_t *new_len
 size_t w4_kv8_evict_workspace_bytes(const w4_kv8_cache *cache, const w4_kv8_batch *batch,
                                     int budget);
 
+/*
+ * Between the products of a decode step: routing, expert sums, logit rules.
+ *
+ * Conventions beside those at the top of this file: every kernel of these
+ * calls is launched as a programmatic dependent and waits for the kernel
+ * before it in the stream before it reads or writes anything, so W4_FLAG_PDL
+ * is accepted and changes nothing.  No call needs a workspace.
+ */
+#define W4_TYPE_BF16 0
+#define W4_TYPE_F32 1
+
+/*
+ * w4_route — the experts that each token goes to, and their weights.
+ *
+ * Page "Running a 26B MoE on an 8 GB Jetson by streaming experts from SSD",
+ * section "Streaming without touching a single GPU kernel": the router's
+ * top-k ids are what w4_dev_pool_stage and w4a16_gemv_id read.  The page
+ * names neither scores nor weights; the usual ones, for a token's logits x:
+ *
+ *   s[e] = exp(x[e]) / sum exp(x)   (W4_ROUTE_SOFTMAX), or 1 / (1 + exp(-x[e]))
+ *   c[e] = s[e] + bias[e]           (the choice only, not the weight)
+ *   with groups > 1 (equal runs of experts): a group's score is the sum of its
+ *   group_best largest c, and only experts of the top_groups groups of largest
+ *   score can be chosen
+ *   ids[t]     = the top_k experts of largest c, in that order
+ *   weights[t] = scale * s[id], or, with renorm, scale * s[id] / (sum of the
+ *                chosen s)  (0 each, should that sum be 0)
+ * Equal scores are in order of number, lowest first, of experts and of
+ * groups.  The choice is that of c in 64 bits: scores are compared in 32 bits,
+ * and a token with two that are nearer than 32 bits can tell goes through 64;
+ * without a bias experts are compared by x itself.  Weights are fp32, off by a
+ * few units in the last place.
+ *
+ * ids, weights int32 and fp32 [rows][top_k].
+ * logits       bf16 or fp32 (W4_TYPE_*), row t at element t * row_stride,
+ *              aligned to its type.
+ * bias         fp32 [experts], or NULL.
+ * A token with a NaN among its logits, with softmax one whose largest is
+ * infinite, and any token when a bias is not finite: W4_ERR_VALUE, and the
+ * token's ids and weights are left unwritten.  A logit of -inf is a score of 0.
+ * flags        W4_FLAG_PDL.
+ */
+#define W4_ROUTE_SOFTMAX 0
+#define W4_ROUTE_SIGMOID 1
+#define W4_ROUTE_MAX_EXPERTS 1024
+#define W4_ROUTE_MAX_TOP_K 32
+#define W4_ROUTE_MAX_GROUPS 32
+typedef struct w4_router {
+    int experts;      /* 1 .. W4_ROUTE_MAX_EXPERTS */
+    int top_k;        /* 1 .. W4_ROUTE_MAX_TOP_K, at most top_groups * (experts / groups) */
+    int groups;       /* divides experts, 1 .. W4_ROUTE_MAX_GROUPS; 1: no groups */
+    int top_groups;   /* 1 .. groups */
+    int group_best;   /* 1 or 2 (2 counts as 1 in groups of one expert) */
+    int score;        /* W4_ROUTE_SOFTMAX or W4_ROUTE_SIGMOID */
+    int renorm;       /* 0 or 1 */
+    float scale;      /* finite */
+} w4_router;
+
+w4_status w4_route(int32_t *ids, float *weights, const w4_router *router, const void *logits,
+                   int logits_type, size_t row_stride, const float *bias, int rows,
+                   int32_t *status_dev, unsigned flags, w4_stream_t stream);
+
+/*
+ * w4_moe_combine — the chosen experts' output rows added up by their weights.
+ *
+ *   out[t][n] = bf16( add[t][n] + sum_j weights[t][j] * y[t * top_k + j][n] )
+ * fp32, one fused multiply-add a row in order of j, from add (0 without).
+ *
+ * out          bf16 [rows][N]; may be add itself (each value is read before it
+ *              is written), nothing else that the call reads.
+ * y            bf16 [rows * top_k][N], as w4a16_gemv_id writes it for ids
+ *              [rows][top_k].
+ * weights      fp32 [rows][top_k].
+ * ids          int32 [rows][top_k] or NULL.  Given, a token with an id outside
+ *              [0, num_experts), whose row of y the product left unwritten,
+ *              leaves out[t] unwritten too: W4_ERR_INDEX.
+ * num_experts  >= 1 with ids; ignored without.
+ * add          bf16 [rows][N] (the layer's dense branch), or NULL.
+ * rows, N      >= 1;  top_k 1 .. W4_ROUTE_MAX_TOP_K.
+ * flags        W4_FLAG_PDL.
+ */
+w4_status w4_moe_combine(void *out, const void *y, const float *weights, const int32_t *ids,
+                         int num_experts, const void *add, int rows, int top_k, int N,
+                         int32_t *status_dev, unsigned flags, w4_stream_t stream);
+
+/*
+ * w4_logits_adjust — penalties for repeated tokens, biases and a grammar's mask.
+ *
+ * The output product's logits (w4a16_gemv over the tied table) before a token
+ * is drawn from them.  With n the number of times that token v occurs in its
+ * row's history after the prompt, x = logits[b][v]:
+ *
+ *   v in the history:  x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *   n > 0:             x = x - frequency[b] * n - presence[b]
+ *   v in the biases:   x = x + bias
+ *   v not allowed:     x = -inf
+ * in fp32 in this order, rounded once to the logits' type, in place.  Logits
+ * that no rule names keep their bits; a logit that is not allowed is not read.
+ * A mask that allows nothing leaves a row of -inf.
+ *
+ * logits       bf16 or fp32 (W4_TYPE_*), row b at element b * row_stride.
+ * A row with a history, prompt or bias count outside its bounds or a token
+ * outside [0, V) among them, a mask row outside [-1, num_masks): W4_ERR_INDEX;
+ * with a repetition that is not positive and finite, or a presence or
+ * frequency that is not finite: W4_ERR_VALUE.  Such a row is left as it was.
+ * rows         1 .. W4_KV8_MAX_BATCH;  V 1 .. 2^30.
+ * flags        W4_FLAG_PDL.
+ */
+#define W4_LOGITS_MAX_HISTORY ((1 << 19) - 1)
+#define W4_LOGITS_MAX_BIAS 4095
+typedef struct w4_logit_rules {          /* device arrays; NULL where there is no such rule */
+    const int32_t *tokens;     /* [rows] histories at token_stride */
+    const int32_t *lens;       /* [rows] tokens of each, up to max_tokens */
+    const int32_t *prompt;     /* [rows] how many of them, from the first on, were the prompt:
+                                  0 .. lens[b]; NULL: none */
+    const float *repetition;   /* [rows]; NULL: 1 */
+    const float *presence;     /* [rows]; NULL: 0 */
+    const float *frequency;    /* [rows]; NULL: 0 */
+    const int32_t *bias_ids;   /* [rows] lists at bias_stride; of a token named twice the later
+                                  entry counts */
+    const float *bias;         /* likewise */
+    const int32_t *n_bias;     /* [rows] entries of each, up to max_bias; NULL: max_bias */
+    const uint32_t *mask;      /* [num_masks] rows at mask_stride words: bit v % 32 of word v / 32
+                                  is 1 where token v is allowed */
+    const int32_t *mask_rows;  /* [rows] the mask of each row, -1: none; NULL: row b's is b */
+    size_t token_stride, bias_stride, mask_stride;
+    int max_tokens;            /* 0 .. W4_LOGITS_MAX_HISTORY */
+    int max_bias;              /* 0 .. W4_LOGITS_MAX_BIAS */
+    int num_masks;
+} w4_logit_rules;
+
+w4_status w4_logits_adjust(void *logits, int logits_type, size_t row_stride, int rows, int V,
+                           const w4_logit_rules *rules, int32_t *status_dev, unsigned flags,
+                           w4_stream_t stream);
+
+/*
+ * kv8 pages — who has which page: sequences that fork, grow and end, and the
+ * pool made dense again.
+ *
+ * refs int32 [num_pages] counts how often a page is named by the sequences'
+ * rows of a page table (a row of lens[b] tokens names its first
+ * ceil(lens[b] / page_tokens) entries), and by whatever else keeps it; a page
+ * with 0 is free.  The calls hold to the conventions of w4_kv8_*.  They move
+ * pages of several caches at once: a model's layers, with one table for all.
+ * Pages are taken from the lowest free number on, in order of rows.
+ *
+ * workspace  w4_kv8_pages_workspace_bytes(batch, num_pages) bytes with the
+ *            largest batch of the calls, 16-byte aligned; its first
+ *            W4_WORKSPACE_HEAD bytes are left as they are.  As with w4_kv8_attn one
+ *            buffer, the largest call's, serves calls of every kind in turn.
+ * caches     host array (read during the call), equal in num_pages, kv_heads,
+ *            page_tokens and head_dim; ranges and weight of each go along if given.
+ */
+#define W4_KV8_MAX_CACHES 128
+size_t w4_kv8_pages_workspace_bytes(int batch, int num_pages);
+
+/*
+ * w4_kv8_fork — sequences that go on from others, or end.
+ *
+ * Row b of the new table continues row parents[b] of the old one, or nothing
+ * (-1): one call lets beams follow their parents, a prompt continue many
+ * times, and ended sequences give back their pages (old rows from new_batch
+ * on end too).  Pages are shared, and a page that a sequence will write its next
+ * token to (its last, if not full) is its own: of the new rows that end in
+ * the same such page the lowest keeps it, if nothing else names it, and the
+ * others get copies of the tokens in use, steps, ranges and weights, in every cache.
+ * Parents that all are their own rows change nothing, unless such a page is shared.
+ *
+ * new_table  int32 [new_batch][max_pages]: entries past a row's pages are left
+ *            as they were.
+ * new_lens   int32 [new_batch]: lens[parents[b]], or 0.
+ * new_refs   int32 [num_pages].  refs - the old rows' + the new rows'.
+ * table, lens, refs are not changed, and must not overlap the new ones.  They stay
+ * as good as they were until something is written into a page that they name.
+ * A parent outside [-1, batch), or one whose length or pages break their
+ * bounds: W4_ERR_INDEX, new_lens[b] = -1, and row b's own old pages stay counted.  An
+ * old row that breaks them gives nothing back (W4_ERR_INDEX).
+ * Fewer free pages than copies: W4_ERR_STATE; every new_lens is -1, no cache
+ * is touched, and new_table and new_refs may hold anything.
+ * flags: W4_FLAG_PDL.
+ */
+w4_status w4_kv8_fork(int32_t *new_table, int32_t *new_lens, int32_t *new_refs, int new_batch,
+                      const int32_t *parents, const int32_t *table, const int32_t *lens,
+                      const int32_t *refs, int batch, int max_pages,
+                      const w4_kv8_cache *caches, int n_caches, void *workspace,
+                      size_t workspace_bytes, int32_t *status_dev, unsigned flags,
+                      w4_stream_t stream);
+
+/*
+ * w4_kv8_reserve — pages for each sequence's next tokens.
+ *
+ * lens[b] += grow[b], and the entries of table that the new length adds name
+ * free pages, whose refs become 1; table, lens and refs are changed in place, and
+ * w4_kv8_append can store the tokens.
+ *
+ * grow       int32 [batch], or NULL: one token for each row that has any.
+ * A negative grow, a length that breaks its bounds before or after: W4_ERR_INDEX,
+ * that row is left as it was.  Fewer free pages than the call needs:
+ * W4_ERR_STATE, nothing is changed.
+ * page_tokens  16, 32, 64 or 128.
+ * flags: W4_FLAG_PDL.
+ */
+w4_status w4_kv8_reserve(int32_t *table, int32_t *lens, int32_t *refs, const int32_t *grow,
+                         int batch, int max_pages, int num_pages, int page_tokens,
+                         void *workspace, size_t workspace_bytes, int32_t *status_dev,
+                         unsigned flags, w4_stream_t stream);
+
+/*
+ * w4_kv8_compact — the pages in use at the lowest numbers.
+ *
+ * With n pages in use, those numbered n and above move to the free ones below,
+ * in order (lowest to lowest), in every cache.  A page that something else than
+ * the table's rows names (refs above its number of entries) stays where it is.
+ *
+ * new_table  int32 [batch][max_pages]: entries past a row's pages are left as
+ *            they were.
+ * new_refs   int32 [num_pages].
+ * used       int32 [1]: one past the highest page in use after the call.
+ * table and refs are not changed, and must not overlap the new ones; the pages that
+ * moved keep their old contents until they are taken again.
+ * A row whose length or pages break their bounds: W4_ERR_INDEX, its new row is left
+ * unwritten, and pages that it alone names stay.
+ * flags: W4_FLAG_PDL.
+ */
+w4_status w4_kv8_compact(int32_t *new_table, int32_t *new_refs, int32_t *used,
+                         const int32_t *table, const int32_t *lens, const int32_t *refs,
+                         int batch, int max_pages, const w4_kv8_cache *caches, int n_caches,
+                         void *workspace, size_t workspace_bytes, int32_t *status_dev,
+                         unsigned flags, w4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
