@@ -4,13 +4,20 @@
 // section "Streaming without touching a single GPU kernel": the router's top-k
 // ids go to the slot pool and the routed product.
 //
-// route_kernel<V>: one warp a token, V neighbouring experts a lane.  Scores
-// c = s + bias become 32-bit keys in the order of the floats; each of the
-// top_k rounds is one warp maximum and one ballot, and the lane that held it
-// looks for its next one.  Without a bias the key is the logit itself, whose
-// order is the scores'.  With one, fp32 scores carry rounding errors: two that
-// are compared and lie within `tol` of each other (bounded below) send the
-// token through refine(), which chooses among doubles.
+// route_kernel<V, F32>: one warp a token.  Every group has as many lanes (a power
+// of two; without groups all 32), each with up to V neighbouring experts, so
+// that a group's best scores are a butterfly away.  Instructions bound it, so a
+// candidate is one word: its score as a fixed-point number above its place,
+// places counted down.  One integer maximum over the warp then gives value,
+// expert and the lowest number among equals, and a lane's candidates, sorted once
+// by a network of minima and maxima, only move up.  What the word says of the
+// score:
+//   bf16 logits, no bias   the logit itself, exactly
+//   fp32 logits, no bias   (logit - largest) in 2^-18, as far as 32 below
+//   with a bias            score + (bias - least bias) in about 2^-23 of their range
+// Of candidates, or groups, that are nearer than this (and the scores' fp32
+// errors) can tell, the order is found from 64-bit scores of those few alone; of
+// more than 32 such candidates by refine() over all experts.
 #include "kv8.cuh"
 
 namespace w4 {
@@ -26,6 +33,7 @@ struct RouteParams {
   const float* bias;
   long long stride;
   int rows, E, k, G, size, top_groups, best;   // size: experts of a group
+  int shift, each;   // lanes of a group: 1 << shift; experts of a lane
   bool sigmoid, renorm, f32, vec;
   float scale;
   int32_t* status;
@@ -36,8 +44,27 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t b = __float_as_uint(f + 0.0f);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+
+// Largest of the warp's values, NaN if one of them is.
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float m;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+__device__ __forceinline__ float warp_min_f(float v) {
+  float m;
+  asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+__device__ __forceinline__ float warp_max_f(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
 }
 
 __device__ __forceinline__ float logit(const RouteParams& p, long long row, int e) {
@@ -124,211 +151,368 @@ __device__ __noinline__ int refine(const RouteParams& p, long long row, double* 
   return mine;
 }
 
+// 64-bit sum of a softmax's exponentials; 1 where no score needs it: a sigmoid, or scores that are
+// compared without a bias (all have the same divisor).
+__device__ __noinline__ double divisor(const RouteParams& p, long long row, float top) {
+  if (p.sigmoid || p.bias == nullptr) return 1.0;
+  double z = 0.0;
+  for (int e = threadIdx.x & 31; e < p.E; e += 32) z += exp((double)logit(p, row, e) - (double)top);
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+  return z;
+}
+
+__device__ __forceinline__ double exact_score(const RouteParams& p, long long row, int e, float top,
+                                              double z) {
+  const double x = (double)logit(p, row, e);
+  const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top) / z;
+  return p.bias != nullptr ? s + (double)__ldg(p.bias + e) : s;
+}
+
+// Order of the first `cnt` candidates by 64-bit scores (without a bias by the logits), equal ones
+// by number: lane j gives the expert e_j and gets the j-th.
+__device__ __noinline__ int exact_order(const RouteParams& p, long long row, int e, int cnt, float top,
+                                        int* sm) {
+  const int lane = threadIdx.x & 31;
+  const double z = divisor(p, row, top);
+  double c = 0.0;
+  if (lane < cnt)
+    c = p.bias != nullptr ? exact_score(p, row, e, top, z) : (double)logit(p, row, e);
+  int rank = 0;
+  for (int j = 0; j < cnt; ++j) {
+    const double o = __shfl_sync(kFull, c, j);
+    const int oe = __shfl_sync(kFull, e, j);
+    rank += o > c || (o == c && oe < e);
+  }
+  __syncwarp();
+  if (lane < cnt) sm[rank] = e;
+  __syncwarp();
+  return lane < cnt ? sm[lane] : 0;
+}
+
+// Whether this lane's group is chosen, of groups whose 32-bit scores leave it open: those within
+// `slack` of the border have their best experts' scores (`mine`: bits of this lane's that can be
+// among them) added up in 64 bits, the others stand as they are.
+__device__ __noinline__ bool exact_group(const RouteParams& p, long long row, int e0, uint32_t mine_lo,
+                                         uint32_t mine_hi, float gs, bool in, float least, float next,
+                                         float slack, float top) {
+  const int lane = threadIdx.x & 31, g = lane >> p.shift;
+  const bool open = g < p.G && gs < next + slack && gs > least - slack;
+  const bool first = (lane & ((1 << p.shift) - 1)) == 0;
+  const int left = p.top_groups - __popc(__ballot_sync(kFull, first && in && !open));
+  const double z = divisor(p, row, top);
+  double a = -INFINITY, b = -INFINITY;
+  unsigned long long mask = open ? ((unsigned long long)mine_hi << 32) | mine_lo : 0ull;
+  while (mask != 0) {
+    const int i = __ffsll((long long)mask) - 1;
+    mask &= mask - 1;
+    const double c = exact_score(p, row, e0 + i, top, z);
+    b = fmax(b, fmin(a, c));
+    a = fmax(a, c);
+  }
+  for (int o = 1; o < (1 << p.shift); o <<= 1) {
+    const double oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
+    b = fmax(fmax(b, ob), fmin(a, oa));
+    a = fmax(a, oa);
+  }
+  const double sum = p.best == 2 ? a + b : a;
+  int rank = 0;
+  for (int i = 0; i < p.G; ++i) {
+    const double o = __shfl_sync(kFull, sum, i << p.shift);
+    const bool there = __shfl_sync(kFull, (int)open, i << p.shift);
+    rank += there && (o > sum || (o == sum && i < g));
+  }
+  return open ? rank < left : in;
+}
+
 template <int V>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteParams p) {
+struct Log2 {
+  static constexpr int value = 1 + Log2<V / 2>::value;
+};
+template <>
+struct Log2<1> {
+  static constexpr int value = 0;
+};
+
+// Descending order of V words by a network (odd-even merges).
+template <int V>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[V]) {
+#pragma unroll
+  for (int lp = 0; lp < Log2<V>::value; ++lp)
+#pragma unroll
+    for (int lq = lp; lq >= 0; --lq) {
+      const int p = 1 << lp, q = 1 << lq, j = q % p;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i >= j && (i - j) % (2 * q) < q && i + q < V && i / (2 * p) == (i + q) / (2 * p)) {
+          const uint32_t a = k[i], b = k[i + q];
+          k[i] = max(a, b);
+          k[i + q] = min(a, b);
+        }
+    }
+}
+
+template <int V, bool F32>
+__global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ double refine_sm[];
+  constexpr int kPlace = V <= 8 ? 8 : 5 + Log2<V>::value;       // bits of a place
+  constexpr int kBits = 32 - kPlace < 23 ? 32 - kPlace : 23;    // bits of a fixed-point score
+  constexpr float kOne = (float)(1 << kBits), kBase = 8388608.0f;   // 2^23: the unit is 1
+  constexpr bool kSorted = V <= 16;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long row = (long long)blockIdx.x * kRouteWarps + warp;
-  if (row >= p.rows) return;
-  const int e0 = lane * V;
-  float x[V];
-  if (p.vec) {   // E = 32 V and every row on a 16-byte boundary
-    if (p.f32) {
-      const float4* src = reinterpret_cast<const float4*>(
-          static_cast<const float*>(p.logits) + row * p.stride + e0);
+  const int g = lane >> p.shift, l = lane & ((1 << p.shift) - 1);
+  const int e0 = g * p.size + l * p.each;
+  const int n = g < p.G ? min(max(p.size - l * p.each, 0), p.each) : 0;   // experts of this lane
+  const bool biased = p.bias != nullptr, groups = p.G > 1;
+  const bool sums = biased || (groups && p.best == 2);   // scores themselves are compared
+  const bool fixed = biased || F32;                      // not the logits' own order
+  const uint32_t places = (1u << kPlace) - 1;
+  // biases above the least of them
+  float b[V], range = 1.0f;
+  bool bad_bias = false;
+  if (biased) {
+    float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const float4 w = __ldg(src + i);
-        x[4 * i] = w.x;
-        x[4 * i + 1] = w.y;
-        x[4 * i + 2] = w.z;
-        x[4 * i + 3] = w.w;
-      }
-    } else {
-      const uint2* src = reinterpret_cast<const uint2*>(
-          static_cast<const uint16_t*>(p.logits) + row * p.stride + e0);
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const uint2 w = __ldg(src + i);
-        x[4 * i] = bf16_bits_to_float(w.x & 0xFFFFu);
-        x[4 * i + 1] = __uint_as_float(w.x & 0xFFFF0000u);
-        x[4 * i + 2] = bf16_bits_to_float(w.y & 0xFFFFu);
-        x[4 * i + 3] = __uint_as_float(w.y & 0xFFFF0000u);
+    for (int i = 0; i < V; ++i) {
+      b[i] = i < n ? __ldg(p.bias + e0 + i) : 0.0f;
+      if (i < n) {
+        bad_bias |= !isfinite(b[i]);
+        lo = fminf(lo, b[i]);
+        hi = fmaxf(hi, b[i]);
       }
     }
-  } else {
+    bad_bias = __any_sync(kFull, bad_bias);
+    lo = warp_min_f(lo);
+    hi = warp_max_f(hi);
+    range = 1.0f + (hi - lo);
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = e0 + i < p.E ? logit(p, row, e0 + i) : -INFINITY;
+    for (int i = 0; i < V; ++i) b[i] -= lo;
   }
-  float top = -INFINITY;
-  bool bad = false;
+  const bool wide = !(range < 1e30f);   // no fixed point holds it
+  const float unit = __fdividef(kOne - 8.0f, range);
+  for (long long row = (long long)blockIdx.x * kRouteWarps + warp; row < p.rows;
+       row += (long long)gridDim.x * kRouteWarps) {
+    float x[V];
+    if (p.vec) {   // whole aligned vectors of four experts
+      if constexpr (V >= 4) {
+        if constexpr (F32) {
+          const float4* src = reinterpret_cast<const float4*>(
+              static_cast<const float*>(p.logits) + row * p.stride + e0);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bad |= isnan(x[i]);
-    top = fmaxf(top, x[i]);
-  }
+          for (int i = 0; i < V / 4; ++i) {
+            const float4 w = n > 0 ? __ldg(src + i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            x[4 * i] = w.x;
+            x[4 * i + 1] = w.y;
+            x[4 * i + 2] = w.z;
+            x[4 * i + 3] = w.w;
+          }
+        } else {
+          const uint2* src = reinterpret_cast<const uint2*>(
+              static_cast<const uint16_t*>(p.logits) + row * p.stride + e0);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  if (!p.sigmoid && isinf(top)) bad = true;
-  uint32_t key[V];
-  const bool groups = p.G > 1;
-  const bool sums = p.bias != nullptr || (groups && p.best == 2);   // scores themselves compared
-  float z = 1.0f, tol = 0.0f;
-  float c[V];
-  if (sums || (!p.renorm && !p.sigmoid)) {
-    // Errors of a score s: the exponential's 2 units and the division's and sum's few for a
-    // sigmoid, 2^-21 s in all; a softmax's sum adds (V + 5) / 2 units and x - top its own half.
-    if (p.sigmoid) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = sigmoid(x[i]);
-      tol = 0x1p-20f * sigmoid(top);
-    } else {
-      z = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        c[i] = expf(x[i] - top);
-        z += c[i];
-      }
-      z = warp_sum(z);
-      const float r = __fdividef(1.0f, z);
-#pragma unroll
-      for (int i = 0; i < V; ++i) c[i] *= r;
-      tol = 0x1p-17f * r;
-    }
-    if (p.bias != nullptr) {
-      float most = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float b = e0 + i < p.E ? __ldg(p.bias + e0 + i) : 0.0f;
-        bad |= !isfinite(b);
-        c[i] += b;
-        most = fmaxf(most, fabsf(c[i]));
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
-      tol += 0x1p-22f * most;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) c[i] = 0.0f;
-  }
-  if (__any_sync(kFull, bad)) {
-    if (lane == 0) report(p.status, W4_ERR_VALUE);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    key[i] = e0 + i < p.E ? order_key(p.bias != nullptr ? c[i] : x[i]) : 0u;
-  bool close = false;   // two compared scores nearer than fp32 can tell
-  if (groups) {
-    const bool by_sum = p.best == 2;
-    float gs = 0.0f;       // lane g: the score of group g (its key where one logit decides)
-    uint32_t gk = 0;
-    for (int g = 0; g < p.G; ++g) {
-      const int lo = g * p.size, hi = lo + p.size;
-      uint32_t a = 0;
-      float f1 = -INFINITY, f2 = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (e0 + i >= lo && e0 + i < hi) {
-          a = max(a, key[i]);
-          f2 = fmaxf(f2, fminf(f1, c[i]));
-          f1 = fmaxf(f1, c[i]);
+          for (int i = 0; i < V / 4; ++i) {
+            const uint2 w = n > 0 ? __ldg(src + i) : make_uint2(0xFF80FF80u, 0xFF80FF80u);
+            x[4 * i] = __uint_as_float(w.x << 16);
+            x[4 * i + 1] = __uint_as_float(w.x & 0xFFFF0000u);
+            x[4 * i + 2] = __uint_as_float(w.y << 16);
+            x[4 * i + 3] = __uint_as_float(w.y & 0xFFFF0000u);
+          }
         }
-      if (by_sum) {
+      }
+    } else {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
+      for (int i = 0; i < V; ++i) x[i] = i < n ? logit(p, row, e0 + i) : -INFINITY;
+    }
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) top = max_nan(top, x[i]);
+    top = warp_max_nan(top);
+    if (isnan(top) || (!p.sigmoid && isinf(top)) || bad_bias) {
+      if (lane == 0) report(p.status, W4_ERR_VALUE);
+      continue;
+    }
+    // Scores.  A sigmoid's error is below 2^-21 whatever its size (the exponential's argument
+    // is off by |x| 2^-24, which s (1 - s) |x| < 0.23 holds down; quotient and sum add 2^-22); a
+    // softmax's below 2^-18 of the largest (its sum adds (V + 5) 2^-24).  c: with the bias;
+    // two of them differ by 2^-20 (or 2^-17 of the largest) and four roundings of 2^-24 of the
+    // range more or less than they should.
+    float z = 1.0f, tol = 0.0f, f1 = -INFINITY, f2 = -INFINITY;   // a lane's two best
+    uint32_t key[V];
+    float c[V];
+    if (sums || (!p.renorm && !p.sigmoid)) {
+      if (p.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = __fdividef(1.0f, 1.0f + __expf(-x[i]));
+        tol = 0x1p-20f + 0x1p-22f * range;
+      } else {
+        z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          c[i] = __expf(x[i] - top);
+          z += c[i];
+        }
+        z = warp_sum(z);
+        const float r = __fdividef(1.0f, z);
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] *= r;
+        tol = 0x1p-17f * r + 0x1p-22f * range;
+      }
+      if (biased) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          c[i] += b[i];
+          const float f = fmaf(c[i], unit, kBase + 4.0f);
+          key[i] = (__float_as_uint(f) << kPlace) | (places - (lane * V + i));
+        }
+      }
+      if (groups) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float v = i < n ? c[i] : -INFINITY;
+          f2 = fmaxf(f2, fminf(f1, v));
+          f1 = fmaxf(f1, v);
+        }
+      }
+    }
+    if (!biased) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (F32) {
+          const float f = fmaxf(fmaf(x[i] - top, kOne / 32.0f, kBase + (kOne - 2.0f)), kBase + 1.0f);
+          key[i] = (__float_as_uint(f) << kPlace) | (places - (lane * V + i));
+        } else {
+          key[i] = (order_key(x[i]) & 0xFFFF0000u) | (0xFFFFu - (lane * V + i));
+        }
+      }
+    }
+    bool close = wide;   // too many compared scores nearer than fp32 can tell
+    if (groups) {
+      // the group's score in each of its lanes; one logit alone decides where no sum is taken
+      float gs;
+      if (sums) {
+        for (int o = 1; o < (1 << p.shift); o <<= 1) {
           const float o1 = __shfl_xor_sync(kFull, f1, o), o2 = __shfl_xor_sync(kFull, f2, o);
           f2 = fmaxf(fmaxf(f2, o2), fminf(f1, o1));
           f1 = fmaxf(f1, o1);
         }
-        if (lane == g) gs = f1 + f2;
+        gs = p.best == 2 ? f1 + f2 : f1;
       } else {
-        a = __reduce_max_sync(kFull, a);
-        if (lane == g) gk = a;
+        gs = x[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) gs = fmaxf(gs, x[i]);
+        for (int o = 1; o < (1 << p.shift); o <<= 1)
+          gs = fmaxf(gs, __shfl_xor_sync(kFull, gs, o));
+      }
+      int rank = 0;
+      for (int i = 0; i < p.G; ++i) {
+        const float o = __shfl_sync(kFull, gs, i << p.shift);
+        rank += o > gs || (o == gs && i < g);
+      }
+      bool in = g < p.G && rank < p.top_groups;
+      if (sums) {
+        const float least = warp_min_f(in ? gs : INFINITY);
+        const float next = warp_max_f(in || g >= p.G ? -INFINITY : gs);
+        if (least - next < 3.0f * tol && !wide) {
+          uint32_t can[2] = {0, 0};
+          const float from = (p.best == 2 ? f2 : f1) - tol;
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (i < n && c[i] >= from) can[i / 32] |= 1u << (i % 32);
+          in = exact_group(p, row, e0, can[0], can[1], gs, in, least, next, 3.0f * tol, top);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = in && i < n ? key[i] : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = i < n ? key[i] : 0u;
+    }
+    uint32_t mine = 0, my = 0, m = 0, kth = 0;
+    if constexpr (kSorted) {
+      sort_down<V>(key);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) mine = max(mine, key[i]);
+    }
+    auto pop = [&]() {   // the largest word of the warp, which is then gone
+      if constexpr (kSorted) {
+        m = __reduce_max_sync(kFull, key[0]);
+        const bool hit = key[0] == m;
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i) key[i] = hit ? key[i + 1] : key[i];
+        key[V - 1] = hit ? 0u : key[V - 1];
+      } else {
+        m = __reduce_max_sync(kFull, mine);
+        if (mine == m) {
+          mine = 0;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            key[i] = key[i] == m ? 0u : key[i];
+            mine = max(mine, key[i]);
+          }
+        }
+      }
+    };
+    int cnt = 0;
+    for (; cnt < p.k; ++cnt) {
+      pop();
+      if (lane == cnt) my = m;
+    }
+    kth = m;
+    uint32_t near = 0;
+    if (fixed) {
+      // Units that two scores can be apart and still be in the wrong order: their errors and the
+      // rounding of the word.  Candidates are taken as far as the last one is clear of the k-th.
+      near = 3 + (biased ? (uint32_t)fminf(tol * unit, kOne) : 1u);
+      while (true) {
+        pop();
+        if (m == 0 || (kth >> kPlace) - (m >> kPlace) >= near) break;
+        if (cnt == 32) {
+          close = true;
+          break;
+        }
+        if (lane == cnt) my = m;
+        ++cnt;
       }
     }
-    if (by_sum) gk = lane < p.G ? order_key(gs) : 0u;
-    uint32_t in = 0, last = 0;
-    for (int j = 0; j <= p.top_groups && j < p.G; ++j) {
-      const uint32_t m = __reduce_max_sync(kFull, gk);
-      if (j == p.top_groups) {   // the best of those left out
-        if (sums) close |= key_value(last) - key_value(m) < 3.0f * tol;
-        break;
-      }
-      last = m;
-      const uint32_t who = __ballot_sync(kFull, gk == m);
-      in |= who & (0u - who);
-      if (lane == __ffs(who) - 1) gk = 0;
-    }
-    int g = e0 / p.size, left = (g + 1) * p.size - e0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (left == 0) {
-        ++g;
-        left = p.size;
-      }
-      --left;
-      if (!((in >> (g & 31)) & 1)) key[i] = 0;
-    }
-  }
-  uint32_t mine = 0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) mine = max(mine, key[i]);
-  int my_id = 0, prev_id = 0;
-  uint32_t prev = 0;
-  const bool check = p.bias != nullptr;
-  const int rounds = p.k + (check ? 1 : 0);
-  for (int j = 0; j < rounds; ++j) {
-    const uint32_t m = __reduce_max_sync(kFull, mine);
-    if (m == 0) break;   // as many experts as there are: none left to compare with
-    const int src = __ffs(__ballot_sync(kFull, mine == m)) - 1;
-    int at = 0;
-    if (lane == src) {
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i) at = key[i] == m ? i : at;
-      mine = 0;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (i == at) key[i] = 0;
-        mine = max(mine, key[i]);
-      }
-      at += e0;
-    }
-    at = __shfl_sync(kFull, at, src);
-    if (check && j > 0 && key_value(prev) - key_value(m) < tol) {
+    // lane j's candidate
+    const uint32_t place = (fixed ? places : 0xFFFFu) - (my & (fixed ? places : 0xFFFFu));
+    const int pl = (int)(place / V), pi = (int)(place % V);
+    int e = (pl >> p.shift) * p.size + (pl & ((1 << p.shift) - 1)) * p.each + pi;
+    float xl = lane < cnt ? logit(p, row, e) : -INFINITY;
+    if (fixed) {
       // equal inputs are equal scores at any width, and in order already
-      const bool same = logit(p, row, at) == logit(p, row, prev_id) &&
-                        __ldg(p.bias + at) == __ldg(p.bias + prev_id);
-      close |= !same;
+      const float bl = biased && lane < cnt ? __ldg(p.bias + e) : 0.0f;
+      const uint32_t up = __shfl_up_sync(kFull, my, 1);
+      const float xu = __shfl_up_sync(kFull, xl, 1), bu = __shfl_up_sync(kFull, bl, 1);
+      const bool unsure = lane > 0 && lane < cnt && (up >> kPlace) - (my >> kPlace) < near &&
+                          !(xu == xl && bu == bl);
+      double* sm = refine_sm + warp * (p.E > 32 ? p.E : 32);
+      if (close || __any_sync(kFull, unsure)) {
+        e = close ? refine(p, row, sm) : exact_order(p, row, e, cnt, top, reinterpret_cast<int*>(sm));
+        xl = lane < p.k ? logit(p, row, e) : -INFINITY;
+      }
     }
-    prev = m;
-    prev_id = at;
-    if (lane == j && j < p.k) my_id = at;
-  }
-  if (close) my_id = refine(p, row, refine_sm + warp * p.E);
-  // weights: relative to the largest chosen logit where they are divided by their sum, so that
-  // small scores do not vanish
-  const bool has = lane < p.k;
-  const float xl = has ? logit(p, row, my_id) : -INFINITY;
-  float w;
-  if (p.renorm) {
-    float m = xl;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    if (p.sigmoid) m = fminf(m, 0.0f);
-    w = has && xl > -INFINITY ? (p.sigmoid && m == 0.0f ? sigmoid(xl) : expf(xl - m)) : 0.0f;
-    if (p.sigmoid && m < 0.0f) w = __fdividef(w, 1.0f + expf(xl));
-    const float sum = warp_sum(w);
-    w = sum > 0.0f ? p.scale * __fdividef(w, sum) : 0.0f;
-  } else {
-    w = p.scale * (p.sigmoid ? sigmoid(xl) : __fdividef(expf(xl - top), z));
-  }
-  if (has) {
-    p.ids[row * p.k + lane] = my_id;
-    p.weights[row * p.k + lane] = w;
+    // weights: relative to the largest chosen logit where they are divided by their sum, so that
+    // small scores do not vanish
+    const bool has = lane < p.k;
+    if (!has) xl = -INFINITY;
+    float w;
+    if (p.renorm) {
+      float t = warp_max_f(xl);
+      if (p.sigmoid) t = fminf(t, 0.0f);
+      w = xl > -INFINITY ? (p.sigmoid && t == 0.0f ? sigmoid(xl) : expf(xl - t)) : 0.0f;
+      if (p.sigmoid && t < 0.0f) w = __fdividef(w, 1.0f + expf(xl));
+      const float sum = warp_sum(w);
+      w = sum > 0.0f ? p.scale * __fdividef(w, sum) : 0.0f;
+    } else {
+      w = p.scale * (p.sigmoid ? sigmoid(xl) : __fdividef(expf(xl - top), z));
+    }
+    if (has) {
+      p.ids[row * p.k + lane] = e;
+      p.weights[row * p.k + lane] = w;
+    }
   }
 }
 
@@ -457,8 +641,8 @@ extern "C" w4_status w4_route(int32_t* ids, float* weights, const w4_router* rou
   p.rows = rows;
   p.E = r.experts;
   p.k = r.top_k;
-  p.size = r.experts / r.groups;
   p.G = r.top_groups == r.groups ? 1 : r.groups;   // every group in: as without groups
+  p.size = r.experts / p.G;
   p.top_groups = r.top_groups;
   p.best = p.size == 1 ? 1 : r.group_best;
   p.sigmoid = r.score == W4_ROUTE_SIGMOID;
@@ -466,19 +650,30 @@ extern "C" w4_status w4_route(int32_t* ids, float* weights, const w4_router* rou
   p.f32 = logits_type == W4_TYPE_F32;
   p.scale = r.scale;
   p.status = status_dev;
-  const bool sums = bias != nullptr || (p.G > 1 && p.best == 2);
-  const size_t smem = sums ? (size_t)kRouteWarps * p.E * sizeof(double) : 0;
-  const unsigned grid = (unsigned)((rows + kRouteWarps - 1) / kRouteWarps);
-  auto go = [&](auto kern, int v) {
-    p.vec = v >= 4 && p.E == 32 * v && !kv8::misaligned(logits, 16) && row_stride * el % 16 == 0;
-    return kv8::launch(kern, dim3(grid), 32 * kRouteWarps, smem, stream, p);
+  while ((32 >> p.shift) > p.G && p.shift < 5) ++p.shift;
+  if ((32 >> p.shift) < p.G) --p.shift;
+  p.each = (p.size + (1 << p.shift) - 1) >> p.shift;
+  // room for the 64-bit scores, where such may be needed
+  const bool fixed = bias != nullptr || p.f32;
+  const size_t smem = fixed ? (size_t)kRouteWarps * (p.E > 32 ? p.E : 32) * sizeof(double) : 0;
+  // a warp's rows share what it makes of the biases: at most the CTAs that are resident together
+  // (8 an SM by their registers; 6 or 12 an SM with theirs, or a CTA for every four rows, were
+  // 18 to 22 us where this is 18.5: 16384 tokens, 256 experts in 8 groups, biases)
+  const long long ctas = ((long long)rows + kRouteWarps - 1) / kRouteWarps;
+  const unsigned grid = (unsigned)(ctas < 152 * 8 ? ctas : 152 * 8);
+  auto go = [&](auto bf16, auto f32, int v) {
+    p.vec = v >= 4 && p.each == v && p.size == v << p.shift && !kv8::misaligned(logits, 16) &&
+            row_stride * el % 16 == 0;
+    return p.f32 ? kv8::launch(f32, dim3(grid), 32 * kRouteWarps, smem, stream, p)
+                 : kv8::launch(bf16, dim3(grid), 32 * kRouteWarps, smem, stream, p);
   };
-  if (p.E <= 32) return go(route_kernel<1>, 1);
-  if (p.E <= 64) return go(route_kernel<2>, 2);
-  if (p.E <= 128) return go(route_kernel<4>, 4);
-  if (p.E <= 256) return go(route_kernel<8>, 8);
-  if (p.E <= 512) return go(route_kernel<16>, 16);
-  return go(route_kernel<32>, 32);
+  if (p.each <= 1) return go(route_kernel<1, false>, route_kernel<1, true>, 1);
+  if (p.each <= 2) return go(route_kernel<2, false>, route_kernel<2, true>, 2);
+  if (p.each <= 4) return go(route_kernel<4, false>, route_kernel<4, true>, 4);
+  if (p.each <= 8) return go(route_kernel<8, false>, route_kernel<8, true>, 8);
+  if (p.each <= 16) return go(route_kernel<16, false>, route_kernel<16, true>, 16);
+  if (p.each <= 32) return go(route_kernel<32, false>, route_kernel<32, true>, 32);
+  return go(route_kernel<64, false>, route_kernel<64, true>, 64);
 }
 
 extern "C" w4_status w4_moe_combine(void* out, const void* y, const float* weights,
