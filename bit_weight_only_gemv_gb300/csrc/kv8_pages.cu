@@ -1,14 +1,19 @@
 // Who has which page of the 8-bit cache: forks, growth and compaction
 // (w4_kv8_fork, w4_kv8_reserve, w4_kv8_compact).
 //
-// Each call decides in one cluster of kRanks CTAs, whose barrier separates its
-// phases: counts of references by atomics (whole numbers, so their order does
-// not matter), decisions in row order by block scans that every CTA repeats,
-// free pages in page order by a scan over the cluster's contiguous shares of
-// the pages.  Tables are walked in pieces of kPiece entries, one piece a warp,
-// so that one long row has as many readers as many short ones.  What has to be
-// copied goes into a list in the workspace; copy_kernel moves it in every
-// cache, one warp for the keys or values of one (page, head).
+// Each call decides in one kernel whose barriers separate its phases: counts of
+// references by atomics (whole numbers, so their order does not matter),
+// decisions in row order by block scans, free pages in page order by a scan over
+// contiguous shares of the pages.  A small pool is decided by one CTA with its
+// counts in shared memory, a large one by a cluster of 8 with counts in the
+// workspace (Team<R>; every CTA repeats the scans over rows).  Latency bounds
+// both: a phase is a chain of a barrier and one or two loads.  Tables are
+// walked in pieces of kPiece entries, one piece a warp, so that one long row has
+// as many readers as many short ones.  What has to be copied goes into a list in
+// the workspace; copy_kernel moves it in every cache, one warp for the keys or
+// values of one (page, head).
+#include <mutex>
+
 #include "kv8.cuh"
 
 namespace w4 {
@@ -16,8 +21,9 @@ namespace kv8 {
 namespace {
 
 constexpr int kRanks = 8, kPlanThreads = 1024;
-constexpr int kAll = kRanks * kPlanThreads;
 constexpr int kPiece = 128;
+constexpr int kOnePages = 16384;      // one CTA's largest pool: three counts a page in its shared memory,
+constexpr long long kOnePieces = 1024;   // and its most pieces of a table
 constexpr int kRowsEach = W4_KV8_MAX_BATCH / kPlanThreads;   // rows a thread decides
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -60,13 +66,28 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Everything that the cluster's threads wrote before is seen after (global
-// memory through L2: what other CTAs write is read by __ldcg).
-__device__ __forceinline__ void cluster_sync() {
-  __threadfence();
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
+// The threads that decide: one CTA, or a cluster of R.  sync(): what any of them wrote before is
+// seen after; words that others wrote are read by get(), through L2 where they may be global.
+template <int R>
+struct Team {
+  static constexpr int kAll = R * kPlanThreads;
+  static __device__ __forceinline__ uint32_t rank() {
+    if constexpr (R == 1) return 0;
+    return cluster_rank();
+  }
+  static __device__ __forceinline__ void sync() {
+    if constexpr (R == 1) {
+      __syncthreads();
+    } else {
+      asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    }
+  }
+  static __device__ __forceinline__ int get(const int32_t* p) {
+    if constexpr (R == 1) return *p;
+    return __ldcg(p);
+  }
+};
 __device__ __forceinline__ int remote(const int* p, uint32_t rank) {
   uint32_t a, v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
@@ -114,19 +135,22 @@ struct Rows {
   }
 };
 
-// Pages of every old row into s.row_pages, -1 where its length or one of its
-// entries breaks its bounds.  Ends in a cluster barrier.
-__device__ void check_rows(const Rows& r, const Scratch& s, uint32_t rank, int32_t* status) {
+// Pages of every old row into row_pages, -1 where its length or one of its
+// entries breaks its bounds.  Ends in a barrier.
+template <int R>
+__device__ __forceinline__ void check_rows(const Rows& r, int32_t* row_pages, uint32_t rank,
+                                           int32_t* status) {
+  using T = Team<R>;
   const int gt = rank * kPlanThreads + threadIdx.x;
-  for (int b = gt; b < r.batch; b += kAll) {
+  for (int b = gt; b < r.batch; b += T::kAll) {
     const int np = r.pages(__ldg(r.lens + b));
-    s.row_pages[b] = np;
+    row_pages[b] = np;
     if (np < 0) report(status, W4_ERR_INDEX);
   }
-  cluster_sync();
+  T::sync();
   const int lane = threadIdx.x & 31;
   const long long pieces = (r.max_pages + kPiece - 1) / kPiece;
-  for (long long i = gt >> 5; i < pieces * r.batch; i += kAll / 32) {
+  for (long long i = gt >> 5; i < pieces * r.batch; i += T::kAll / 32) {
     const int b = (int)(i / pieces), at = (int)(i % pieces) * kPiece;
     const int np = min(r.pages(__ldg(r.lens + b)), at + kPiece);
     bool bad = false;
@@ -135,28 +159,36 @@ __device__ void check_rows(const Rows& r, const Scratch& s, uint32_t rank, int32
       bad |= pg < 0 || pg >= r.num_pages;
     }
     if (__any_sync(kFull, bad) && lane == 0) {
-      s.row_pages[b] = -1;
+      row_pages[b] = -1;
       report(status, W4_ERR_INDEX);
     }
   }
-  cluster_sync();
+  T::sync();
 }
 
-// This thread's share of the pages, in page order over the cluster.
+// This thread's share of the pages, in page order over the team.
+template <int R>
 __device__ __forceinline__ void my_share(int num_pages, uint32_t rank, int* lo, int* hi) {
-  const long long each = ((long long)num_pages + kAll - 1) / kAll;
+  const long long all = Team<R>::kAll;
+  const long long each = ((num_pages + all - 1) / all) | 1;   // odd: no two threads of a warp in one bank
   const long long a = ((long long)rank * kPlanThreads + threadIdx.x) * each;
   *lo = (int)min(a, (long long)num_pages);
   *hi = (int)min(a + each, (long long)num_pages);
 }
 
 // Sum of `mine` (the same in all threads of a CTA) over the ranks before this
-// one, and over all.  slot: shared memory of this use alone.
+// one, and over all.  slot: shared memory of this use alone.  A barrier.
+template <int R>
 __device__ __forceinline__ int before_rank(int mine, int* slot, uint32_t rank, int* total) {
+  if constexpr (R == 1) {
+    __syncthreads();
+    *total = mine;
+    return 0;
+  }
   if (threadIdx.x == 0) *slot = mine;
-  cluster_sync();
+  Team<R>::sync();
   int before = 0, all = 0;
-  for (int i = 0; i < kRanks; ++i) {
+  for (int i = 0; i < R; ++i) {
     const int v = remote(slot, i);
     all += v;
     if (i < (int)rank) before += v;
@@ -166,26 +198,28 @@ __device__ __forceinline__ int before_rank(int mine, int* slot, uint32_t rank, i
 }
 
 // The lowest `want` free pages into list, in order; false (everywhere) if there
-// are fewer.  Ends in a cluster barrier: what every rank read before the call
-// may be written after it.
-__device__ bool take_free(const int32_t* refs, int num_pages, long long want, int32_t* list,
-                          uint32_t rank, int* red, int* slot) {
+// are fewer.  Ends in a barrier: what every rank read before the call may be
+// written after it.
+template <int R>
+__device__ __forceinline__ bool take_free(const int32_t* refs, int num_pages, long long want, int32_t* list,
+                                          uint32_t rank, int* red, int* slot) {
+  using T = Team<R>;
   if (want == 0) {
-    cluster_sync();
+    T::sync();
     return true;
   }
   int lo, hi;
-  my_share(num_pages, rank, &lo, &hi);
+  my_share<R>(num_pages, rank, &lo, &hi);
   int free = 0;
-  for (int i = lo; i < hi; ++i) free += __ldcg(refs + i) == 0;
+  for (int i = lo; i < hi; ++i) free += T::get(refs + i) == 0;
   int total, all;
   int at = block_scan(free, red, &total);
-  at += before_rank(total, slot, rank, &all);
+  at += before_rank<R>(total, slot, rank, &all);
   const bool ok = all >= want;
   if (ok && free > 0 && at < want)
     for (int i = lo; i < hi && at < want; ++i)
-      if (__ldcg(refs + i) == 0) list[at++] = i;
-  cluster_sync();
+      if (T::get(refs + i) == 0) list[at++] = i;
+  T::sync();
   return ok;
 }
 
@@ -201,56 +235,68 @@ struct ForkParams {
   int32_t* status;
 };
 
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kPlanThreads)
-    fork_kernel(ForkParams p) {
+template <int R>
+__global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const __grid_constant__ ForkParams p) {
+  using T = Team<R>;
+  extern __shared__ int32_t sm[];
   __shared__ int red[33], slot;
+  // one CTA: what it knows of its rows (old ones' pages; new ones' lengths and last pages) and takes
+  __shared__ int32_t of_rows[4][R == 1 ? kOnePieces : 1];
   pdl_launch_dependents();
   pdl_wait();
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = T::rank();
   const int gt = rank * kPlanThreads + threadIdx.x, lane = threadIdx.x & 31;
   const Rows& r = p.old;
-  for (int i = gt; i < r.num_pages; i += kAll) {
-    p.new_refs[i] = __ldg(p.refs + i);
-    p.s.count[i] = 0;
-    p.s.first[i] = 0x7fffffff;
+  int32_t* refs = R == 1 ? sm : p.new_refs;
+  int32_t* count = R == 1 ? sm + r.num_pages : p.s.count;
+  int32_t* first = R == 1 ? sm + 2 * r.num_pages : p.s.first;
+  int32_t* row_pages = R == 1 ? of_rows[0] : p.s.row_pages;
+  int32_t* new_lens = R == 1 ? of_rows[1] : p.new_lens;
+  int32_t* list = R == 1 ? of_rows[3] : p.s.dst;
+  for (int i = gt; i < r.num_pages; i += T::kAll) {
+    refs[i] = __ldg(p.refs + i);
+    count[i] = 0;
+    first[i] = 0x7fffffff;
   }
-  check_rows(r, p.s, rank, p.status);
+  check_rows<R>(r, row_pages, rank, p.status);
   // the old rows' names go, the new rows' come
   const long long pieces = (r.max_pages + kPiece - 1) / kPiece;
   const int rows = max(r.batch, p.new_batch);
-  for (long long i = gt >> 5; i < pieces * rows; i += kAll / 32) {
+  for (long long i = gt >> 5; i < pieces * rows; i += T::kAll / 32) {
     const int b = (int)(i / pieces), at = (int)(i % pieces) * kPiece;
     const int par = b < p.new_batch ? __ldg(p.parents + b) : -1;
-    int had = b < r.batch ? __ldcg(p.s.row_pages + b) : 0, np = 0, len = 0;
+    const int had = b < r.batch ? T::get(row_pages + b) : 0;
+    int np = 0, len = 0;
     bool ok = par >= -1 && par < r.batch;
     if (ok && par >= 0) {
-      np = __ldcg(p.s.row_pages + par);
+      np = T::get(row_pages + par);
       len = __ldg(r.lens + par);
       ok = np >= 0;
     }
     if (!ok) {
       if (at == 0 && lane == 0) {
-        p.new_lens[b] = -1;
+        new_lens[b] = -1;
         report(p.status, W4_ERR_INDEX);
       }
       continue;
     }
     if (par != b)
       for (int e = at + lane; e < min(had, at + kPiece); e += 32)
-        atomicSub(p.new_refs + __ldg(r.table + (long long)b * r.max_pages + e), 1);
+        atomicSub(refs + __ldg(r.table + (long long)b * r.max_pages + e), 1);
     if (b >= p.new_batch) continue;
     for (int e = at + lane; e < min(np, at + kPiece); e += 32) {
       const int pg = __ldg(r.table + (long long)par * r.max_pages + e);
       p.new_table[(long long)b * r.max_pages + e] = pg;
-      if (par != b) atomicAdd(p.new_refs + pg, 1);
+      if (par != b) atomicAdd(refs + pg, 1);
       if (e == np - 1 && (len & ((1 << r.shift) - 1)) != 0) {   // a page to be written to
-        atomicAdd(p.s.count + pg, 1);
-        atomicMin(p.s.first + pg, b);
+        atomicAdd(count + pg, 1);
+        atomicMin(first + pg, b);
+        if constexpr (R == 1) of_rows[2][b] = pg;
       }
     }
-    if (at == 0 && lane == 0) p.new_lens[b] = len;
+    if (at == 0 && lane == 0) new_lens[b] = len;
   }
-  cluster_sync();
+  T::sync();
   // rows that need a page of their own, in order
   int page[kRowsEach], used[kRowsEach], last[kRowsEach], mine = 0;
 #pragma unroll
@@ -258,38 +304,44 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kPlanThreads)
     const int b = threadIdx.x * kRowsEach + z;
     page[z] = -1;
     if (b >= p.new_batch) continue;
-    const int len = __ldcg(p.new_lens + b);
+    const int len = T::get(new_lens + b);
     used[z] = len & ((1 << r.shift) - 1);
     if (len <= 0 || used[z] == 0) continue;
     last[z] = r.pages(len) - 1;
-    const int pg = __ldcg(p.new_table + (long long)b * r.max_pages + last[z]);
-    if (__ldcg(p.s.count + pg) == __ldcg(p.new_refs + pg) && __ldcg(p.s.first + pg) == b) continue;
+    const int pg = R == 1 ? of_rows[2][b]
+                          : T::get(p.new_table + (long long)b * r.max_pages + last[z]);
+    if (T::get(count + pg) == T::get(refs + pg) && T::get(first + pg) == b) continue;
     page[z] = pg;
     ++mine;
   }
   int want;
   int at = block_scan(mine, red, &want);
-  const bool ok = take_free(p.new_refs, r.num_pages, want, p.s.dst, rank, red, &slot);
-  if (rank == 0) {
-    if (threadIdx.x == 0) {
-      *p.s.n_copies = ok ? want : 0;
-      if (!ok) report(p.status, W4_ERR_STATE);
-    }
-    if (!ok) {
-      for (int b = threadIdx.x; b < p.new_batch; b += kPlanThreads) p.new_lens[b] = -1;
-    } else {
+  const bool ok = take_free<R>(refs, r.num_pages, want, list, rank, red, &slot);
+  if (rank != 0) return;
+  if (threadIdx.x == 0) {
+    *p.s.n_copies = ok ? want : 0;
+    if (!ok) report(p.status, W4_ERR_STATE);
+  }
+  if (!ok) {
+    for (int b = threadIdx.x; b < p.new_batch; b += kPlanThreads) p.new_lens[b] = -1;
+    return;
+  }
 #pragma unroll
-      for (int z = 0; z < kRowsEach; ++z) {
-        if (page[z] < 0) continue;
-        const int to = __ldcg(p.s.dst + at);
-        p.new_table[(long long)(threadIdx.x * kRowsEach + z) * r.max_pages + last[z]] = to;
-        atomicSub(p.new_refs + page[z], 1);
-        p.new_refs[to] = 1;
-        p.s.src[at] = page[z];
-        p.s.tokens[at] = used[z];
-        ++at;
-      }
-    }
+  for (int z = 0; z < kRowsEach; ++z) {
+    if (page[z] < 0) continue;
+    const int to = T::get(list + at);
+    p.new_table[(long long)(threadIdx.x * kRowsEach + z) * r.max_pages + last[z]] = to;
+    atomicSub(refs + page[z], 1);
+    refs[to] = 1;
+    p.s.src[at] = page[z];
+    if constexpr (R == 1) p.s.dst[at] = to;
+    p.s.tokens[at] = used[z];
+    ++at;
+  }
+  if constexpr (R == 1) {
+    for (int b = threadIdx.x; b < p.new_batch; b += kPlanThreads) p.new_lens[b] = new_lens[b];
+    __syncthreads();
+    for (int i = threadIdx.x; i < r.num_pages; i += kPlanThreads) p.new_refs[i] = refs[i];
   }
 }
 
@@ -303,13 +355,14 @@ struct ReserveParams {
   int32_t* status;
 };
 
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kPlanThreads)
-    reserve_kernel(ReserveParams p) {
+template <int R>
+__global__ void __launch_bounds__(kPlanThreads, 1) reserve_kernel(const __grid_constant__ ReserveParams p) {
+  using T = Team<R>;
   __shared__ long long red64[33];
   __shared__ int red[33], slot;
   pdl_launch_dependents();
   pdl_wait();
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = T::rank();
   int from[kRowsEach], to[kRowsEach], len[kRowsEach];
   long long mine = 0;
 #pragma unroll
@@ -333,7 +386,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kPlanThreads)
   }
   long long want;
   long long at = block_scan(mine, red64, &want);
-  const bool ok = take_free(p.refs, p.r.num_pages, want, p.s.dst, rank, red, &slot);
+  const bool ok = take_free<R>(p.refs, p.r.num_pages, want, p.s.dst, rank, red, &slot);
   if (rank != 0) return;
   if (!ok) {
     if (threadIdx.x == 0) report(p.status, W4_ERR_STATE);
@@ -344,7 +397,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kPlanThreads)
     if (len[z] < 0) continue;
     const int b = threadIdx.x * kRowsEach + z;
     for (int e = from[z]; e < to[z]; ++e) {
-      const int pg = __ldcg(p.s.dst + at++);
+      const int pg = T::get(p.s.dst + at++);
       p.table[(long long)b * p.r.max_pages + e] = pg;
       p.refs[pg] = 1;
     }
@@ -362,74 +415,82 @@ struct CompactParams {
   int32_t* status;
 };
 
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kPlanThreads)
-    compact_kernel(CompactParams p) {
+template <int R>
+__global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const __grid_constant__ CompactParams p) {
+  using T = Team<R>;
+  extern __shared__ int32_t sm[];
   __shared__ int red[33], slot[3];
+  __shared__ int32_t of_rows[R == 1 ? kOnePieces : 1];
   pdl_launch_dependents();
   pdl_wait();
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = T::rank();
   const int gt = rank * kPlanThreads + threadIdx.x, lane = threadIdx.x & 31;
   const Rows& r = p.r;
-  int32_t* to = p.s.first;   // where each page goes
-  for (int i = gt; i < r.num_pages; i += kAll) {
-    p.new_refs[i] = __ldg(p.refs + i);
-    p.s.count[i] = 0;
+  int32_t* refs = R == 1 ? sm : p.new_refs;
+  int32_t* count = R == 1 ? sm + r.num_pages : p.s.count;
+  int32_t* to = R == 1 ? sm + 2 * r.num_pages : p.s.first;   // where each page goes
+  for (int i = gt; i < r.num_pages; i += T::kAll) {
+    refs[i] = __ldg(p.refs + i);
+    count[i] = 0;
     to[i] = i;
   }
+  int32_t* row_pages = R == 1 ? of_rows : p.s.row_pages;
   if (gt == 0) *p.used = 0;
-  check_rows(r, p.s, rank, p.status);
+  check_rows<R>(r, row_pages, rank, p.status);
   const long long pieces = (r.max_pages + kPiece - 1) / kPiece;
-  for (long long i = gt >> 5; i < pieces * r.batch; i += kAll / 32) {
+  for (long long i = gt >> 5; i < pieces * r.batch; i += T::kAll / 32) {
     const int b = (int)(i / pieces), at = (int)(i % pieces) * kPiece;
-    const int np = min(__ldcg(p.s.row_pages + b), at + kPiece);
+    const int np = min(T::get(row_pages + b), at + kPiece);
     for (int e = at + lane; e < np; e += 32)
-      atomicAdd(p.s.count + __ldg(r.table + (long long)b * r.max_pages + e), 1);
+      atomicAdd(count + __ldg(r.table + (long long)b * r.max_pages + e), 1);
   }
   int lo, hi;
-  my_share(r.num_pages, rank, &lo, &hi);
+  my_share<R>(r.num_pages, rank, &lo, &hi);
   int live = 0, total, n;
-  for (int i = lo; i < hi; ++i) live += __ldg(p.refs + i) != 0;
+  for (int i = lo; i < hi; ++i) live += T::get(refs + i) != 0;
   block_scan(live, red, &total);
-  before_rank(total, slot, rank, &n);   // a barrier: the counts are complete
+  before_rank<R>(total, slot, rank, &n);   // a barrier: the counts are complete
   int from = 0, hole = 0;
   for (int i = lo; i < hi; ++i) {
-    const int c = __ldg(p.refs + i);
-    from += i >= n && c != 0 && __ldcg(p.s.count + i) == c;
+    const int c = T::get(refs + i);
+    from += i >= n && c != 0 && T::get(count + i) == c;
     hole += i < n && c == 0;
   }
   int moves, holes;
   int fat = block_scan(from, red, &total);
-  fat += before_rank(total, slot + 1, rank, &moves);
+  fat += before_rank<R>(total, slot + 1, rank, &moves);
   int hat = block_scan(hole, red, &total);
-  hat += before_rank(total, slot + 2, rank, &holes);
+  hat += before_rank<R>(total, slot + 2, rank, &holes);
   for (int i = lo; i < hi; ++i) {
-    const int c = __ldg(p.refs + i);
-    if (i >= n && c != 0 && __ldcg(p.s.count + i) == c) p.s.src[fat++] = i;
+    const int c = T::get(refs + i);
+    if (i >= n && c != 0 && T::get(count + i) == c) p.s.src[fat++] = i;
     if (i < n && c == 0 && hat < moves) p.s.dst[hat++] = i;
   }
-  cluster_sync();
-  for (int j = gt; j < moves; j += kAll) {
-    const int a = __ldcg(p.s.src + j), b = __ldcg(p.s.dst + j);
+  T::sync();
+  for (int j = gt; j < moves; j += T::kAll) {
+    const int a = T::get(p.s.src + j), b = T::get(p.s.dst + j);
     to[a] = b;
-    p.new_refs[b] = __ldg(p.refs + a);
-    p.new_refs[a] = 0;
+    refs[b] = __ldg(p.refs + a);
+    refs[a] = 0;
     p.s.tokens[j] = 1 << r.shift;
   }
   if (gt == 0) *p.s.n_copies = moves;
-  cluster_sync();
-  for (long long i = gt >> 5; i < pieces * r.batch; i += kAll / 32) {
+  T::sync();
+  for (long long i = gt >> 5; i < pieces * r.batch; i += T::kAll / 32) {
     const int b = (int)(i / pieces), at = (int)(i % pieces) * kPiece;
-    const int np = min(__ldcg(p.s.row_pages + b), at + kPiece);
+    const int np = min(T::get(row_pages + b), at + kPiece);
     for (int e = at + lane; e < np; e += 32) {
       const long long o = (long long)b * r.max_pages + e;
-      p.new_table[o] = __ldcg(to + __ldg(r.table + o));
+      p.new_table[o] = T::get(to + __ldg(r.table + o));
     }
   }
   int most = 0;
   for (int i = lo; i < hi; ++i)
-    if (__ldcg(p.new_refs + i) != 0) most = i + 1;
+    if (T::get(refs + i) != 0) most = i + 1;
   most = __reduce_max_sync(kFull, most);
   if (lane == 0 && most > 0) atomicMax(p.used, most);
+  if constexpr (R == 1)
+    for (int i = threadIdx.x; i < r.num_pages; i += kPlanThreads) p.new_refs[i] = refs[i];
 }
 
 // ---------------------------------------------------------------- copies
@@ -471,20 +532,39 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     const uint4* a = reinterpret_cast<const uint4*>(codes + from * c.page_stride);
     uint4* b = reinterpret_cast<uint4*>(codes + to * c.page_stride);
     const int n = tokens * p.D / 16;
-#pragma unroll 4
-    for (int e = lane; e < n; e += 32) b[e] = a[e];
     const long long ph = (long long)from * p.H + h, qh = (long long)to * p.H + h;
-    if (is_v) {
-      if (lane == 0) c.vs[qh] = c.vs[ph];
-      if (c.weight != nullptr)
-        for (int e = lane; e < tokens; e += 32) c.weight[qh * p.P + e] = c.weight[ph * p.P + e];
-    } else {
-      if (lane == 0) c.ks[qh] = c.ks[ph];
-      if (c.ranges != nullptr)
-        for (int e = lane; e < p.D / 8; e += 32)
-          reinterpret_cast<uint4*>(c.ranges + qh * 2 * p.D)[e] =
-              reinterpret_cast<const uint4*>(c.ranges + ph * 2 * p.D)[e];
+    // what goes with the codes, on its way with the first of them
+    float step = 0.0f, weight[4] = {};
+    uint4 range = {};
+    const bool ranged = !is_v && c.ranges != nullptr && lane < p.D / 8;
+    const bool weighed = is_v && c.weight != nullptr;
+    if (lane == 0) step = (is_v ? c.vs : c.ks)[ph];
+    if (ranged) range = reinterpret_cast<const uint4*>(c.ranges + ph * 2 * p.D)[lane];
+    if (weighed)
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        if (lane + 32 * z < tokens) weight[z] = c.weight[ph * p.P + lane + 32 * z];
+    int e = lane;
+    for (; e + 96 < n; e += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) v[z] = a[e + 32 * z];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) b[e + 32 * z] = v[z];
     }
+    uint4 v[3];
+#pragma unroll
+    for (int z = 0; z < 3; ++z)
+      if (e + 32 * z < n) v[z] = a[e + 32 * z];
+#pragma unroll
+    for (int z = 0; z < 3; ++z)
+      if (e + 32 * z < n) b[e + 32 * z] = v[z];
+    if (lane == 0) (is_v ? c.vs : c.ks)[qh] = step;
+    if (ranged) reinterpret_cast<uint4*>(c.ranges + qh * 2 * p.D)[lane] = range;
+    if (weighed)
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        if (lane + 32 * z < tokens) c.weight[qh * p.P + lane + 32 * z] = weight[z];
   }
 }
 
@@ -537,6 +617,54 @@ w4_status copy(const CopyParams& p, long long most, w4_stream_t stream) {
   return launch(copy_kernel, dim3((unsigned)min(ctas, 152ll * 8)), kCopyThreads, 0, stream, p);
 }
 
+// The decision of a call: by one CTA where the pool and the table are small.
+template <typename P>
+w4_status decide(void (*one)(P), void (*team)(P), const P& p, long long rows, int max_pages, int num_pages,
+                 int words, w4_stream_t stream) {
+  const long long pieces = (max_pages + kPiece - 1) / kPiece;
+  if (num_pages <= kOnePages && rows * pieces <= kOnePieces) {
+    const size_t smem = (size_t)words * 4 * num_pages;
+    if (smem > 24 << 10) {   // once for each device and kernel: more shared memory than the default
+      static std::mutex mu;
+      static bool done[64] = {};
+      int dev = 0;
+      if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4_ERR_DEVICE;
+      std::lock_guard<std::mutex> lock(mu);
+      if (!done[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   words * 4 * kOnePages);
+        if (e != cudaSuccess) {
+          note_cuda_error(e);
+          (void)cudaGetLastError();
+          return W4_ERR_LAUNCH;
+        }
+        done[dev] = true;
+      }
+    }
+    return launch(one, dim3(1), kPlanThreads, smem, stream, p);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kRanks);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kRanks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, team, p);
+  if (e != cudaSuccess) {
+    note_cuda_error(e);
+    (void)cudaGetLastError();
+    return W4_ERR_LAUNCH;
+  }
+  return W4_OK;
+}
+
 }  // namespace
 }  // namespace kv8
 }  // namespace w4
@@ -584,7 +712,7 @@ extern "C" w4_status w4_kv8_fork(int32_t* new_table, int32_t* new_lens, int32_t*
   p.new_batch = new_batch;
   kv8::carve(workspace, most, num, &p.s);
   p.status = status_dev;
-  st = kv8::launch(kv8::fork_kernel, dim3(kv8::kRanks), kv8::kPlanThreads, 0, stream, p);
+  st = kv8::decide(kv8::fork_kernel<1>, kv8::fork_kernel<kv8::kRanks>, p, most, max_pages, num, 3, stream);
   if (st != W4_OK) return st;
   c.n_copies = p.s.n_copies;
   c.src = p.s.src;
@@ -612,7 +740,7 @@ extern "C" w4_status w4_kv8_reserve(int32_t* table, int32_t* lens, int32_t* refs
   p.grow = grow;
   kv8::carve(workspace, batch, num_pages, &p.s);
   p.status = status_dev;
-  return kv8::launch(kv8::reserve_kernel, dim3(kv8::kRanks), kv8::kPlanThreads, 0, stream, p);
+  return kv8::decide(kv8::reserve_kernel<1>, kv8::reserve_kernel<kv8::kRanks>, p, 1, 1, num_pages, 0, stream);
 }
 
 extern "C" w4_status w4_kv8_compact(int32_t* new_table, int32_t* new_refs, int32_t* used,
@@ -646,7 +774,7 @@ extern "C" w4_status w4_kv8_compact(int32_t* new_table, int32_t* new_refs, int32
   p.used = used;
   kv8::carve(workspace, batch, num, &p.s);
   p.status = status_dev;
-  st = kv8::launch(kv8::compact_kernel, dim3(kv8::kRanks), kv8::kPlanThreads, 0, stream, p);
+  st = kv8::decide(kv8::compact_kernel<1>, kv8::compact_kernel<kv8::kRanks>, p, batch, max_pages, num, 3, stream);
   if (st != W4_OK) return st;
   c.n_copies = p.s.n_copies;
   c.src = p.s.src;

@@ -6,24 +6,130 @@
 //   bit  19      occurs in the prompt
 //   bits 20..31  1 + index of its last bias
 // The CTA reads the row's bias list and history once, keeps what falls into its
-// tile, and then walks the tile: a token that no rule names and the mask
-// allows costs no global access, one that the mask forbids a store.  Every CTA
-// of a row sees the whole lists, so all of them find the same errors.
+// tile, and then walks the tile: a token that no rule names and the mask allows
+// costs no global access, one that the mask forbids a store.  The warps take
+// pieces of 256 tokens in turn, since the tokens that a history names are
+// neighbours in most vocabularies (the frequent ones come first).  Tiles start
+// on 16-byte boundaries of the row in memory, wherever the row does, so that
+// a lane's eight logits are whole vectors but for a row's ends.
+// Every CTA of a row sees the whole lists, so all of them find the same errors.
+// Chains of loads bound it (counts, lists, logits), so each link has many in
+// flight: a warp's mask words come before the lists, the lists eight at a time, a
+// warp's logits all together.
+#include <mutex>
+
 #include "kv8.cuh"
 
 namespace w4 {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr uint32_t kCount = (1u << 19) - 1, kPrompt = 1u << 19;
 constexpr int kBiasShift = 20;
+constexpr int kPiece = 256;   // tokens that a warp takes at a time, four times over
+constexpr unsigned kFull = 0xffffffffu;
 
 struct LogitParams {
   void* logits;
   long long stride;
-  int V, tile;
+  int V;
   w4_logit_rules r;
   int32_t* status;
+};
+
+// What a row's rules are, and logits under them.  The quotient by the repetition is a product
+// with its reciprocal, one rounding more, which the fused product with the frequency saves; far from
+// 1, where the reciprocal would be rounded harder, it is a division.
+struct RowRules {
+  float rep, inv, pres, freq;
+  bool divide;
+  const float* bias;
+
+  __device__ __forceinline__ float apply(float f, uint32_t w) const {
+    const uint32_t c = w & kCount;
+    if ((w & (kCount | kPrompt)) != 0)
+      f = f > 0.0f ? (divide ? __fdiv_rn(f, rep) : f * inv) : f * rep;
+    if (c != 0) f = fmaf(-freq, (float)c, f) - pres;
+    if ((w >> kBiasShift) != 0) f += __ldg(bias + (w >> kBiasShift) - 1);
+    return f;
+  }
+  // Eight at once, the same without branches but where one of them has a bias.
+  __device__ __forceinline__ void apply8(float (&f)[8], const uint32_t (&w)[8], uint32_t any) const {
+    if (divide) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = apply(f[i], w[i]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t c = w[i] & kCount;
+      const float g = f[i] * (f[i] > 0.0f ? inv : rep);
+      f[i] = (w[i] & (kCount | kPrompt)) != 0 ? g : f[i];
+      const float h = fmaf(-freq, (float)c, f[i]) - pres;
+      f[i] = c != 0 ? h : f[i];
+    }
+    if ((any >> kBiasShift) != 0)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((w[i] >> kBiasShift) != 0) f[i] += __ldg(bias + (w[i] >> kBiasShift) - 1);
+  }
+};
+
+// Eight neighbouring logits as they are stored.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    *reinterpret_cast<float4*>(p) = a;
+    *reinterpret_cast<float4*>(p + 4) = b;
+  }
+  __device__ __forceinline__ void forbid() { a = b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
+  __device__ __forceinline__ void adjust(const RowRules& r, const uint32_t (&w)[8], uint32_t any,
+                                         uint32_t allowed) {
+    float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (any != 0) r.apply8(f, w, any);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (allowed >> i) & 1 ? f[i] : -INFINITY;
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ void forbid() { v = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
+  __device__ __forceinline__ void adjust(const RowRules& r, const uint32_t (&w)[8], uint32_t any,
+                                         uint32_t allowed) {
+    uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    if (any != 0) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+      r.apply8(f, w, any);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {   // logits that no rule names keep their bits
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        const uint32_t keep = (w[2 * i] != 0 ? 0u : 0xFFFFu) | (w[2 * i + 1] != 0 ? 0u : 0xFFFF0000u);
+        u[i] = (u[i] & keep) | (*reinterpret_cast<const uint32_t*>(&b) & ~keep);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t off = (allowed >> (2 * i) & 1 ? 0u : 0xFFFFu) | (allowed >> (2 * i + 1) & 1 ? 0u : 0xFFFF0000u);
+      u[i] = (u[i] & ~off) | (0xFF80FF80u & off);
+    }
+    v = make_uint4(u[0], u[1], u[2], u[3]);
+  }
 };
 
 __device__ __forceinline__ float load(const float* p) { return *p; }
@@ -31,73 +137,189 @@ __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat1
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(LogitParams p) {
-  extern __shared__ uint32_t word[];
+// kThreads * 32 tokens a CTA; kAhead of a warp's four pieces have their logits loaded together.
+template <typename T, int kThreads, int kAhead, int kResident>
+__global__ void __launch_bounds__(kThreads, kResident) adjust_kernel(const __grid_constant__ LogitParams p) {
+  extern __shared__ uint32_t word[];   // 32 for each thread
   pdl_launch_dependents();
-  const int tid = threadIdx.x, row = blockIdx.y;
-  const int v0 = blockIdx.x * p.tile, n = min(p.tile, p.V - v0);
-  for (int i = tid; i < n; i += kThreads) word[i] = 0;
+  constexpr int threads = kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y;
+  T* const logits = static_cast<T*>(p.logits) + (long long)row * p.stride;
+  // logits before the row since a 16-byte boundary; the tile's tokens v0 .. v0 + tile - 1, of which
+  // some may lie outside the vocabulary
+  const int before = (int)(reinterpret_cast<uintptr_t>(logits) % 16 / sizeof(T));
+  const int tile = threads * 32, v0 = (int)blockIdx.x * tile - before;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(word)[tid + i * threads] = make_uint4(0, 0, 0, 0);
   pdl_wait();
   const w4_logit_rules& r = p.r;
   const int len = r.tokens != nullptr ? __ldg(r.lens + row) : 0;
   const int prompt = r.prompt != nullptr ? __ldg(r.prompt + row) : 0;
   const int nb = r.bias_ids == nullptr ? 0 : r.n_bias != nullptr ? __ldg(r.n_bias + row) : r.max_bias;
-  const float rep = r.repetition != nullptr ? __ldg(r.repetition + row) : 1.0f;
-  const float pres = r.presence != nullptr ? __ldg(r.presence + row) : 0.0f;
-  const float freq = r.frequency != nullptr ? __ldg(r.frequency + row) : 0.0f;
   const int mrow = r.mask == nullptr ? -1 : r.mask_rows != nullptr ? __ldg(r.mask_rows + row) : row;
+  RowRules rules;
+  rules.rep = r.repetition != nullptr ? __ldg(r.repetition + row) : 1.0f;
+  rules.pres = r.presence != nullptr ? __ldg(r.presence + row) : 0.0f;
+  rules.freq = r.frequency != nullptr ? __ldg(r.frequency + row) : 0.0f;
+  rules.inv = __frcp_rn(rules.rep);
+  rules.divide = !(rules.rep > 0x1p-100f && rules.rep < 0x1p100f);
+  rules.bias = r.bias + (long long)row * r.bias_stride;
   int bad = 0;
   if (len < 0 || len > r.max_tokens || prompt < 0 || prompt > len || nb < 0 || nb > r.max_bias ||
       mrow < -1 || (mrow >= r.num_masks && r.mask != nullptr))
     bad = W4_ERR_INDEX;
-  else if (!(rep > 0.0f) || isinf(rep) || !isfinite(pres) || !isfinite(freq))
+  else if (!(rules.rep > 0.0f) || isinf(rules.rep) || !isfinite(rules.pres) || !isfinite(rules.freq))
     bad = W4_ERR_VALUE;
   if (bad != 0) {
     if (tid == 0 && blockIdx.x == 0) report(p.status, bad);
     return;
   }
+  // 32 tokens' bits of the mask for each lane: tokens from v0 + at on
+  const int warps = threads >> 5;
+  uint32_t allow = kFull;
+  if (mrow >= 0) {
+    const int at = ((lane >> 3) * warps + warp) * kPiece + (lane & 7) * 32;
+    const uint32_t* mask = r.mask + (long long)mrow * r.mask_stride;
+    const int words = (p.V + 31) / 32, w = (v0 + at + 32) / 32 - 1;   // rounded down, from -1 on
+    const uint32_t lo = w >= 0 && w < words ? __ldg(mask + w) : 0u;
+    const uint32_t hi = before != 0 && w + 1 < words ? __ldg(mask + w + 1) : 0u;
+    allow = __funnelshift_r(lo, hi, v0 & 31);
+  }
   __syncthreads();
   bool out = false;
   const int32_t* bias_ids = r.bias_ids + (long long)row * r.bias_stride;
-  for (int i = tid; i < nb; i += kThreads) {
+  for (int i = tid; i < nb; i += threads) {
     const int v = __ldg(bias_ids + i);
     out |= v < 0 || v >= p.V;
-    if ((unsigned)(v - v0) < (unsigned)n) atomicMax(word + (v - v0), (uint32_t)(i + 1) << kBiasShift);
+    if ((unsigned)(v - v0) < (unsigned)tile) atomicMax(word + (v - v0), (uint32_t)(i + 1) << kBiasShift);
   }
   __syncthreads();
+  // the history, the prompt's tokens, then the others: vectors of four tokens between 16-byte
+  // boundaries, each token a subtraction, two comparisons and an atomic under a predicate
   const int32_t* tokens = r.tokens + (long long)row * r.token_stride;
-  for (int i = tid; i < len; i += kThreads) {
-    const int v = __ldg(tokens + i);
-    out |= v < 0 || v >= p.V;
-    if ((unsigned)(v - v0) < (unsigned)n) {
-      if (i >= prompt)
-        atomicAdd(word + (v - v0), 1u);
-      else
-        atomicOr(word + (v - v0), kPrompt);
+  uint32_t most = 0;   // a token below 0 is a large number
+  const uint32_t words = smem_addr(word);
+  auto walk = [&](int from, int to, auto note) {
+    auto take = [&](int v) {
+      most = max(most, (uint32_t)v);
+      note((uint32_t)(v - v0));
+    };
+    const int32_t* t = tokens + from;
+    const int n = to - from;
+    const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(t) & 15)) & 15) / 4);
+    const int vecs = (n - head) / 4, tail = head + 4 * vecs;
+    if (tid < head) take(__ldg(t + tid));
+    if (tid < n - tail) take(__ldg(t + tail + tid));
+    const int4* body = reinterpret_cast<const int4*>(t + head);
+    int i = tid;
+    for (; i + 3 * threads < vecs; i += 4 * threads) {
+      int4 v[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) v[z] = __ldg(body + i + z * threads);
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        take(v[z].x);
+        take(v[z].y);
+        take(v[z].z);
+        take(v[z].w);
+      }
     }
-  }
+#pragma unroll 3
+    for (; i < vecs; i += threads) {
+      const int4 v = __ldg(body + i);
+      take(v.x);
+      take(v.y);
+      take(v.z);
+      take(v.w);
+    }
+  };
+  walk(0, prompt, [&](uint32_t i) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.lt.u32 q, %0, %1;\n\t@q red.shared.or.b32 [%2], %3;\n\t}" ::"r"(i),
+                 "r"((uint32_t)tile), "r"(words + 4 * i), "r"(kPrompt)
+                 : "memory");
+  });
+  walk(prompt, len, [&](uint32_t i) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.lt.u32 q, %0, %1;\n\t@q red.shared.add.u32 [%2], 1;\n\t}" ::"r"(i),
+                 "r"((uint32_t)tile), "r"(words + 4 * i)
+                 : "memory");
+  });
+  out |= most >= (uint32_t)p.V;
   if (__syncthreads_or(out)) {
     if (tid == 0 && blockIdx.x == 0) report(p.status, W4_ERR_INDEX);
     return;
   }
-  T* x = static_cast<T*>(p.logits) + (long long)row * p.stride + v0;
-  const float* bias = r.bias + (long long)row * r.bias_stride;
-  const uint32_t* mask = r.mask + (long long)max(mrow, 0) * r.mask_stride + v0 / 32;
-  for (int i = tid; i < n; i += kThreads) {
-    const bool allowed = mrow < 0 || ((__ldg(mask + i / 32) >> (i & 31)) & 1);
-    const uint32_t w = word[i];
-    if (!allowed) {
-      store(x + i, -INFINITY);
-    } else if (w != 0) {
-      float f = load(x + i);
-      const uint32_t c = w & kCount;
-      if ((w & (kCount | kPrompt)) != 0) f = f > 0.0f ? __fdiv_rn(f, rep) : f * rep;
-      if (c != 0) f = f - __fmul_rn(freq, (float)c) - pres;
-      if ((w >> kBiasShift) != 0) f += __ldg(bias + (w >> kBiasShift) - 1);
-      store(x + i, f);
+#pragma unroll 1
+  for (int s0 = 0; s0 < 4; s0 += kAhead) {
+    Eight<T> f[kAhead];
+    uint32_t any[kAhead], may[kAhead];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const int at = ((s0 + s) * warps + warp) * kPiece + lane * 8, v = v0 + at;
+      may[s] = (__shfl_sync(kFull, allow, (s0 + s) * 8 + (lane >> 2)) >> (8 * (lane & 3))) & 0xFFu;
+      const uint4 a = *reinterpret_cast<const uint4*>(word + at), b = *reinterpret_cast<const uint4*>(word + at + 4);
+      any[s] = a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w;
+      if (may[s] != 0 && (may[s] != 0xFFu || any[s] != 0) && v >= 0 && v + 8 <= p.V) f[s].load(logits + v);
+    }
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const int at = ((s0 + s) * warps + warp) * kPiece + lane * 8, v = v0 + at;
+      if (may[s] == 0xFFu && any[s] == 0) continue;
+      if (v < 0 || v + 8 > p.V) {   // a row's ends
+        for (int i = max(0, -v); i < min(8, p.V - v); ++i) {
+          const uint32_t w = word[at + i];
+          if (!((may[s] >> i) & 1))
+            store(logits + v + i, -INFINITY);
+          else if (w != 0)
+            store(logits + v + i, rules.apply(load(logits + v + i), w));
+        }
+        continue;
+      }
+      if (may[s] == 0) {
+        f[s].forbid();
+      } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(word + at), b = *reinterpret_cast<const uint4*>(word + at + 4);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        f[s].adjust(rules, w, any[s], may[s]);
+      }
+      f[s].store(logits + v);
     }
   }
+}
+
+template <typename T, int kThreads, int kAhead, int kResident>
+w4_status run(const LogitParams& p, long long span, int rows, w4_stream_t stream) {
+  constexpr size_t smem = (size_t)kThreads * 128;
+  auto kern = adjust_kernel<T, kThreads, kAhead, kResident>;
+  if (smem > 48 << 10) {   // once for each device: more shared memory than the default
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4_ERR_DEVICE;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) {
+        note_cuda_error(e);
+        (void)cudaGetLastError();
+        return W4_ERR_LAUNCH;
+      }
+      done[dev] = true;
+    }
+  }
+  const dim3 grid((unsigned)((span - 1) / (32 * kThreads) + 1), (unsigned)rows);
+  return kv8::launch(kern, grid, kThreads, smem, stream, p);
+}
+
+// While the CTAs of 256 threads and 8192 tokens are few, each with all its logits on their way at
+// once; of more work than fits the GPU that way, CTAs of 512 threads and 16384 tokens, which read
+// the histories half as often and of which three are resident (24 rows of 262144 tokens under
+// masks 14.5 -> 13.3 us, 64 of 100277 with histories of 30000 23.3 -> 17.9 us; one row 4.8 us
+// against 5.9 us, 64 of 32000 7.9 against 10.8).
+template <typename T>
+w4_status run(const LogitParams& p, bool aligned, int rows, w4_stream_t stream) {
+  const long long span = (long long)p.V + (aligned ? 0 : 16 / (int)sizeof(T) - 1);
+  return ((span - 1) / 16384 + 1) * rows > 304 ? run<T, 512, 1, 3>(p, span, rows, stream)
+                                               : run<T, 256, 4, 4>(p, span, rows, stream);
 }
 
 }  // namespace
@@ -135,11 +357,9 @@ extern "C" w4_status w4_logits_adjust(void* logits, int logits_type, size_t row_
   p.logits = logits;
   p.stride = (long long)row_stride;
   p.V = V;
-  p.tile = 8192;
   p.status = status_dev;
-  const dim3 grid((unsigned)((V - 1) / p.tile + 1), (unsigned)rows);
-  const size_t smem = (size_t)p.tile * 4;
-  return logits_type == W4_TYPE_F32
-             ? kv8::launch(adjust_kernel<float>, grid, kThreads, smem, stream, p)
-             : kv8::launch(adjust_kernel<__nv_bfloat16>, grid, kThreads, smem, stream, p);
+  const int el = logits_type == W4_TYPE_F32 ? 4 : 2;
+  const bool aligned = !kv8::misaligned(logits, 16) && (rows == 1 || row_stride * el % 16 == 0);
+  return logits_type == W4_TYPE_F32 ? run<float>(p, aligned, rows, stream)
+                                    : run<__nv_bfloat16>(p, aligned, rows, stream);
 }

@@ -136,8 +136,9 @@ def test_compact_of_rows_out_of_bounds(cuda_lib, spoil):
     p.to_gpu().compact()
 
 
-def test_a_pool_of_many_pages(cuda_lib):
-    p = Pages(14, [700, 333, 90], H=1, D=64, spare=70001, optional=False).to_gpu(most_rows=8)
+@pytest.mark.parametrize("spare", [3000, 9001, 16300, 17000, 70001])
+def test_a_pool_of_many_pages(cuda_lib, spare):
+    p = Pages(14, [700, 333, 90], H=1, D=64, spare=spare, optional=False).to_gpu(most_rows=8)
     p.fork([0, 0, 1, 1, 2, 2])
     p.reserve()
     p.compact()
