@@ -25,6 +25,14 @@ __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A value that an earlier kernel may have written, read after pdl_wait().  The non-coherent loads
+// (__ldg) are not ordered by that wait: the compiler may take them to the kernel's start, where
+// a kernel before it that has let its dependents start is still running.
+template <typename T>
+__device__ __forceinline__ T load_in(const T* p) {
+  return *p;
+}
+
 // ---------------------------------------------------------------- L2 prefetch
 // Byte ranges to bring into L2 once a launch has requested its own tiles
 // (w4a16_gemv_prefetch_l2): normally the next call's weights, so that HBM

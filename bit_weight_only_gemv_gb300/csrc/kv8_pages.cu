@@ -23,7 +23,7 @@ namespace {
 constexpr int kRanks = 8, kPlanThreads = 1024;
 constexpr int kPiece = 128;
 constexpr int kOnePages = 16384;      // one CTA's largest pool: three counts a page in its shared memory,
-constexpr long long kOnePieces = 1024;   // and its most pieces of a table
+constexpr long long kOnePieces = 256;   // and its most pieces of a table
 constexpr int kRowsEach = W4_KV8_MAX_BATCH / kPlanThreads;   // rows a thread decides
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -135,6 +135,35 @@ struct Rows {
   }
 };
 
+// The pieces of a warp: every 32nd (or 256th) of the rows' pieces in turn, without a division each.
+struct Pieces {
+  int each, row, piece, row_step, piece_step;
+
+  __device__ __forceinline__ Pieces(int max_pages, int warp, int warps) {
+    each = (max_pages - 1) / kPiece + 1;
+    row = warp / each;
+    piece = warp % each;
+    row_step = warps / each;
+    piece_step = warps % each;
+  }
+  __device__ __forceinline__ void next() {
+    row += row_step;
+    piece += piece_step;
+    if (piece >= each) {
+      piece -= each;
+      ++row;
+    }
+  }
+};
+
+// A lane's entries of a piece, all on their way at once; kNone past the row's pages.
+constexpr int kNone = (int)0x80000000;
+__device__ __forceinline__ void load_piece(const Rows& r, int b, int first, int pages, int (&pg)[kPiece / 32]) {
+  const int32_t* row = r.table + (long long)b * r.max_pages + first;
+#pragma unroll
+  for (int z = 0; z < kPiece / 32; ++z) pg[z] = first + 32 * z < pages ? load_in(row + 32 * z) : kNone;
+}
+
 // Pages of every old row into row_pages, -1 where its length or one of its
 // entries breaks its bounds.  Ends in a barrier.
 template <int R>
@@ -143,21 +172,19 @@ __device__ __forceinline__ void check_rows(const Rows& r, int32_t* row_pages, ui
   using T = Team<R>;
   const int gt = rank * kPlanThreads + threadIdx.x;
   for (int b = gt; b < r.batch; b += T::kAll) {
-    const int np = r.pages(__ldg(r.lens + b));
+    const int np = r.pages(load_in(r.lens + b));
     row_pages[b] = np;
     if (np < 0) report(status, W4_ERR_INDEX);
   }
   T::sync();
   const int lane = threadIdx.x & 31;
-  const long long pieces = (r.max_pages + kPiece - 1) / kPiece;
-  for (long long i = gt >> 5; i < pieces * r.batch; i += T::kAll / 32) {
-    const int b = (int)(i / pieces), at = (int)(i % pieces) * kPiece;
-    const int np = min(r.pages(__ldg(r.lens + b)), at + kPiece);
+  for (Pieces i(r.max_pages, gt >> 5, T::kAll / 32); i.row < r.batch; i.next()) {
+    const int b = i.row, at = i.piece * kPiece;
+    int pg[kPiece / 32];
+    load_piece(r, b, at + lane, T::get(row_pages + b), pg);
     bool bad = false;
-    for (int e = at + lane; e < np; e += 32) {
-      const int pg = __ldg(r.table + (long long)b * r.max_pages + e);
-      bad |= pg < 0 || pg >= r.num_pages;
-    }
+#pragma unroll
+    for (int z = 0; z < kPiece / 32; ++z) bad |= pg[z] != kNone && (pg[z] < 0 || pg[z] >= r.num_pages);
     if (__any_sync(kFull, bad) && lane == 0) {
       row_pages[b] = -1;
       report(status, W4_ERR_INDEX);
@@ -197,28 +224,37 @@ __device__ __forceinline__ int before_rank(int mine, int* slot, uint32_t rank, i
   return before;
 }
 
-// The lowest `want` free pages into list, in order; false (everywhere) if there
-// are fewer.  Ends in a barrier: what every rank read before the call may be
-// written after it.
+// Free pages of this thread's share.
 template <int R>
-__device__ __forceinline__ bool take_free(const int32_t* refs, int num_pages, long long want, int32_t* list,
-                                          uint32_t rank, int* red, int* slot) {
+__device__ __forceinline__ int count_free(const int32_t* refs, int num_pages, uint32_t rank) {
+  int lo, hi, free = 0;
+  my_share<R>(num_pages, rank, &lo, &hi);
+#pragma unroll 4
+  for (int i = lo; i < hi; ++i) free += Team<R>::get(refs + i) == 0;
+  return free;
+}
+
+// The lowest `want` free pages into list, in order; false (everywhere) if there
+// are fewer.  free: count_free().  Ends in a barrier: what every rank read before
+// the call may be written after it.
+template <int R>
+__device__ __forceinline__ bool take_free(const int32_t* refs, int num_pages, long long want, int free,
+                                          int32_t* list, uint32_t rank, int* red, int* slot) {
   using T = Team<R>;
   if (want == 0) {
     T::sync();
     return true;
   }
-  int lo, hi;
-  my_share<R>(num_pages, rank, &lo, &hi);
-  int free = 0;
-  for (int i = lo; i < hi; ++i) free += T::get(refs + i) == 0;
   int total, all;
   int at = block_scan(free, red, &total);
   at += before_rank<R>(total, slot, rank, &all);
   const bool ok = all >= want;
-  if (ok && free > 0 && at < want)
+  if (ok && free > 0 && at < want) {
+    int lo, hi;
+    my_share<R>(num_pages, rank, &lo, &hi);
     for (int i = lo; i < hi && at < want; ++i)
       if (T::get(refs + i) == 0) list[at++] = i;
+  }
   T::sync();
   return ok;
 }
@@ -240,9 +276,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const __grid_cons
   using T = Team<R>;
   extern __shared__ int32_t sm[];
   __shared__ int red[33], slot;
-  // one CTA: what it knows of its rows (old ones' pages; new ones' lengths and last pages) and takes
-  __shared__ int32_t of_rows[4][R == 1 ? kOnePieces : 1];
-  pdl_launch_dependents();
+  // one CTA: what it knows of its rows (old ones' pages; new ones' lengths, last pages and parents)
+  // and the pages that it takes
+  __shared__ int32_t of_rows[5][R == 1 ? kOnePieces : 1];
   pdl_wait();
   const uint32_t rank = T::rank();
   const int gt = rank * kPlanThreads + threadIdx.x, lane = threadIdx.x & 31;
@@ -253,24 +289,26 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const __grid_cons
   int32_t* row_pages = R == 1 ? of_rows[0] : p.s.row_pages;
   int32_t* new_lens = R == 1 ? of_rows[1] : p.new_lens;
   int32_t* list = R == 1 ? of_rows[3] : p.s.dst;
+  const int32_t* parents = R == 1 ? of_rows[4] : p.parents;
+  if constexpr (R == 1)
+    for (int b = threadIdx.x; b < p.new_batch; b += kPlanThreads) of_rows[4][b] = load_in(p.parents + b);
   for (int i = gt; i < r.num_pages; i += T::kAll) {
-    refs[i] = __ldg(p.refs + i);
+    refs[i] = load_in(p.refs + i);
     count[i] = 0;
     first[i] = 0x7fffffff;
   }
   check_rows<R>(r, row_pages, rank, p.status);
   // the old rows' names go, the new rows' come
-  const long long pieces = (r.max_pages + kPiece - 1) / kPiece;
   const int rows = max(r.batch, p.new_batch);
-  for (long long i = gt >> 5; i < pieces * rows; i += T::kAll / 32) {
-    const int b = (int)(i / pieces), at = (int)(i % pieces) * kPiece;
-    const int par = b < p.new_batch ? __ldg(p.parents + b) : -1;
+  for (Pieces i(r.max_pages, gt >> 5, T::kAll / 32); i.row < rows; i.next()) {
+    const int b = i.row, at = i.piece * kPiece;
+    const int par = b < p.new_batch ? T::get(parents + b) : -1;
     const int had = b < r.batch ? T::get(row_pages + b) : 0;
     int np = 0, len = 0;
     bool ok = par >= -1 && par < r.batch;
     if (ok && par >= 0) {
       np = T::get(row_pages + par);
-      len = __ldg(r.lens + par);
+      len = load_in(r.lens + par);
       ok = np >= 0;
     }
     if (!ok) {
@@ -280,12 +318,17 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const __grid_cons
       }
       continue;
     }
-    if (par != b)
-      for (int e = at + lane; e < min(had, at + kPiece); e += 32)
-        atomicSub(refs + __ldg(r.table + (long long)b * r.max_pages + e), 1);
+    int mine[kPiece / 32], come[kPiece / 32];
+    load_piece(r, b, at + lane, par != b ? had : 0, mine);
+    load_piece(r, par, at + lane, np, come);
+#pragma unroll
+    for (int z = 0; z < kPiece / 32; ++z)
+      if (mine[z] != kNone) atomicSub(refs + mine[z], 1);
     if (b >= p.new_batch) continue;
-    for (int e = at + lane; e < min(np, at + kPiece); e += 32) {
-      const int pg = __ldg(r.table + (long long)par * r.max_pages + e);
+#pragma unroll
+    for (int z = 0; z < kPiece / 32; ++z) {
+      const int pg = come[z], e = at + lane + 32 * z;
+      if (pg == kNone) continue;
       p.new_table[(long long)b * r.max_pages + e] = pg;
       if (par != b) atomicAdd(refs + pg, 1);
       if (e == np - 1 && (len & ((1 << r.shift) - 1)) != 0) {   // a page to be written to
@@ -316,7 +359,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const __grid_cons
   }
   int want;
   int at = block_scan(mine, red, &want);
-  const bool ok = take_free<R>(refs, r.num_pages, want, list, rank, red, &slot);
+  const int free = want != 0 ? count_free<R>(refs, r.num_pages, rank) : 0;
+  const bool ok = take_free<R>(refs, r.num_pages, want, free, list, rank, red, &slot);
   if (rank != 0) return;
   if (threadIdx.x == 0) {
     *p.s.n_copies = ok ? want : 0;
@@ -360,9 +404,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) reserve_kernel(const __grid_c
   using T = Team<R>;
   __shared__ long long red64[33];
   __shared__ int red[33], slot;
-  pdl_launch_dependents();
   pdl_wait();
   const uint32_t rank = T::rank();
+  const int free = count_free<R>(p.refs, p.r.num_pages, rank);   // needed by most calls; beside the lengths
   int from[kRowsEach], to[kRowsEach], len[kRowsEach];
   long long mine = 0;
 #pragma unroll
@@ -370,8 +414,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) reserve_kernel(const __grid_c
     const int b = threadIdx.x * kRowsEach + z;
     from[z] = to[z] = len[z] = -1;
     if (b >= p.r.batch) continue;
-    const int now = __ldcg(p.lens + b);
-    const int g = p.grow != nullptr ? __ldg(p.grow + b) : now > 0;
+    const int now = load_in(p.lens + b);
+    const int g = p.grow != nullptr ? load_in(p.grow + b) : now > 0;
     const long long then = (long long)now + g;
     const int a = p.r.pages(now);
     const int e = g < 0 || then > 0x7fffffffll ? -1 : p.r.pages((int)then);
@@ -386,7 +430,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) reserve_kernel(const __grid_c
   }
   long long want;
   long long at = block_scan(mine, red64, &want);
-  const bool ok = take_free<R>(p.refs, p.r.num_pages, want, p.s.dst, rank, red, &slot);
+  const bool ok = take_free<R>(p.refs, p.r.num_pages, want, free, p.s.dst, rank, red, &slot);
   if (rank != 0) return;
   if (!ok) {
     if (threadIdx.x == 0) report(p.status, W4_ERR_STATE);
@@ -421,7 +465,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const __grid_c
   extern __shared__ int32_t sm[];
   __shared__ int red[33], slot[3];
   __shared__ int32_t of_rows[R == 1 ? kOnePieces : 1];
-  pdl_launch_dependents();
   pdl_wait();
   const uint32_t rank = T::rank();
   const int gt = rank * kPlanThreads + threadIdx.x, lane = threadIdx.x & 31;
@@ -430,19 +473,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const __grid_c
   int32_t* count = R == 1 ? sm + r.num_pages : p.s.count;
   int32_t* to = R == 1 ? sm + 2 * r.num_pages : p.s.first;   // where each page goes
   for (int i = gt; i < r.num_pages; i += T::kAll) {
-    refs[i] = __ldg(p.refs + i);
+    refs[i] = load_in(p.refs + i);
     count[i] = 0;
     to[i] = i;
   }
   int32_t* row_pages = R == 1 ? of_rows : p.s.row_pages;
   if (gt == 0) *p.used = 0;
   check_rows<R>(r, row_pages, rank, p.status);
-  const long long pieces = (r.max_pages + kPiece - 1) / kPiece;
-  for (long long i = gt >> 5; i < pieces * r.batch; i += T::kAll / 32) {
-    const int b = (int)(i / pieces), at = (int)(i % pieces) * kPiece;
-    const int np = min(T::get(row_pages + b), at + kPiece);
-    for (int e = at + lane; e < np; e += 32)
-      atomicAdd(count + __ldg(r.table + (long long)b * r.max_pages + e), 1);
+  for (Pieces i(r.max_pages, gt >> 5, T::kAll / 32); i.row < r.batch; i.next()) {
+    const int b = i.row, at = i.piece * kPiece;
+    int pg[kPiece / 32];
+    load_piece(r, b, at + lane, T::get(row_pages + b), pg);
+#pragma unroll
+    for (int z = 0; z < kPiece / 32; ++z)
+      if (pg[z] != kNone) atomicAdd(count + pg[z], 1);
   }
   int lo, hi;
   my_share<R>(r.num_pages, rank, &lo, &hi);
@@ -470,19 +514,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const __grid_c
   for (int j = gt; j < moves; j += T::kAll) {
     const int a = T::get(p.s.src + j), b = T::get(p.s.dst + j);
     to[a] = b;
-    refs[b] = __ldg(p.refs + a);
+    refs[b] = load_in(p.refs + a);
     refs[a] = 0;
     p.s.tokens[j] = 1 << r.shift;
   }
   if (gt == 0) *p.s.n_copies = moves;
   T::sync();
-  for (long long i = gt >> 5; i < pieces * r.batch; i += T::kAll / 32) {
-    const int b = (int)(i / pieces), at = (int)(i % pieces) * kPiece;
-    const int np = min(T::get(row_pages + b), at + kPiece);
-    for (int e = at + lane; e < np; e += 32) {
-      const long long o = (long long)b * r.max_pages + e;
-      p.new_table[o] = T::get(to + __ldg(r.table + o));
-    }
+  for (Pieces i(r.max_pages, gt >> 5, T::kAll / 32); i.row < r.batch; i.next()) {
+    const int b = i.row, at = i.piece * kPiece;
+    int pg[kPiece / 32];
+    load_piece(r, b, at + lane, T::get(row_pages + b), pg);
+#pragma unroll
+    for (int z = 0; z < kPiece / 32; ++z)
+      if (pg[z] != kNone)
+        p.new_table[(long long)b * r.max_pages + at + lane + 32 * z] = T::get(to + pg[z]);
   }
   int most = 0;
   for (int i = lo; i < hi; ++i)
@@ -515,19 +560,28 @@ struct CopyParams {
 };
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
-  pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warps = gridDim.x * (kCopyThreads / 32);
-  const long long items = (long long)__ldg(p.n_copies) * p.n * p.H * 2;
-  for (long long i = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); i < items;
-       i += warps) {
-    const bool is_v = i & 1;
-    long long j = i >> 1;
-    const int h = (int)(j % p.H);
-    j /= p.H;
-    const One& c = p.c[j % p.n];
-    j /= p.n;
-    const int from = __ldg(p.src + j), to = __ldg(p.dst + j), tokens = __ldg(p.tokens + j);
+  const int lane = threadIdx.x & 31, copies = load_in(p.n_copies);
+  // the warp's items: (copy, cache, head, keys or values) in turn, without a division each
+  const int warps = gridDim.x * (kCopyThreads / 32), first = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
+  int kv = first & 1, h = (first >> 1) % p.H, l = (first >> 1) / p.H % p.n, j = (first >> 1) / p.H / p.n;
+  const int kv_step = warps & 1, h_step = (warps >> 1) % p.H, l_step = (warps >> 1) / p.H % p.n,
+            j_step = (warps >> 1) / p.H / p.n;
+  auto next = [&]() {
+    kv += kv_step;
+    h += h_step + (kv >> 1);
+    kv &= 1;
+    int carry = h >= p.H;
+    h -= carry ? p.H : 0;
+    l += l_step + carry;
+    carry = l >= p.n;
+    l -= carry ? p.n : 0;
+    j += j_step + carry;
+  };
+  for (; j < copies; next()) {
+    const bool is_v = kv != 0;
+    const One& c = p.c[l];
+    const int from = load_in(p.src + j), to = load_in(p.dst + j), tokens = load_in(p.tokens + j);
     uint8_t* codes = (is_v ? c.vc : c.kc) + h * c.head_stride;
     const uint4* a = reinterpret_cast<const uint4*>(codes + from * c.page_stride);
     uint4* b = reinterpret_cast<uint4*>(codes + to * c.page_stride);
@@ -604,7 +658,8 @@ w4_status check_table(const int32_t* table, const int32_t* lens, const int32_t* 
   if (table == nullptr || lens == nullptr || refs == nullptr || batch < 1 || max_pages < 1 ||
       num_pages < 1)
     return W4_ERR_ARG;
-  if (batch > W4_KV8_MAX_BATCH || (P != 16 && P != 32 && P != 64 && P != 128)) return W4_ERR_SHAPE;
+  if (batch > W4_KV8_MAX_BATCH || max_pages > (1 << 26) || (P != 16 && P != 32 && P != 64 && P != 128))
+    return W4_ERR_SHAPE;
   if (misaligned(table, 4) || misaligned(lens, 4) || misaligned(refs, 4)) return W4_ERR_ALIGN;
   return W4_OK;
 }

@@ -49,7 +49,7 @@ struct RowRules {
     if ((w & (kCount | kPrompt)) != 0)
       f = f > 0.0f ? (divide ? __fdiv_rn(f, rep) : f * inv) : f * rep;
     if (c != 0) f = fmaf(-freq, (float)c, f) - pres;
-    if ((w >> kBiasShift) != 0) f += __ldg(bias + (w >> kBiasShift) - 1);
+    if ((w >> kBiasShift) != 0) f += load_in(bias + (w >> kBiasShift) - 1);
     return f;
   }
   // Eight at once, the same without branches but where one of them has a bias.
@@ -70,7 +70,7 @@ struct RowRules {
     if ((any >> kBiasShift) != 0)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if ((w[i] >> kBiasShift) != 0) f[i] += __ldg(bias + (w[i] >> kBiasShift) - 1);
+        if ((w[i] >> kBiasShift) != 0) f[i] += load_in(bias + (w[i] >> kBiasShift) - 1);
   }
 };
 
@@ -141,7 +141,6 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2
 template <typename T, int kThreads, int kAhead, int kResident>
 __global__ void __launch_bounds__(kThreads, kResident) adjust_kernel(const __grid_constant__ LogitParams p) {
   extern __shared__ uint32_t word[];   // 32 for each thread
-  pdl_launch_dependents();
   constexpr int threads = kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y;
   T* const logits = static_cast<T*>(p.logits) + (long long)row * p.stride;
@@ -153,14 +152,14 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_kernel(const __gri
   for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(word)[tid + i * threads] = make_uint4(0, 0, 0, 0);
   pdl_wait();
   const w4_logit_rules& r = p.r;
-  const int len = r.tokens != nullptr ? __ldg(r.lens + row) : 0;
-  const int prompt = r.prompt != nullptr ? __ldg(r.prompt + row) : 0;
-  const int nb = r.bias_ids == nullptr ? 0 : r.n_bias != nullptr ? __ldg(r.n_bias + row) : r.max_bias;
-  const int mrow = r.mask == nullptr ? -1 : r.mask_rows != nullptr ? __ldg(r.mask_rows + row) : row;
+  const int len = r.tokens != nullptr ? load_in(r.lens + row) : 0;
+  const int prompt = r.prompt != nullptr ? load_in(r.prompt + row) : 0;
+  const int nb = r.bias_ids == nullptr ? 0 : r.n_bias != nullptr ? load_in(r.n_bias + row) : r.max_bias;
+  const int mrow = r.mask == nullptr ? -1 : r.mask_rows != nullptr ? load_in(r.mask_rows + row) : row;
   RowRules rules;
-  rules.rep = r.repetition != nullptr ? __ldg(r.repetition + row) : 1.0f;
-  rules.pres = r.presence != nullptr ? __ldg(r.presence + row) : 0.0f;
-  rules.freq = r.frequency != nullptr ? __ldg(r.frequency + row) : 0.0f;
+  rules.rep = r.repetition != nullptr ? load_in(r.repetition + row) : 1.0f;
+  rules.pres = r.presence != nullptr ? load_in(r.presence + row) : 0.0f;
+  rules.freq = r.frequency != nullptr ? load_in(r.frequency + row) : 0.0f;
   rules.inv = __frcp_rn(rules.rep);
   rules.divide = !(rules.rep > 0x1p-100f && rules.rep < 0x1p100f);
   rules.bias = r.bias + (long long)row * r.bias_stride;
@@ -181,15 +180,15 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_kernel(const __gri
     const int at = ((lane >> 3) * warps + warp) * kPiece + (lane & 7) * 32;
     const uint32_t* mask = r.mask + (long long)mrow * r.mask_stride;
     const int words = (p.V + 31) / 32, w = (v0 + at + 32) / 32 - 1;   // rounded down, from -1 on
-    const uint32_t lo = w >= 0 && w < words ? __ldg(mask + w) : 0u;
-    const uint32_t hi = before != 0 && w + 1 < words ? __ldg(mask + w + 1) : 0u;
+    const uint32_t lo = w >= 0 && w < words ? load_in(mask + w) : 0u;
+    const uint32_t hi = before != 0 && w + 1 < words ? load_in(mask + w + 1) : 0u;
     allow = __funnelshift_r(lo, hi, v0 & 31);
   }
   __syncthreads();
   bool out = false;
   const int32_t* bias_ids = r.bias_ids + (long long)row * r.bias_stride;
   for (int i = tid; i < nb; i += threads) {
-    const int v = __ldg(bias_ids + i);
+    const int v = load_in(bias_ids + i);
     out |= v < 0 || v >= p.V;
     if ((unsigned)(v - v0) < (unsigned)tile) atomicMax(word + (v - v0), (uint32_t)(i + 1) << kBiasShift);
   }
@@ -208,14 +207,14 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_kernel(const __gri
     const int n = to - from;
     const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(t) & 15)) & 15) / 4);
     const int vecs = (n - head) / 4, tail = head + 4 * vecs;
-    if (tid < head) take(__ldg(t + tid));
-    if (tid < n - tail) take(__ldg(t + tail + tid));
+    if (tid < head) take(load_in(t + tid));
+    if (tid < n - tail) take(load_in(t + tail + tid));
     const int4* body = reinterpret_cast<const int4*>(t + head);
     int i = tid;
     for (; i + 3 * threads < vecs; i += 4 * threads) {
       int4 v[4];
 #pragma unroll
-      for (int z = 0; z < 4; ++z) v[z] = __ldg(body + i + z * threads);
+      for (int z = 0; z < 4; ++z) v[z] = load_in(body + i + z * threads);
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
         take(v[z].x);
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_kernel(const __gri
     }
 #pragma unroll 3
     for (; i < vecs; i += threads) {
-      const int4 v = __ldg(body + i);
+      const int4 v = load_in(body + i);
       take(v.x);
       take(v.y);
       take(v.z);

@@ -69,8 +69,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 __device__ __forceinline__ float logit(const RouteParams& p, long long row, int e) {
   const long long i = row * p.stride + e;
-  return p.f32 ? __ldg(static_cast<const float*>(p.logits) + i)
-               : bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(p.logits) + i));
+  return p.f32 ? load_in(static_cast<const float*>(p.logits) + i)
+               : bf16_bits_to_float(load_in(static_cast<const uint16_t*>(p.logits) + i));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -99,7 +99,7 @@ __device__ __noinline__ int refine(const RouteParams& p, long long row, double* 
   }
   for (int e = lane; e < p.E; e += 32) {
     const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)logit(p, row, e))) : sm[e] / z;
-    sm[e] = s + (p.bias != nullptr ? (double)__ldg(p.bias + e) : 0.0);
+    sm[e] = s + (p.bias != nullptr ? (double)load_in(p.bias + e) : 0.0);
   }
   __syncwarp();
   uint32_t in = kFull;   // chosen groups
@@ -165,7 +165,7 @@ __device__ __forceinline__ double exact_score(const RouteParams& p, long long ro
                                               double z) {
   const double x = (double)logit(p, row, e);
   const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top) / z;
-  return p.bias != nullptr ? s + (double)__ldg(p.bias + e) : s;
+  return p.bias != nullptr ? s + (double)load_in(p.bias + e) : s;
 }
 
 // Order of the first `cnt` candidates by 64-bit scores (without a bias by the logits), equal ones
@@ -258,7 +258,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel
   constexpr int kBits = 32 - kPlace < 23 ? 32 - kPlace : 23;    // bits of a fixed-point score
   constexpr float kOne = (float)(1 << kBits), kBase = 8388608.0f;   // 2^23: the unit is 1
   constexpr bool kSorted = V <= 16;
-  pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> p.shift, l = lane & ((1 << p.shift) - 1);
@@ -275,7 +274,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel
     float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      b[i] = i < n ? __ldg(p.bias + e0 + i) : 0.0f;
+      b[i] = i < n ? load_in(p.bias + e0 + i) : 0.0f;
       if (i < n) {
         bad_bias |= !isfinite(b[i]);
         lo = fminf(lo, b[i]);
@@ -301,7 +300,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel
               static_cast<const float*>(p.logits) + row * p.stride + e0);
 #pragma unroll
           for (int i = 0; i < V / 4; ++i) {
-            const float4 w = n > 0 ? __ldg(src + i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            const float4 w = n > 0 ? load_in(src + i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             x[4 * i] = w.x;
             x[4 * i + 1] = w.y;
             x[4 * i + 2] = w.z;
@@ -312,7 +311,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel
               static_cast<const uint16_t*>(p.logits) + row * p.stride + e0);
 #pragma unroll
           for (int i = 0; i < V / 4; ++i) {
-            const uint2 w = n > 0 ? __ldg(src + i) : make_uint2(0xFF80FF80u, 0xFF80FF80u);
+            const uint2 w = n > 0 ? load_in(src + i) : make_uint2(0xFF80FF80u, 0xFF80FF80u);
             x[4 * i] = __uint_as_float(w.x << 16);
             x[4 * i + 1] = __uint_as_float(w.x & 0xFFFF0000u);
             x[4 * i + 2] = __uint_as_float(w.y << 16);
@@ -483,7 +482,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel
     float xl = lane < cnt ? logit(p, row, e) : -INFINITY;
     if (fixed) {
       // equal inputs are equal scores at any width, and in order already
-      const float bl = biased && lane < cnt ? __ldg(p.bias + e) : 0.0f;
+      const float bl = biased && lane < cnt ? load_in(p.bias + e) : 0.0f;
       const uint32_t up = __shfl_up_sync(kFull, my, 1);
       const float xu = __shfl_up_sync(kFull, xl, 1), bu = __shfl_up_sync(kFull, bl, 1);
       const bool unsure = lane > 0 && lane < cnt && (up >> kPlace) - (my >> kPlace) < near &&
@@ -531,7 +530,6 @@ struct CombineParams {
 
 template <int VEC>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineParams p) {
-  pdl_launch_dependents();
   pdl_wait();
   const long long row = blockIdx.x / p.chunks;
   const int chunk = blockIdx.x % p.chunks;
@@ -540,7 +538,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineParams 
   if (p.ids != nullptr) {
     bool ok = true;
     for (int j = 0; j < p.k; ++j) {
-      const int id = __ldg(p.ids + row * p.k + j);
+      const int id = load_in(p.ids + row * p.k + j);
       ok = ok && id >= 0 && id < p.num_experts;
     }
     if (!ok) {
@@ -571,12 +569,12 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineParams 
       uint4 v[8];
 #pragma unroll
       for (int z = 0; z < 8; ++z)
-        v[z] = __ldg(reinterpret_cast<const uint4*>(y + (long long)(j + z) * p.N));
+        v[z] = load_in(reinterpret_cast<const uint4*>(y + (long long)(j + z) * p.N));
 #pragma unroll
       for (int z = 0; z < 8; ++z) {
         float f[8];
         spread(v[z], f);
-        const float w = __ldg(wt + j + z);
+        const float w = load_in(wt + j + z);
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
       }
@@ -584,8 +582,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineParams 
 #pragma unroll 2
     for (; j < p.k; ++j) {
       float f[8];
-      spread(__ldg(reinterpret_cast<const uint4*>(y + (long long)j * p.N)), f);
-      const float w = __ldg(wt + j);
+      spread(load_in(reinterpret_cast<const uint4*>(y + (long long)j * p.N)), f);
+      const float w = load_in(wt + j);
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
     }
@@ -600,7 +598,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineParams 
     acc[0] = p.add != nullptr ? __bfloat162float(p.add[row * p.N + n]) : 0.0f;
 #pragma unroll 8
     for (int j = 0; j < p.k; ++j)
-      acc[0] = fmaf(__ldg(wt + j), __bfloat162float(__ldg(y + (long long)j * p.N)), acc[0]);
+      acc[0] = fmaf(load_in(wt + j), __bfloat162float(load_in(y + (long long)j * p.N)), acc[0]);
     p.out[row * p.N + n] = __float2bfloat16_rn(acc[0]);
   }
 }

@@ -1031,7 +1031,8 @@ w4_status w4_logits_adjust(void *logits, int logits_type, size_t row_stride, int
  * ceil(lens[b] / page_tokens) entries), and by whatever else keeps it; a page
  * with 0 is free.  The calls hold to the conventions of w4_kv8_*.  They move
  * pages of several caches at once: a model's layers, with one table for all.
- * Pages are taken from the lowest free number on, in order of rows.
+ * Pages are taken from the lowest free number on, in order of rows.  Tables have
+ * at most W4_KV8_MAX_BATCH rows of 2^26 entries.
  *
  * workspace  w4_kv8_pages_workspace_bytes(batch, num_pages) bytes with the
  *            largest batch of the calls, 16-byte aligned; its first

@@ -187,3 +187,14 @@ def test_calls_in_a_graph(cuda_lib):
                                              (t.cpu().numpy() for t in old))), copies)
             for name, t in zip(want, d.tensors):
                 assert np.array_equal(t.cpu().numpy(), want[name])
+
+
+def test_copies_follow_the_decision_of_their_call(cuda_lib):
+    """What the copying kernel reads is what the deciding one wrote, not what the workspace held before:
+    many times, since a load before its time would not show every time."""
+    for rep in range(60):
+        lens, parents = ([0, 5], [0, 0, 1, 1]) if rep % 2 else ([1, 16, 17, 31], [1, 1, 3, 3])
+        p = Pages(rep, lens, layers=2, spare=12).to_gpu(most_rows=4)
+        if rep % 3 == 0:
+            p.ws[4096:] = 1
+        assert p.fork(parents)[3]
