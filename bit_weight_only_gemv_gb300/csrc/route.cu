@@ -34,6 +34,7 @@ struct RouteParams {
   long long stride;
   int rows, E, k, G, size, top_groups, best;   // size: experts of a group
   int shift, each;   // lanes of a group: 1 << shift; experts of a lane
+  int shift8;        // the same of eight lanes
   bool sigmoid, renorm, f32, vec;
   float scale;
   int32_t* status;
@@ -251,15 +252,15 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[V]) {
     }
 }
 
+// Rows first, first + step, ... below end, one after another; sm: this warp's room for 64-bit scores.
 template <int V, bool F32>
-__global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel(const __grid_constant__ RouteParams p) {
-  extern __shared__ double refine_sm[];
+__device__ __forceinline__ void route_rows(const RouteParams& p, long long first, long long step,
+                                           long long end, double* sm) {
   constexpr int kPlace = V <= 8 ? 8 : 5 + Log2<V>::value;       // bits of a place
   constexpr int kBits = 32 - kPlace < 23 ? 32 - kPlace : 23;    // bits of a fixed-point score
   constexpr float kOne = (float)(1 << kBits), kBase = 8388608.0f;   // 2^23: the unit is 1
   constexpr bool kSorted = V <= 16;
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const int g = lane >> p.shift, l = lane & ((1 << p.shift) - 1);
   const int e0 = g * p.size + l * p.each;
   const int n = g < p.G ? min(max(p.size - l * p.each, 0), p.each) : 0;   // experts of this lane
@@ -290,8 +291,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel
   }
   const bool wide = !(range < 1e30f);   // no fixed point holds it
   const float unit = __fdividef(kOne - 8.0f, range);
-  for (long long row = (long long)blockIdx.x * kRouteWarps + warp; row < p.rows;
-       row += (long long)gridDim.x * kRouteWarps) {
+  for (long long row = first; row < end; row += step) {
     float x[V];
     if (p.vec) {   // whole aligned vectors of four experts
       if constexpr (V >= 4) {
@@ -487,7 +487,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel
       const float xu = __shfl_up_sync(kFull, xl, 1), bu = __shfl_up_sync(kFull, bl, 1);
       const bool unsure = lane > 0 && lane < cnt && (up >> kPlace) - (my >> kPlace) < near &&
                           !(xu == xl && bu == bl);
-      double* sm = refine_sm + warp * (p.E > 32 ? p.E : 32);
       if (close || __any_sync(kFull, unsure)) {
         e = close ? refine(p, row, sm) : exact_order(p, row, e, cnt, top, reinterpret_cast<int*>(sm));
         xl = lane < p.k ? logit(p, row, e) : -INFINITY;
@@ -512,6 +511,276 @@ __global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel
       p.ids[row * p.k + lane] = e;
       p.weights[row * p.k + lane] = w;
     }
+  }
+}
+
+template <int V, bool F32>
+__global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 1) route_kernel(const __grid_constant__ RouteParams p) {
+  extern __shared__ double refine_sm[];
+  pdl_wait();
+  const int warp = threadIdx.x >> 5;
+  route_rows<V, F32>(p, (long long)blockIdx.x * kRouteWarps + warp, (long long)gridDim.x * kRouteWarps, p.rows,
+                     refine_sm + warp * (p.E > 32 ? p.E : 32));
+}
+
+template <int V, bool F32>
+__device__ __noinline__ void route_again(const RouteParams& p, long long row, double* sm) {
+  route_rows<V, F32>(p, row, 1, row + 1, sm);
+}
+
+// Four tokens a warp, eight lanes each with V neighbouring experts: what a warp does for one token
+// it does here for four.  A lane keeps its best eight words, sorted.  Whatever this cannot settle (a
+// NaN, scores too near each other, a lane whose eight were all taken) is left to route_rows.
+constexpr int kManyWarps = 4;
+constexpr int kManyRows = 4096;   // tokens from which on it is the faster one
+
+template <int V, bool F32>
+__global__ void __launch_bounds__(32 * kManyWarps) route_many_kernel(const __grid_constant__ RouteParams p) {
+  extern __shared__ double refine_sm[];
+  __shared__ float4 bias_sm[8 * V / 4];   // biases above the least: vector i of lane l at 8 i + l
+  __shared__ float ends_sm[2 * kManyWarps];
+  constexpr float kOne = 8388608.0f, kBase = 8388608.0f;   // 23 bits of a score, 8 of a place
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7;
+  const int g = l >> p.shift8;
+  const bool biased = p.bias != nullptr, groups = p.G > 1;
+  const bool sums = biased || (groups && p.best == 2);
+  const bool fixed = biased || F32;
+  float range = 1.0f;
+  bool again = false;
+  if (biased) {
+    float lo = INFINITY, hi = -INFINITY;
+    bool bad = false;
+    for (int e = threadIdx.x; e < 8 * V; e += 32 * kManyWarps) {
+      const float v = load_in(p.bias + e);
+      bad |= !isfinite(v);
+      lo = fminf(lo, v);
+      hi = fmaxf(hi, v);
+    }
+    lo = warp_min_f(lo);
+    hi = warp_max_f(hi);
+    if (lane == 0) {
+      ends_sm[warp] = lo;
+      ends_sm[kManyWarps + warp] = hi;
+    }
+    again = __syncthreads_or(bad);
+    for (int i = 0; i < kManyWarps; ++i) {
+      lo = fminf(lo, ends_sm[i]);
+      hi = fmaxf(hi, ends_sm[kManyWarps + i]);
+    }
+    for (int e = threadIdx.x; e < 8 * V; e += 32 * kManyWarps)
+      reinterpret_cast<float*>(bias_sm + (e % V / 4 * 8 + e / V))[e % 4] = load_in(p.bias + e) - lo;
+    __syncthreads();
+    range = 1.0f + (hi - lo);
+    again |= !(range < 1e30f);
+  }
+  const float unit = __fdividef(kOne - 8.0f, range);
+  const long long steps = ((long long)p.rows + 3) / 4;
+  for (long long r4 = (long long)blockIdx.x * kManyWarps + warp; r4 < steps; r4 += (long long)gridDim.x * kManyWarps) {
+    const long long row = min(4 * r4 + (lane >> 3), (long long)p.rows - 1);
+    float x[V];
+    if constexpr (F32) {
+      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + row * p.stride + l * V);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const float4 w = load_in(src + i);
+        x[4 * i] = w.x;
+        x[4 * i + 1] = w.y;
+        x[4 * i + 2] = w.z;
+        x[4 * i + 3] = w.w;
+      }
+    } else {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.logits) + row * p.stride + l * V);
+#pragma unroll
+      for (int i = 0; i < V / 8; ++i) {
+        const uint4 w = load_in(src + i);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          x[8 * i + 2 * z] = __uint_as_float(u[z] << 16);
+          x[8 * i + 2 * z + 1] = __uint_as_float(u[z] & 0xFFFF0000u);
+        }
+      }
+    }
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) top = max_nan(top, x[i]);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, o));
+    bool redo = again || isnan(top) || (!p.sigmoid && isinf(top));
+    float z = 1.0f, tol = 0.0f, f1 = -INFINITY, f2 = -INFINITY;
+    uint32_t key[V];
+    if (sums || (!p.renorm && !p.sigmoid)) {   // errors as in route_rows
+      float scale = 1.0f;
+      if (p.sigmoid) {
+        tol = 0x1p-20f + 0x1p-22f * range;
+      } else {
+        float part[4] = {};   // summed in the order of 32 lanes, a quarter of this one's experts each
+#pragma unroll
+        for (int i = 0; i < V; ++i) part[i / (V / 4)] += __expf(x[i] - top);
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) part[q] += __shfl_xor_sync(kFull, part[q], o);
+        z = (part[0] + part[2]) + (part[1] + part[3]);
+        scale = __fdividef(1.0f, z);
+        tol = 0x1p-17f * scale + 0x1p-22f * range;
+      }
+      if (sums) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+          float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (biased) b = bias_sm[8 * i + l];
+          const float add[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int at = 4 * i + y;
+            const float s = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x[at])) : __expf(x[at] - top) * scale;
+            const float c = s + add[y];
+            f2 = fmaxf(f2, fminf(f1, c));
+            f1 = fmaxf(f1, c);
+            key[at] = (__float_as_uint(fmaf(c, unit, kBase + 4.0f)) << 8) | (255 - (l * V + at));
+          }
+        }
+      }
+    }
+    if (!biased) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (F32) {
+          const float f = fmaxf(fmaf(x[i] - top, kOne / 32.0f, kBase + (kOne - 2.0f)), kBase + 1.0f);
+          key[i] = (__float_as_uint(f) << 8) | (255 - (l * V + i));
+        } else {
+          key[i] = (order_key(x[i]) & 0xFFFF0000u) | (0xFFFFu - (l * V + i));
+        }
+      }
+    }
+    // the lane's best eight, sorted: eights sorted, and of two the better half sorted again
+#pragma unroll
+    for (int q = 0; q < V / 8; ++q) sort_down<8>(reinterpret_cast<uint32_t(&)[8]>(key[8 * q]));
+#pragma unroll
+    for (int q = 1; q < V / 8; ++q) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) key[i] = max(key[i], key[8 * q + 7 - i]);
+#pragma unroll
+      for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((i & d) == 0) {
+            const uint32_t a = key[i], c = key[i + d];
+            key[i] = max(a, c);
+            key[i + d] = min(a, c);
+          }
+    }
+    if (groups) {
+      float gs;
+      if (sums) {
+        for (int o = 1; o < (1 << p.shift8); o <<= 1) {
+          const float o1 = __shfl_xor_sync(kFull, f1, o), o2 = __shfl_xor_sync(kFull, f2, o);
+          f2 = fmaxf(fmaxf(f2, o2), fminf(f1, o1));
+          f1 = fmaxf(f1, o1);
+        }
+        gs = p.best == 2 ? f1 + f2 : f1;
+      } else {
+        gs = x[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) gs = fmaxf(gs, x[i]);
+        for (int o = 1; o < (1 << p.shift8); o <<= 1) gs = fmaxf(gs, __shfl_xor_sync(kFull, gs, o));
+      }
+      int rank = 0;
+      float nearest = INFINITY;
+      for (int i = 0; i < p.G; ++i) {
+        const float o = __shfl_sync(kFull, gs, (lane & 24) | (i << p.shift8));
+        rank += o > gs || (o == gs && i < g);
+        nearest = i == g ? nearest : fminf(nearest, fabsf(o - gs));
+      }
+      // a group at the border and another too near it
+      redo |= sums && (rank == p.top_groups || rank == p.top_groups - 1) && nearest < 3.0f * tol;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) key[i] = rank < p.top_groups ? key[i] : 0u;
+    }
+    uint32_t my = 0, m = 0;
+    int taken = 0;
+    auto pop = [&]() {
+      m = key[0];
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+      const bool hit = key[0] == m;
+      taken += hit;
+#pragma unroll
+      for (int i = 0; i < 7; ++i) key[i] = hit ? key[i + 1] : key[i];
+      key[7] = hit ? 0u : key[7];
+    };
+    for (int j = 0; j < p.k; ++j) {
+      pop();
+      my = l == j ? m : my;
+    }
+    const uint32_t mask = fixed ? 255u : 0xFFFFu, place = mask - (my & mask);
+    int e = min((int)place, p.E - 1);   // (none left: redone)
+    const bool has = l < p.k;
+    float xl = has ? logit(p, row, e) : -INFINITY;
+    if (fixed) {
+      const uint32_t near = 3 + (biased ? (uint32_t)fminf(tol * unit, kOne) : 1u);
+      const uint32_t kth = m;
+      pop();
+      redo |= m != 0 && (kth >> 8) - (m >> 8) < near;
+      const float bl = biased && has ? load_in(p.bias + e) : 0.0f;
+      const uint32_t up = __shfl_up_sync(kFull, my, 1, 8);
+      const float xu = __shfl_up_sync(kFull, xl, 1, 8), bu = __shfl_up_sync(kFull, bl, 1, 8);
+      const bool unsure = l > 0 && has && (up >> 8) - (my >> 8) < near && !(xu == xl && bu == bl);
+      if (biased && !p.sigmoid) redo |= unsure;   // a sum over all experts in 64 bits
+      // a row's own chosen experts in the order of their 64-bit scores (without a bias of the logits)
+      const uint32_t who = __ballot_sync(kFull, unsure);
+      if (who != 0 && (!biased || p.sigmoid)) {
+        double c = (double)xl;
+        if (biased) c = 1.0 / (1.0 + exp(-c)) + (double)bl;
+        int rank = 0;
+        for (int i = 0; i < p.k; ++i) {
+          const double o = __shfl_sync(kFull, c, (lane & 24) | i);
+          const int oe = __shfl_sync(kFull, e, (lane & 24) | i);
+          rank += o > c || (o == c && oe < e);
+        }
+        const bool mine = ((who >> (lane & 24)) & 255u) != 0;
+        int to = e;
+        float xto = xl;
+        for (int i = 0; i < p.k; ++i) {
+          const int place_i = __shfl_sync(kFull, rank, (lane & 24) | i);
+          const int oe = __shfl_sync(kFull, e, (lane & 24) | i);
+          const float ox = __shfl_sync(kFull, xl, (lane & 24) | i);
+          if (mine && has && place_i == l) {
+            to = oe;
+            xto = ox;
+          }
+        }
+        e = to;
+        xl = xto;
+      }
+    }
+    redo |= V > 8 && taken >= 8;   // its ninth may belong among them
+    float w;
+    if (p.renorm) {
+      float t = xl;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, o));
+      if (p.sigmoid) t = fminf(t, 0.0f);
+      w = xl > -INFINITY ? (p.sigmoid && t == 0.0f ? sigmoid(xl) : expf(xl - t)) : 0.0f;
+      if (p.sigmoid && t < 0.0f) w = __fdividef(w, 1.0f + expf(xl));
+      float sum = w;
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);   // as 32 lanes do
+      w = sum > 0.0f ? p.scale * __fdividef(w, sum) : 0.0f;
+    } else {
+      w = p.scale * (p.sigmoid ? sigmoid(xl) : __fdividef(expf(xl - top), z));
+    }
+    const uint32_t undone = __ballot_sync(kFull, redo && 4 * r4 + (lane >> 3) < p.rows);
+    if (has && 4 * r4 + (lane >> 3) < p.rows && ((undone >> (lane & 24)) & 255u) == 0) {
+      p.ids[row * p.k + l] = e;
+      p.weights[row * p.k + l] = w;
+    }
+    if (undone != 0)
+      for (int q = 0; q < 4; ++q)
+        if (((undone >> (8 * q)) & 255u) != 0)
+          route_again<V / 4, F32>(p, 4 * r4 + q, refine_sm + warp * p.E);
   }
 }
 
@@ -665,6 +934,27 @@ extern "C" w4_status w4_route(int32_t* ids, float* weights, const w4_router* rou
     return p.f32 ? kv8::launch(f32, dim3(grid), 32 * kRouteWarps, smem, stream, p)
                  : kv8::launch(bf16, dim3(grid), 32 * kRouteWarps, smem, stream, p);
   };
+  // Many tokens over experts that eight lanes hold in whole vectors: half the instructions a token,
+  // a quarter of the warps (16384 tokens 19.5 -> 15.4 us over 256 experts in groups with biases,
+  // 7.8 -> 5.4 us over 128 without; 4000 tokens 9.1 -> 10.3 and 3.2 -> 2.7 us; 500 of them 3.3 -> 4.4).
+  if (rows >= kManyRows && p.k <= 8 && (p.E == 256 || p.E == 128 || p.E == 64) && (p.G & (p.G - 1)) == 0 && p.G <= 8 &&
+      !kv8::misaligned(logits, 16) && row_stride * el % 16 == 0) {
+    while ((8 >> p.shift8) > p.G) ++p.shift8;
+    // a lane's eight words are too few where one lane holds all that can be chosen
+    if (p.k < 8 || p.G == 1 || p.top_groups << p.shift8 > 1) {
+      p.vec = p.each % 4 == 0;   // for the rows that are left to route_rows
+      const long long steps = ((long long)rows + 3) / 4, most = ((steps + kManyWarps - 1) / kManyWarps);
+      const unsigned many = (unsigned)(most < 152 * 6 ? most : 152 * 6);
+      const size_t room = (size_t)kManyWarps * p.E * sizeof(double);
+      auto run = [&](auto bf16, auto f32) {
+        return p.f32 ? kv8::launch(f32, dim3(many), 32 * kManyWarps, room, stream, p)
+                     : kv8::launch(bf16, dim3(many), 32 * kManyWarps, room, stream, p);
+      };
+      if (p.E == 64) return run(route_many_kernel<8, false>, route_many_kernel<8, true>);
+      if (p.E == 128) return run(route_many_kernel<16, false>, route_many_kernel<16, true>);
+      return run(route_many_kernel<32, false>, route_many_kernel<32, true>);
+    }
+  }
   if (p.each <= 1) return go(route_kernel<1, false>, route_kernel<1, true>, 1);
   if (p.each <= 2) return go(route_kernel<2, false>, route_kernel<2, true>, 2);
   if (p.each <= 4) return go(route_kernel<4, false>, route_kernel<4, true>, 4);

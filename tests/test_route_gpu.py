@@ -196,3 +196,48 @@ def test_combine_keeps_what_is_not_finite(cuda_lib):
     out = lib.moe_combine(y, w).double().cpu().numpy()
     assert out[0, 1] == np.inf and np.isnan(out[0, 2]) and out[0, 3] == 0
     assert np.isfinite(out[1]).all()
+
+
+@pytest.mark.parametrize("E,k,G,tg", [(256, 8, 8, 4), (256, 8, 1, 1), (256, 3, 8, 1), (256, 8, 4, 1), (256, 8, 8, 1),
+                                      (128, 8, 1, 1), (128, 5, 2, 1), (64, 6, 1, 1), (64, 8, 8, 5)])
+@pytest.mark.parametrize("score,bias,best,dtype", [
+    ("softmax", False, 1, torch.bfloat16), ("softmax", True, 2, torch.float32),
+    ("sigmoid", True, 2, torch.bfloat16), ("sigmoid", False, 2, torch.float32),
+    ("sigmoid", False, 1, torch.bfloat16)])
+def test_many_tokens_as_each_alone(cuda_lib, E, k, G, tg, score, bias, best, dtype):
+    """4099 tokens in one call, the ids of calls of 1000, and of the reference for some: near scores,
+    ties, extremes and refused tokens among them."""
+    rng = np.random.default_rng(E + k + G)
+    T = 4099
+    x = rng.normal(size=(T, E)) * 2
+    x[5] = x[5, 0]                                     # all equal
+    x[100:140] = np.round(x[100:140])                  # many ties
+    x[200, 3] = np.nan
+    x[201, :] = -np.inf
+    x[202, 7] = np.inf
+    x[300:310, E // 2:] = -np.inf
+    x[400:420] *= 30
+    x[500:520, :E // 16] += 12                         # one lane's experts all the best
+    x[T - 1, 1] = np.nan
+    b = rng.normal(size=E) * 0.05 if bias else None
+    if bias:                                           # scores that 32 bits cannot tell apart
+        xf = torch.from_numpy(x[600].astype(np.float32)).to(dtype).double().numpy()
+        s = serve.scores(xf, score == "sigmoid")
+        b = np.float32(np.median(s + b)) - s
+        b += rng.normal(size=E) * 0.03 * (rng.random(E) < 0.8)
+    renorm = k != 6 and G != 1
+    ids, w, status, held = run(x, k, G, tg, best, score, renorm, 1.0, b, dtype)
+    assert status == lib.STATUS_CODE["W4_ERR_VALUE"]
+    for t0 in range(0, T, 1000):
+        i1, w1, _, _ = run(x[t0:t0 + 1000], k, G, tg, best, score, renorm, 1.0, b, dtype)
+        assert np.array_equal(i1, ids[t0:t0 + 1000])
+        assert np.array_equal(w1, w[t0:t0 + 1000])
+        # (the same bits, however many tokens a call has)
+    part = np.r_[0:10, 100:105, 198:204, 300:303, 400:405, 500:505, 598:603, T - 4:T]
+    b64 = None if b is None else b.astype(np.float32).astype(np.float64)
+    for t in part:
+        ref = serve.route_row(held[t], b64, k, G, tg, best, score == "sigmoid", renorm, 1.0)
+        if ref is None:
+            assert (ids[t] == POISON).all() and (w[t] == POISON).all()
+        else:
+            assert np.array_equal(ids[t], ref[0]), (t, ids[t], ref[0])
