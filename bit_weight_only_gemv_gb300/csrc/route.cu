@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineParams 
   pdl_wait();
   const long long row = blockIdx.x / p.chunks;
   const int chunk = blockIdx.x % p.chunks;
-  const int n = (chunk * kCombineThreads + threadIdx.x) * VEC;
+  const long long n = ((long long)chunk * kCombineThreads + threadIdx.x) * VEC;
   const float* wt = p.weights + row * p.k;
   if (p.ids != nullptr) {
     bool ok = true;

@@ -983,9 +983,9 @@ w4_status w4_moe_combine(void *out, const void *y, const float *weights, const i
  *   n > 0:             x = x - frequency[b] * n - presence[b]
  *   v in the biases:   x = x + bias
  *   v not allowed:     x = -inf
- * in fp32 in this order, rounded once to the logits' type, in place.  Logits
- * that no rule names keep their bits; a logit that is not allowed is not read.
- * A mask that allows nothing leaves a row of -inf.
+ * in fp32 in this order, rounded once to the logits' type, in place (the quotient
+ * is a product with the reciprocal, frequency's product fused).  Logits that no
+ * rule names keep their bits.  A mask that allows nothing leaves a row of -inf.
  *
  * logits       bf16 or fp32 (W4_TYPE_*), row b at element b * row_stride.
  * A row with a history, prompt or bias count outside its bounds or a token
@@ -1029,7 +1029,10 @@ w4_status w4_logits_adjust(void *logits, int logits_type, size_t row_stride, int
  * refs int32 [num_pages] counts how often a page is named by the sequences'
  * rows of a page table (a row of lens[b] tokens names its first
  * ceil(lens[b] / page_tokens) entries), and by whatever else keeps it; a page
- * with 0 is free.  The calls hold to the conventions of w4_kv8_*.  They move
+ * with 0 is free.  A caller starts from refs of 0 and empty rows, and lets these
+ * calls do the counting (counts that do not agree with the rows can hand a page
+ * to two of them).  Pages for w4_kv8_evict's kept tokens come from w4_kv8_reserve on a
+ * table of empty rows.  The calls hold to the conventions of w4_kv8_*.  They move
  * pages of several caches at once: a model's layers, with one table for all.
  * Pages are taken from the lowest free number on, in order of rows.  Tables have
  * at most W4_KV8_MAX_BATCH rows of 2^26 entries.
@@ -1055,6 +1058,7 @@ size_t w4_kv8_pages_workspace_bytes(int batch, int num_pages);
  * the same such page the lowest keeps it, if nothing else names it, and the
  * others get copies of the tokens in use, steps, ranges and weights, in every cache.
  * Parents that all are their own rows change nothing, unless such a page is shared.
+ * Sequences that share a page cannot be weighed (w4_kv8_weigh) in one call.
  *
  * new_table  int32 [new_batch][max_pages]: entries past a row's pages are left
  *            as they were.
