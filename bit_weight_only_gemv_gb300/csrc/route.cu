@@ -528,9 +528,17 @@ __device__ __noinline__ void route_again(const RouteParams& p, long long row, do
   route_rows<V, F32>(p, row, 1, row + 1, sm);
 }
 
+// A 64-bit score that needs no other expert's: with a sigmoid, or without a bias, where a softmax's
+// common divisor changes no comparison.  One copy of the code, which few calls run.
+__device__ __noinline__ double exact_alone(const RouteParams& p, long long row, int e, float top) {
+  return exact_score(p, row, e, top, 1.0);
+}
+
 // Four tokens a warp, eight lanes each with V neighbouring experts: what a warp does for one token
-// it does here for four.  A lane keeps its best eight words, sorted.  Whatever this cannot settle (a
-// NaN, scores too near each other, a lane whose eight were all taken) is left to route_rows.
+// it does here for four.  A lane keeps its best eight words, sorted.  Scores too near each other are
+// compared in 64 bits by the lanes that have them, all at once, since a token that takes long is what
+// the call's end waits for; whatever this cannot settle (a NaN, a softmax with a bias, too many of
+// them, a lane whose eight were all taken) is left to route_rows.
 constexpr int kManyWarps = 4;
 constexpr int kManyRows = 4096;   // tokens from which on it is the faster one
 
@@ -608,6 +616,7 @@ __global__ void __launch_bounds__(32 * kManyWarps) route_many_kernel(const __gri
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, o));
     bool redo = again || isnan(top) || (!p.sigmoid && isinf(top));
+    const bool alone = p.sigmoid || !biased;
     float z = 1.0f, tol = 0.0f, f1 = -INFINITY, f2 = -INFINITY;
     uint32_t key[V];
     if (sums || (!p.renorm && !p.sigmoid)) {   // errors as in route_rows
@@ -672,6 +681,8 @@ __global__ void __launch_bounds__(32 * kManyWarps) route_many_kernel(const __gri
             key[i + d] = min(a, c);
           }
     }
+    const uint32_t near = 3 + (biased ? (uint32_t)fminf(tol * unit, kOne) : 1u);
+    const uint32_t low = fixed ? 255u : 0xFFFFu;   // bits of a place
     if (groups) {
       float gs;
       if (sums) {
@@ -694,8 +705,33 @@ __global__ void __launch_bounds__(32 * kManyWarps) route_many_kernel(const __gri
         rank += o > gs || (o == gs && i < g);
         nearest = i == g ? nearest : fminf(nearest, fabsf(o - gs));
       }
-      // a group at the border and another too near it
-      redo |= sums && (rank == p.top_groups || rank == p.top_groups - 1) && nearest < 3.0f * tol;
+      // a group at the border and another too near it: all groups again, by the 64-bit scores of each
+      // lane's three best words, among which its two best experts are
+      const bool open = sums && (rank == p.top_groups || rank == p.top_groups - 1) && nearest < 3.0f * tol;
+      const uint32_t rows_open = __ballot_sync(kFull, open && !redo);
+      if (rows_open != 0) {
+        const bool mine = ((rows_open >> (lane & 24)) & 255u) != 0;
+        redo |= mine && (!alone || (fixed && key[3] != 0 && (key[1] >> 8) - (key[3] >> 8) < near));
+        double a = -INFINITY, b = -INFINITY;
+        for (int i = 0; i < 3; ++i) {
+          const uint32_t word = i == 0 ? key[0] : i == 1 ? key[1] : key[2];
+          const double c = exact_alone(p, row, min((int)(low - (word & low)), p.E - 1), top);
+          b = fmax(b, fmin(a, c));
+          a = fmax(a, c);
+        }
+        for (int o = 1; o < (1 << p.shift8); o <<= 1) {
+          const double oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
+          b = fmax(fmax(b, ob), fmin(a, oa));
+          a = fmax(a, oa);
+        }
+        const double sum = p.best == 2 ? a + b : a;
+        int exact_rank = 0;
+        for (int i = 0; i < p.G; ++i) {
+          const double o = __shfl_sync(kFull, sum, (lane & 24) | (i << p.shift8));
+          exact_rank += o > sum || (o == sum && i < g);
+        }
+        rank = mine ? exact_rank : rank;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) key[i] = rank < p.top_groups ? key[i] : 0u;
     }
@@ -715,39 +751,36 @@ __global__ void __launch_bounds__(32 * kManyWarps) route_many_kernel(const __gri
       pop();
       my = l == j ? m : my;
     }
-    const uint32_t mask = fixed ? 255u : 0xFFFFu, place = mask - (my & mask);
-    int e = min((int)place, p.E - 1);   // (none left: redone)
+    int e = min((int)(low - (my & low)), p.E - 1);   // (none left: redone)
     const bool has = l < p.k;
     float xl = has ? logit(p, row, e) : -INFINITY;
     if (fixed) {
-      const uint32_t near = 3 + (biased ? (uint32_t)fminf(tol * unit, kOne) : 1u);
       const uint32_t kth = m;
       pop();
-      redo |= m != 0 && (kth >> 8) - (m >> 8) < near;
+      redo |= m != 0 && (kth >> 8) - (m >> 8) < near;   // the best left out is too near the last chosen
       const float bl = biased && has ? load_in(p.bias + e) : 0.0f;
       const uint32_t up = __shfl_up_sync(kFull, my, 1, 8);
       const float xu = __shfl_up_sync(kFull, xl, 1, 8), bu = __shfl_up_sync(kFull, bl, 1, 8);
       const bool unsure = l > 0 && has && (up >> 8) - (my >> 8) < near && !(xu == xl && bu == bl);
-      if (biased && !p.sigmoid) redo |= unsure;   // a sum over all experts in 64 bits
-      // a row's own chosen experts in the order of their 64-bit scores (without a bias of the logits)
-      const uint32_t who = __ballot_sync(kFull, unsure);
-      if (who != 0 && (!biased || p.sigmoid)) {
-        double c = (double)xl;
-        if (biased) c = 1.0 / (1.0 + exp(-c)) + (double)bl;
+      redo |= unsure && !alone;
+      // a row's chosen experts in the order of their 64-bit scores (without a bias of the logits)
+      const uint32_t who = __ballot_sync(kFull, unsure && !redo);
+      if (who != 0) {
+        const bool mine = ((who >> (lane & 24)) & 255u) != 0;
+        const double c = biased ? exact_alone(p, row, e, top) : (double)xl;
         int rank = 0;
         for (int i = 0; i < p.k; ++i) {
           const double o = __shfl_sync(kFull, c, (lane & 24) | i);
           const int oe = __shfl_sync(kFull, e, (lane & 24) | i);
           rank += o > c || (o == c && oe < e);
         }
-        const bool mine = ((who >> (lane & 24)) & 255u) != 0;
         int to = e;
         float xto = xl;
         for (int i = 0; i < p.k; ++i) {
-          const int place_i = __shfl_sync(kFull, rank, (lane & 24) | i);
+          const int place = __shfl_sync(kFull, rank, (lane & 24) | i);
           const int oe = __shfl_sync(kFull, e, (lane & 24) | i);
           const float ox = __shfl_sync(kFull, xl, (lane & 24) | i);
-          if (mine && has && place_i == l) {
+          if (mine && has && place == l) {
             to = oe;
             xto = ox;
           }
@@ -935,8 +968,8 @@ extern "C" w4_status w4_route(int32_t* ids, float* weights, const w4_router* rou
                  : kv8::launch(bf16, dim3(grid), 32 * kRouteWarps, smem, stream, p);
   };
   // Many tokens over experts that eight lanes hold in whole vectors: half the instructions a token,
-  // a quarter of the warps (16384 tokens 19.5 -> 15.4 us over 256 experts in groups with biases,
-  // 7.8 -> 5.4 us over 128 without; 4000 tokens 9.1 -> 10.3 and 3.2 -> 2.7 us; 500 of them 3.3 -> 4.4).
+  // a quarter of the warps (16384 tokens 19.5 -> 14.1 us over 256 experts in groups with biases,
+  // 7.8 -> 5.4 us over 128 without; 4096 tokens 9.1 -> 6.6 and 3.2 -> 2.7 us; 500 of them 3.3 -> 4.4).
   if (rows >= kManyRows && p.k <= 8 && (p.E == 256 || p.E == 128 || p.E == 64) && (p.G & (p.G - 1)) == 0 && p.G <= 8 &&
       !kv8::misaligned(logits, 16) && row_stride * el % 16 == 0) {
     while ((8 >> p.shift8) > p.G) ++p.shift8;
