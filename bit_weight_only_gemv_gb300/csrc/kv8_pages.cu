@@ -11,7 +11,10 @@
 // walked in pieces of kPiece entries, one piece a warp, so that one long row has
 // as many readers as many short ones.  What has to be copied goes into a list in
 // the workspace; copy_kernel moves it in every cache, one warp for the keys or
-// values of one (page, head).
+// values of one (page, head), four 16-byte loads a lane in flight.
+// Four beams forked and grown 9.9 us, 128 beams over 30 layers 21 us (30 with
+// everything cold: half of it the decision, whose tables come from memory), 3400
+// pages of 16 layers made dense 149 us, 7.3 TB/s.
 #include <mutex>
 
 #include "kv8.cuh"
@@ -22,8 +25,10 @@ namespace {
 
 constexpr int kRanks = 8, kPlanThreads = 1024;
 constexpr int kPiece = 128;
-constexpr int kOnePages = 16384;      // one CTA's largest pool: three counts a page in its shared memory,
-constexpr long long kOnePieces = 256;   // and its most pieces of a table
+// One CTA's largest pool (three counts a page in its shared memory) and most pieces of a table: a
+// fork of 128 pieces takes it 11.5 us, the cluster 18; of 512 pieces 30 and 21.
+constexpr int kOnePages = 16384;
+constexpr long long kOnePieces = 256;
 constexpr int kRowsEach = W4_KV8_MAX_BATCH / kPlanThreads;   // rows a thread decides
 constexpr unsigned kFull = 0xffffffffu;
 

@@ -18,6 +18,9 @@
 // Of candidates, or groups, that are nearer than this (and the scores' fp32
 // errors) can tell, the order is found from 64-bit scores of those few alone; of
 // more than 32 such candidates by refine() over all experts.
+// One token takes 1.9 us in a graph, 192 tokens over 256 experts in 8 groups with
+// biases 3.3 us (latency: about 800 instructions a warp); for many tokens
+// route_many_kernel takes a quarter of the warps.
 #include "kv8.cuh"
 
 namespace w4 {
@@ -818,6 +821,8 @@ __global__ void __launch_bounds__(32 * kManyWarps) route_many_kernel(const __gri
 }
 
 // ---------------------------------------------------------------- combine
+// Eight columns a thread, its token's k rows all on their way at once: HBM bounds it.  4001 tokens'
+// 8 rows of 2816 and one added: 34.5 us, 6.55 TB/s (a copy: 6.65).
 constexpr int kCombineThreads = 128;
 
 struct CombineParams {
