@@ -52,17 +52,17 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 // Largest of the warp's values, NaN if one of them is.
 __device__ __forceinline__ float warp_max_nan(float v) {
   float m;
-  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
   return m;
 }
 __device__ __forceinline__ float warp_min_f(float v) {
   float m;
-  asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
   return m;
 }
 __device__ __forceinline__ float warp_max_f(float v) {
   float m;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
   return m;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {

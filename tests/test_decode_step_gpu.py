@@ -236,3 +236,39 @@ def test_calls_on_another_stream(cuda_lib):
         got = lib.route(m.route, z, m.bias, stream=side)
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_one_workspace_for_every_call(cuda_lib):
+    """A split-K product, attention and the page calls on one buffer, in turn: the results of buffers
+    of their own."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    w = lib.quantize(torch.randn((16, 21504), generator=gen, device="cuda") * 0.01)
+    x = torch.randn((1, 21504), generator=gen, device="cuda").to(torch.bfloat16)
+    cache = new_cache(40)
+    for t in cache.tensors[:2]:
+        t.random_(0, 256, generator=gen)
+    for t in cache.tensors[2:4]:
+        t.fill_(2.0 ** -7)
+    table = torch.randperm(40, generator=gen, device="cuda")[:16].to(torch.int32).view(2, 8).contiguous()
+    lens = torch.tensor([120, 87], dtype=torch.int32, device="cuda")
+    refs = torch.zeros((40,), dtype=torch.int32, device="cuda")
+    refs[table[0].long()] = 1
+    refs[table[1, :6].long()] = 1
+    q = torch.randn((2, HQ, D), generator=gen, device="cuda").to(torch.bfloat16)
+    batch = lib.KV8Batch(table, lens, max_len=128)
+    parents = torch.tensor([1, 0, 1, 0, 0], dtype=torch.int32, device="cuda")
+    sizes = [lib.workspace_bytes(1, 16, 21504), lib.kv8_attn_workspace_bytes(cache, batch, HQ),
+             lib.kv8_pages_workspace_bytes(5, 40)]
+    assert all(sizes)
+    one = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+
+    def calls(ws):
+        got = [lib.gemv(*w, x, workspace=ws(0)), lib.kv8_attn(cache, batch, q, 0.125, workspace=ws(1))]
+        t, n, r = lib.kv8_fork(cache, table, lens, refs, parents, ws(2))
+        lib.kv8_reserve(t, n, r, P, None, ws(2))
+        got += [t, n, r, *lib.kv8_compact(cache, t, n, r, ws(2))]
+        return [g.clone() for g in got]
+
+    want = calls(lambda i: torch.zeros(sizes[i], dtype=torch.uint8, device="cuda"))
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(want, calls(lambda i: one)))
