@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kRanks = 8, kPlanThreads = 1024;
 constexpr int kPiece = 128;
+constexpr int kTogether = 4;   // pieces, or pages, of a warp or thread that are on their way at once
 // One CTA's largest pool (three counts a page in its shared memory) and most pieces of a table: a
 // fork of 128 pieces takes it 11.5 us, the cluster 18; of 512 pieces 30 and 21.
 constexpr int kOnePages = 16384;
@@ -146,10 +147,16 @@ struct Pieces {
 
   __device__ __forceinline__ Pieces(int max_pages, int warp, int warps) {
     each = (max_pages - 1) / kPiece + 1;
-    row = warp / each;
-    piece = warp % each;
-    row_step = warps / each;
-    piece_step = warps % each;
+    row = warp;
+    piece = 0;
+    row_step = warps;
+    piece_step = 0;
+    if (each > 1) {   // divisions that a CTA of 32 warps feels
+      row = warp / each;
+      piece = warp - row * each;
+      row_step = warps / each;
+      piece_step = warps - row_step * each;
+    }
   }
   __device__ __forceinline__ void next() {
     row += row_step;
@@ -170,29 +177,40 @@ __device__ __forceinline__ void load_piece(const Rows& r, int b, int first, int 
 }
 
 // Pages of every old row into row_pages, -1 where its length or one of its
-// entries breaks its bounds.  Ends in a barrier.
+// entries breaks its bounds.  len: the length of row gt, if there is one.  Ends in a barrier.
 template <int R>
-__device__ __forceinline__ void check_rows(const Rows& r, int32_t* row_pages, uint32_t rank,
+__device__ __forceinline__ void check_rows(const Rows& r, int len, int32_t* row_pages, uint32_t rank,
                                            int32_t* status) {
   using T = Team<R>;
   const int gt = rank * kPlanThreads + threadIdx.x;
-  for (int b = gt; b < r.batch; b += T::kAll) {
-    const int np = r.pages(load_in(r.lens + b));
-    row_pages[b] = np;
+  static_assert(W4_KV8_MAX_BATCH <= kRanks * kPlanThreads && kOnePieces <= kPlanThreads, "a row a thread");
+  if (gt < r.batch) {
+    const int np = r.pages(len);
+    row_pages[gt] = np;
     if (np < 0) report(status, W4_ERR_INDEX);
   }
   T::sync();
   const int lane = threadIdx.x & 31;
-  for (Pieces i(r.max_pages, gt >> 5, T::kAll / 32); i.row < r.batch; i.next()) {
-    const int b = i.row, at = i.piece * kPiece;
-    int pg[kPiece / 32];
-    load_piece(r, b, at + lane, T::get(row_pages + b), pg);
-    bool bad = false;
+  // several pieces' entries on their way at once: in a cold table each is a trip to memory
+  for (Pieces i(r.max_pages, gt >> 5, T::kAll / 32); i.row < r.batch;) {
+    int pg[kTogether][kPiece / 32], row[kTogether];
 #pragma unroll
-    for (int z = 0; z < kPiece / 32; ++z) bad |= pg[z] != kNone && (pg[z] < 0 || pg[z] >= r.num_pages);
-    if (__any_sync(kFull, bad) && lane == 0) {
-      row_pages[b] = -1;
-      report(status, W4_ERR_INDEX);
+    for (int y = 0; y < kTogether; ++y) {
+      row[y] = i.row;
+      const bool there = i.row < r.batch;
+      load_piece(r, there ? i.row : 0, i.piece * kPiece + lane, there ? T::get(row_pages + i.row) : 0, pg[y]);
+      i.next();
+    }
+#pragma unroll
+    for (int y = 0; y < kTogether; ++y) {
+      bool bad = false;
+#pragma unroll
+      for (int z = 0; z < kPiece / 32; ++z)
+        bad |= pg[y][z] != kNone && (pg[y][z] < 0 || pg[y][z] >= r.num_pages);
+      if (__any_sync(kFull, bad) && lane == 0) {
+        row_pages[row[y]] = -1;
+        report(status, W4_ERR_INDEX);
+      }
     }
   }
   T::sync();
@@ -295,14 +313,26 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const __grid_cons
   int32_t* new_lens = R == 1 ? of_rows[1] : p.new_lens;
   int32_t* list = R == 1 ? of_rows[3] : p.s.dst;
   const int32_t* parents = R == 1 ? of_rows[4] : p.parents;
-  if constexpr (R == 1)
-    for (int b = threadIdx.x; b < p.new_batch; b += kPlanThreads) of_rows[4][b] = load_in(p.parents + b);
-  for (int i = gt; i < r.num_pages; i += T::kAll) {
-    refs[i] = load_in(p.refs + i);
-    count[i] = 0;
-    first[i] = 0x7fffffff;
+  // what a call starts from comes in one trip to memory
+  const int len = gt < r.batch ? load_in(r.lens + gt) : 0;
+  const int parent = R == 1 && gt < p.new_batch ? load_in(p.parents + gt) : 0;
+  for (int i0 = gt; i0 < r.num_pages; i0 += kTogether * T::kAll) {
+    int v[kTogether];
+#pragma unroll
+    for (int z = 0; z < kTogether; ++z)
+      if (i0 + z * T::kAll < r.num_pages) v[z] = load_in(p.refs + i0 + z * T::kAll);
+#pragma unroll
+    for (int z = 0; z < kTogether; ++z) {
+      const int i = i0 + z * T::kAll;
+      if (i >= r.num_pages) break;
+      refs[i] = v[z];
+      count[i] = 0;
+      first[i] = 0x7fffffff;
+    }
   }
-  check_rows<R>(r, row_pages, rank, p.status);
+  if constexpr (R == 1)
+    if (gt < p.new_batch) of_rows[4][gt] = parent;
+  check_rows<R>(r, len, row_pages, rank, p.status);
   // the old rows' names go, the new rows' come
   const int rows = max(r.batch, p.new_batch);
   for (Pieces i(r.max_pages, gt >> 5, T::kAll / 32); i.row < rows; i.next()) {
@@ -326,15 +356,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const __grid_cons
     int mine[kPiece / 32], come[kPiece / 32];
     load_piece(r, b, at + lane, par != b ? had : 0, mine);
     load_piece(r, par, at + lane, np, come);
-#pragma unroll
-    for (int z = 0; z < kPiece / 32; ++z)
-      if (mine[z] != kNone) atomicSub(refs + mine[z], 1);
-    if (b >= p.new_batch) continue;
+    int32_t* row = p.new_table + (long long)b * r.max_pages + at + lane;
 #pragma unroll
     for (int z = 0; z < kPiece / 32; ++z) {
+      if (at + 32 * z >= max(had, np)) break;
+      if (mine[z] != kNone) atomicSub(refs + mine[z], 1);
       const int pg = come[z], e = at + lane + 32 * z;
       if (pg == kNone) continue;
-      p.new_table[(long long)b * r.max_pages + e] = pg;
+      row[32 * z] = pg;
       if (par != b) atomicAdd(refs + pg, 1);
       if (e == np - 1 && (len & ((1 << r.shift) - 1)) != 0) {   // a page to be written to
         atomicAdd(count + pg, 1);
@@ -342,7 +371,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const __grid_cons
         if constexpr (R == 1) of_rows[2][b] = pg;
       }
     }
-    if (at == 0 && lane == 0) new_lens[b] = len;
+    if (at == 0 && lane == 0 && b < p.new_batch) new_lens[b] = len;
   }
   T::sync();
   // rows that need a page of their own, in order
@@ -477,14 +506,24 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const __grid_c
   int32_t* refs = R == 1 ? sm : p.new_refs;
   int32_t* count = R == 1 ? sm + r.num_pages : p.s.count;
   int32_t* to = R == 1 ? sm + 2 * r.num_pages : p.s.first;   // where each page goes
-  for (int i = gt; i < r.num_pages; i += T::kAll) {
-    refs[i] = load_in(p.refs + i);
-    count[i] = 0;
-    to[i] = i;
+  const int len = gt < r.batch ? load_in(r.lens + gt) : 0;
+  for (int i0 = gt; i0 < r.num_pages; i0 += kTogether * T::kAll) {
+    int v[kTogether];
+#pragma unroll
+    for (int z = 0; z < kTogether; ++z)
+      if (i0 + z * T::kAll < r.num_pages) v[z] = load_in(p.refs + i0 + z * T::kAll);
+#pragma unroll
+    for (int z = 0; z < kTogether; ++z) {
+      const int i = i0 + z * T::kAll;
+      if (i >= r.num_pages) break;
+      refs[i] = v[z];
+      count[i] = 0;
+      to[i] = i;
+    }
   }
   int32_t* row_pages = R == 1 ? of_rows : p.s.row_pages;
   if (gt == 0) *p.used = 0;
-  check_rows<R>(r, row_pages, rank, p.status);
+  check_rows<R>(r, len, row_pages, rank, p.status);
   for (Pieces i(r.max_pages, gt >> 5, T::kAll / 32); i.row < r.batch; i.next()) {
     const int b = i.row, at = i.piece * kPiece;
     int pg[kPiece / 32];
@@ -519,7 +558,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const __grid_c
   for (int j = gt; j < moves; j += T::kAll) {
     const int a = T::get(p.s.src + j), b = T::get(p.s.dst + j);
     to[a] = b;
-    refs[b] = load_in(p.refs + a);
+    refs[b] = T::get(refs + a);
     refs[a] = 0;
     p.s.tokens[j] = 1 << r.shift;
   }
@@ -663,7 +702,7 @@ w4_status check_table(const int32_t* table, const int32_t* lens, const int32_t* 
   if (table == nullptr || lens == nullptr || refs == nullptr || batch < 1 || max_pages < 1 ||
       num_pages < 1)
     return W4_ERR_ARG;
-  if (batch > W4_KV8_MAX_BATCH || max_pages > (1 << 26) || (P != 16 && P != 32 && P != 64 && P != 128))
+  if (batch > W4_KV8_MAX_BATCH || max_pages > (1 << 26) || num_pages > (1 << 30) || (P != 16 && P != 32 && P != 64 && P != 128))
     return W4_ERR_SHAPE;
   if (misaligned(table, 4) || misaligned(lens, 4) || misaligned(refs, 4)) return W4_ERR_ALIGN;
   return W4_OK;

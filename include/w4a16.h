@@ -1035,7 +1035,7 @@ w4_status w4_logits_adjust(void *logits, int logits_type, size_t row_stride, int
  * table of empty rows.  The calls hold to the conventions of w4_kv8_*.  They move
  * pages of several caches at once: a model's layers, with one table for all.
  * Pages are taken from the lowest free number on, in order of rows.  Tables have
- * at most W4_KV8_MAX_BATCH rows of 2^26 entries.
+ * at most W4_KV8_MAX_BATCH rows of 2^26 entries, pools at most 2^30 pages.
  *
  * workspace  w4_kv8_pages_workspace_bytes(batch, num_pages) bytes with the
  *            largest batch of the calls, 16-byte aligned; its first

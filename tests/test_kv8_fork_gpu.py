@@ -189,6 +189,12 @@ def test_calls_in_a_graph(cuda_lib):
                 assert np.array_equal(t.cpu().numpy(), want[name])
 
 
+def test_as_many_caches_as_a_call_takes(cuda_lib):
+    p = Pages(17, [20, 7], H=1, D=64, layers=128, spare=4).to_gpu(most_rows=4)
+    p.fork([1, 0, 0, 1])
+    p.compact()
+
+
 def test_copies_follow_the_decision_of_their_call(cuda_lib):
     """What the copying kernel reads is what the deciding one wrote, not what the workspace held before:
     many times, since a load before its time would not show every time."""

@@ -102,7 +102,7 @@ ALL = ("fork", "reserve", "compact")
 @pytest.mark.parametrize("names,over,code", [
     (ALL, dict(table=None), ARG), (ALL, dict(lens=None), ARG), (ALL, dict(refs=None), ARG),
     (ALL, dict(batch=0), ARG), (ALL, dict(max_pages=0), ARG), (ALL, dict(num=0), ARG),
-    (ALL, dict(flags=2), ARG), (ALL, dict(batch=4097), SHAPE), (ALL, dict(max_pages=(1 << 26) + 1), SHAPE), (ALL, dict(P=24), SHAPE),
+    (ALL, dict(flags=2), ARG), (ALL, dict(batch=4097), SHAPE), (ALL, dict(max_pages=(1 << 26) + 1), SHAPE), (ALL, dict(num=(1 << 30) + 1), SHAPE), (ALL, dict(P=24), SHAPE),
     (ALL, dict(table=P0 + 2), ALIGN), (ALL, dict(ws=P0 + 8), ALIGN), (ALL, dict(ws=None), SPACE),
     (ALL, dict(ws_bytes=4096), SPACE), (("reserve",), dict(grow=P0 + 1), ALIGN),
     (("fork",), dict(parents=None), ARG), (("fork",), dict(new_batch=0), ARG),
