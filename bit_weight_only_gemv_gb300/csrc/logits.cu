@@ -14,8 +14,8 @@
 // a lane's eight logits are whole vectors but for a row's ends.
 // Every CTA of a row sees the whole lists, so all of them find the same errors.
 // Chains of loads bound it (counts, lists, logits), so each link has many in
-// flight: a warp's mask words come before the lists, the lists eight at a time, a
-// warp's logits all together.
+// flight: a warp's mask words come before the lists, histories sixteen tokens a
+// thread at a time; what the walk costs is instructions.
 #include <mutex>
 
 #include "kv8.cuh"
@@ -313,11 +313,11 @@ w4_status run(const LogitParams& p, long long span, int rows, w4_stream_t stream
 // once; of more work than fits the GPU that way, CTAs of 512 threads and 16384 tokens, which read
 // the histories half as often and of which three are resident (24 rows of 262144 tokens under
 // masks 14.5 -> 13.3 us, 64 of 100277 with histories of 30000 23.3 -> 17.9 us; one row 4.8 us
-// against 5.9 us, 64 of 32000 7.9 against 10.8).
+// against 5.9 us).  Not where a row fits the smaller tile.
 template <typename T>
 w4_status run(const LogitParams& p, bool aligned, int rows, w4_stream_t stream) {
   const long long span = (long long)p.V + (aligned ? 0 : 16 / (int)sizeof(T) - 1);
-  return ((span - 1) / 16384 + 1) * rows > 304 ? run<T, 512, 1, 3>(p, span, rows, stream)
+  return span > 8192 && ((span - 1) / 16384 + 1) * rows > 304 ? run<T, 512, 1, 3>(p, span, rows, stream)
                                                : run<T, 256, 4, 4>(p, span, rows, stream);
 }
 
