@@ -6,9 +6,11 @@
 //   bit  19      occurs in the prompt
 //   bits 20..31  1 + index of its last bias
 // The CTA reads the row's bias list and history once, keeps what falls into its
-// tile, and then walks the tile: a token that no rule names and the mask allows
-// costs no global access, one that the mask forbids a store.  The warps take
-// pieces of 256 tokens in turn, since the tokens that a history names are
+// tile, and then walks the tile, eight tokens a lane: tokens that no rule names
+// and the mask allows cost no global access, eight that the mask forbids a store.
+// Where few of a warp's eights have a token named, those go token by token, a
+// token a lane; among the frequent ones all eights are worked through.  The warps
+// take pieces of 256 tokens in turn, since the tokens that a history names are
 // neighbours in most vocabularies (the frequent ones come first).  Tiles start
 // on 16-byte boundaries of the row in memory, wherever the row does, so that
 // a lane's eight logits are whole vectors but for a row's ends.
@@ -27,6 +29,7 @@ constexpr uint32_t kCount = (1u << 19) - 1, kPrompt = 1u << 19;
 constexpr int kBiasShift = 20;
 constexpr int kPiece = 256;   // tokens that a warp takes at a time, four times over
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kSparse = 4;    // eights of a piece with a token named that go token by token
 
 struct LogitParams {
   void* logits;
@@ -98,6 +101,16 @@ struct Eight<float> {
     a = make_float4(f[0], f[1], f[2], f[3]);
     b = make_float4(f[4], f[5], f[6], f[7]);
   }
+  __device__ __forceinline__ void mask(uint32_t allowed) {
+    a.x = allowed & 1 ? a.x : -INFINITY;
+    a.y = allowed & 2 ? a.y : -INFINITY;
+    a.z = allowed & 4 ? a.z : -INFINITY;
+    a.w = allowed & 8 ? a.w : -INFINITY;
+    b.x = allowed & 16 ? b.x : -INFINITY;
+    b.y = allowed & 32 ? b.y : -INFINITY;
+    b.z = allowed & 64 ? b.z : -INFINITY;
+    b.w = allowed & 128 ? b.w : -INFINITY;
+  }
 };
 template <>
 struct Eight<__nv_bfloat16> {
@@ -123,6 +136,15 @@ struct Eight<__nv_bfloat16> {
         u[i] = (u[i] & keep) | (*reinterpret_cast<const uint32_t*>(&b) & ~keep);
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t off = (allowed >> (2 * i) & 1 ? 0u : 0xFFFFu) | (allowed >> (2 * i + 1) & 1 ? 0u : 0xFFFF0000u);
+      u[i] = (u[i] & ~off) | (0xFF80FF80u & off);
+    }
+    v = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  __device__ __forceinline__ void mask(uint32_t allowed) {
+    uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t off = (allowed >> (2 * i) & 1 ? 0u : 0xFFFFu) | (allowed >> (2 * i + 1) & 1 ? 0u : 0xFFFF0000u);
@@ -261,26 +283,47 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_kernel(const __gri
     }
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
-      const int at = ((s0 + s) * warps + warp) * kPiece + lane * 8, v = v0 + at;
-      if (may[s] == 0xFFu && any[s] == 0) continue;
-      if (v < 0 || v + 8 > p.V) {   // a row's ends
-        for (int i = max(0, -v); i < min(8, p.V - v); ++i) {
-          const uint32_t w = word[at + i];
-          if (!((may[s] >> i) & 1))
-            store(logits + v + i, -INFINITY);
-          else if (w != 0)
-            store(logits + v + i, rules.apply(load(logits + v + i), w));
-        }
-        continue;
-      }
-      if (may[s] == 0) {
+      const int first = ((s0 + s) * warps + warp) * kPiece, at = first + lane * 8, v = v0 + at;
+      const bool ends = v < 0 || v + 8 > p.V;   // a row's ends
+      const uint32_t named = __ballot_sync(kFull, any[s] != 0 && may[s] != 0 && !ends);
+      const bool dense = __popc(named) > kSparse;
+      if (ends) {
+        if (may[s] != 0xFFu || any[s] != 0)
+          for (int i = max(0, -v); i < min(8, p.V - v); ++i) {
+            const uint32_t w = word[at + i];
+            if (!((may[s] >> i) & 1))
+              store(logits + v + i, -INFINITY);
+            else if (w != 0)
+              store(logits + v + i, rules.apply(load(logits + v + i), w));
+          }
+      } else if (may[s] == 0) {
         f[s].forbid();
-      } else {
+        f[s].store(logits + v);
+      } else if (dense && any[s] != 0) {
         const uint4 a = *reinterpret_cast<const uint4*>(word + at), b = *reinterpret_cast<const uint4*>(word + at + 4);
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         f[s].adjust(rules, w, any[s], may[s]);
+        f[s].store(logits + v);
+      } else if (may[s] != 0xFFu) {
+        f[s].mask(may[s]);
+        f[s].store(logits + v);
       }
-      f[s].store(logits + v);
+      if (!dense && named != 0) {
+        // few of the warp's eights have a token named: four of them at a time, a token a lane
+        __syncwarp();   // what the mask changed beside them is stored
+        for (uint32_t left = named; left != 0;) {
+          uint32_t mine = left;
+          for (int q = lane >> 3; q > 0; --q) mine &= mine - 1;
+          const int src = mine != 0 ? __ffs((int)mine) - 1 : 0, i = first + src * 8 + (lane & 7);
+          const uint32_t ok = __shfl_sync(kFull, may[s], src);
+          const uint32_t w = word[i];
+          if (mine != 0 && w != 0 && ((ok >> (lane & 7)) & 1)) store(logits + v0 + i, rules.apply(load(logits + v0 + i), w));
+          left &= left - 1;
+          left &= left - 1;
+          left &= left - 1;
+          left &= left - 1;
+        }
+      }
     }
   }
 }
@@ -309,16 +352,19 @@ w4_status run(const LogitParams& p, long long span, int rows, w4_stream_t stream
   return kv8::launch(kern, grid, kThreads, smem, stream, p);
 }
 
-// While the CTAs of 256 threads and 8192 tokens are few, each with all its logits on their way at
-// once; of more work than fits the GPU that way, CTAs of 512 threads and 16384 tokens, which read
-// the histories half as often and of which three are resident (24 rows of 262144 tokens under
-// masks 14.5 -> 13.3 us, 64 of 100277 with histories of 30000 23.3 -> 17.9 us; one row 4.8 us
-// against 5.9 us).  Not where a row fits the smaller tile.
+// While the CTAs of 256 threads and 8192 tokens are resident together (four an SM), each with all
+// its logits on their way at once.  Of more work, as many as registers allow, one piece's
+// logits at a time; with long histories CTAs of 512 threads and 16384 tokens, which read them half
+// as often.  Measured, in this order of variants: one row of 262144 tokens 4.4, 5.0 and 5.4 us; 24
+// rows under masks, histories to 4096, 13.5, 11.4 and 11.9 us; 64 rows of 100277 with histories to
+// 30000 25, 20 and 17.6 us; 2000 rows of 4000 18.7, 18.4 and 28 us.
 template <typename T>
 w4_status run(const LogitParams& p, bool aligned, int rows, w4_stream_t stream) {
   const long long span = (long long)p.V + (aligned ? 0 : 16 / (int)sizeof(T) - 1);
-  return span > 8192 && ((span - 1) / 16384 + 1) * rows > 304 ? run<T, 512, 1, 3>(p, span, rows, stream)
-                                               : run<T, 256, 4, 4>(p, span, rows, stream);
+  if (((span - 1) / 8192 + 1) * rows <= 4 * 152) return run<T, 256, 4, 4>(p, span, rows, stream);
+  if (span > 8192 && p.r.tokens != nullptr && p.r.max_tokens > 8192)
+    return run<T, 512, 1, 3>(p, span, rows, stream);
+  return run<T, 256, 1, 6>(p, span, rows, stream);
 }
 
 }  // namespace

@@ -72,6 +72,7 @@ class Case:
         got, got_bits = self.logits.double().cpu().numpy(), bits(self.logits)
         assert np.array_equal(around[:, self.V:], bits(self.full)[:, self.V:])
         half = torch.finfo(self.dtype).eps / 2
+        least = 5 * 2.0 ** -150 + (2.0 ** -134 if self.dtype == torch.bfloat16 else 0.0)
         for b in range(self.B):
             if b in left:
                 assert np.array_equal(got_bits[b], was_bits[b])
@@ -86,7 +87,13 @@ class Case:
                 if nb else (), mask=self.allowed[b])
             assert np.array_equal(got_bits[b][~named], was_bits[b][~named])
             with np.errstate(invalid="ignore"):
-                near = np.abs(got[b] - ref) <= 5 * 2.0 ** -24 * size + half * np.abs(ref)
+                # (below the smallest normal number a rounding is half the smallest number: 2^-150 of
+                # 32 bits, 2^-134 of bf16)
+                near = np.abs(got[b] - ref) <= 5 * 2.0 ** -24 * size + half * np.abs(ref) + least
+            # beyond the type's largest number the result is infinite (or, by less than half a step,
+            # that number)
+            big = np.abs(ref) > torch.finfo(self.dtype).max
+            near |= big & (got[b] == np.sign(ref) * np.inf)
             assert np.all(near | (got[b] == ref) | (np.isnan(ref) & np.isnan(got[b]))), b
 
 
@@ -178,4 +185,16 @@ def test_a_token_outside_the_vocabulary(cuda_lib, key, value):
     c.args["prompt"][:] = 4
     c.args["n_bias"][:] = 9
     c.args[key][2, 9] = value
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,V,hist,nb,masks,pad", [
+    (16, 131075, 3, 2, [0.5, None, 0.999, 0.001], 0),          # a token or two named here and there
+    (20, 262144, 9000, 40, [None, 0.97, 0.5, 0.02], 0),        # long histories, much work
+    (90, 65536, 500, 10, [None, 0.9], 3), (700, 1000, 100, 3, [0.3, None], 0)])
+def test_many_rows(cuda_lib, dtype, B, V, hist, nb, masks, pad):
+    c = Case(B, B, V, hist, nb, [masks[b % len(masks)] for b in range(B)], dtype, pad)
+    c.args["repetition"][3] = 1e-39            # a quotient that no reciprocal gives
+    c.args["repetition"][4] = 3e38
     c.check()
