@@ -12,9 +12,8 @@
 // as many readers as many short ones.  What has to be copied goes into a list in
 // the workspace; copy_kernel moves it in every cache, one warp for the keys or
 // values of one (page, head), four 16-byte loads a lane in flight.
-// Four beams forked and grown 9.9 us, 128 beams over 30 layers 21 us (30 with
-// everything cold: half of it the decision, whose tables come from memory), 3400
-// pages of 16 layers made dense 149 us, 7.3 TB/s.
+// Four beams forked and grown 9.8 us, 128 beams over 30 layers 21 us (27 with
+// everything cold), 3400 pages of 16 layers made dense 147 us, 7.4 TB/s.
 #include <mutex>
 
 #include "kv8.cuh"
