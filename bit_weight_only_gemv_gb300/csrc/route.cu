@@ -389,6 +389,7 @@ __device__ __forceinline__ void route_rows(const RouteParams& p, long long first
       }
     }
     bool close = wide;   // too many compared scores nearer than fp32 can tell
+    bool in = true;      // whether this lane's group is chosen
     if (groups) {
       // the group's score in each of its lanes; one logit alone decides where no sum is taken
       float gs;
@@ -411,7 +412,7 @@ __device__ __forceinline__ void route_rows(const RouteParams& p, long long first
         const float o = __shfl_sync(kFull, gs, i << p.shift);
         rank += o > gs || (o == gs && i < g);
       }
-      bool in = g < p.G && rank < p.top_groups;
+      in = g < p.G && rank < p.top_groups;
       if (sums) {
         const float least = warp_min_f(in ? gs : INFINITY);
         const float next = warp_max_f(in || g >= p.G ? -INFINITY : gs);
@@ -471,7 +472,21 @@ __device__ __forceinline__ void route_rows(const RouteParams& p, long long first
         pop();
         if (m == 0 || (kth >> kPlace) - (m >> kPlace) >= near) break;
         if (cnt == 32) {
-          close = true;
+          // still none: experts of the k-th one's own inputs have its score, and are in order already
+          const uint32_t kp = places - (kth & places);
+          const int kl = (int)(kp / V);
+          const int ek = (kl >> p.shift) * p.size + (kl & ((1 << p.shift) - 1)) * p.each + (int)(kp % V);
+          const float xk = logit(p, row, ek), bk = biased ? load_in(p.bias + ek) : 0.0f;
+          bool other = false;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float f = biased ? fmaf(c[i], unit, kBase + 4.0f)
+                                   : fmaxf(fmaf(x[i] - top, kOne / 32.0f, kBase + (kOne - 2.0f)), kBase + 1.0f);
+            const int far = (int)((__float_as_uint(f) << kPlace) >> kPlace) - (int)(kth >> kPlace);
+            if (in && i < n && (uint32_t)abs(far) < near && !(x[i] == xk && (!biased || load_in(p.bias + e0 + i) == bk)))
+              other = true;
+          }
+          close |= __any_sync(kFull, other);
           break;
         }
         if (lane == cnt) my = m;

@@ -272,3 +272,41 @@ def test_one_workspace_for_every_call(cuda_lib):
     want = calls(lambda i: torch.zeros(sizes[i], dtype=torch.uint8, device="cuda"))
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(want, calls(lambda i: one)))
+
+
+def test_two_streams_at_once(cuda_lib):
+    """The same calls on buffers of their own, on two streams at the same time: the results of each alone."""
+    from _pages import Pages
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sides = []
+    for i in range(2):
+        p = Pages(20 + i, [300, 41, 77, 16], layers=6, spare=30).to_gpu(most_rows=8)
+        gen = torch.Generator(device="cuda").manual_seed(i)
+        sides.append(dict(p=p, parents=torch.tensor([0, 0, 1, 2, 3, 0], dtype=torch.int32, device="cuda"),
+                          x=torch.randn((700, 64), generator=gen, device="cuda"),
+                          head=torch.randn((9, 5001), generator=gen, device="cuda"),
+                          hist=torch.randint(0, 5001, (9, 800), generator=gen, device="cuda", dtype=torch.int32)))
+
+    def calls(s, stream):
+        p = s["p"]
+        ids, w = lib.route(lib.Router(64, 5, groups=8, top_groups=3, score="sigmoid"), s["x"], stream=stream)
+        head = s["head"].clone()
+        rules = lib.LogitRules(tokens=s["hist"], lens=torch.full((9,), 800, dtype=torch.int32, device="cuda"),
+                               frequency=torch.full((9,), 0.25, device="cuda"))
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        lib.adjust_logits(head, rules, p.status, stream=stream)
+        t, n, r = lib.kv8_fork(p.dev, p.table, p.lens, p.refs, s["parents"], p.ws, p.status, stream=stream)
+        lib.kv8_reserve(t, n, r, p.P, None, p.ws, p.status, stream=stream)
+        return [ids, w, head, t, n, r, rules]
+
+    alone = []
+    for s in sides:
+        alone.append(calls(s, None)[:-1])
+        torch.cuda.synchronize()
+    for _ in range(25):
+        both = [calls(s, stream) for s, stream in zip(sides, streams)]
+        torch.cuda.synchronize()
+        for one, two in zip(alone, both):
+            assert all(torch.equal(a, b) for a, b in zip(one, two))
+    assert all(int(s["p"].status) == 0 for s in sides)

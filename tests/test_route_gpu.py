@@ -241,3 +241,15 @@ def test_many_tokens_as_each_alone(cuda_lib, E, k, G, tg, score, bias, best, dty
             assert (ids[t] == POISON).all() and (w[t] == POISON).all()
         else:
             assert np.array_equal(ids[t], ref[0]), (t, ids[t], ref[0])
+
+
+@pytest.mark.parametrize("E,pad,dtype", [(256, 1, torch.bfloat16), (128, 2, torch.float32), (250, 0, torch.bfloat16)])
+def test_many_tokens_at_any_stride(cuda_lib, E, pad, dtype):
+    rng = np.random.default_rng(E)
+    x, b = rng.normal(size=(4200, E)), rng.normal(size=E) * 0.05
+    ids, w, status, held = run(x, 6, 2, 1, 1, "sigmoid", True, 1.0, b, dtype, pad)
+    assert status == 0
+    for t in (0, 1, 2047, 4198, 4199):
+        ref = serve.route_row(held[t], b.astype(np.float32).astype(np.float64), 6, 2, 1, 1, True, True, 1.0)
+        assert np.array_equal(ids[t], ref[0]) and np.allclose(w[t], ref[1], rtol=2.0 ** -18, atol=0)
+    check(x[4100:], 6, 2, 1, 1, "sigmoid", True, 1.0, b, dtype, pad)
