@@ -804,16 +804,27 @@ def _kv8_bytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+_handles = {}   # stream handles as ctypes pointers
+_CONVERTED = (ctypes._SimpleCData, ctypes.Array, type(ctypes.byref(ctypes.c_int())))
+
+
 def _kv8_call(fn, name, args, keep):
     """call(pdl=False, stream=None) that enqueues fn(*args) again."""
     dev = keep[0].device.index
     if dev is None:
         dev = torch.cuda.current_device()
     raw = torch._C._cuda_getCurrentRawStream   # current_stream() builds an object each time
+    # the arguments converted once: the same function, without types to convert by at each call
+    bare = load()[name]
+    bare.restype = ctypes.c_int
+    args = tuple(a if isinstance(a, _CONVERTED) else t(a) for t, a in zip(fn.argtypes, args))
 
     def call(pdl: bool = False, stream=None):
-        code = fn(*args, W4_FLAG_PDL if pdl else 0,
-                  raw(dev) if stream is None else stream.cuda_stream)
+        handle = raw(dev) if stream is None else stream.cuda_stream
+        at = _handles.get(handle)
+        if at is None:
+            at = _handles[handle] = ctypes.c_void_p(handle)
+        code = bare(*args, W4_FLAG_PDL if pdl else 0, at)
         if code:
             _check(code, name)
 

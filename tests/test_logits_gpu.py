@@ -61,8 +61,9 @@ class Case:
     def check(self, left=(), code=None):
         """Rows in `left` keep their bits, and the call reports `code`.
 
-        A quotient or product, a product and two differences, one sum: five roundings of 2^-24 of
-        the terms' magnitudes at most, then half a step of the type."""
+        The repetition's reciprocal and its product, the frequency's fused product and difference, the
+        presence's difference, the bias's sum: five roundings of 2^-24 of the terms' magnitudes at
+        most, then half a step of the type."""
         a = self.args
         was, was_bits, around = self.logits.double().cpu().numpy(), bits(self.logits), bits(self.full)
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
