@@ -9,7 +9,7 @@
 // values that are not finite), a second one, from registers or L1, writes the
 // codes; older codes are touched only when the step grows.  Latency bounds
 // it: the chain is lengths, then rows and page together, then the old step.
-// One token for each of 8 sequences: 3.4 us, of which the host's call is as
+// One token for each of 8 sequences: 3.1 us, of which the host's call is as
 // much; 16 chunks of up to 256 tokens, 8 heads of 128 channels: 8.4 us, 1.5 TB/s.
 #include "kv8.cuh"
 
