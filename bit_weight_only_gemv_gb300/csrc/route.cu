@@ -108,11 +108,15 @@ __device__ __noinline__ int refine(const RouteParams& p, long long row, double* 
   __syncwarp();
   uint32_t in = kFull;   // chosen groups
   if (p.G > 1) {
+    // by one logit alone where no sum is taken, as everywhere: scores that are 1 or 0 in 64 bits are
+    // equal where their logits are not
+    const bool by_logit = p.bias == nullptr && p.best == 1;
     double gs = -INFINITY;
     if (lane < p.G) {
       double a = -INFINITY, b = -INFINITY;
       for (int i = 0; i < p.size; ++i) {
-        const double c = sm[lane * p.size + i];
+        const int e = lane * p.size + i;
+        const double c = by_logit ? (double)logit(p, row, e) : sm[e];
         b = fmax(b, fmin(a, c));
         a = fmax(a, c);
       }

@@ -917,8 +917,8 @@ size_t w4_kv8_evict_workspace_bytes(const w4_kv8_cache *cache, const w4_kv8_batc
  * Equal scores are in order of number, lowest first, of experts and of
  * groups.  The choice is that of c in 64 bits: scores are compared in 32 bits,
  * and a token with two that are nearer than 32 bits can tell goes through 64;
- * without a bias experts are compared by x itself.  Weights are fp32, off by a
- * few units in the last place.
+ * without a bias experts, and groups with group_best 1, are compared by x itself.
+ * Weights are fp32, off by a few units in the last place.
  *
  * ids, weights int32 and fp32 [rows][top_k].
  * logits       bf16 or fp32 (W4_TYPE_*), row t at element t * row_stride,

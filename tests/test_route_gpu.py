@@ -253,3 +253,22 @@ def test_many_tokens_at_any_stride(cuda_lib, E, pad, dtype):
         ref = serve.route_row(held[t], b.astype(np.float32).astype(np.float64), 6, 2, 1, 1, True, True, 1.0)
         assert np.array_equal(ids[t], ref[0]) and np.allclose(w[t], ref[1], rtol=2.0 ** -18, atol=0)
     check(x[4100:], 6, 2, 1, 1, "sigmoid", True, 1.0, b, dtype, pad)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("spread", [20, 60, 1000])
+@pytest.mark.parametrize("T,E,G,tg,k", [(300, 256, 8, 4, 8), (4099, 256, 8, 4, 8), (4099, 128, 4, 2, 6),
+                                        (200, 512, 16, 5, 16), (200, 1024, 8, 2, 3)])
+def test_groups_by_their_best_logit_alone(cuda_lib, score, spread, T, E, G, tg, k):
+    """Scores of 1 or of 0, in 64 bits too, do not make groups equal whose logits are not: with
+    group_best 1 and no bias the groups' order is that of their largest logits, in either type."""
+    rng = np.random.default_rng(spread + E)
+    x = torch.from_numpy(rng.normal(size=(T, E)) * spread).bfloat16().double().numpy()   # both types hold it
+    got = {}
+    for dtype in (torch.float32, torch.bfloat16):
+        got[dtype], _, status, held = run(x, k, G, tg, 1, score, True, 1.0, None, dtype)
+        assert status == 0 and np.array_equal(held, x)
+    assert np.array_equal(got[torch.float32], got[torch.bfloat16])
+    for t in range(0, T, max(1, T // 300)):
+        ref = serve.route_row(x[t], None, k, G, tg, 1, score == "sigmoid", True, 1.0)
+        assert np.array_equal(got[torch.float32][t], ref[0]), (t, got[torch.float32][t], ref[0])
