@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         const uint8_t* sti = tk.st;
         bool ok = true;
         if (tk.ids != nullptr) {
-          const int e = __ldg(tk.ids + item);
+          const int e = load_in(tk.ids + item);
           ok = e >= 0 && e < tk.num_experts;
           qwi += (unsigned long long)(ok ? e : 0) * tk.qw_stride16 * 16ull;
           sti += (unsigned long long)(ok ? e : 0) * tk.st_stride16 * 16ull;

@@ -26,8 +26,9 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 
 // A value that an earlier kernel may have written, read after pdl_wait().  The non-coherent loads
-// (__ldg) are not ordered by that wait: the compiler may take them to the kernel's start, where
-// a kernel before it that has let its dependents start is still running.
+// (__ldg, or plain ones through const __restrict__ pointers) are not ordered by that wait: the
+// compiler may take them to the kernel's start, where a kernel before it that has let its dependents
+// start is still running.  They are left for weights alone.
 template <typename T>
 __device__ __forceinline__ T load_in(const T* p) {
   return *p;

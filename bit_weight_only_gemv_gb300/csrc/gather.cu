@@ -14,11 +14,11 @@ namespace w4 {
 __global__ void __launch_bounds__(256) gather_kernel(__nv_bfloat16* __restrict__ out,
                                                       const uint32_t* __restrict__ qw,
                                                       const uint16_t* __restrict__ st,
-                                                      const int32_t* __restrict__ ids, int V,
-                                                      int K, int32_t* status) {
+                                                      const int32_t* ids, int V, int K,
+                                                      int32_t* status) {
   pdl_wait();   // ids and the output may belong to the previous kernel
   const int t = blockIdx.y;
-  const int id = __ldg(ids + t);
+  const int id = load_in(ids + t);
   if (id < 0 || id >= V) {
     if (threadIdx.x == 0 && blockIdx.x == 0) report(status, W4_ERR_INDEX);
     return;

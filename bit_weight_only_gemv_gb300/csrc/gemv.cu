@@ -144,8 +144,8 @@ __device__ __noinline__ void stage_x_gated(const GemvParams& p, int nslots, uint
       uint4 gv[4], uv[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        gv[i] = __ldg(gs + i);
-        uv[i] = __ldg(us + i);
+        gv[i] = load_in(gs + i);
+        uv[i] = load_in(us + i);
       }
       mx = silu_mul_group(gv, uv, h);
     } else {
@@ -169,7 +169,7 @@ __device__ void stage_x(const GemvParams& p, int item0, int nslots, uint8_t* xs,
       const uint4* src =
           reinterpret_cast<const uint4*>(p.x + (long long)xrow * p.K + (long long)g * 32);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __ldg(src + i);
+      for (int i = 0; i < 4; ++i) v[i] = load_in(src + i);
     }
     store_staged_group(v, xs + (long long)j * 4 * p.Kgp * 16 + g * 16, p.Kgp * 16,
                        xscale + (long long)j * p.Kgp + g, g < p.Kg);
@@ -220,7 +220,7 @@ __device__ __forceinline__ bool item_arrays(const GemvParams& p, int item, const
                                             const uint8_t** s) {
   long long blk = item;
   if (p.ids != nullptr) {
-    const int e = __ldg(p.ids + item);
+    const int e = load_in(p.ids + item);
     if (e < 0 || e >= p.num_experts) return false;
     blk = e;
   }
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas(MR, RW))
         break;
       }
       int rid = 0;   // real expert id (RID), loaded together with the routed id
-      if constexpr (RID) rid = __ldg(p.eids + wk.item);
+      if constexpr (RID) rid = load_in(p.eids + wk.item);
       if (bad || (!p.dyn && !dense && !item_arrays(p, wk.item, &qwi, &sti))) {
         if (!reported && lane == 0) report(p.status, W4_ERR_INDEX);
         reported = true;
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas(MR, RW))
       int wcode = W4_OK;
       if constexpr (RID) {
         const bool in_range = rid >= 0 && rid < p.num_real;
-        const int holder = p.slot_expert != nullptr ? __ldg(p.slot_expert + __ldg(p.ids + wk.item))
+        const int holder = p.slot_expert != nullptr ? load_in(p.slot_expert + load_in(p.ids + wk.item))
                                                     : rid;
         const long long rr = in_range ? rid : 0;
         if (p.escale != nullptr) ov.s = p.escale + rr * p.N + wk.row0;

@@ -46,10 +46,10 @@ struct Seq {
 
 __device__ __forceinline__ Seq sequence(const Batch& bt, int P, int b) {
   Seq s;
-  s.len = __ldg(bt.lens + b);
+  s.len = load_in(bt.lens + b);
   if (bt.offsets != nullptr) {
-    s.row0 = __ldg(bt.offsets + b);
-    s.n = __ldg(bt.offsets + b + 1) - s.row0;
+    s.row0 = load_in(bt.offsets + b);
+    s.n = load_in(bt.offsets + b + 1) - s.row0;
   } else {
     s.row0 = b;
     s.n = 1;

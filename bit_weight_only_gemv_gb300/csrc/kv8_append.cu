@@ -40,8 +40,8 @@ __device__ __forceinline__ void unpack8(const uint4& w, float f[8]) {
 }
 
 __global__ void __launch_bounds__(256) append_kernel(Cache c, Batch bt,
-                                                     const __nv_bfloat16* __restrict__ k,
-                                                     const __nv_bfloat16* __restrict__ v,
+                                                     const __nv_bfloat16* k,
+                                                     const __nv_bfloat16* v,
                                                      long long row_stride, int32_t* status) {
   __shared__ uint32_t red[8];
   __shared__ uint32_t lo_sm[256 / 2][4], hi_sm[256 / 2][4];   // [thread][2 words] halves
@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(256) append_kernel(Cache c, Batch bt,
 #pragma unroll
   for (int z = 0; z < kHeld; ++z)
     if (r0 + z * rstep < rows)
-      held[z] = __ldg(reinterpret_cast<const uint4*>(src + (r0 + z * rstep) * row_stride));
-  const int page = __ldg(bt.table + (long long)b * bt.max_pages + lp);
+      held[z] = load_in(reinterpret_cast<const uint4*>(src + (r0 + z * rstep) * row_stride));
+  const int page = load_in(bt.table + (long long)b * bt.max_pages + lp);
   if (page < 0 || page >= c.num_pages) {
     if (tid == 0) report(status, W4_ERR_INDEX);
     return;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(256) append_kernel(Cache c, Batch bt,
   for (int z = 0; z < kHeld; ++z)
     if (r0 + z * rstep < rows) look(held[z]);
   for (int r = r0 + kHeld * rstep; r < rows; r += rstep)
-    look(__ldg(reinterpret_cast<const uint4*>(src + r * row_stride)));
+    look(load_in(reinterpret_cast<const uint4*>(src + r * row_stride)));
   top = __reduce_max_sync(0xffffffffu, top);
   if ((tid & 31) == 0) red[tid >> 5] = top;
   __syncthreads();
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(256) append_kernel(Cache c, Batch bt,
   for (int z = 0; z < kHeld; ++z)
     if (r0 + z * rstep < rows) store(held[z], r0 + z * rstep);
   for (int r = r0 + kHeld * rstep; r < rows; r += rstep)
-    store(__ldg(reinterpret_cast<const uint4*>(src + r * row_stride)), r);
+    store(load_in(reinterpret_cast<const uint4*>(src + r * row_stride)), r);
   const bool grow = has_old && step != s0;
   const float ratio = grow ? __fdiv_rn(s0, step) : 1.0f;
   if (grow) {

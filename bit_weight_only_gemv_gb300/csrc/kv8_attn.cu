@@ -100,7 +100,7 @@ struct AttnParams {
 
 // Pages chosen for a (sequence, head); a count that is none is 0 (refused later).
 __device__ __forceinline__ int chosen(const AttnParams& p, long long bh, bool* bad) {
-  const int n = __ldg(p.n_sel + bh);
+  const int n = load_in(p.n_sel + bh);
   if (n < 0 || n > p.max_sel) {
     *bad = true;
     return 0;
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
         if (n_pages >= 0) {
           const int per = p.c.P / kSlice, e = sl / per;
           if (e < n_pages) {
-            lp = __ldg(p.sel + bh * p.max_sel + e);
+            lp = load_in(p.sel + bh * p.max_sel + e);
             if (lp < 0 || (long long)lp * p.c.P >= s.len) {
               bad = true;
             } else {
@@ -258,13 +258,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQ>::kPerSm)
           read = d.tok < t.hi;
         }
         if (read) {
-          const int page = __ldg(table + lp);
+          const int page = load_in(table + lp);
           if (page < 0 || page >= p.c.num_pages) {
             bad = true;
           } else {
             d.page = page;
-            ks = __ldg(p.c.ks + p.c.pair(page, h));
-            vs = __ldg(p.c.vs + p.c.pair(page, h));
+            ks = load_in(p.c.ks + p.c.pair(page, h));
+            vs = load_in(p.c.vs + p.c.pair(page, h));
           }
         }
         meta[k & (kRing - 1)] = d;

@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
           } else {
             float2 m = make_float2(0.0f, 0.0f);
             if (tok < u.t.hi) {
-              page = __ldg(table + tok / p.c.P);
+              page = load_in(table + tok / p.c.P);
               if (page < 0 || page >= p.c.num_pages) {
                 page = -1;
                 refused[unit % kUnitRing] = 1;

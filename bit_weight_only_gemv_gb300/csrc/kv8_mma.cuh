@@ -85,7 +85,7 @@ __device__ __forceinline__ void load_query(const __nv_bfloat16* row, int j, uint
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
     const int ch = D == 64 ? 16 * j + 4 * s : 128 * (s / 8) + 32 * j + 4 * (s % 8);
-    raw[s] = row == nullptr ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(row + ch));
+    raw[s] = row == nullptr ? make_uint2(0, 0) : load_in(reinterpret_cast<const uint2*>(row + ch));
   }
 }
 

@@ -274,15 +274,15 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
       const int i = i0 + k * per + sub;
-      page[k] = i < c1 ? __ldg(table + i) : 0;
+      page[k] = i < c1 ? load_in(table + i) : 0;
     }
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
       const bool ok = page[k] >= 0 && page[k] < p.c.num_pages;
       if (!ok) page[k] = 0;
-      r[k] = __ldg(reinterpret_cast<const int4*>(p.c.ranges + p.c.pair(page[k], h) * 2 * D) + l);
+      r[k] = load_in(reinterpret_cast<const int4*>(p.c.ranges + p.c.pair(page[k], h) * 2 * D) + l);
       // a page that is none: a mark that the choice refuses (no score is it)
-      ks[k] = ok ? __ldg(p.c.ks + p.c.pair(page[k], h)) : __uint_as_float(kNoPage);
+      ks[k] = ok ? load_in(p.c.ks + p.c.pair(page[k], h)) : __uint_as_float(kNoPage);
     }
   };
   int i0 = c0 + warp * (32 / lanes);
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kTopThreads) evict_top_kernel(const EvictParam
   pdl_wait();
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const int P = p.c.P;
-  const int len = __ldg(p.bt.lens + b);
+  const int len = load_in(p.bt.lens + b);
   const long long bh = (long long)b * p.c.H + h;
   const int32_t* table = p.bt.table + (long long)b * p.bt.max_pages;
   bool bad = len < 0 || len > p.bt.max_len;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kTopThreads) evict_top_kernel(const EvictParam
 #pragma unroll
     for (int k = 0; k < per; ++k) keys[k] = 0u;
     if (t0 < n) {
-      const int page = __ldg(table + t0 / P);
+      const int page = load_in(table + t0 / P);
       if (page < 0 || page >= p.c.num_pages) {
         bad = true;
       } else {
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kTopThreads) evict_top_kernel(const EvictParam
   } else {
     uint32_t* keys = p.keys + bh * p.keys_row;
     for (int t = tid; t < n; t += nth) {
-      const int page = __ldg(table + t / P);
+      const int page = load_in(table + t / P);
       uint32_t u = kForced;
       if (page < 0 || page >= p.c.num_pages)
         bad = true;
@@ -472,10 +472,10 @@ __global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const Evict
   const int P = p.c.P, D = p.c.D;
   const long long bh = (long long)b * p.c.H + h;
   if (j >= p.dst_pages || __ldcg(p.go + bh) != 1) return;   // refused before
-  const int count = min(__ldg(p.bt.lens + b), p.budget);
+  const int count = min(load_in(p.bt.lens + b), p.budget);
   const int n = min(P, count - j * P);
   if (n <= 0) return;
-  const int dst = __ldg(p.dst_table + (long long)b * p.dst_pages + j);
+  const int dst = load_in(p.dst_table + (long long)b * p.dst_pages + j);
   if (dst < 0 || dst >= p.c.num_pages) {
     if (lane == 0) report(p.status, W4_ERR_INDEX);
     return;
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(const Evict
   float mk = 0.0f, mv = 0.0f;
   for (int i = lane; i < n; i += 32) {
     const int t = __ldcg(p.kept + bh * p.budget + (long long)j * P + i);
-    const int page = __ldg(p.bt.table + (long long)b * p.bt.max_pages + t / P);   // checked before
+    const int page = load_in(p.bt.table + (long long)b * p.bt.max_pages + t / P);   // checked before
     const long long pr = p.c.pair(page, h);
     const Token x = {p.c.block(page, h) + (long long)(t % P) * D, p.c.ks[pr], p.c.vs[pr]};
     p.c.weight[p.c.pair(dst, h) * P + i] = p.c.weight[pr * P + t % P];

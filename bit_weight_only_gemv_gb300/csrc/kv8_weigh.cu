@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const Seq s = sequence(p.bt, p.c.P, kSel ? e / p.c.H : e);
     if (!s.ok || s.n == 0) return 0;
     if (kSel) {
-      const int n = __ldg(p.n_sel + e);
+      const int n = load_in(p.n_sel + e);
       if (n <= 0 || n > p.max_sel) {
         if (n != 0 && blockIdx.x == 0) report(p.status, W4_ERR_INDEX);
         return 0;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int b = kSel ? entry / p.c.H : entry;
     const Seq s = sequence(p.bt, p.c.P, b);
     Tile t = tile_of(s, p.G, p.window, 0, kRows, kSlice);   // one row tile
-    if (kSel) t.slices = __ldg(p.n_sel + entry) * per;
+    if (kSel) t.slices = load_in(p.n_sel + entry) * per;
     const int h = kSel ? entry - b * p.c.H : quotient(off, t.slices);
     const int sl0 = kSel ? (int)off : (int)(off - (long long)h * t.slices);
     const int sl1 = (int)min((long long)t.slices, sl0 + (run.g1 - g));
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             Meta d = {-1, t.lo + sl * kSlice, 0.0f, 0};
             bool read = d.tok < t.hi;
             if (kSel) {
-              const int lp = __ldg(p.sel + (long long)entry * p.max_sel + sl / per);
+              const int lp = load_in(p.sel + (long long)entry * p.max_sel + sl / per);
               read = lp >= 0 && (long long)lp * p.c.P < s.len;
               if (!read) report(p.status, W4_ERR_INDEX);
               d.tok = read ? lp * p.c.P + sl % per * kSlice : 0;
@@ -166,12 +166,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                       !(p.window > 0 && d.tok + kSlice <= (long long)t.pmin + 1 - p.window);
             }
             if (read) {
-              const int page = __ldg(table + d.tok / p.c.P);
+              const int page = load_in(table + d.tok / p.c.P);
               if (page < 0 || page >= p.c.num_pages) {
                 report(p.status, W4_ERR_INDEX);
               } else {
                 d.page = page;
-                ks = __ldg(p.c.ks + p.c.pair(page, h));
+                ks = load_in(p.c.ks + p.c.pair(page, h));
               }
             }
             meta[kk & (kRing - 1)] = d;
@@ -328,22 +328,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     page[z] = -1;
     f[z] = sum[z][0] = sum[z][1] = 0.0f;
     if (tok[z] < s.len) {
-      page[z] = __ldg(p.bt.table + (long long)b * p.bt.max_pages + tok[z] / p.c.P);
+      page[z] = load_in(p.bt.table + (long long)b * p.bt.max_pages + tok[z] / p.c.P);
       if (page[z] < 0 || page[z] >= p.c.num_pages) {
         page[z] = -1;
         if (lane == 0) report(p.status, W4_ERR_INDEX);
       }
     }
     const bool have = page[z] >= 0;
-    if (have) f[z] = __ldg(p.c.ks + p.c.pair(page[z], h)) * (p.scale * kLog2e);
+    if (have) f[z] = load_in(p.c.ks + p.c.pair(page[z], h)) * (p.scale * kLog2e);
     const uint8_t* blk = p.c.kc + (have ? p.c.block(page[z], h) + (long long)(tok[z] % p.c.P) * D : 0);
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       const int chunk = D == 64 ? j : 8 * (c / 2) + 2 * j + (c & 1);
       uint4 x = make_uint4(0, 0, 0, 0), y = x;
       if (have) {
-        x = __ldg(reinterpret_cast<const uint4*>(blk + i * D + chunk * 16));
-        y = __ldg(reinterpret_cast<const uint4*>(blk + (i + 8) * D + chunk * 16));
+        x = load_in(reinterpret_cast<const uint4*>(blk + i * D + chunk * 16));
+        y = load_in(reinterpret_cast<const uint4*>(blk + (i + 8) * D + chunk * 16));
       }
       const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll

@@ -108,6 +108,13 @@ struct Units {
       h -= up * p.c.H;
       b += step_b + up;
       s = sequence(p.bt, p.c.P, seq);
+      // the same in every lane, which the compiler knows of a reduction and not of a load: without
+      // it a unit's loops are compiled as if lanes could part (38.2 -> 41.0 us)
+      const unsigned lanes = __activemask();
+      s.len = __reduce_max_sync(lanes, s.len);
+      s.n = __reduce_max_sync(lanes, s.n);
+      s.row0 = __reduce_max_sync(lanes, s.row0);
+      s.ok = __any_sync(lanes, s.ok);
       if (!s.ok) {
         if (reports && blk0 == 0 && head == 0) report(p.status, W4_ERR_INDEX);
         continue;
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       const int kb = n % kKeyBufs;
       const int32_t* table = p.bt.table + (long long)u.seq * p.bt.max_pages;
       auto page_of = [&](int t) {
-        return u.blk0 + t < u.s.len ? __ldg(table + ((u.blk0 + t) >> lg)) : -1;
+        return u.blk0 + t < u.s.len ? load_in(table + ((u.blk0 + t) >> lg)) : -1;
       };
       int pages[kEach], own[kTokens / kKeyThreads];
       float f[kTokens / kKeyThreads];
@@ -295,20 +302,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
       for (int i = 0; i < kTokens / kKeyThreads; ++i) {
         f[i] = 0.0f;
         if ((unsigned)own[i] < (unsigned)p.c.num_pages)
-          f[i] = __ldg(p.c.ks + p.c.pair(own[i], u.head));
+          f[i] = load_in(p.c.ks + p.c.pair(own[i], u.head));
       }
       const uint32_t keys = sb + kb * kTiles * S::kBytes;
+      uint4 v[kBatch];
+      auto fetch = [&](int z) {   // the z-th chunk of this thread
+        const int x = kt + z * kKeyThreads, tok = u.blk0 + x / kChunks;
+        uint4& w = v[z % kBatch];
+        w = make_uint4(0, 0, 0, 0);
+        if ((unsigned)pages[z] < (unsigned)p.c.num_pages)
+          w = load_in(reinterpret_cast<const uint4*>(p.c.kc + p.c.block(pages[z], u.head) +
+                                                     (tok & (p.c.P - 1)) * D + x % kChunks * 16));
+      };
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) fetch(i);
 #pragma unroll
       for (int i0 = 0; i0 < kEach; i0 += kBatch) {
-        uint4 v[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int x = kt + (i0 + i) * kKeyThreads, tok = u.blk0 + x / kChunks;
-          v[i] = make_uint4(0, 0, 0, 0);
-          if ((unsigned)pages[i0 + i] < (unsigned)p.c.num_pages)
-            v[i] = __ldg(reinterpret_cast<const uint4*>(p.c.kc + p.c.block(pages[i0 + i], u.head) +
-                                                        (tok & (p.c.P - 1)) * D + x % kChunks * 16));
-        }
         if (i0 == 0) {
           // the first loads are on their way before the keys' place is free.  A
           // unit's factors stay until its weights are done, which this does not
@@ -336,6 +345,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                  codes_bf16(v[i].y, 0x4140), codes_bf16(v[i].y, 0x4342));
           sts128(to + (((e + 1) ^ (r & 7)) << 4), codes_bf16(v[i].z, 0x4140),
                  codes_bf16(v[i].z, 0x4342), codes_bf16(v[i].w, 0x4140), codes_bf16(v[i].w, 0x4342));
+          // in the place of what is stored, so that as many loads stay on their way
+          if (i0 + kBatch < kEach) fetch(i0 + kBatch + i);
         }
       }
       if (!ok) break;
