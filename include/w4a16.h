@@ -1064,8 +1064,9 @@ size_t w4_kv8_pages_workspace_bytes(int batch, int num_pages);
  *            as they were.
  * new_lens   int32 [new_batch]: lens[parents[b]], or 0.
  * new_refs   int32 [num_pages].  refs - the old rows' + the new rows'.
- * table, lens, refs are not changed, and must not overlap the new ones.  They stay
- * as good as they were until something is written into a page that they name.
+ * table, lens, refs and parents are not changed, and none of the new arrays may
+ * overlap them or each other (W4_ERR_ARG).  The old ones stay as good as they were
+ * until something is written into a page that they name.
  * A parent outside [-1, batch), or one whose length or pages break their
  * bounds: W4_ERR_INDEX, new_lens[b] = -1, and row b's own old pages stay counted.  An
  * old row that breaks them gives nothing back (W4_ERR_INDEX).
@@ -1110,8 +1111,9 @@ w4_status w4_kv8_reserve(int32_t *table, int32_t *lens, int32_t *refs, const int
  *            they were.
  * new_refs   int32 [num_pages].
  * used       int32 [1]: one past the highest page in use after the call.
- * table and refs are not changed, and must not overlap the new ones; the pages that
- * moved keep their old contents until they are taken again.
+ * table, lens and refs are not changed, and none of new_table, new_refs and used may
+ * overlap them or each other (W4_ERR_ARG); the pages that moved keep their old
+ * contents until they are taken again.
  * A row whose length or pages break their bounds: W4_ERR_INDEX, its new row is left
  * unwritten, and pages that it alone names stay.
  * flags: W4_FLAG_PDL.

@@ -211,3 +211,28 @@ def test_page_references_keep_their_counts():
         for b, n in enumerate(l3):
             k = -(-int(n) // P)
             assert [back.get(p, p) for p in t4[b, :k]] == t3[b, :k].tolist()
+
+
+@pytest.mark.parametrize("name,over", [
+    ("fork", dict(new_lens=4 * P0)),                    # the parents' own array
+    ("fork", dict(new_lens=4 * P0 + 8)), ("fork", dict(new_table=4 * P0 - 44)),
+    ("fork", dict(new_refs=4 * P0 - 28)), ("fork", dict(new_lens=3 * P0 + 28)),
+    ("fork", dict(new_refs=2 * P0 + 8)), ("fork", dict(new_table=2 * P0 - 44)), ("fork", dict(new_lens=P0 + 44)),
+    ("fork", dict(new_lens=5 * P0)), ("fork", dict(new_refs=5 * P0 + 44)), ("fork", dict(new_lens=7 * P0 + 28)),
+    ("compact", dict(used=P0)), ("compact", dict(used=2 * P0 + 8)), ("compact", dict(used=3 * P0 + 28)),
+    ("compact", dict(used=5 * P0 + 44)), ("compact", dict(used=7 * P0)), ("compact", dict(new_table=2 * P0)),
+    ("compact", dict(new_refs=2 * P0 + 8)), ("compact", dict(new_refs=5 * P0 + 44))])
+def test_page_outputs_overlap_nothing(name, over):
+    """An output that lies on an input or on another output, by one word at the least: a large pool's
+    CTAs would read the one while others write the other.  (Without a workspace nothing ever starts.)"""
+    assert pages(name, ws_bytes=0, **over) == ARG
+
+
+@pytest.mark.parametrize("name,over", [
+    ("fork", dict(new_lens=4 * P0 + 12)), ("fork", dict(new_lens=4 * P0 - 12)), ("fork", dict(new_table=4 * P0 - 48)),
+    ("fork", dict(new_refs=2 * P0 + 12)), ("fork", dict(new_refs=5 * P0 + 48)), ("fork", dict(new_lens=7 * P0 + 32)),
+    ("compact", dict(used=P0 - 4)), ("compact", dict(used=2 * P0 + 12)), ("compact", dict(used=5 * P0 + 48)),
+    ("compact", dict(new_refs=3 * P0 + 32))])
+def test_page_outputs_may_touch_others(name, over):
+    """Arrays end to end, as in one allocation (the call is refused for its workspace, which comes last)."""
+    assert pages(name, ws_bytes=0, **over) == SPACE
