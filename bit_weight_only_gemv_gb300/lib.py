@@ -1301,7 +1301,16 @@ class LogitRules:
         self.per_row_mask = mask is not None and mask_rows is None
         self.tensors = (tokens, lens, prompt, repetition, presence, frequency, bias_ids, bias,
                         n_bias, mask, mask_rows)
-        self.struct = LogitRulesStruct(*[None if t is None else t.data_ptr() for t in self.tensors],
+        # a list of no columns has no address, and a null one would say that there is no such rule: its
+        # counts' stands for it, since nothing is read there
+        def place(t, counts):
+            t = counts if t is not None and t.dim() == 2 and t.shape[1] == 0 else t
+            return None if t is None else t.data_ptr()
+
+        self.struct = LogitRulesStruct(place(tokens, lens),
+                                       *[place(t, None) for t in self.tensors[1:6]],
+                                       place(bias_ids, n_bias), place(bias, n_bias),
+                                       *[place(t, None) for t in self.tensors[8:]],
                                        strides["tokens"], strides["bias"], strides["mask"],
                                        widths["tokens"], widths["bias"], self.masks)
 

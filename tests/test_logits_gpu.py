@@ -199,3 +199,30 @@ def test_many_rows(cuda_lib, dtype, B, V, hist, nb, masks, pad):
     c.args["repetition"][3] = 1e-39            # a quotient that no reciprocal gives
     c.args["repetition"][4] = 3e38
     c.check()
+
+
+@pytest.mark.parametrize("which", ["both", "tokens", "bias", "bias without counts", "slices"])
+def test_lists_of_no_columns(cuda_lib, which):
+    """No tokens yet, no biases in this batch: lists [rows, 0], which have no address of their own."""
+    c = Case(13, 3, 4099, 8, 5, [0.5, None, 0.9])
+    if which != "bias" and which != "bias without counts":
+        c.args["tokens"] = c.args["tokens"][:, :0]
+        c.args["lens"][:] = c.args["prompt"][:] = 0
+    if which != "tokens":
+        c.args["bias"], c.args["bias_ids"] = c.args["bias"][:, :0], c.args["bias_ids"][:, :0]
+        c.args["n_bias"][:] = 0
+    if which == "bias without counts":
+        del c.args["n_bias"]
+    if which == "slices":      # of tensors that are not empty
+        rules, wide = c.rules, torch.full((3, 9), 7, dtype=torch.int32, device="cuda")
+        c.rules = lambda: rules(tokens=wide[:, :0], bias_ids=wide[:, 3:3], bias=wide.float()[:, 2:2])
+    c.check()
+
+
+def test_counts_beyond_lists_of_no_columns(cuda_lib):
+    c = Case(14, 4, 4099, 8, 5, [0.5, None, 0.9, None])
+    c.args["tokens"] = c.args["tokens"][:, :0]
+    c.args["bias"], c.args["bias_ids"] = c.args["bias"][:, :0], c.args["bias_ids"][:, :0]
+    c.args["lens"][:] = c.args["prompt"][:] = c.args["n_bias"][:] = 0
+    c.args["lens"][1] = c.args["n_bias"][3] = 1
+    c.check(left=(1, 3), code="W4_ERR_INDEX")
