@@ -1098,8 +1098,11 @@ def _on(stream, *tensors):
 def bind_kv8_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
                      page_tokens: int, grow: torch.Tensor = None, workspace: torch.Tensor = None,
                      status: torch.Tensor = None):
-    """w4_kv8_reserve with its arguments marshalled once: returns call(pdl=False, stream=None)."""
+    """w4_kv8_reserve with its arguments marshalled once: returns call(pdl=False, stream=None).
+    workspace: kv8_pages_workspace_bytes(batch, pages) bytes."""
     _kv8_table(table, lens, refs)
+    if workspace is None:
+        raise ValueError("workspace must be a tensor of kv8_pages_workspace_bytes(batch, pages) bytes")
     if grow is not None:
         _need(grow, torch.int32, "grow")
         if grow.shape != lens.shape:
@@ -1115,7 +1118,12 @@ def kv8_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, pag
                 grow: torch.Tensor = None, workspace: torch.Tensor = None,
                 status: torch.Tensor = None, pdl: bool = False, stream=None):
     """lens += grow (None: one token for each row that has any), with pages for the new tokens, in
-    place."""
+    place.  workspace: None allocates one for this call."""
+    if workspace is None:
+        _kv8_table(table, lens, refs)
+        workspace = torch.empty(kv8_pages_workspace_bytes(lens.numel(), refs.numel()),
+                                dtype=torch.uint8, device=table.device)
+        _on(stream, workspace)
     bind_kv8_reserve(table, lens, refs, page_tokens, grow, workspace, status)(pdl, stream)
 
 

@@ -204,3 +204,18 @@ def test_copies_follow_the_decision_of_their_call(cuda_lib):
         if rep % 3 == 0:
             p.ws[4096:] = 1
         assert p.fork(parents)[3]
+
+
+@pytest.mark.parametrize("on_a_stream", [False, True])
+def test_reserve_brings_its_own_workspace(cuda_lib, on_a_stream):
+    p, q = (Pages(18, [16, 0, 15, 31], spare=16, max_pages=20).to_gpu() for _ in range(2))
+    p.reserve([1, 40, 0, 2])
+    stream = torch.cuda.Stream() if on_a_stream else None
+    grow = torch.tensor([1, 40, 0, 2], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    lib.kv8_reserve(q.table, q.lens, q.refs, q.P, grow, stream=stream)
+    torch.cuda.synchronize()
+    for a, b in ((p.table, q.table), (p.lens, q.lens), (p.refs, q.refs)):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        lib.bind_kv8_reserve(q.table, q.lens, q.refs, q.P)
