@@ -83,7 +83,20 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// (A quick quotient, two units of the last place off where a rounded one is half of one: weights stay
+// within the bound that w4_route states, and the choice does not hang on them.)
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
+
+// exp(a - b), a <= b, b finite, with what the difference loses by its rounding: |a - b| 2^-24 of the
+// result, which would be most of a small weight's error.  That rest is a number of its own (the
+// error of a sum, by six additions), and exp(d + rest) = exp(d) (1 + rest) to 2^-34.  Off by 5 2^-24
+// of the result: expf two units in the last place, the product half of one.
+__device__ __forceinline__ float exp_of_difference(float a, float b) {
+  const float d = a - b, back = d - a;
+  const float rest = (a - (d - back)) - (b + back);
+  const float f = expf(d);
+  return d > -110.0f ? fmaf(f, rest, f) : f;   // (0 from there on; the rest of an infinite d is none)
+}
 
 // The choice of one token with scores in 64 bits; sm holds E doubles of this
 // warp.  Lane j < k gets the j-th expert.
@@ -522,12 +535,12 @@ __device__ __forceinline__ void route_rows(const RouteParams& p, long long first
     if (p.renorm) {
       float t = warp_max_f(xl);
       if (p.sigmoid) t = fminf(t, 0.0f);
-      w = xl > -INFINITY ? (p.sigmoid && t == 0.0f ? sigmoid(xl) : expf(xl - t)) : 0.0f;
+      w = xl > -INFINITY ? (p.sigmoid && t == 0.0f ? sigmoid(xl) : exp_of_difference(xl, t)) : 0.0f;
       if (p.sigmoid && t < 0.0f) w = __fdividef(w, 1.0f + expf(xl));
       const float sum = warp_sum(w);
       w = sum > 0.0f ? p.scale * __fdividef(w, sum) : 0.0f;
     } else {
-      w = p.scale * (p.sigmoid ? sigmoid(xl) : __fdividef(expf(xl - top), z));
+      w = p.scale * (p.sigmoid ? sigmoid(xl) : __fdividef(exp_of_difference(xl, top), z));
     }
     if (has) {
       p.ids[row * p.k + lane] = e;
@@ -818,14 +831,14 @@ __global__ void __launch_bounds__(32 * kManyWarps) route_many_kernel(const __gri
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, o));
       if (p.sigmoid) t = fminf(t, 0.0f);
-      w = xl > -INFINITY ? (p.sigmoid && t == 0.0f ? sigmoid(xl) : expf(xl - t)) : 0.0f;
+      w = xl > -INFINITY ? (p.sigmoid && t == 0.0f ? sigmoid(xl) : exp_of_difference(xl, t)) : 0.0f;
       if (p.sigmoid && t < 0.0f) w = __fdividef(w, 1.0f + expf(xl));
       float sum = w;
 #pragma unroll
       for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);   // as 32 lanes do
       w = sum > 0.0f ? p.scale * __fdividef(w, sum) : 0.0f;
     } else {
-      w = p.scale * (p.sigmoid ? sigmoid(xl) : __fdividef(expf(xl - top), z));
+      w = p.scale * (p.sigmoid ? sigmoid(xl) : __fdividef(exp_of_difference(xl, top), z));
     }
     const uint32_t undone = __ballot_sync(kFull, redo && 4 * r4 + (lane >> 3) < p.rows);
     if (has && 4 * r4 + (lane >> 3) < p.rows && ((undone >> (lane & 24)) & 255u) == 0) {

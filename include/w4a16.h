@@ -918,7 +918,8 @@ size_t w4_kv8_evict_workspace_bytes(const w4_kv8_cache *cache, const w4_kv8_batc
  * groups.  The choice is that of c in 64 bits: scores are compared in 32 bits,
  * and a token with two that are nearer than 32 bits can tell goes through 64;
  * without a bias experts, and groups with group_best 1, are compared by x itself.
- * Weights are fp32, off by a few units in the last place.
+ * Weights are fp32, off by at most 2^-18 of their size (2^-17 where they are shares of
+ * a softmax over all experts, without renorm), and by 2^-125 * scale below that.
  *
  * ids, weights int32 and fp32 [rows][top_k].
  * logits       bf16 or fp32 (W4_TYPE_*), row t at element t * row_stride,

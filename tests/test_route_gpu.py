@@ -272,3 +272,33 @@ def test_groups_by_their_best_logit_alone(cuda_lib, score, spread, T, E, G, tg, 
     for t in range(0, T, max(1, T // 300)):
         ref = serve.route_row(x[t], None, k, G, tg, 1, score == "sigmoid", True, 1.0)
         assert np.array_equal(got[torch.float32][t], ref[0]), (t, got[torch.float32][t], ref[0])
+
+
+@pytest.mark.parametrize("T", [200, 4099])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score,renorm,offset", [
+    ("softmax", True, 60.3), ("softmax", True, 0.7), ("softmax", False, 60.3), ("softmax", False, 0.7),
+    ("sigmoid", True, -60.3), ("sigmoid", True, 5.3), ("sigmoid", False, -60.3), ("sigmoid", False, 5.3)])
+@pytest.mark.parametrize("E,k", [(128, 8), (1024, 8), (60, 32)])
+def test_weights_to_their_last_units(cuda_lib, T, dtype, score, renorm, offset, E, k):
+    """The bounds that w4_route states, in units of 2^-24 of a weight: expf 4, a quick quotient 4, a sum,
+    a product or a fused one 1 each.  Divided by their sum: softmax terms 5 (an exponential of a
+    difference and its rest), their sum 5 + 5 additions, quotient 4, scale 1: 20; sigmoids
+    exp / (1 + exp) 5 + 3 + 4, their sum 12 + 5, quotient 4, scale 1: 34.  A sigmoid alone 4 + 1 + 4 + 1:
+    10.  A softmax's share 5 + 4 + 1 and the whole sum: at most 63 + 5 additions, and quick exponentials
+    4 + 3.4 |d| each, with |d| at most ln(experts) on the average of their weights, 7: 106."""
+    rng = np.random.default_rng(E + k + T)
+    x = rng.normal(size=(T, E))
+    if score == "softmax":
+        x[:, rng.integers(0, E)] = offset           # far above the others, or among them
+    else:
+        x += offset
+    ids, w, status, held = run(x, k, 1, 1, 2, score, renorm, 1.5, None, dtype)
+    assert status == 0
+    units = {("softmax", True): 20, ("sigmoid", True): 34, ("sigmoid", False): 10, ("softmax", False): 106}
+    tol = units[score, renorm] * 2.0 ** -24
+    for t in range(0, T, max(1, T // 200)):
+        ref = serve.route_row(held[t], None, k, 1, 1, 2, score == "sigmoid", renorm, 1.5)
+        assert np.array_equal(ids[t], ref[0])
+        assert np.all(np.abs(w[t] - ref[1]) <= tol * ref[1] + 1.5 * 2.0 ** -125), \
+            (t, np.max(np.abs(w[t] / ref[1] - 1)) * 2.0 ** 24)
