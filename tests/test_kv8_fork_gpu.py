@@ -219,3 +219,76 @@ def test_reserve_brings_its_own_workspace(cuda_lib, on_a_stream):
         assert torch.equal(a, b)
     with pytest.raises(ValueError):
         lib.bind_kv8_reserve(q.table, q.lens, q.refs, q.P)
+
+
+# ---------------------------------------------------------------- refusals where a cluster decides
+# (more than 16384 pages, or more than 256 pieces of 128 table entries)
+LARGE = {"pages": dict(spare=17000), "pieces": dict(spare=40, max_pages=12000)}
+
+
+def large(seed, lens, size, H=1, **over):
+    return Pages(seed, lens, H=H, D=64, optional=False, **{**LARGE[size], **over})
+
+
+def spoil(p, how, b, at):
+    if how == "length":
+        p.pool.lens[b] = p.pool.table.shape[1] * p.P + 1
+    elif how == "negative":
+        p.pool.lens[b] = -1
+    elif how == "page":
+        p.pool.table[b, at] = -1
+    elif how == "high page":
+        p.pool.table[b, at] = p.num
+
+
+@pytest.mark.parametrize("how,at", [("parent", 0), ("low parent", 0), ("length", 0), ("negative", 0), ("page", 1),
+                                    ("high page", 1), ("page", 127), ("high page", 128), ("page", 311),
+                                    ("high page", 312)])
+@pytest.mark.parametrize("size", ["pages", "pieces", "small"])
+def test_fork_of_rows_out_of_bounds_at_any_size(cuda_lib, size, how, at):
+    """The last entry of row 2 is number 312, of its third piece."""
+    lens = [40, 5000, 5007, 2100]
+    p = large(20, lens, size) if size in LARGE else Pages(20, lens, H=1, spare=20, optional=False)
+    parents = [0, 0, 2, 2, 1, 3, -1]
+    if how == "parent":
+        parents[1] = 4
+    elif how == "low parent":
+        parents[1] = -2
+    spoil(p, how, 2, at)
+    p.to_gpu(most_rows=8).fork(parents)
+    assert int(p.status) == lib.STATUS_CODE["W4_ERR_INDEX"]
+
+
+@pytest.mark.parametrize("size", ["pages", "pieces"])
+def test_fork_with_one_page_too_few_in_a_large_pool(cuda_lib, size):
+    """Five rows that end in two pages: three copies.  What is free is kept by something else but for
+    three or two pages."""
+    for free in (3, 2):
+        p = large(21, [33, 17], size)
+        unused = np.flatnonzero(p.pool.refs == 0)
+        p.pool.refs[unused[:len(unused) - free]] += 1
+        copies = p.to_gpu(most_rows=5).fork([0, 0, 0, 1, 1])[3]
+        assert (copies is None) == (free == 2)
+
+
+@pytest.mark.parametrize("size", ["pages", "pieces"])
+@pytest.mark.parametrize("grow", [[1, 0, 40, 3000], [-1, 3, 2 ** 31 - 1, 64], None])
+@pytest.mark.parametrize("free", [None, 190, 5, 0])
+def test_reserve_in_a_large_pool(cuda_lib, size, grow, free):
+    p = large(22, [31, 16, 5000, 0], size, max_pages=12000)
+    if free is not None:
+        unused = np.flatnonzero(p.pool.refs == 0)
+        p.pool.refs[unused[:max(0, len(unused) - free)]] += 1
+    p.to_gpu().reserve(grow)
+
+
+@pytest.mark.parametrize("how,at", [("length", 0), ("negative", 0), ("page", 2), ("high page", 200), (None, 0)])
+@pytest.mark.parametrize("size", ["pages", "pieces", "small"])
+def test_compact_with_pages_that_stay(cuda_lib, size, how, at):
+    """Pages that something else keeps, and those of a row out of bounds, among the ones that move."""
+    lens, share = [40, 4000, 60, 3000], {3: (1, 100)}
+    p = large(23, lens, size, share=share, pins=15) if size in LARGE else \
+        Pages(23, lens, H=1, share=share, pins=15, spare=60, optional=False)
+    spoil(p, how, 1, at)
+    p.to_gpu().compact()
+    assert int(p.status) == (lib.STATUS_CODE["W4_ERR_INDEX"] if how else 0)
