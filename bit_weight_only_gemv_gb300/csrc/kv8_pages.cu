@@ -13,7 +13,9 @@
 // the workspace; copy_kernel moves it in every cache, one warp for the keys or
 // values of one (page, head), four 16-byte loads a lane in flight.
 // Four beams forked and grown 9.8 us, 128 beams over 30 layers 21 us (27 with
-// everything cold), 3400 pages of 16 layers made dense 147 us, 7.4 TB/s.
+// everything cold), 3400 pages of 16 layers made dense 147 us, 7.4 TB/s.  Growth by
+// many pages is serial: a prompt of 131072 tokens in pages of 16 takes 249 us in a small
+// pool and 1290 in a large one, where each free page comes through L2.
 #include <initializer_list>
 #include <mutex>
 

@@ -17,7 +17,8 @@
 // Every CTA of a row sees the whole lists, so all of them find the same errors.
 // Chains of loads bound it (counts, lists, logits), so each link has many in
 // flight: a warp's mask words come before the lists, histories sixteen tokens a
-// thread at a time; what the walk costs is instructions.
+// thread at a time.  Half of a warp's time is waiting for global loads (24 rows of 262144
+// under masks: 1.8 of 4 instructions issued a cycle at 32 warps an SM).
 #include <mutex>
 
 #include "kv8.cuh"
@@ -40,8 +41,9 @@ struct LogitParams {
 };
 
 // What a row's rules are, and logits under them.  The quotient by the repetition is a product
-// with its reciprocal, one rounding more, which the fused product with the frequency saves; far from
-// 1, where the reciprocal would be rounded harder, it is a division.
+// with its reciprocal: a logit has two roundings of 2^-24 there instead of one (a division is some ten
+// instructions for each of a lane's eight); far from 1, where the reciprocal would be rounded harder, it
+// is a division.  The product with the frequency is fused, one rounding less.
 struct RowRules {
   float rep, inv, pres, freq;
   bool divide;

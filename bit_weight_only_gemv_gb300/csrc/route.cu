@@ -6,8 +6,8 @@
 //
 // route_kernel<V, F32>: one warp a token.  Every group has as many lanes (a power
 // of two; without groups all 32), each with up to V neighbouring experts, so
-// that a group's best scores are a butterfly away.  Instructions bound it, so a
-// candidate is one word: its score as a fixed-point number above its place,
+// that a group's best scores are a butterfly away.  The chain of a token's instructions
+// bounds it (at 16384 tokens 1.65 of 4 issued a cycle and SM), so a candidate is one word: its score as a fixed-point number above its place,
 // places counted down.  One integer maximum over the warp then gives value,
 // expert and the lowest number among equals, and a lane's candidates, sorted once
 // by a network of minima and maxima, only move up.  What the word says of the
@@ -17,7 +17,8 @@
 //   with a bias            score + (bias - least bias) in about 2^-23 of their range
 // Of candidates, or groups, that are nearer than this (and the scores' fp32
 // errors) can tell, the order is found from 64-bit scores of those few alone; of
-// more than 32 such candidates by refine() over all experts.
+// more than 32 such candidates by refine() over all experts.  Such tokens are slow: 16384 random
+// ones over 256 experts in 8 groups take 15 us, with a spread that saturates the scores up to 1260.
 // One token takes 1.9 us in a graph, 192 tokens over 256 experts in 8 groups with
 // biases 3.3 us (latency: about 800 instructions a warp); for many tokens
 // route_many_kernel takes a quarter of the warps.
@@ -575,7 +576,7 @@ __device__ __noinline__ double exact_alone(const RouteParams& p, long long row, 
 // the call's end waits for; whatever this cannot settle (a NaN, a softmax with a bias, too many of
 // them, a lane whose eight were all taken) is left to route_rows.
 constexpr int kManyWarps = 4;
-constexpr int kManyRows = 4096;   // tokens from which on it is the faster one
+constexpr int kManyRows = 4096;   // tokens from which on it is the faster one, for any experts and groups
 
 template <int V, bool F32>
 __global__ void __launch_bounds__(32 * kManyWarps) route_many_kernel(const __grid_constant__ RouteParams p) {
@@ -1005,8 +1006,9 @@ extern "C" w4_status w4_route(int32_t* ids, float* weights, const w4_router* rou
                  : kv8::launch(bf16, dim3(grid), 32 * kRouteWarps, smem, stream, p);
   };
   // Many tokens over experts that eight lanes hold in whole vectors: half the instructions a token,
-  // a quarter of the warps (16384 tokens 19.5 -> 14.1 us over 256 experts in groups with biases,
-  // 7.8 -> 5.4 us over 128 without; 4096 tokens 9.1 -> 6.6 and 3.2 -> 2.7 us; 500 of them 3.3 -> 4.4).
+  // a quarter of the warps (16384 tokens 20 -> 16 us over 256 experts in groups with biases,
+  // 7.9 -> 5.6 us over 128 without; 4096 tokens 8.4 to 9.9 -> 7.6 to 8.8 and 3.2 -> 2.75; 3000 of them
+  // 7.0 -> 8.8 and 2.65 -> 2.7; 500 of them 3.1 -> 8.5 and 2.1 -> 2.5).
   if (rows >= kManyRows && p.k <= 8 && (p.E == 256 || p.E == 128 || p.E == 64) && (p.G & (p.G - 1)) == 0 && p.G <= 8 &&
       !kv8::misaligned(logits, 16) && row_stride * el % 16 == 0) {
     while ((8 >> p.shift8) > p.G) ++p.shift8;

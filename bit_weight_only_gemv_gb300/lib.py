@@ -976,7 +976,9 @@ def kv8_weigh(cache: KV8Cache, batch: KV8Batch, q: torch.Tensor, lse: torch.Tens
               window: int = 0, status: torch.Tensor = None, pdl: bool = False, stream=None,
               sel: torch.Tensor = None, n_sel: torch.Tensor = None):
     """Add the attention weight that each cached token receives from the new rows to
-    cache.weight (lse as given by kv8_attn for the same rows, with the same selection)."""
+    cache.weight (lse as given by kv8_attn for the same rows, with the same selection).  No two
+    sequences of the batch may share a page (as rows that kv8_fork made do): they would race on its
+    weights."""
     bind_kv8_weigh(cache, batch, q, lse, scale, window, status, sel, n_sel)(pdl, stream)
 
 
@@ -1074,7 +1076,7 @@ def kv8_fork(caches, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
              pdl: bool = False, stream=None):
     """(new_table, new_lens, new_refs): row b goes on from row parents[b] of the old table (-1:
     it is empty); the pages that rows will write to are their own.  Entries past a row's pages
-    are -1."""
+    are -1.  Rows that share pages cannot be weighed in one kv8_weigh call."""
     shape = (parents.numel(), table.shape[1])
     new_table = torch.full(shape, -1, dtype=torch.int32, device=table.device)
     new_lens, new_refs = torch.empty_like(parents), torch.empty_like(refs)

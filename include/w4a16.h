@@ -915,8 +915,8 @@ size_t w4_kv8_evict_workspace_bytes(const w4_kv8_cache *cache, const w4_kv8_batc
  *   weights[t] = scale * s[id], or, with renorm, scale * s[id] / (sum of the
  *                chosen s)  (0 each, should that sum be 0)
  * Equal scores are in order of number, lowest first, of experts and of
- * groups.  The choice is that of c in 64 bits: scores are compared in 32 bits,
- * and a token with two that are nearer than 32 bits can tell goes through 64;
+ * groups.  The choice is that of c in 64 bits, to their rounding: scores are compared in
+ * 32 bits, and a token with two that are nearer than 32 bits can tell goes through 64;
  * without a bias experts, and groups with group_best 1, are compared by x itself.
  * Weights are fp32, off by at most 2^-18 of their size (2^-17 where they are shares of
  * a softmax over all experts, without renorm), and by 2^-125 * scale below that.
