@@ -26,7 +26,7 @@
 //
 // 24 sequences of 4k to 16k tokens, 64 heads on 8 of 128 channels: 96 us, 5.5
 // TB/s (81% of a plain copy's rate), DRAM reads 1.000 of the bytes counted.
-// One token on 700 (512-token window, 8 heads on 2 of 256 channels): 15.7 us, a chain
+// One token on 700 (512-token window, 8 heads on 2 of 256 channels): 15.9 us, a chain
 // of about ten memory latencies: lengths, query and page ids, copies, the
 // join in shared memory, the parts, the arrival, the last CTA's join.
 #include <algorithm>

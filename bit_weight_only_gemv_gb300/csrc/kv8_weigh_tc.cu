@@ -16,7 +16,7 @@
 // copies of query tiles, two that bring their log sums, one that issues the MMAs.
 // Every wait is bounded.
 //
-// 2 x 256 rows of 32 heads on 8 of 128 channels, 8k keys: 37 us, 0.62 PFLOP/s
+// 2 x 256 rows of 32 heads on 8 of 128 channels, 8k keys: 38 us, 0.61 PFLOP/s
 // (a CTA a unit with its start in the open: 51; keys as legacy MMA fragments
 // in every warp: 120).  The weights' warps bound it: without their work 26.
 #include <algorithm>
